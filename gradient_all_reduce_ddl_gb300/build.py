@@ -1,8 +1,8 @@
 """Builds libddl.so in-tree for sm_103a (nvcc, no CMake).
 
 Sources compile in parallel into ``_build/``; the shared library lands next to
-this file, where the binding loads it.  No fast-math: the kernels' adds and
-multiplies must be single IEEE operations.
+this file, where the binding loads it.  No fast-math: the all-reduce kernels' adds
+and multiplies must be single IEEE operations.
 """
 from __future__ import annotations
 
@@ -18,7 +18,10 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(HERE, "libddl.so")
 BUILD = os.path.join(ROOT, "_build", "ddl")
 
-SOURCES = ["plan.cpp", "ddl_api.cu", "fold_kernels.cu", "step_kernels.cu", "noalloc.cu", "sgd_kernels.cu"]
+SOURCES = ["plan.cpp", "ddl_api.cu", "fold_kernels.cu", "step_kernels.cu", "noalloc.cu", "sgd_kernels.cu",
+           "product_kernels.cu", "linear_kernels.cu", "linear_api.cu", "ortho_kernels.cu", "ortho_api.cu"]
+# contractions with no bit-exact contract: fused multiply-adds allowed
+FMA_SOURCES = {"product_kernels.cu", "linear_kernels.cu", "ortho_kernels.cu"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC,-Wall",
          "-I", INCLUDE, "-I", CSRC]
@@ -38,7 +41,8 @@ def _stale() -> bool:
 
 def _compile(src: str, extra) -> str:
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-    cmd = ["nvcc", *ARCH, *FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    flags = [f for f in FLAGS if f != "-fmad=false"] if src in FMA_SOURCES else FLAGS
+    cmd = ["nvcc", *ARCH, *flags, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
     if src.endswith(".cpp"):
         cmd.insert(1, "-x")
         cmd.insert(2, "c++")

@@ -1,0 +1,367 @@
+// linear_api.cu -- the C entry points of the linear layers (include/ddl.h).
+#include <cuda_runtime.h>
+
+#include <cstring>
+#include <new>
+
+#include "api_util.h"
+#include "ddl.h"
+#include "linear_kernels.h"
+#include "product.h"
+
+namespace {
+
+struct Buffer {  // device memory that grows with the first calls that need it
+  void* p = nullptr;
+  size_t bytes = 0;
+};
+
+}  // namespace
+
+struct ddl_linear {
+  int64_t max_tokens, n_in, n_out;
+  int type;  // ddl::ElemType of x, w, y
+  int act;
+  int device = -1;
+  int sms = 0;
+  uint32_t* d_err = nullptr;
+  Buffer x, w, dz[ddl::kMaxPlanes], partial;
+};
+
+namespace {
+
+using ddl::Range;
+
+constexpr int64_t kMaxFeatures = 1 << 22;
+constexpr int64_t kMaxTokens = (1ll << 31) - 256;
+// What a tensor map and a tile index can address.
+constexpr int64_t kMaxTiles = (1ll << 31) - 1;
+
+ddl_status_t bind(ddl_linear* h) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  if (h->device >= 0) return h->device == dev ? DDL_OK : DDL_ERR_INVALID_ARG;
+  uint32_t* err = nullptr;
+  e = ddl::device_alloc(reinterpret_cast<void**>(&err), sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaMemset(err, 0, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) {
+    cudaFree(err);
+    return ddl::status_of(e);
+  }
+  h->d_err = err;
+  h->device = dev;
+  return DDL_OK;
+}
+
+ddl_status_t need(Buffer* b, size_t bytes) {
+  if (b->bytes >= bytes) return DDL_OK;
+  void* p = nullptr;
+  const cudaError_t e = ddl::device_alloc(&p, bytes);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  // never outgrown: the sizes asked for are the handle's maxima
+  b->p = p;
+  b->bytes = bytes;
+  return DDL_OK;
+}
+
+// A rows x cols 16-bit matrix as the caller gave it.
+struct Mat {
+  const void* p;
+  int64_t rows, cols, ld;
+  Range range(int esize) const {
+    return Range(p, p && rows ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)esize : 0);
+  }
+  bool tma() const { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+  bool vec4(int esize) const { return reinterpret_cast<uintptr_t>(p) % (4 * (size_t)esize) == 0 && ld % 4 == 0; }
+};
+
+bool fits(int64_t rows, int64_t ld, int64_t cols) {
+  return ld >= cols && ld <= (1ll << 31) && rows <= (1ll << 60) / ld;
+}
+
+// The matrix itself, or its copy with 16-byte aligned rows.
+ddl_status_t aligned(const Mat& m, int64_t max_rows, Buffer* b, cudaStream_t s, Mat* out) {
+  *out = m;
+  if (m.tma()) return DDL_OK;
+  const int64_t ldp = (int64_t)ddl::round8((uint64_t)m.cols);
+  const ddl_status_t st = need(b, (size_t)max_rows * (size_t)ldp * 2);
+  if (st != DDL_OK) return st;
+  *out = Mat{b->p, m.rows, m.cols, ldp};
+  return ddl::status_of(ddl::launch_pack16(m.p, m.ld, b->p, ldp, m.rows, m.cols, s));
+}
+
+bool map_of(ddl::ProductLaunch* L, int k, const Mat& m, int box_rows) {
+  return ddl::make_map(&L->maps[k], m.p, (uint64_t)m.rows, (uint64_t)m.cols, (uint64_t)m.ld, box_rows, L->bf16 != 0);
+}
+
+int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
+
+bool distinct(const Range* out, int n_out, const Range* in, int n_in) {
+  for (int i = 0; i < n_out; ++i) {
+    if (out[i].wraps()) return false;
+    for (int j = i + 1; j < n_out; ++j)
+      if (out[i].overlaps(out[j])) return false;
+    for (int j = 0; j < n_in; ++j)
+      if (in[j].wraps() || out[i].overlaps(in[j])) return false;
+  }
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+ddl_status_t ddl_linear_create(size_t max_tokens, size_t in_features, size_t out_features, ddl_dtype_t dtype,
+                               ddl_act_t act, ddl_linear_t* out) {
+  if (!out) return DDL_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (max_tokens < 1 || in_features < 1 || out_features < 1) return DDL_ERR_INVALID_ARG;
+  if (act < DDL_ACT_NONE || act > DDL_ACT_SILU) return DDL_ERR_INVALID_ARG;
+  if (dtype != DDL_FP32 && dtype != DDL_FP16 && dtype != DDL_BF16) return DDL_ERR_INVALID_ARG;
+  if (dtype == DDL_FP32 || max_tokens > (size_t)kMaxTokens || in_features > (size_t)kMaxFeatures ||
+      out_features > (size_t)kMaxFeatures)
+    return DDL_ERR_UNSUPPORTED;
+  ddl_linear* h = new (std::nothrow) ddl_linear();
+  if (!h) return DDL_ERR_OOM;
+  h->max_tokens = (int64_t)max_tokens;
+  h->n_in = (int64_t)in_features;
+  h->n_out = (int64_t)out_features;
+  h->type = dtype == DDL_BF16 ? ddl::kBF16 : ddl::kF16;
+  h->act = (int)act;
+  *out = h;
+  return DDL_OK;
+}
+
+ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
+                                const void* bias, const void* residual, size_t ldr, void* z, size_t ldz, void* y,
+                                size_t ldy, void* stream) {
+  if (!h || tokens > (size_t)h->max_tokens) return DDL_ERR_INVALID_ARG;
+  const int64_t T = (int64_t)tokens, K = h->n_in, N = h->n_out;
+  if (T == 0) return DDL_OK;
+  if (!x || !w || !y) return DDL_ERR_INVALID_ARG;
+  if (!fits(T, (int64_t)ldx, K) || !fits(N, (int64_t)ldw, K) || !fits(T, (int64_t)ldy, N) ||
+      (residual && !fits(T, (int64_t)ldr, N)) || (z && !fits(T, (int64_t)ldz, N)))
+    return DDL_ERR_INVALID_ARG;
+  const Mat mx{x, T, K, (int64_t)ldx}, mw{w, N, K, (int64_t)ldw}, my{y, T, N, (int64_t)ldy},
+      mz{z, T, N, (int64_t)ldz}, mr{residual, T, N, (int64_t)ldr}, mb{bias, 1, N, N};
+  for (const Mat* m : {&mx, &mw, &my, &mz, &mr, &mb})
+    if (reinterpret_cast<uintptr_t>(m->p) % 2) return DDL_ERR_INVALID_ARG;
+  // y may be the residual itself (each element is read before it is written, by the same thread)
+  const bool in_place = residual && residual == y && ldr == ldy;
+  const Range outs[2] = {my.range(2), mz.range(2)};
+  const Range ins[4] = {mx.range(2), mw.range(2), mb.range(2), in_place ? Range(nullptr, 0) : mr.range(2)};
+  if (!distinct(outs, 2, ins, 4)) return DDL_ERR_INVALID_ARG;
+  if (in_place && mr.range(2).overlaps(mz.range(2))) return DDL_ERR_INVALID_ARG;
+
+  // Few tokens: their side becomes the narrow side of the tiles, 32 or 64 wide, and the 128-row side
+  // walks the weights, which are the traffic then.
+  const int tile_n = T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const bool swap = tile_n < 128;
+  const int64_t tiles = swap ? blocks_of(N, ddl::kTileM) : blocks_of(T, ddl::kTileM) * blocks_of(N, tile_n);
+  if (tiles * 8 > kMaxTiles) return DDL_ERR_UNSUPPORTED;
+
+  ddl_status_t st = bind(h);
+  if (st != DDL_OK) return st;
+  for (const void* p : {x, w, bias, residual, (const void*)z, (const void*)y})
+    if (p && !ddl::device_pointer(p, h->device)) return DDL_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  Mat ax, aw;
+  if ((st = aligned(mx, h->max_tokens, &h->x, s, &ax)) != DDL_OK) return st;
+  if ((st = aligned(mw, N, &h->w, s, &aw)) != DDL_OK) return st;
+
+  ddl::ProductLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  L.bf16 = h->type == ddl::kBF16;
+  if (!map_of(&L, 0, ax, swap && tile_n == 32 ? 32 : ddl::kBoxRows) || !map_of(&L, 1, aw, ddl::kBoxRows))
+    return DDL_ERR_CUDA;
+  ddl::Product& P = L.inl[0];
+  P.M = (int32_t)(swap ? N : T);
+  P.N = (int32_t)(swap ? T : N);
+  P.K = (int32_t)K;
+  P.n_pass = 1;
+  P.a[0] = swap ? 1 : 0;
+  P.b[0] = swap ? 0 : 1;
+  P.scale[0] = 1.f;
+  P.chunk = (int32_t)blocks_of(K, ddl::kBlockK);
+  P.epi = ddl::kEpiLinear;
+  P.swap = swap;
+  P.type = h->type;
+  P.act = h->act;
+  P.vec = my.vec4(2) && (!z || mz.vec4(2)) && (!residual || mr.vec4(2)) && reinterpret_cast<uintptr_t>(bias) % 8 == 0;
+  P.bias = bias;
+  P.add = residual;
+  P.ld_add = mr.ld;
+  P.z = z;
+  P.ldz = mz.ld;
+  P.out = y;
+  P.ldo = my.ld;
+  L.n_inl = 1;
+  L.inl_tiles[0] = (int32_t)tiles;
+  L.n_tiles = (int32_t)tiles;
+  L.splits = ddl::choose_splits(tiles, P.chunk, h->sms);
+  L.err = h->d_err;
+  return ddl::status_of(ddl::launch_product(L, tile_n, false, h->sms, s));
+}
+
+ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, size_t ldy, const void* x, size_t ldx,
+                                 const void* w, size_t ldw, const void* z, size_t ldz, void* dx, size_t lddx, void* dw,
+                                 size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate, void* stream) {
+  if (!h || tokens > (size_t)h->max_tokens || (grad_dtype != DDL_FP32 && grad_dtype != DDL_FP16)) return DDL_ERR_INVALID_ARG;
+  if (!dx && !dw && !db) return DDL_ERR_INVALID_ARG;
+  const int64_t T = (int64_t)tokens, K = h->n_in, N = h->n_out;
+  const int ge = grad_dtype == DDL_FP32 ? 4 : 2;
+  if (T > 0 && (!dy || (dw && !x) || (dx && !w) || (h->act != ddl::kActNone && !z))) return DDL_ERR_INVALID_ARG;
+  const bool has_z = h->act != ddl::kActNone;
+  if (!fits(N, (int64_t)lddw, K) && dw) return DDL_ERR_INVALID_ARG;
+  if (T > 0 && (!fits(T, (int64_t)ldy, N) || (dw && !fits(T, (int64_t)ldx, K)) || (dx && !fits(N, (int64_t)ldw, K)) ||
+                (has_z && !fits(T, (int64_t)ldz, N)) || (dx && !fits(T, (int64_t)lddx, K))))
+    return DDL_ERR_INVALID_ARG;
+  const Mat mdy{dy, T, N, (int64_t)ldy}, mx{dw ? x : nullptr, T, K, (int64_t)ldx}, mw{dx ? w : nullptr, N, K, (int64_t)ldw},
+      mz{has_z ? z : nullptr, T, N, (int64_t)ldz}, mdx{dx, T, K, (int64_t)lddx}, mdw{dw, N, K, (int64_t)lddw},
+      mdb{db, 1, N, N};
+  for (const Mat* m : {&mdy, &mx, &mw, &mz, &mdx})
+    if (reinterpret_cast<uintptr_t>(m->p) % 2) return DDL_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(dw) % ge || reinterpret_cast<uintptr_t>(db) % ge) return DDL_ERR_INVALID_ARG;
+  const Range outs[3] = {mdx.range(2), mdw.range(ge), mdb.range(ge)};
+  const Range ins[4] = {mdy.range(2), mx.range(2), mw.range(2), mz.range(2)};
+  if (!distinct(outs, 3, ins, 4)) return DDL_ERR_INVALID_ARG;
+
+  const int64_t dx_tiles = dx ? blocks_of(T, ddl::kTileM) * blocks_of(K, 128) : 0;
+  const int64_t dw_tiles = dw ? blocks_of(N, ddl::kTileM) * blocks_of(K, 128) : 0;
+  if ((dx_tiles + dw_tiles) * 8 > kMaxTiles) return DDL_ERR_UNSUPPORTED;
+  ddl_status_t st = bind(h);
+  if (st != DDL_OK) return st;
+  for (const void* p : {mdy.p, mx.p, mw.p, mz.p, (const void*)dx, (const void*)dw, (const void*)db})
+    if (p && !ddl::device_pointer(p, h->device)) return DDL_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (T == 0) {  // an empty sum
+    cudaError_t e = cudaSuccess;
+    if (dw && !accumulate)
+      e = cudaMemset2DAsync(dw, (size_t)lddw * (size_t)ge, 0, (size_t)K * (size_t)ge, (size_t)N, s);
+    if (e == cudaSuccess && db && !accumulate) e = cudaMemsetAsync(db, 0, (size_t)N * (size_t)ge, s);
+    return ddl::status_of(e);
+  }
+
+  // dz: dy itself where it can be; else planes of dy act'(z).  GELU's and SiLU's slopes are not
+  // 16-bit numbers: a binary32 gradient sums 22 (binary16) or 24 (bfloat16) bits of dz, while 16-bit
+  // results take dz rounded to 16 bits, as they are rounded themselves.
+  const bool curved = h->act == ddl::kActGelu || h->act == ddl::kActSilu;
+  const bool f16 = h->type == ddl::kF16;
+  const int dw_planes = dw && curved && grad_dtype == DDL_FP32 ? (f16 ? 2 : 3) : 1;
+  const bool own_dz = (dx || dw) && (has_z || !mdy.tma());
+  const int n_planes = own_dz ? dw_planes : 0;
+  const int64_t ldp = own_dz ? (int64_t)ddl::round8((uint64_t)N) : mdy.ld;
+  for (int k = 0; k < n_planes; ++k)
+    if ((st = need(&h->dz[k], (size_t)h->max_tokens * (size_t)ldp * 2)) != DDL_OK) return st;
+  const int64_t row_blocks = blocks_of(T, ddl::kDzRows);
+  if (db && (st = need(&h->partial, (size_t)blocks_of(h->max_tokens, ddl::kDzRows) * (size_t)N * 4)) != DDL_OK) return st;
+  Mat ax, aw;
+  if (dw && (st = aligned(mx, h->max_tokens, &h->x, s, &ax)) != DDL_OK) return st;
+  if (dx && (st = aligned(mw, N, &h->w, s, &aw)) != DDL_OK) return st;
+  if (n_planes || db) {
+    ddl::DzParams d;
+    std::memset(&d, 0, sizeof(d));
+    d.dy = dy;
+    d.ldy = mdy.ld;
+    d.z = mz.p;
+    d.ldz = mz.ld;
+    d.rows = T;
+    d.cols = N;
+    d.type = h->type;
+    d.act = h->act;
+    d.n_planes = n_planes;
+    for (int k = 0; k < n_planes; ++k) d.planes[k] = static_cast<uint16_t*>(h->dz[k].p);
+    d.ldp = ldp;
+    d.partial = db ? static_cast<float*>(h->partial.p) : nullptr;
+    d.vec = mdy.vec4(2) && (!has_z || mz.vec4(2)) && N % 4 == 0;
+    cudaError_t e = ddl::launch_dz(d, s);
+    if (e == cudaSuccess && db)
+      e = ddl::launch_db(d.partial, row_blocks, N, db, grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16, accumulate, s);
+    if (e != cudaSuccess) return ddl::status_of(e);
+  }
+  if (!dx && !dw) return DDL_OK;
+
+  ddl::ProductLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  L.bf16 = !f16;
+  L.err = h->d_err;
+  const int planes = n_planes ? n_planes : 1;
+  for (int k = 0; k < planes; ++k)
+    if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBoxRows)) return DDL_ERR_CUDA;
+  if ((dw && !map_of(&L, 3, ax, ddl::kBoxRows)) || (dx && !map_of(&L, 4, aw, ddl::kBoxRows))) return DDL_ERR_CUDA;
+  int64_t longest = 0;
+  if (dw) {  // dw[n][k] = sum_t dz[t][n] x[t][k]: both operands with their rows contiguous
+    ddl::Product& P = L.inl[L.n_inl];
+    P.M = (int32_t)N;
+    P.N = (int32_t)K;
+    P.K = (int32_t)T;
+    P.a_mn = P.b_mn = 1;
+    P.n_pass = planes;
+    for (int k = 0; k < planes; ++k) {
+      P.a[k] = k;
+      P.b[k] = 3;
+      P.scale[k] = ddl::plane_scale(h->type, planes, k);
+    }
+    P.chunk = grad_dtype == DDL_FP32 ? 4 : (int32_t)blocks_of(T, ddl::kBlockK);
+    P.epi = ddl::kEpiStore;
+    P.out_type = grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16;
+    P.accumulate = accumulate ? 1 : 0;
+    P.vec = mdw.vec4(ge);
+    P.out = dw;
+    P.ldo = mdw.ld;
+    L.inl_tiles[L.n_inl++] = (int32_t)dw_tiles;
+    longest = blocks_of(T, ddl::kBlockK);
+  }
+  if (dx) {  // dx[t][k] = sum_n dz[t][n] w[n][k]
+    ddl::Product& P = L.inl[L.n_inl];
+    P.M = (int32_t)T;
+    P.N = (int32_t)K;
+    P.K = (int32_t)N;
+    P.b_mn = 1;
+    P.n_pass = 1;
+    P.b[0] = 4;
+    P.scale[0] = ddl::plane_scale(h->type, planes, 0);
+    P.chunk = (int32_t)blocks_of(N, ddl::kBlockK);
+    P.epi = ddl::kEpiStore;
+    P.out_type = h->type;
+    P.vec = mdx.vec4(2);
+    P.out = dx;
+    P.ldo = mdx.ld;
+    L.inl_tiles[L.n_inl++] = (int32_t)dx_tiles;
+    if (P.chunk > longest) longest = P.chunk;
+  }
+  L.n_tiles = L.inl_tiles[0] + L.inl_tiles[1];
+  L.splits = ddl::choose_splits(L.n_tiles, longest, h->sms);
+  return ddl::status_of(ddl::launch_product(L, 128, false, h->sms, s));
+}
+
+ddl_status_t ddl_linear_check(ddl_linear_t h, void* stream) {
+  if (!h) return DDL_ERR_INVALID_ARG;
+  if (h->device < 0) return DDL_OK;  // no GPU call yet
+  ddl_status_t st = bind(h);
+  if (st != DDL_OK) return st;
+  uint32_t v = 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(&v, h->d_err, sizeof(v), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && v) e = cudaMemsetAsync(h->d_err, 0, sizeof(v), s);
+  if (e == cudaSuccess && v) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  return v ? DDL_ERR_DEVICE_CHECK : DDL_OK;
+}
+
+ddl_status_t ddl_linear_destroy(ddl_linear_t h) {
+  if (!h) return DDL_OK;
+  cudaError_t e = cudaSuccess;
+  for (void* p : {(void*)h->d_err, h->x.p, h->w.p, h->dz[0].p, h->dz[1].p, h->dz[2].p, h->partial.p})
+    if (p) {
+      const cudaError_t f = cudaFree(p);  // waits for the device
+      if (e == cudaSuccess) e = f;
+    }
+  delete h;
+  return ddl::status_of(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,426 @@
+// ortho_api.cu -- the C entry points of the orthogonalised update (include/ddl.h).
+//
+// A handle holds the matrices' places in the flat buffers, and on the device
+// their planes (two X iterates in turn, the Gram matrix A, the polynomial B),
+// the products of each Newton-Schulz step and the tables of their tiles.  All
+// matrices go through each product in one launch.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+#include <new>
+#include <vector>
+
+#include "api_util.h"
+#include "ddl.h"
+#include "ortho_kernels.h"
+#include "product.h"
+
+namespace {
+
+// A launch of one kind of product over all matrices: products, tiles.
+struct Stage {
+  std::vector<ddl::Product> products;
+  std::vector<ddl::Tile> tiles;
+  ddl::Product* d_products = nullptr;
+  ddl::Tile* d_tiles = nullptr;
+  int splits = 1;
+};
+
+enum { kGram0, kGram1, kPoly, kApply0, kApply1, kLast0, kLast1, kStages };  // 0/1: the X iterate read
+
+}  // namespace
+
+struct ddl_ortho {
+  std::vector<ddl_matrix_t> mats;
+  int type;
+  int steps = 5;
+  float coeff[3] = {3.4445f, -4.7750f, 2.0315f};
+  float eps = 1e-7f;
+  uint64_t extent = 0;  // elements of the flat buffers that the matrices reach
+  int device = -1;
+  int sms = 0;
+  bool ready = false;
+  uint32_t* d_err = nullptr;
+  void* d_planes = nullptr;  // one block: every plane
+  CUtensorMap* d_maps = nullptr;
+  ddl::OrthoMatrix* d_mats = nullptr;
+  ddl::OrthoItem* d_items = nullptr;
+  double* d_partial = nullptr;
+  int n_items = 0;
+  Stage stage[kStages];
+};
+
+namespace {
+
+template <typename T>
+cudaError_t upload(T** dst, const T* src, size_t n) {
+  cudaError_t e = ddl::device_alloc(reinterpret_cast<void**>(dst), n * sizeof(T));
+  if (e == cudaSuccess) e = cudaMemcpy(*dst, src, n * sizeof(T), cudaMemcpyHostToDevice);
+  return e;
+}
+
+cudaError_t release(ddl_ortho* o) {
+  cudaError_t e = cudaSuccess;
+  auto drop = [&e](auto** p) {
+    if (*p) {
+      const cudaError_t f = cudaFree(*p);  // waits for the device
+      if (e == cudaSuccess) e = f;
+    }
+    *p = nullptr;
+  };
+  drop(&o->d_err);
+  drop(&o->d_planes);
+  drop(&o->d_maps);
+  drop(&o->d_mats);
+  drop(&o->d_items);
+  drop(&o->d_partial);
+  for (Stage& s : o->stage) {
+    drop(&s.d_products);
+    drop(&s.d_tiles);
+    s.products.clear();
+    s.tiles.clear();
+  }
+  o->ready = false;
+  return e;
+}
+
+// Planes of one matrix: X twice, A, B, each hi and lo.
+struct Planes {
+  uint64_t x[2][2], a[2], b[2];  // element offsets in d_planes
+  int64_t ldx, lds;
+};
+
+int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
+
+// x = hi + 2^-11 lo, so a product of two such operands is three passes; lo lo is below the last bit kept.
+void split_passes(ddl::Product* P, int a_hi, int b_hi) {
+  P->n_pass = 3;
+  const int a[3] = {a_hi, a_hi, a_hi + 1}, b[3] = {b_hi, b_hi + 1, b_hi};
+  for (int k = 0; k < 3; ++k) {
+    P->a[k] = a[k];
+    P->b[k] = b[k];
+    P->scale[k] = k == 0 ? 1.f : 1.f / 2048.f;
+  }
+  P->chunk = 4;
+}
+
+void add_tiles(Stage* st, int product, int64_t M, int64_t N, bool symmetric) {
+  const int tm = (int)blocks_of(M, ddl::kTileM), tn = (int)blocks_of(N, 128);
+  for (int i = 0; i < tm; ++i)
+    for (int j = 0; j < (symmetric ? i + 1 : tn); ++j) st->tiles.push_back({product, i, j, symmetric && j < i});
+}
+
+// Builds the device side: planes, maps, products and tiles.
+ddl_status_t build(ddl_ortho* o) {
+  const int n = (int)o->mats.size();
+  std::vector<Planes> pl(n);
+  uint64_t at = 0;
+  auto take = [&at](uint64_t elems) {
+    const uint64_t here = at;
+    at += (elems + 127) / 128 * 128;  // 256-byte aligned planes
+    return here;
+  };
+  for (int i = 0; i < n; ++i) {
+    const ddl_matrix_t& m = o->mats[i];
+    const uint64_t s = std::min(m.rows, m.cols);
+    pl[i].ldx = (int64_t)ddl::round8(m.cols);
+    pl[i].lds = (int64_t)ddl::round8(s);
+    for (auto& x : pl[i].x)
+      for (uint64_t& v : x) v = take(m.rows * (uint64_t)pl[i].ldx);
+    for (uint64_t& v : pl[i].a) v = take(s * (uint64_t)pl[i].lds);
+    for (uint64_t& v : pl[i].b) v = take(s * (uint64_t)pl[i].lds);
+  }
+  cudaError_t e = ddl::device_alloc(&o->d_planes, at * 2);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  uint16_t* base = static_cast<uint16_t*>(o->d_planes);
+
+  std::vector<CUtensorMap> maps((size_t)n * 8);
+  std::vector<ddl::OrthoMatrix> mats(n);
+  std::vector<ddl::OrthoItem> items;
+  for (int i = 0; i < n; ++i) {
+    const ddl_matrix_t& m = o->mats[i];
+    const uint64_t s = std::min(m.rows, m.cols);
+    const Planes& p = pl[i];
+    // maps 8 i + {0, 1}: X0, {2, 3}: X1, {4, 5}: A, {6, 7}: B
+    const uint64_t where[8] = {p.x[0][0], p.x[0][1], p.x[1][0], p.x[1][1], p.a[0], p.a[1], p.b[0], p.b[1]};
+    for (int k = 0; k < 8; ++k)
+      if (!ddl::make_map(&maps[(size_t)i * 8 + k], base + where[k], k < 4 ? m.rows : s, k < 4 ? m.cols : s,
+                         (uint64_t)(k < 4 ? p.ldx : p.lds), ddl::kBoxRows, false))
+        return DDL_ERR_CUDA;
+    ddl::OrthoMatrix& d = mats[i];
+    d.offset = (int64_t)m.offset;
+    d.ld = (int64_t)m.ld;
+    d.rows = (int64_t)m.rows;
+    d.cols = (int64_t)m.cols;
+    d.hi = base + p.x[0][0];
+    d.lo = base + p.x[0][1];
+    d.ldp = p.ldx;
+    d.item0 = (int32_t)items.size();
+    const int64_t elems = d.rows * d.cols;
+    for (int64_t b = 0; b < elems; b += ddl::kOrthoItemElems)
+      items.push_back({i, 0, b, std::min<int64_t>(elems, b + ddl::kOrthoItemElems)});
+    d.n_items = (int32_t)items.size() - d.item0;
+
+    const bool wide = m.rows <= m.cols;
+    const int map = 8 * i;
+    for (int k = 0; k < kStages; ++k) {
+      ddl::Product P;
+      std::memset(&P, 0, sizeof(P));
+      const int xi = k == kGram1 || k == kApply1 || k == kLast1 ? 1 : 0;  // the iterate read
+      bool symmetric = true;
+      if (k == kGram0 || k == kGram1) {  // A = X X^T, or X^T X when X is tall
+        P.M = P.N = (int32_t)s;
+        P.K = (int32_t)(wide ? m.cols : m.rows);
+        P.a_mn = P.b_mn = wide ? 0 : 1;
+        split_passes(&P, map + 2 * xi, map + 2 * xi);
+        P.epi = ddl::kEpiGram;
+      } else if (k == kPoly) {  // B = b A + c A A
+        P.M = P.N = P.K = (int32_t)s;
+        split_passes(&P, map + 4, map + 4);
+        P.epi = ddl::kEpiPoly;
+        P.c_hi = base + p.a[0];
+        P.c_lo = base + p.a[1];
+        P.ldc = p.lds;
+      } else {  // X' = a X + B X, or a X + X B when X is tall
+        symmetric = false;
+        P.M = (int32_t)m.rows;
+        P.N = (int32_t)m.cols;
+        P.K = (int32_t)s;
+        P.b_mn = wide ? 1 : 0;  // X as [K][N]; B is its own transpose
+        split_passes(&P, wide ? map + 6 : map + 2 * xi, wide ? map + 2 * xi : map + 6);
+        P.epi = k == kApply0 || k == kApply1 ? ddl::kEpiApply : ddl::kEpiOrtho;
+        P.c_hi = base + p.x[xi][0];
+        P.c_lo = base + p.x[xi][1];
+        P.ldc = p.ldx;
+        P.ldo = (int64_t)m.ld;
+        P.offset = (int64_t)m.offset;
+        P.shape_scale = wide ? 1.f : (float)std::sqrt((double)m.rows / (double)m.cols);
+      }
+      P.p_hi = base + (k == kPoly ? p.b[0] : k == kApply0 || k == kApply1 ? p.x[1 - xi][0] : p.a[0]);
+      P.p_lo = base + (k == kPoly ? p.b[1] : k == kApply0 || k == kApply1 ? p.x[1 - xi][1] : p.a[1]);
+      P.ldp = k == kApply0 || k == kApply1 ? p.ldx : p.lds;
+      // planes always allow 4-element accesses; the flat buffers' rows do where the offset and ld do
+      P.vec = k >= kLast0 ? (m.offset % 4 == 0 && m.ld % 4 == 0) : 1;
+      o->stage[k].products.push_back(P);
+      add_tiles(&o->stage[k], i, P.M, P.N, symmetric);
+    }
+  }
+  for (Stage& st : o->stage) {
+    // longest contractions first, so that the last tiles to start are short
+    std::stable_sort(st.tiles.begin(), st.tiles.end(), [&st](const ddl::Tile& x, const ddl::Tile& y) {
+      return st.products[x.product].K > st.products[y.product].K;
+    });
+    st.splits = ddl::choose_splits((int64_t)st.tiles.size(), blocks_of(st.products[st.tiles[0].product].K, ddl::kBlockK),
+                                   o->sms);
+    if (e == cudaSuccess) e = upload(&st.d_products, st.products.data(), st.products.size());
+    if (e == cudaSuccess) e = upload(&st.d_tiles, st.tiles.data(), st.tiles.size());
+  }
+  o->n_items = (int)items.size();
+  if (e == cudaSuccess) e = upload(&o->d_maps, maps.data(), maps.size());
+  if (e == cudaSuccess) e = upload(&o->d_mats, mats.data(), mats.size());
+  if (e == cudaSuccess) e = upload(&o->d_items, items.data(), items.size());
+  if (e == cudaSuccess) e = ddl::device_alloc(reinterpret_cast<void**>(&o->d_partial), items.size() * sizeof(double));
+  const uint32_t zero = 0;
+  if (e == cudaSuccess) e = upload(&o->d_err, &zero, 1);
+  return ddl::status_of(e);
+}
+
+// Binds the handle to the current device and builds its device side once.
+ddl_status_t bind(ddl_ortho* o) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  if (o->ready) return o->device == dev ? DDL_OK : DDL_ERR_INVALID_ARG;
+  e = cudaDeviceGetAttribute(&o->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  ddl_status_t st;
+  try {
+    st = build(o);
+  } catch (const std::bad_alloc&) {
+    st = DDL_ERR_OOM;
+  }
+  if (st != DDL_OK) {
+    release(o);
+    return st;
+  }
+  o->device = dev;
+  o->ready = true;
+  return DDL_OK;
+}
+
+// The products of every step; `last` is the kind of the final epilogue.
+ddl_status_t products(ddl_ortho* o, ddl::ProductLaunch* L, int last, bool vec, cudaStream_t s) {
+  L->g_maps = o->d_maps;
+  L->err = o->d_err;
+  L->ca = o->coeff[0];
+  L->cb = o->coeff[1];
+  L->cc = o->coeff[2];
+  L->last_epi = last;
+  L->flat_vec = vec;
+  int x = 0;
+  for (int k = 0; k < o->steps; ++k, x ^= 1) {
+    const int order[3] = {x ? kGram1 : kGram0, kPoly,
+                          k + 1 < o->steps ? (x ? kApply1 : kApply0) : (x ? kLast1 : kLast0)};
+    for (int kind : order) {
+      const Stage& st = o->stage[kind];
+      L->g_products = st.d_products;
+      L->g_tiles = st.d_tiles;
+      L->n_tiles = (int32_t)st.tiles.size();
+      L->splits = st.splits;
+      const cudaError_t e = ddl::launch_product(*L, 128, true, o->sms, s);
+      if (e != cudaSuccess) return ddl::status_of(e);
+    }
+  }
+  return DDL_OK;
+}
+
+int elem_size(int type) { return type == ddl::kF32 ? 4 : 2; }
+
+bool aligned4(const void* p, int esize) { return reinterpret_cast<uintptr_t>(p) % (4 * (size_t)esize) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+ddl_status_t ddl_ortho_create(int n_matrices, const ddl_matrix_t* matrices, ddl_dtype_t dtype, ddl_ortho_t* out) {
+  if (!out) return DDL_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (n_matrices < 1 || !matrices) return DDL_ERR_INVALID_ARG;
+  if (dtype != DDL_FP32 && dtype != DDL_FP16 && dtype != DDL_BF16) return DDL_ERR_INVALID_ARG;
+  constexpr uint64_t kMaxDim = 1 << 22, kMaxOffset = 1ull << 60;
+  uint64_t extent = 0, tiles = 0, items = 0;
+  bool unsupported = n_matrices > (1 << 20);
+  for (int i = 0; i < n_matrices; ++i) {
+    const ddl_matrix_t& m = matrices[i];
+    if (m.rows < 1 || m.cols < 1 || m.ld < m.cols || m.offset > kMaxOffset || m.ld > kMaxOffset / m.rows)
+      return DDL_ERR_INVALID_ARG;
+    if (m.rows > kMaxDim || m.cols > kMaxDim) {
+      unsupported = true;
+      continue;
+    }
+    extent = std::max<uint64_t>(extent, m.offset + (m.rows - 1) * m.ld + m.cols);
+    tiles += (uint64_t)blocks_of((int64_t)m.rows, 128) * (uint64_t)blocks_of((int64_t)m.cols, 128);
+    items += m.rows * m.cols / ddl::kOrthoItemElems + 1;
+  }
+  if (unsupported || tiles > (1ull << 27) || items > (1ull << 27)) return DDL_ERR_UNSUPPORTED;
+  ddl_ortho* o = new (std::nothrow) ddl_ortho();
+  if (!o) return DDL_ERR_OOM;
+  try {
+    o->mats.assign(matrices, matrices + n_matrices);
+    // a matrix's rows must not meet another's: compare the spans in order of their first element
+    std::vector<const ddl_matrix_t*> by(n_matrices);
+    for (int i = 0; i < n_matrices; ++i) by[i] = &o->mats[i];
+    std::sort(by.begin(), by.end(), [](const ddl_matrix_t* a, const ddl_matrix_t* b) { return a->offset < b->offset; });
+    for (int i = 0; i + 1 < n_matrices; ++i)
+      if (by[i]->offset + (by[i]->rows - 1) * by[i]->ld + by[i]->cols > by[i + 1]->offset) {
+        delete o;
+        return DDL_ERR_INVALID_ARG;
+      }
+  } catch (const std::bad_alloc&) {
+    delete o;
+    return DDL_ERR_OOM;
+  }
+  o->type = dtype == DDL_FP32 ? ddl::kF32 : dtype == DDL_FP16 ? ddl::kF16 : ddl::kBF16;
+  o->extent = extent;
+  *out = o;
+  return DDL_OK;
+}
+
+ddl_status_t ddl_ortho_set_polynomial(ddl_ortho_t o, int steps, float a, float b, float c, float eps) {
+  if (!o || steps < 1 || steps > 32 || !(eps >= 0.f)) return DDL_ERR_INVALID_ARG;
+  o->steps = steps;
+  o->coeff[0] = a;
+  o->coeff[1] = b;
+  o->coeff[2] = c;
+  o->eps = eps;
+  return DDL_OK;
+}
+
+ddl_status_t ddl_ortho_run(ddl_ortho_t o, const void* in, void* out, void* stream) {
+  if (!o || !in || !out) return DDL_ERR_INVALID_ARG;
+  const int es = elem_size(o->type);
+  if (reinterpret_cast<uintptr_t>(in) % es || reinterpret_cast<uintptr_t>(out) % es) return DDL_ERR_INVALID_ARG;
+  const ddl::Range ri(in, o->extent * es), ro(out, o->extent * es);
+  if (ri.wraps() || ro.wraps() || (in != out && ri.overlaps(ro))) return DDL_ERR_INVALID_ARG;
+  ddl_status_t st = bind(o);
+  if (st != DDL_OK) return st;
+  if (!ddl::device_pointer(in, o->device) || !ddl::device_pointer(out, o->device)) return DDL_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ddl::OrthoPrep p = {o->d_mats, o->d_items, o->d_partial, in, o->type, nullptr, 0.f, 0, o->eps, o->n_items};
+  cudaError_t e = ddl::launch_ortho_norms(p, s);
+  if (e == cudaSuccess) e = ddl::launch_ortho_planes(p, s);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  ddl::ProductLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  L.flat_out = out;
+  L.flat_type = o->type;
+  return products(o, &L, ddl::kEpiOrtho, aligned4(out, es), s);
+}
+
+ddl_status_t ddl_ortho_muon(ddl_ortho_t o, const void* grad, int n_copies, float* const* param_bufs, float* mom, float lr,
+                            float momentum, float weight_decay, int nesterov, void* stream) {
+  if (!o || !grad || !mom || n_copies < 1 || !param_bufs) return DDL_ERR_INVALID_ARG;
+  if (n_copies > ddl::kMaxCopies || o->type == ddl::kBF16) return DDL_ERR_UNSUPPORTED;
+  const int es = elem_size(o->type);
+  if (reinterpret_cast<uintptr_t>(grad) % es || reinterpret_cast<uintptr_t>(mom) % 4) return DDL_ERR_INVALID_ARG;
+  ddl::ProductLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  bool vec = true;
+  uintptr_t at[ddl::kMaxCopies + 1];
+  const uint64_t bytes = o->extent * 4;
+  const ddl::Range rg(grad, o->extent * es);
+  for (int r = 0; r <= n_copies; ++r) {
+    float* p = r < n_copies ? param_bufs[r] : mom;
+    const ddl::Range rp(p, bytes);
+    if (!p || reinterpret_cast<uintptr_t>(p) % 4 || rp.wraps() || rg.wraps() || rp.overlaps(rg)) return DDL_ERR_INVALID_ARG;
+    if (r < n_copies) {
+      L.copies[r] = p;
+      vec = vec && aligned4(p, 4);
+    }
+    at[r] = reinterpret_cast<uintptr_t>(p);
+  }
+  std::sort(at, at + n_copies + 1);
+  for (int r = 0; r < n_copies; ++r)
+    if (at[r] + bytes > at[r + 1]) return DDL_ERR_INVALID_ARG;
+  ddl_status_t st = bind(o);
+  if (st != DDL_OK) return st;
+  if (!ddl::device_pointer(grad, o->device) || !ddl::device_pointer(mom, o->device)) return DDL_ERR_INVALID_ARG;
+  for (int r = 0; r < n_copies; ++r)
+    if (!ddl::device_pointer(param_bufs[r], o->device)) return DDL_ERR_INVALID_ARG;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ddl::OrthoPrep p = {o->d_mats, o->d_items, o->d_partial, grad, o->type, mom, momentum, nesterov ? 1 : 0, o->eps,
+                      o->n_items};
+  cudaError_t e = ddl::launch_ortho_norms(p, s);
+  if (e == cudaSuccess) e = ddl::launch_ortho_planes(p, s);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  L.lr = lr;
+  L.decay = 1.f - lr * weight_decay;
+  L.n_copies = n_copies;
+  return products(o, &L, ddl::kEpiMuon, vec, s);
+}
+
+ddl_status_t ddl_ortho_check(ddl_ortho_t o, void* stream) {
+  if (!o) return DDL_ERR_INVALID_ARG;
+  if (!o->ready) return DDL_OK;  // no GPU call yet
+  const ddl_status_t st = bind(o);
+  if (st != DDL_OK) return st;
+  uint32_t v = 0;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaMemcpyAsync(&v, o->d_err, sizeof(v), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess && v) e = cudaMemsetAsync(o->d_err, 0, sizeof(v), s);
+  if (e == cudaSuccess && v) e = cudaStreamSynchronize(s);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  return v ? DDL_ERR_DEVICE_CHECK : DDL_OK;
+}
+
+ddl_status_t ddl_ortho_destroy(ddl_ortho_t o) {
+  if (!o) return DDL_OK;
+  const cudaError_t e = release(o);
+  delete o;
+  return ddl::status_of(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,109 @@
+// product.h -- launch records of the matrix products (internal).
+//
+// One kernel carries every product of the linear layers and of the
+// Newton-Schulz steps: D = sum over passes of scale * A B^T on the tensor
+// cores, then an epilogue on the binary32 sums.  Passes let an operand be the
+// sum of several 16-bit planes (x ~ hi + 2^-11 lo), which is how results that
+// are kept in binary32 get products of more than 11 bits.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace ddl {
+
+constexpr int kTileM = 128;      // output rows per tile
+constexpr int kBlockK = 64;      // contraction elements per stage (one 128-byte swizzle row)
+constexpr int kBoxRows = 64;     // rows of a TMA box
+constexpr int kMaxPasses = 3;
+constexpr int kMaxMaps = 8;      // tensor maps carried in the launch record
+constexpr int kMaxCopies = 256;  // parameter copies of the Muon step
+
+enum ElemType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
+enum ActKind : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
+enum EpilogueKind : int {
+  kEpiLinear = 0,  // z = D + bias; y = act(z) + residual
+  kEpiStore = 1,   // out = D (+ out)
+  kEpiGram = 2,    // planes of D, and of its transpose
+  kEpiPoly = 3,    // planes of b C + c D (C, D symmetric), and of the transpose
+  kEpiApply = 4,   // planes of a C + D
+  kEpiOrtho = 5,   // out = a C + D, in the matrix's place of a flat buffer
+  kEpiMuon = 6     // p = p (1 - lr wd) - lr s (a C + D) in every parameter copy
+};
+
+// One product.  A is M x K, B is N x K; a_mn / b_mn: stored with the rows
+// contiguous instead ([K][M], [K][N]).
+struct Product {
+  int32_t M, N, K;
+  int32_t a_mn, b_mn;
+  int32_t n_pass;
+  int32_t a[kMaxPasses], b[kMaxPasses];  // tensor map of each pass's operands
+  float scale[kMaxPasses];
+  int32_t chunk;   // K blocks summed in the tensor core before they are added in binary32 registers
+  int32_t epi;     // EpilogueKind
+  int32_t swap;    // D is the transpose of the output: D(i, j) belongs at out[j][i]
+  int32_t type;    // ElemType of bias, add, z
+  int32_t act;
+  int32_t out_type;
+  int32_t accumulate;
+  int32_t vec;     // every pointer and row stride of the epilogue allows 4-element accesses
+  const void* bias;
+  const void* add;   // residual
+  int64_t ld_add;
+  void* z;
+  int64_t ldz;
+  void* out;         // kEpiOrtho: element offset added to the launch's buffer
+  int64_t ldo;
+  // Newton-Schulz: C's planes, the result's planes (row strides ldc, ldp)
+  const uint16_t* c_hi;
+  const uint16_t* c_lo;
+  int64_t ldc;
+  uint16_t* p_hi;
+  uint16_t* p_lo;
+  int64_t ldp;
+  int64_t offset;    // the matrix's first element in the flat buffers
+  float shape_scale; // s of the Muon step
+};
+
+struct Tile {
+  int32_t product, ti, tj, mirror;
+};
+
+// Launch record.  Grouped launches read products, tiles and maps from device
+// memory; single launches carry up to two products and their maps here.
+struct ProductLaunch {
+  CUtensorMap maps[kMaxMaps];
+  Product inl[2];
+  int32_t n_inl;            // products in inl (0: grouped)
+  int32_t inl_tiles[2];     // tiles of each
+  const CUtensorMap* g_maps;
+  const Product* g_products;
+  const Tile* g_tiles;
+  int32_t n_tiles;
+  int32_t splits;           // CTAs of a cluster that share a tile's contraction
+  int32_t bf16;             // operands are bfloat16, else binary16
+  uint32_t* err;
+  // Newton-Schulz coefficients and the flat buffers of its last product
+  float ca, cb, cc;
+  int32_t last_epi;         // kEpiOrtho or kEpiMuon, where a product's own is kEpiOrtho
+  int32_t flat_vec;         // those buffers allow 4-element accesses
+  void* flat_out;
+  int32_t flat_type;
+  float lr, decay;          // decay = 1 - lr * weight_decay
+  int32_t n_copies;
+  float* copies[kMaxCopies];
+};
+
+// tile_n: 128, 64 or 32 output columns per tile.
+cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream);
+
+// Tensor map of a row-major 16-bit matrix (rows x cols, ld elements between
+// rows; 16-byte aligned base and row stride), boxes of 64 columns x box_rows.
+bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_rows, bool bf16);
+
+// Error word bits of these kernels.
+enum : uint32_t { kErrProductWait = 16u };
+
+}  // namespace ddl

@@ -25,13 +25,15 @@ _lib = ctypes.CDLL(LIB_PATH)
 # ddl_status_t
 DDL_OK, DDL_ERR_INVALID_ARG, DDL_ERR_UNSUPPORTED, DDL_ERR_OOM, DDL_ERR_CUDA, DDL_ERR_DEVICE_CHECK = range(6)
 # ddl_dtype_t
-DDL_FP32, DDL_FP16 = 0, 1
+DDL_FP32, DDL_FP16, DDL_BF16 = 0, 1, 2
 # ddl_topo_kind_t
 DDL_RING, DDL_MULTIRING, DDL_TORUS = 0, 1, 2
 # ddl_mode_t
 DDL_MODE_FUSED, DDL_MODE_STEPWISE, DDL_MODE_RANKORDER = 0, 1, 2
 # ddl_kernel_t
 DDL_KERNEL_AUTO, DDL_KERNEL_LDG, DDL_KERNEL_BULK_LOAD, DDL_KERNEL_CHUNKED = 0, 1, 3, 5
+# ddl_act_t
+DDL_ACT_NONE, DDL_ACT_RELU, DDL_ACT_GELU, DDL_ACT_SILU = range(4)
 
 EXPORTS = [
     "ddl_plan_create", "ddl_plan_set_layers", "ddl_plan_set_mode", "ddl_plan_set_kernel", "ddl_allreduce",
@@ -40,11 +42,19 @@ EXPORTS = [
     "ddl_plan_launches", "ddl_plan_kernel_name", "ddl_plan_check", "ddl_status_string", "ddl_plan_destroy",
     "ddl_allreduce_noalloc", "ddl_plan_cost", "ddl_plan_set_torus_dims", "ddl_allreduce_sgd", "ddl_selftest_wait_timeout",
     "ddl_allreduce_slab", "ddl_noalloc_check",
+    "ddl_linear_create", "ddl_linear_forward", "ddl_linear_backward", "ddl_linear_check", "ddl_linear_destroy",
+    "ddl_ortho_create", "ddl_ortho_set_polynomial", "ddl_ortho_run", "ddl_ortho_muon", "ddl_ortho_check",
+    "ddl_ortho_destroy",
 ]
 
 
 class ddl_topology_t(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("k", ctypes.c_int32), ("X", ctypes.c_int32), ("Y", ctypes.c_int32)]
+
+
+class ddl_matrix_t(ctypes.Structure):
+    _fields_ = [("offset", ctypes.c_size_t), ("rows", ctypes.c_size_t), ("cols", ctypes.c_size_t),
+                ("ld", ctypes.c_size_t)]
 
 
 _vp, _i, _sz, _u64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_float
@@ -84,6 +94,17 @@ _sig("ddl_status_string", ctypes.c_char_p, _i)
 _sig("ddl_plan_destroy", _i, _vp)
 _sig("ddl_allreduce_noalloc", _i, _i, _sz, _i, ddl_topology_t, _sz, _i, _P(_sz), _P(_vp), _f, _vp)
 _sig("ddl_noalloc_check", _i, _vp)
+_sig("ddl_linear_create", _i, _sz, _sz, _sz, _i, _i, _P(_vp))
+_sig("ddl_linear_forward", _i, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _vp, _sz, _vp, _sz, _vp, _sz, _vp)
+_sig("ddl_linear_backward", _i, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _i, _i, _vp)
+_sig("ddl_linear_check", _i, _vp, _vp)
+_sig("ddl_linear_destroy", _i, _vp)
+_sig("ddl_ortho_create", _i, _i, _P(ddl_matrix_t), _i, _P(_vp))
+_sig("ddl_ortho_set_polynomial", _i, _vp, _i, _f, _f, _f, _f)
+_sig("ddl_ortho_run", _i, _vp, _vp, _vp, _vp)
+_sig("ddl_ortho_muon", _i, _vp, _vp, _i, _P(_vp), _vp, _f, _f, _f, _i, _vp)
+_sig("ddl_ortho_check", _i, _vp, _vp)
+_sig("ddl_ortho_destroy", _i, _vp)
 
 
 class DDLError(RuntimeError):
@@ -269,6 +290,66 @@ def ddl_noalloc_check(stream=None):
     _ok(_lib.ddl_noalloc_check(_stream_handle(stream)), "ddl_noalloc_check")
 
 
+def ddl_linear_create(max_tokens, in_features, out_features, dtype, act=DDL_ACT_NONE):
+    h = ctypes.c_void_p()
+    _ok(_lib.ddl_linear_create(max_tokens, in_features, out_features, dtype, act, ctypes.byref(h)), "ddl_linear_create")
+    return h
+
+
+def ddl_linear_forward(layer, tokens, x, ldx, w, ldw, bias, residual, ldr, z, ldz, y, ldy, stream=None):
+    """Device pointers (or None) and row strides in elements."""
+    _ok(_lib.ddl_linear_forward(layer, tokens, x, ldx, w, ldw, bias, residual, ldr, z, ldz, y, ldy,
+                                _stream_handle(stream)), "ddl_linear_forward")
+
+
+def ddl_linear_backward(layer, tokens, dy, ldy, x, ldx, w, ldw, z, ldz, dx, lddx, dw, lddw, db, grad_dtype,
+                        accumulate=False, stream=None):
+    """Device pointers (or None) and row strides in elements."""
+    _ok(_lib.ddl_linear_backward(layer, tokens, dy, ldy, x, ldx, w, ldw, z, ldz, dx, lddx, dw, lddw, db, grad_dtype,
+                                 1 if accumulate else 0, _stream_handle(stream)), "ddl_linear_backward")
+
+
+def ddl_linear_check(layer, stream=None):
+    _ok(_lib.ddl_linear_check(layer, _stream_handle(stream)), "ddl_linear_check")
+
+
+def ddl_linear_destroy(layer):
+    _ok(_lib.ddl_linear_destroy(layer), "ddl_linear_destroy")
+
+
+def ddl_ortho_create(matrices, dtype):
+    """matrices: (offset, rows, cols) or (offset, rows, cols, ld) each."""
+    arr = (ddl_matrix_t * max(1, len(matrices)))()
+    for a, m in zip(arr, matrices):
+        a.offset, a.rows, a.cols = (int(v) for v in m[:3])
+        a.ld = int(m[3]) if len(m) > 3 else a.cols
+    h = ctypes.c_void_p()
+    _ok(_lib.ddl_ortho_create(len(matrices), arr, dtype, ctypes.byref(h)), "ddl_ortho_create")
+    return h
+
+
+def ddl_ortho_set_polynomial(ortho, steps, a, b, c, eps):
+    _ok(_lib.ddl_ortho_set_polynomial(ortho, steps, a, b, c, eps), "ddl_ortho_set_polynomial")
+
+
+def ddl_ortho_run(ortho, inp, out, stream=None):
+    _ok(_lib.ddl_ortho_run(ortho, *_dev_ptrs([inp, out]), _stream_handle(stream)), "ddl_ortho_run")
+
+
+def ddl_ortho_muon(ortho, grad, param_bufs, mom, lr, momentum=0.95, weight_decay=0.0, nesterov=True, stream=None):
+    g, m = _dev_ptrs([grad, mom])
+    _ok(_lib.ddl_ortho_muon(ortho, g, len(param_bufs), _ptr_array(_dev_ptrs(param_bufs)), m, lr, momentum,
+                            weight_decay, 1 if nesterov else 0, _stream_handle(stream)), "ddl_ortho_muon")
+
+
+def ddl_ortho_check(ortho, stream=None):
+    _ok(_lib.ddl_ortho_check(ortho, _stream_handle(stream)), "ddl_ortho_check")
+
+
+def ddl_ortho_destroy(ortho):
+    _ok(_lib.ddl_ortho_destroy(ortho), "ddl_ortho_destroy")
+
+
 # -- convenience object --------------------------------------------------------
 
 # the per-call path of Plan.allreduce: the same entry point without argtypes,
@@ -281,6 +362,8 @@ _NO_STREAM = object()  # no stream object seen yet (None means the current strea
 
 TOPOLOGIES = {"ring": DDL_RING, "multiring": DDL_MULTIRING, "torus": DDL_TORUS, "torus_nd": DDL_RING}
 DTYPES = {"f32": DDL_FP32, "f16": DDL_FP16}
+OPERAND_DTYPES = {"f32": DDL_FP32, "f16": DDL_FP16, "bf16": DDL_BF16}
+ACTIVATIONS = {"none": DDL_ACT_NONE, "relu": DDL_ACT_RELU, "gelu": DDL_ACT_GELU, "silu": DDL_ACT_SILU}
 MODES = {"fused": DDL_MODE_FUSED, "stepwise": DDL_MODE_STEPWISE, "rankorder": DDL_MODE_RANKORDER}
 KERNELS = {"auto": DDL_KERNEL_AUTO, "ldg": DDL_KERNEL_LDG, "bulkload": DDL_KERNEL_BULK_LOAD,
            "chunked": DDL_KERNEL_CHUNKED}
@@ -432,6 +515,147 @@ class Plan:
             ddl_plan_destroy(self.handle)
             self.handle = None
             self._c_handle = ctypes.c_void_p(None)  # a later call gets DDL_ERR_INVALID_ARG
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001 - interpreter shutdown
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+def _matrix(t, rows, cols, dtype, name):
+    """(pointer, row stride) of a rows x cols tensor with contiguous rows; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if tuple(t.shape) != (rows, cols):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
+    if str(t.dtype) != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+        raise ValueError(f"{name}: expected a CUDA tensor with contiguous, non-overlapping rows, strides {t.stride()}")
+    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+
+
+def _vector(t, n, dtype, name):
+    if t is None:
+        return None
+    if tuple(t.shape) != (n,):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n,)}")
+    if str(t.dtype) != dtype:
+        raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if not t.is_cuda or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name}: expected a contiguous CUDA vector")
+    return t.data_ptr()
+
+
+_TORCH_NAMES = {"f32": "torch.float32", "f16": "torch.float16", "bf16": "torch.bfloat16"}
+_GRAD_DTYPES = {"torch.float32": DDL_FP32, "torch.float16": DDL_FP16}
+
+
+class Linear:
+    """A linear layer y = act(x w^T + bias) + residual and its backward pass
+    (owns a ddl_linear_t).  Tensors are the caller's: 16-bit of ``dtype``, rows
+    contiguous at any stride; gradients binary32 or binary16, e.g. views into a
+    rank's flat gradient buffer."""
+
+    def __init__(self, in_features, out_features, max_tokens, dtype="f16", act="none"):
+        self.n_in, self.n_out, self.max_tokens, self.dtype, self.act = in_features, out_features, max_tokens, dtype, act
+        self._name = _TORCH_NAMES[dtype]
+        self.handle = None
+        self.handle = ddl_linear_create(max_tokens, in_features, out_features, OPERAND_DTYPES[dtype], ACTIVATIONS[act])
+
+    def forward(self, x, w, y, bias=None, residual=None, z=None, stream=None):
+        """Writes y (and the pre-activations z, where given); returns y."""
+        t, d = x.shape[0], self._name
+        px, ldx = _matrix(x, t, self.n_in, d, "x")
+        pw, ldw = _matrix(w, self.n_out, self.n_in, d, "w")
+        pr, ldr = _matrix(residual, t, self.n_out, d, "residual")
+        pz, ldz = _matrix(z, t, self.n_out, d, "z")
+        py, ldy = _matrix(y, t, self.n_out, d, "y")
+        ddl_linear_forward(self.handle, t, px, ldx, pw, ldw, _vector(bias, self.n_out, d, "bias"), pr, ldr, pz, ldz, py,
+                           ldy, stream)
+        return y
+
+    def backward(self, dy, x=None, w=None, z=None, dx=None, dw=None, db=None, accumulate=False, stream=None):
+        """Writes dx; writes dw and db, or adds to them."""
+        t, d = dy.shape[0], self._name
+        g = str((dw if dw is not None else db).dtype) if dw is not None or db is not None else "torch.float32"
+        if g not in _GRAD_DTYPES:
+            raise ValueError(f"gradients: dtype {g}, expected torch.float32 or torch.float16")
+        pdy, ldy = _matrix(dy, t, self.n_out, d, "dy")
+        px, ldx = _matrix(x, t, self.n_in, d, "x")
+        pw, ldw = _matrix(w, self.n_out, self.n_in, d, "w")
+        pz, ldz = _matrix(z, t, self.n_out, d, "z")
+        pdx, lddx = _matrix(dx, t, self.n_in, d, "dx")
+        pdw, lddw = _matrix(dw, self.n_out, self.n_in, g, "dw")
+        ddl_linear_backward(self.handle, t, pdy, ldy, px, ldx, pw, ldw, pz, ldz, pdx, lddx, pdw, lddw,
+                            _vector(db, self.n_out, g, "db"), _GRAD_DTYPES[g], accumulate, stream)
+
+    def check(self, stream=None):
+        ddl_linear_check(self.handle, stream)
+
+    def close(self):
+        if self.handle is not None:
+            ddl_linear_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001 - interpreter shutdown
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class Ortho:
+    """Newton-Schulz orthogonalisation of the matrices of a flat buffer, alone
+    or inside the Muon step (owns a ddl_ortho_t).  matrices: (offset, rows,
+    cols) or (offset, rows, cols, ld) each, in elements."""
+
+    def __init__(self, matrices, dtype="f32", steps=5, coefficients=(3.4445, -4.7750, 2.0315), eps=1e-7):
+        self.matrices = [tuple(int(v) for v in m) for m in matrices]
+        self.dtype = dtype
+        self.extent = max((m[0] + (m[1] - 1) * (m[3] if len(m) > 3 else m[2]) + m[2] for m in self.matrices), default=0)
+        self._name = _TORCH_NAMES[dtype]
+        self.handle = None
+        self.handle = ddl_ortho_create(self.matrices, OPERAND_DTYPES[dtype])
+        ddl_ortho_set_polynomial(self.handle, steps, *coefficients, eps)
+
+    def _flat(self, t, dtype, name):
+        if t.dim() != 1 or t.numel() < self.extent or str(t.dtype) != dtype or not t.is_cuda or (
+                t.numel() > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name}: expected a contiguous CUDA vector of {dtype} with at least {self.extent} elements")
+        return t
+
+    def run(self, inp, out, stream=None):
+        """Orthogonalises every matrix of inp into out; returns out."""
+        ddl_ortho_run(self.handle, self._flat(inp, self._name, "inp"), self._flat(out, self._name, "out"), stream)
+        return out
+
+    def muon(self, grad, params, mom, lr, momentum=0.95, weight_decay=0.0, nesterov=True, stream=None):
+        """Updates mom and every copy in params (a list, one per rank) in place."""
+        ddl_ortho_muon(self.handle, self._flat(grad, self._name, "grad"),
+                       [self._flat(p, "torch.float32", "params") for p in params],
+                       self._flat(mom, "torch.float32", "mom"), lr, momentum, weight_decay, nesterov, stream)
+
+    def check(self, stream=None):
+        ddl_ortho_check(self.handle, stream)
+
+    def close(self):
+        if self.handle is not None:
+            ddl_ortho_destroy(self.handle)
+            self.handle = None
 
     def __del__(self):
         try:

@@ -64,7 +64,9 @@ typedef enum {
 
 typedef enum {
   DDL_FP32 = 0, /* binary32 storage and arithmetic */
-  DDL_FP16 = 1  /* binary16 storage and hops, binary32 adds */
+  DDL_FP16 = 1, /* binary16 storage and hops, binary32 adds */
+  DDL_BF16 = 2  /* bfloat16 storage: operands and results of the linear layers and of
+                   ddl_ortho_run; not a type of the all-reduce */
 } ddl_dtype_t;
 
 typedef enum { DDL_RING = 0, DDL_MULTIRING = 1, DDL_TORUS = 2 } ddl_topo_kind_t;
@@ -369,6 +371,130 @@ ddl_status_t ddl_plan_check(ddl_plan_t plan);
  * CUDA context stays usable.  The pages have no counterpart: this checks the
  * library's own failure path without faulting or hanging the GPU. */
 ddl_status_t ddl_selftest_wait_timeout(ddl_plan_t plan, uint32_t limit_us, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Linear layers: the products on either side of a worker's gradient.  The
+ * backward pass writes its gradients where ddl_allreduce takes them: at any
+ * element of a rank's flat gradient buffer, in that buffer's type.  (The web
+ * pages have no counterpart; "forward, backward" are steps of the iteration in
+ * the Baidu write-up, opening paragraph.)
+ *
+ *   forward:   z = x w^T + bias;   y = act(z) + residual
+ *   backward:  dz = dy act'(z);    dx = dz w;    dw (+)= dz^T x;    db (+)= sum over tokens of dz
+ *
+ * x is tokens x in_features, w out_features x in_features, y, z, residual and
+ * dy tokens x out_features, all of the handle's 16-bit type (DDL_FP16 or
+ * DDL_BF16), rows at a stride of ld elements (ld >= columns, at most 2^31), at
+ * any 2-byte address; bias has out_features elements of that type.  Sums run in
+ * binary32 and are rounded once.  Rows that do not start at 16-byte boundaries
+ * (base and stride) are copied to the handle's workspace first; results do not
+ * change.
+ *
+ * A handle owns its workspace and an error word; memory is allocated by the
+ * first call that needs it (make that call before a stream capture).  It binds
+ * to the device that is current at its first GPU call, is not thread-safe, and
+ * its calls must not overlap on the GPU.  Buffers are the caller's; a call
+ * checks that they are device memory, and that nothing it writes overlaps
+ * anything else it was given, before any work is queued. */
+
+typedef enum {
+  DDL_ACT_NONE = 0,
+  DDL_ACT_RELU = 1,  /* max(z, 0); slope 0 at 0 */
+  DDL_ACT_GELU = 2,  /* z Phi(z), Phi the normal distribution function (no tanh approximation) */
+  DDL_ACT_SILU = 3   /* z / (1 + exp(-z)) */
+} ddl_act_t;
+
+typedef struct ddl_linear* ddl_linear_t;
+
+/* max_tokens: the most tokens of any call (sizes the workspace).
+ * in_features, out_features: 1..2^22.  dtype DDL_FP32 returns
+ * DDL_ERR_UNSUPPORTED.  Host-only. */
+ddl_status_t ddl_linear_create(size_t max_tokens, size_t in_features, size_t out_features, ddl_dtype_t dtype,
+                               ddl_act_t act, ddl_linear_t* out);
+
+/* bias, residual, z: NULL = absent.  z, if given, receives the
+ * pre-activations that ddl_linear_backward reads.  y may be the residual
+ * itself (same pointer and stride).  tokens = 0 queues nothing.  One launch
+ * (and a copy per operand with unaligned rows). */
+ddl_status_t ddl_linear_forward(ddl_linear_t layer, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
+                                const void* bias, const void* residual, size_t ldr, void* z, size_t ldz, void* y,
+                                size_t ldy, void* stream);
+
+/* dx (layer's type), dw, db (grad_dtype: DDL_FP32 or DDL_FP16): NULL = not
+ * wanted, at least one given.  x is read for dw, w for dx, z where the
+ * activation is not DDL_ACT_NONE; the others may be NULL.  accumulate != 0
+ * adds to dw and db (earlier micro-batches); 0 overwrites them; dx is always
+ * overwritten.  dw and db need their type's alignment only.  tokens = 0 gives
+ * empty sums.
+ * Rounding: binary32 gradients sum dz to 22 bits (DDL_FP16) or 24 bits
+ * (DDL_BF16); dx and binary16 gradients sum dz rounded to the layer's type
+ * (exact for DDL_ACT_NONE and DDL_ACT_RELU). */
+ddl_status_t ddl_linear_backward(ddl_linear_t layer, size_t tokens, const void* dy, size_t ldy, const void* x,
+                                 size_t ldx, const void* w, size_t ldw, const void* z, size_t ldz, void* dx, size_t lddx,
+                                 void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate, void* stream);
+
+/* Waits for `stream` and reads the handle's error word: DDL_ERR_DEVICE_CHECK
+ * if a bounded wait in a kernel ran out (the word is then cleared; results of
+ * the calls since the last check are not valid). */
+ddl_status_t ddl_linear_check(ddl_linear_t layer, void* stream);
+
+/* Frees the handle and its workspace.  NULL is accepted. */
+ddl_status_t ddl_linear_destroy(ddl_linear_t layer);
+
+/* ---------------------------------------------------------------------------
+ * Orthogonalised updates (Muon).  After the all-reduce every rank holds the
+ * same averaged gradient; a layer's matrix is then stepped along the nearest
+ * orthogonal matrix to its momentum instead of along the momentum itself.  The
+ * orthogonalisation is Newton-Schulz: X = G / (|G|_F + eps), then `steps` times
+ *   A = X X^T (X^T X where rows > cols),   X = a X + (b A + c A A) X,
+ * which drives the singular values towards one.  Operands are kept as pairs of
+ * binary16 numbers (22 bits) and sums in binary32: the polynomial's slope at zero
+ * multiplies early roundings by up to a^steps, so 16-bit operands would cost
+ * two to three digits.
+ *
+ * A handle covers the matrices of one flat buffer (the rank buffers' layout);
+ * all of them go through each product in one launch.  Elements outside every
+ * matrix are neither read nor written.  Ownership, device binding and threads
+ * as for the linear layers; all device memory (about 16 bytes per element) is
+ * allocated by the first GPU call. */
+
+typedef struct {
+  size_t offset;  /* first element in the flat buffers */
+  size_t rows, cols;
+  size_t ld;      /* elements between rows, >= cols */
+} ddl_matrix_t;
+
+typedef struct ddl_ortho* ddl_ortho_t;
+
+/* n_matrices >= 1 matrices, rows and cols 1..2^22, whose spans (first to last
+ * element) do not overlap.  dtype: type of ddl_ortho_run's buffers and of
+ * ddl_ortho_muon's gradient.  The polynomial starts as 5 steps of
+ * (3.4445, -4.7750, 2.0315) with eps = 1e-7.  The array is copied.  Host-only. */
+ddl_status_t ddl_ortho_create(int n_matrices, const ddl_matrix_t* matrices, ddl_dtype_t dtype, ddl_ortho_t* out);
+
+/* Other coefficients a, b, c, step count (1..32) or eps (>= 0).  Host-only. */
+ddl_status_t ddl_ortho_set_polynomial(ddl_ortho_t ortho, int steps, float a, float b, float c, float eps);
+
+/* Orthogonalises every matrix of the flat buffer `in` into `out` (both of the
+ * handle's type, in the handle's layout; out == in is allowed, any other
+ * overlap is refused). */
+ddl_status_t ddl_ortho_run(ddl_ortho_t ortho, const void* in, void* out, void* stream);
+
+/* The Muon step on n_copies (1..256) parameter copies, one per rank, each
+ * updated from its own values; for every matrix
+ *   v = momentum v + g;   u = nesterov ? g + momentum v : v
+ *   p = p (1 - lr weight_decay) - lr sqrt(max(1, rows / cols)) NS(u)
+ * grad: the averaged gradient (any rank's buffer after ddl_allreduce) in the
+ * handle's type, DDL_FP32 or DDL_FP16.  mom: one binary32 momentum buffer (the
+ * ranks' momenta are equal).  All buffers are distinct and in the handle's
+ * layout; parameters outside the matrices (biases, norms) are left to
+ * ddl_allreduce_sgd or the caller. */
+ddl_status_t ddl_ortho_muon(ddl_ortho_t ortho, const void* grad, int n_copies, float* const* param_bufs, float* mom,
+                            float lr, float momentum, float weight_decay, int nesterov, void* stream);
+
+/* As ddl_linear_check, ddl_linear_destroy. */
+ddl_status_t ddl_ortho_check(ddl_ortho_t ortho, void* stream);
+ddl_status_t ddl_ortho_destroy(ddl_ortho_t ortho);
 
 /* A static string for a status code. */
 const char* ddl_status_string(ddl_status_t status);
