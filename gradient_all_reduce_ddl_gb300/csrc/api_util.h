@@ -53,4 +53,12 @@ inline int choose_splits(int64_t tiles, int64_t blocks, int sms) {
   return s;
 }
 
+// Whether a product of `tiles128` 128 x 128 tiles runs faster as `tiles256` 256 x 256 tiles on CTA pairs: both sides'
+// rounds over the SMs, a pair's tile being twice a CTA's work at 1 / kPairGain of its time.
+constexpr double kPairGain = 1.7;
+inline bool prefer_pairs(int64_t tiles128, int64_t tiles256, int sms) {
+  const int64_t rounds128 = (tiles128 + sms - 1) / sms, rounds256 = (tiles256 + sms / 2 - 1) / (sms / 2);
+  return tiles128 > sms / 2 && (double)rounds256 * 2.0 < (double)rounds128 * kPairGain;
+}
+
 }  // namespace ddl

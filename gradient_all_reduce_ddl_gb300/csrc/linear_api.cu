@@ -157,13 +157,18 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
 
   // Few tokens: their side becomes the narrow side of the tiles, 32 or 64 wide, and the 128-row side
   // walks the weights, which are the traffic then.
-  const int tile_n = T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  int tile_n = T <= 32 ? 32 : T <= 64 ? 64 : 128;
   const bool swap = tile_n < 128;
-  const int64_t tiles = swap ? blocks_of(N, ddl::kTileM) : blocks_of(T, ddl::kTileM) * blocks_of(N, tile_n);
+  int64_t tiles = swap ? blocks_of(N, ddl::kTileM) : blocks_of(T, ddl::kTileM) * blocks_of(N, tile_n);
   if (tiles * 8 > kMaxTiles) return DDL_ERR_UNSUPPORTED;
 
   ddl_status_t st = bind(h);
   if (st != DDL_OK) return st;
+  const int64_t tiles256 = blocks_of(T, 256) * blocks_of(N, 256);
+  if (!swap && ddl::prefer_pairs(tiles, tiles256, h->sms)) {
+    tile_n = 256;
+    tiles = tiles256;
+  }
   for (const void* p : {x, w, bias, residual, (const void*)z, (const void*)y})
     if (p && !ddl::device_pointer(p, h->device)) return DDL_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -200,7 +205,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   L.n_inl = 1;
   L.inl_tiles[0] = (int32_t)tiles;
   L.n_tiles = (int32_t)tiles;
-  L.splits = ddl::choose_splits(tiles, P.chunk, h->sms);
+  L.splits = tile_n == 256 ? 1 : ddl::choose_splits(tiles, P.chunk, h->sms);
   L.err = h->d_err;
   return ddl::status_of(ddl::launch_product(L, tile_n, false, h->sms, s));
 }
@@ -228,8 +233,8 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   const Range ins[4] = {mdy.range(2), mx.range(2), mw.range(2), mz.range(2)};
   if (!distinct(outs, 3, ins, 4)) return DDL_ERR_INVALID_ARG;
 
-  const int64_t dx_tiles = dx ? blocks_of(T, ddl::kTileM) * blocks_of(K, 128) : 0;
-  const int64_t dw_tiles = dw ? blocks_of(N, ddl::kTileM) * blocks_of(K, 128) : 0;
+  int64_t dx_tiles = dx ? blocks_of(T, ddl::kTileM) * blocks_of(K, 128) : 0;
+  int64_t dw_tiles = dw ? blocks_of(N, ddl::kTileM) * blocks_of(K, 128) : 0;
   if ((dx_tiles + dw_tiles) * 8 > kMaxTiles) return DDL_ERR_UNSUPPORTED;
   ddl_status_t st = bind(h);
   if (st != DDL_OK) return st;
@@ -292,6 +297,13 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBoxRows)) return DDL_ERR_CUDA;
   if ((dw && !map_of(&L, 3, ax, ddl::kBoxRows)) || (dx && !map_of(&L, 4, aw, ddl::kBoxRows))) return DDL_ERR_CUDA;
   int64_t longest = 0;
+  const int64_t dx256 = dx ? blocks_of(T, 256) * blocks_of(K, 256) : 0;
+  const int64_t dw256 = dw ? blocks_of(N, 256) * blocks_of(K, 256) : 0;
+  const int tile_n = ddl::prefer_pairs(dx_tiles + dw_tiles, dx256 + dw256, h->sms) ? 256 : 128;
+  if (tile_n == 256) {
+    dx_tiles = dx256;
+    dw_tiles = dw256;
+  }
   if (dw) {  // dw[n][k] = sum_t dz[t][n] x[t][k]: both operands with their rows contiguous
     ddl::Product& P = L.inl[L.n_inl];
     P.M = (int32_t)N;
@@ -333,8 +345,8 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     if (P.chunk > longest) longest = P.chunk;
   }
   L.n_tiles = L.inl_tiles[0] + L.inl_tiles[1];
-  L.splits = ddl::choose_splits(L.n_tiles, longest, h->sms);
-  return ddl::status_of(ddl::launch_product(L, 128, false, h->sms, s));
+  L.splits = tile_n == 256 ? 1 : ddl::choose_splits(L.n_tiles, longest, h->sms);
+  return ddl::status_of(ddl::launch_product(L, tile_n, false, h->sms, s));
 }
 
 ddl_status_t ddl_linear_check(ddl_linear_t h, void* stream) {

@@ -1,18 +1,12 @@
 // linear_kernels.cu -- the linear layers' element-wise kernels: dz = dy act'(z)
 // as 16-bit planes with its column sums (the bias gradient), and the copy of
 // matrices whose rows are not 16-byte aligned.  All are bound by HBM traffic.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
+#include "activation.cuh"
 #include "linear_kernels.h"
 #include "product.h"
 
 namespace ddl {
 namespace {
-
-__device__ __forceinline__ float from16(uint16_t u, int type) {
-  return type == kBF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-}
 
 __global__ void pack16_kernel(const uint16_t* __restrict__ src, int64_t ld, uint16_t* __restrict__ dst, int64_t ldp,
                               int64_t rows, int64_t cols) {
@@ -25,19 +19,6 @@ __global__ void pack16_kernel(const uint16_t* __restrict__ src, int64_t ld, uint
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (col0 + 32 * j < cols) dst[r * ldp + col0 + 32 * j] = v[j];
-  }
-}
-
-__device__ __forceinline__ float act_slope(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : 0.f;
-    case kActGelu:
-      return 0.5f * (1.f + erff(z * 0.70710678118654752f)) + z * (expf(-0.5f * z * z) * 0.39894228040143268f);
-    case kActSilu: {
-      const float s = 1.f / (1.f + expf(-z));
-      return s * (1.f + z * (1.f - s));
-    }
-    default: return 1.f;
   }
 }
 

@@ -25,6 +25,7 @@ struct Stage {
   std::vector<ddl::Tile> tiles;
   ddl::Product* d_products = nullptr;
   ddl::Tile* d_tiles = nullptr;
+  int tile = 128;  // rows and columns of a tile: 128, or 256 on CTA pairs
   int splits = 1;
 };
 
@@ -106,10 +107,25 @@ void split_passes(ddl::Product* P, int a_hi, int b_hi) {
   P->chunk = 4;
 }
 
-void add_tiles(Stage* st, int product, int64_t M, int64_t N, bool symmetric) {
-  const int tm = (int)blocks_of(M, ddl::kTileM), tn = (int)blocks_of(N, 128);
-  for (int i = 0; i < tm; ++i)
-    for (int j = 0; j < (symmetric ? i + 1 : tn); ++j) st->tiles.push_back({product, i, j, symmetric && j < i});
+// The tiles of every product of a stage, longest contractions first so that the last to start are short.
+std::vector<ddl::Tile> tiles_of(const Stage& st, int tile, bool symmetric) {
+  std::vector<ddl::Tile> tiles;
+  for (int k = 0; k < (int)st.products.size(); ++k) {
+    const int tm = (int)blocks_of(st.products[k].M, tile), tn = (int)blocks_of(st.products[k].N, tile);
+    for (int i = 0; i < tm; ++i)
+      for (int j = 0; j < (symmetric ? i + 1 : tn); ++j) tiles.push_back({k, i, j, symmetric && j < i});
+  }
+  std::stable_sort(tiles.begin(), tiles.end(), [&st](const ddl::Tile& x, const ddl::Tile& y) {
+    return st.products[x.product].K > st.products[y.product].K;
+  });
+  return tiles;
+}
+
+// K blocks of the busiest of `workers` CTAs (or pairs), which take the tiles in turn.
+int64_t busiest(const Stage& st, const std::vector<ddl::Tile>& tiles, int workers) {
+  std::vector<int64_t> load(workers, 0);
+  for (size_t t = 0; t < tiles.size(); ++t) load[t % workers] += blocks_of(st.products[tiles[t].product].K, ddl::kBlockK);
+  return *std::max_element(load.begin(), load.end());
 }
 
 // Builds the device side: planes, maps, products and tiles.
@@ -169,7 +185,6 @@ ddl_status_t build(ddl_ortho* o) {
       ddl::Product P;
       std::memset(&P, 0, sizeof(P));
       const int xi = k == kGram1 || k == kApply1 || k == kLast1 ? 1 : 0;  // the iterate read
-      bool symmetric = true;
       if (k == kGram0 || k == kGram1) {  // A = X X^T, or X^T X when X is tall
         P.M = P.N = (int32_t)s;
         P.K = (int32_t)(wide ? m.cols : m.rows);
@@ -184,7 +199,6 @@ ddl_status_t build(ddl_ortho* o) {
         P.c_lo = base + p.a[1];
         P.ldc = p.lds;
       } else {  // X' = a X + B X, or a X + X B when X is tall
-        symmetric = false;
         P.M = (int32_t)m.rows;
         P.N = (int32_t)m.cols;
         P.K = (int32_t)s;
@@ -204,16 +218,22 @@ ddl_status_t build(ddl_ortho* o) {
       // planes always allow 4-element accesses; the flat buffers' rows do where the offset and ld do
       P.vec = k >= kLast0 ? (m.offset % 4 == 0 && m.ld % 4 == 0) : 1;
       o->stage[k].products.push_back(P);
-      add_tiles(&o->stage[k], i, P.M, P.N, symmetric);
     }
   }
-  for (Stage& st : o->stage) {
-    // longest contractions first, so that the last tiles to start are short
-    std::stable_sort(st.tiles.begin(), st.tiles.end(), [&st](const ddl::Tile& x, const ddl::Tile& y) {
-      return st.products[x.product].K > st.products[y.product].K;
-    });
-    st.splits = ddl::choose_splits((int64_t)st.tiles.size(), blocks_of(st.products[st.tiles[0].product].K, ddl::kBlockK),
-                                   o->sms);
+  for (int k = 0; k < kStages; ++k) {
+    Stage& st = o->stage[k];
+    const bool symmetric = k == kGram0 || k == kGram1 || k == kPoly;
+    st.tiles = tiles_of(st, 128, symmetric);
+    std::vector<ddl::Tile> pairs = tiles_of(st, 256, symmetric);
+    // a pair's tile is twice a CTA's work at 1 / kPairGain of its time
+    if ((int64_t)st.tiles.size() > o->sms / 2 &&
+        2.0 * (double)busiest(st, pairs, o->sms / 2) < ddl::kPairGain * (double)busiest(st, st.tiles, o->sms)) {
+      st.tiles = std::move(pairs);
+      st.tile = 256;
+    }
+    st.splits = st.tile == 256 ? 1
+                               : ddl::choose_splits((int64_t)st.tiles.size(),
+                                                    blocks_of(st.products[st.tiles[0].product].K, ddl::kBlockK), o->sms);
     if (e == cudaSuccess) e = upload(&st.d_products, st.products.data(), st.products.size());
     if (e == cudaSuccess) e = upload(&st.d_tiles, st.tiles.data(), st.tiles.size());
   }
@@ -269,7 +289,7 @@ ddl_status_t products(ddl_ortho* o, ddl::ProductLaunch* L, int last, bool vec, c
       L->g_tiles = st.d_tiles;
       L->n_tiles = (int32_t)st.tiles.size();
       L->splits = st.splits;
-      const cudaError_t e = ddl::launch_product(*L, 128, true, o->sms, s);
+      const cudaError_t e = ddl::launch_product(*L, st.tile, true, o->sms, s);
       if (e != cudaSuccess) return ddl::status_of(e);
     }
   }

@@ -96,7 +96,8 @@ struct ProductLaunch {
   float* copies[kMaxCopies];
 };
 
-// tile_n: 128, 64 or 32 output columns per tile.
+// tile_n: 128, 64 or 32 output columns per 128-row tile; 256: 256 x 256 tiles on CTA pairs (splits 1).  Grouped
+// launches take 128 or 256.
 cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream);
 
 // Tensor map of a row-major 16-bit matrix (rows x cols, ld elements between

@@ -6,8 +6,8 @@
 // on tcgen05 (128 x tile_n tiles, accumulators in TMEM), then one of the
 // epilogues of product.h.
 //
-// Roles of a CTA's ten warps: warp 0 loads operand boxes by TMA into a ring
-// of shared-memory stages, warp 1 issues the products, warps 2-9 take the
+// Roles of a CTA's warps: warp 0 loads operand boxes by TMA into a ring
+// of shared-memory stages, warp 1 issues the products, warps 4-11 take the
 // finished sums out of TMEM, add them in binary32 registers, pass them through
 // shared memory (so that every global access of the epilogue runs along rows)
 // and write the result.  The two TMEM accumulators alternate, so the epilogue
@@ -24,11 +24,11 @@
 //
 // Every wait is bounded.  One that runs out sets kErrProductWait; the CTA then
 // waits (bounded too) for its own loads and products, frees its TMEM and ends.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
+#include <algorithm>
 #include <atomic>
 
+#include "activation.cuh"
 #include "product.h"
 #include "tc_ptx.cuh"
 
@@ -37,34 +37,31 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;  // warps 2 and 3 only fill the first warpgroup
 constexpr int kEpiWarps = 8;
 constexpr int kBoxBytes = kBoxRows * kBlockK * 2;
 constexpr int kABytes = kTileM * kBlockK * 2;
 constexpr float kLoScale = 2048.f;  // lo planes hold (x - hi) * 2^11
 
-__host__ __device__ constexpr int stages(int bn) { return bn == 128 ? 4 : 6; }
-__host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + bn * kBlockK * 2; }
-__host__ __device__ constexpr int pitch(int bn) { return bn + 4; }  // floats; rows 4 banks apart
+// Per CTA: a pair (tile_n 256) splits both operands' rows between its CTAs.
+__host__ __device__ constexpr int b_rows(int bn) { return bn == 256 ? 128 : bn; }
+__host__ __device__ constexpr int stages(int bn) { return bn >= 128 ? 5 : 6; }
+__host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + b_rows(bn) * kBlockK * 2; }
+__host__ __device__ constexpr int slab(int bn) { return bn < 64 ? bn : 64; }  // columns passed on at a time
+__host__ __device__ constexpr int pitch(int cols) { return cols + 4; }        // floats; rows 4 banks apart
 __host__ __device__ constexpr int smem_bytes(int bn) {
-  return 1024 + stages(bn) * stage_bytes(bn) + kTileM * pitch(bn) * 4;
+  return 1024 + stages(bn) * stage_bytes(bn) + kTileM * pitch(slab(bn)) * 4;
 }
 
 // -- element access -------------------------------------------------------------
-
-__device__ __forceinline__ float from16(uint16_t u, int type) {
-  return type == kBF16 ? __uint_as_float((uint32_t)u << 16) : __half2float(__ushort_as_half(u));
-}
-__device__ __forceinline__ uint16_t to16(float x, int type) {
-  return type == kBF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
-}
 
 template <int V>
 __device__ __forceinline__ void load16(const void* base, int64_t at, int type, float (&v)[V]) {
   const uint16_t* p = static_cast<const uint16_t*>(base) + at;
   if constexpr (V == 4) {
-    const ushort4 u = *reinterpret_cast<const ushort4*>(p);
-    v[0] = from16(u.x, type), v[1] = from16(u.y, type), v[2] = from16(u.z, type), v[3] = from16(u.w, type);
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    const float2 a = from16x2(u.x, type), b = from16x2(u.y, type);
+    v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
   } else {
     v[0] = from16(*p, type);
   }
@@ -74,7 +71,7 @@ template <int V>
 __device__ __forceinline__ void store16(void* base, int64_t at, int type, const float (&v)[V]) {
   uint16_t* p = static_cast<uint16_t*>(base) + at;
   if constexpr (V == 4)
-    *reinterpret_cast<ushort4*>(p) = make_ushort4(to16(v[0], type), to16(v[1], type), to16(v[2], type), to16(v[3], type));
+    *reinterpret_cast<uint2*>(p) = make_uint2(to16x2(v[0], v[1], type), to16x2(v[2], v[3], type));
   else
     *p = to16(v[0], type);
 }
@@ -145,85 +142,116 @@ __device__ __forceinline__ void load_planes(const uint16_t* hi, const uint16_t* 
   for (int k = 0; k < V; ++k) v[k] += l[k] * (1.f / kLoScale);
 }
 
-__device__ __forceinline__ float activate(float z, int act) {
-  switch (act) {
-    case kActRelu: return z > 0.f ? z : (z != z ? z : 0.f);
-    case kActGelu: return z * (0.5f * (1.f + erff(z * 0.70710678118654752f)));
-    case kActSilu: return z / (1.f + expf(-z));
-    default: return z;
-  }
-}
+// -- epilogues ---------------------------------------------------------------------
 
-// -- epilogues: V values of D that belong at output row m, columns n.. ------------
-
-template <int V, bool GROUPED>
-__device__ __forceinline__ void emit(const Product& P, const ProductLaunch& p, int m, int n, float (&v)[V]) {
+// V values of D in each of R rows: rows m[i] of the output (where in[i]), columns n...  Every load of the R rows is
+// issued before the first is used.  v becomes what was stored (before the flat buffers' rounding).
+template <int V, int R, bool GROUPED>
+__device__ __forceinline__ void emit(const Product& P, const ProductLaunch& p, const int (&m)[R], const bool (&in)[R],
+                                     int n, float (&v)[R][V]) {
   if constexpr (!GROUPED) {
     if (P.epi == kEpiLinear) {
-      float t[V];
+      float t[V], add[R][V];
+      if (P.add) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (in[i]) load16(P.add, (int64_t)m[i] * P.ld_add + n, P.type, add[i]);
+      }
       if (P.bias) {
         load16(P.bias, n, P.type, t);
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] += t[k];
-      }
-      if (P.z) store16(P.z, (int64_t)m * P.ldz + n, P.type, v);
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = activate(v[k], P.act);
-      if (P.add) {
-        load16(P.add, (int64_t)m * P.ld_add + n, P.type, t);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[k] += t[k];
+          for (int k = 0; k < V; ++k) v[i][k] += t[k];
       }
-      store16(P.out, (int64_t)m * P.ldo + n, P.type, v);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        if (!in[i]) continue;
+        if (P.z) store16(P.z, (int64_t)m[i] * P.ldz + n, P.type, v[i]);
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][k] = activate(v[i][k], P.act);
+        if (P.add) {
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[i][k] += add[i][k];
+        }
+        store16(P.out, (int64_t)m[i] * P.ldo + n, P.type, v[i]);
+      }
     } else {
-      const int64_t at = (int64_t)m * P.ldo + n;
       if (P.accumulate) {
-        float t[V];
-        load_any(P.out, at, P.out_type, t);
+        float t[R][V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) v[k] += t[k];
+        for (int i = 0; i < R; ++i)
+          if (in[i]) load_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, t[i]);
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int k = 0; k < V; ++k) v[i][k] += t[i][k];
       }
-      store_any(P.out, at, P.out_type, v);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (in[i]) store_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, v[i]);
     }
   } else {
-    if (P.epi == kEpiGram) {
-      store_planes(P.p_hi, P.p_lo, (int64_t)m * P.ldp + n, v);
-      return;
-    }
-    float c[V];
-    load_planes(P.c_hi, P.c_lo, (int64_t)m * P.ldc + n, c);
-    if (P.epi == kEpiPoly) {
+    if (P.epi != kEpiGram) {
+      float c[R][V];
 #pragma unroll
-      for (int k = 0; k < V; ++k) v[k] = p.cb * c[k] + p.cc * v[k];
-      store_planes(P.p_hi, P.p_lo, (int64_t)m * P.ldp + n, v);
-      return;
-    }
+      for (int i = 0; i < R; ++i)
+        if (in[i]) load_planes(P.c_hi, P.c_lo, (int64_t)m[i] * P.ldc + n, c[i]);
+      const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = P.epi == kEpiPoly ? p.cc : 1.f;
 #pragma unroll
-    for (int k = 0; k < V; ++k) v[k] = p.ca * c[k] + v[k];
-    if (P.epi == kEpiApply) {
-      store_planes(P.p_hi, P.p_lo, (int64_t)m * P.ldp + n, v);
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][k] = cc * c[i][k] + cd * v[i][k];
+    }
+    if (P.epi != kEpiOrtho) {
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (in[i]) store_planes(P.p_hi, P.p_lo, (int64_t)m[i] * P.ldp + n, v[i]);
       return;
     }
-    const int64_t at = P.offset + (int64_t)m * P.ldo + n;
     if (p.last_epi == kEpiOrtho) {
-      store_any(p.flat_out, at, p.flat_type, v);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (in[i]) store_any(p.flat_out, P.offset + (int64_t)m[i] * P.ldo + n, p.flat_type, v[i]);
       return;
     }
     const float step = p.lr * P.shape_scale;
-    for (int r = 0; r < p.n_copies; r += 4) {  // four copies' loads in flight
-      float t[4][V];
+    constexpr int kFlight = R >= 4 ? 2 : 4;  // copies loaded at once
+    for (int r = 0; r < p.n_copies; r += kFlight) {
+      float t[kFlight][R][V];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (r + j < p.n_copies) load32(p.copies[r + j] + at, t[j]);
+      for (int j = 0; j < kFlight; ++j)
+        if (r + j < p.n_copies)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (r + j < p.n_copies) {
+          for (int i = 0; i < R; ++i)
+            if (in[i]) load32(p.copies[r + j] + P.offset + (int64_t)m[i] * P.ldo + n, t[j][i]);
 #pragma unroll
-          for (int k = 0; k < V; ++k) t[j][k] = t[j][k] * p.decay - step * v[k];
-          store32(p.copies[r + j] + at, t[j]);
-        }
+      for (int j = 0; j < kFlight; ++j)
+        if (r + j < p.n_copies)
+#pragma unroll
+          for (int i = 0; i < R; ++i) {
+            if (!in[i]) continue;
+#pragma unroll
+            for (int k = 0; k < V; ++k) t[j][i][k] = t[j][i][k] * p.decay - step * v[i][k];
+            store32(p.copies[r + j] + P.offset + (int64_t)m[i] * P.ldo + n, t[j][i]);
+          }
     }
   }
+}
+
+// One element.
+template <bool GROUPED>
+__device__ __forceinline__ float emit_one(const Product& P, const ProductLaunch& p, int m, int n, float x) {
+  const int mm[1] = {m};
+  const bool in[1] = {true};
+  float v[1][1] = {{x}};
+  emit<1, 1, GROUPED>(P, p, mm, in, n, v);
+  return v[0][0];
+}
+
+// The epilogue warps' own barrier.
+__device__ __forceinline__ void bar_sync_epilogue() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
 }
 
 struct Place {
@@ -239,9 +267,10 @@ __device__ __forceinline__ bool wide_access(const Product& P, const ProductLaunc
 
 template <int BN, bool GROUPED>
 __device__ __forceinline__ Place place(const ProductLaunch& p, int t) {
+  constexpr int BM = BN == 256 ? 2 * kTileM : kTileM;
   if constexpr (GROUPED) {
     const int4 u = __ldg(reinterpret_cast<const int4*>(p.g_tiles) + t);
-    return {p.g_products + u.x, u.y * kTileM, u.z * BN, u.w};
+    return {p.g_products + u.x, u.y * BM, u.z * BN, u.w};
   } else {
     int k = 0;
     if (t >= p.inl_tiles[0]) {
@@ -250,19 +279,119 @@ __device__ __forceinline__ Place place(const ProductLaunch& p, int t) {
     }
     const Product* P = &p.inl[k];
     // bands of 16 tile rows, column by column, so that CTAs in flight share operands in L2
-    const int rows = (P->M + kTileM - 1) / kTileM, cols = (P->N + BN - 1) / BN;
+    const int rows = (P->M + BM - 1) / BM, cols = (P->N + BN - 1) / BN;
     const int band = t / (16 * cols), first = band * 16;
     const int height = rows - first < 16 ? rows - first : 16;
     const int in = t - band * 16 * cols;
-    return {P, (first + in % height) * kTileM, in / height * BN, 0};
+    return {P, (first + in % height) * BM, in / height * BN, 0};
   }
 }
 
+// Where a tile's sums lie between the epilogue's two halves: this CTA's shared memory, or the shared memories of a
+// cluster whose CTAs each hold part of every sum.
+struct OwnSums {
+  uint32_t base;
+  __device__ __forceinline__ float one(uint32_t at) const { return ld_shared(base + at); }
+  __device__ __forceinline__ void four(uint32_t at, float (&v)[4]) const { ld_shared4(base + at, v); }
+};
+struct ClusterSums {
+  uint32_t base;
+  int parts;
+  __device__ __forceinline__ float one(uint32_t at) const {
+    float v = 0.f;
+    for (int k = 0; k < parts; ++k) v += ld_peer(peer_addr(base + at, k));
+    return v;
+  }
+  __device__ __forceinline__ void four(uint32_t at, float (&v)[4]) const {
+    v[0] = v[1] = v[2] = v[3] = 0.f;
+    for (int k = 0; k < parts; ++k) {
+      const float4 u = ld_peer4(peer_addr(base + at, k));
+      v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
+    }
+  }
+};
+
+// Writes rows [r0, r1) of 128 x COLS sums that begin at D(row0, col0), along rows of D.  back: the finished values
+// also replace the sums in this CTA's shared memory.
+template <int COLS, bool GROUPED, class Sums>
+__device__ __forceinline__ void write_rows(const Product& P, const ProductLaunch& p, int row0, int col0, int lane, int ew,
+                                           int r0, int r1, bool back, const Sums sums) {
+  constexpr int kPitch = pitch(COLS), kBatch = 4;
+  constexpr int kLanes = COLS / 4 < 32 ? COLS / 4 : 32, kRows = 32 / kLanes;  // lanes on a row, rows at a time
+  const int M = P.M, N = P.N;
+  if (wide_access<GROUPED>(P, p)) {
+    for (int c = lane % kLanes * 4; c < COLS; c += kLanes * 4) {
+      const int n = col0 + c;
+      if (n >= N) continue;
+      for (int rr = r0 + ew * kRows + lane / kLanes; rr < r1; rr += kEpiWarps * kRows * kBatch) {
+        int m[kBatch];
+        bool in[kBatch];
+        float v[kBatch][4];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+          const int r = rr + i * kEpiWarps * kRows;
+          m[i] = row0 + r;
+          in[i] = r < r1 && m[i] < M;
+          if (in[i]) sums.four((r * kPitch + c) * 4, v[i]);
+        }
+        if (n + 4 <= N) {
+          emit<4, kBatch, GROUPED>(P, p, m, in, n, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (in[i] && n + k < N) v[i][k] = emit_one<GROUPED>(P, p, m[i], n + k, v[i][k]);
+        }
+        if (back) {
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            if (in[i]) st_shared4(sums.base + ((rr + i * kEpiWarps * kRows) * kPitch + c) * 4, v[i]);
+        }
+      }
+    }
+  } else {  // rows at any alignment: a warp along a row, element by element
+    for (int r = r0 + ew; r < r1; r += kEpiWarps) {
+      if (row0 + r >= M) break;
+      for (int c = lane; c < COLS; c += 32)
+        if (col0 + c < N) emit_one<GROUPED>(P, p, row0 + r, col0 + c, sums.one((r * kPitch + c) * 4));
+    }
+  }
+}
+
+// Writes the sums with D(i, j) at output row j, column i.  A warp takes 32 rows i, so that its stores run along
+// output rows.  finished: the values are final (symmetric products' mirror images).
+template <int COLS, bool GROUPED, class Sums>
+__device__ __forceinline__ void write_transposed(const Product& P, const ProductLaunch& p, int row0, int col0, int lane,
+                                                 int first, int step, bool finished, const Sums sums) {
+  constexpr int kPitch = pitch(COLS);
+  for (int u = first; u < COLS; u += step) {
+    const int i = (u & 3) * 32 + lane, c = (u >> 2) * 4, n = row0 + i;
+    if (n >= P.M) continue;
+    float v[4];
+    sums.four((i * kPitch + c) * 4, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int m = col0 + c + k;
+      if (m >= P.N) continue;
+      if (finished) {
+        float w[1] = {v[k]};
+        store_planes(P.p_hi, P.p_lo, (int64_t)m * P.ldp + n, w);
+      } else {
+        emit_one<GROUPED>(P, p, m, n, v[k]);
+      }
+    }
+  }
+}
+
+// BN 256: a cluster of two CTAs makes a 256 x 256 tile, each CTA 128 of its rows, from one stream of products that
+// the even CTA issues for both.
 template <int BN, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductLaunch p) {
+  constexpr bool PAIR = BN == 256;
   constexpr int kStages = stages(BN);
-  constexpr int kPitch = pitch(BN);
   constexpr uint32_t kCols = 2 * BN;
+  constexpr int kSlab = slab(BN), kSlabPitch = pitch(kSlab), kHalf = kSlab / 2, kSlabs = BN / kSlab;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5];
   __shared__ uint32_t tmem_slot;
@@ -279,28 +408,34 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     for (int b = 0; b < 2; ++b) {
       bar_init(tfull + 8 * b, 1);
-      bar_init(tempty + 8 * b, kEpiWarps);
+      bar_init(tempty + 8 * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
     }
     bar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_slot), kCols);
+    tmem_alloc<PAIR>(smem_u32(&tmem_slot), kCols);
     fence_before();
   }
   __syncthreads();
+  if constexpr (PAIR) cluster_sync();  // the peer's barriers exist
   fence_after();
   const uint32_t tmem = tmem_slot;
   griddep_launch();
   griddep_wait();
 
-  const int S = p.splits;
-  const int q = S > 1 ? (int)cluster_rank() : 0;
-  const int first = blockIdx.x / S, step = gridDim.x / S;
+  const int S = PAIR ? 1 : p.splits;
+  const int rank = PAIR || S > 1 ? (int)cluster_rank() : 0;
+  const int q = PAIR ? 0 : rank;
+  const int ctas = PAIR ? 2 : S;
+  const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
+  const int my_rows = PAIR ? rank * kTileM : 0;  // this CTA's part of the tile's rows
   const CUtensorMap* maps = GROUPED ? p.g_maps : p.maps;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  // The epilogue's sums want registers: 384 threads of 168 become 128 of 40 and 256 of 232 (64,512 either way).
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0 && lane == 0) {
       uint32_t it = 0;
       bool ok = true;
       for (int t = first; t < p.n_tiles && ok; t += step) {
@@ -317,39 +452,60 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           for (int kb = kb0; kb < kb1; ++kb, ++it) {
             const uint32_t s = it % kStages;
             if (!bar_wait(empty + 8 * s, (it / kStages & 1u) ^ 1u)) {
-              atomicOr(p.err, kErrProductWait);
               ok = false;
               break;
             }
-            const uint32_t sa = ring + s * stage_bytes(BN), sb = sa + kABytes, bar = full + 8 * s;
-            bar_expect(bar, stage_bytes(BN));
-#pragma unroll
-            for (int h = 0; h < kTileM / kBoxRows; ++h) {
-              const int row = pl.row0 + h * kBoxRows;
-              tma_box(sa + h * kBoxBytes, ma, bar, P.a_mn ? row : kb * kBlockK, P.a_mn ? kb * kBlockK : row);
+            const uint32_t sa = ring + s * stage_bytes(BN), sb = sa + kABytes;
+            uint32_t bar = full + 8 * s;
+            if constexpr (PAIR) {  // both CTAs' loads count on the even one's barrier
+              if (rank == 0)
+                bar_expect(bar, 2 * stage_bytes(BN));
+              else
+                bar = peer_addr(bar, 0);
+            } else {
+              bar_expect(bar, stage_bytes(BN));
             }
 #pragma unroll
-            for (int h = 0; h < (BN + kBoxRows - 1) / kBoxRows; ++h) {
-              const int row = pl.col0 + h * kBoxRows;
-              tma_box(sb + h * kBoxBytes, mb, bar, P.b_mn ? row : kb * kBlockK, P.b_mn ? kb * kBlockK : row);
+            for (int h = 0; h < kTileM / kBoxRows; ++h) {
+              const int row = pl.row0 + my_rows + h * kBoxRows;
+              const int x = P.a_mn ? row : kb * kBlockK, y = P.a_mn ? kb * kBlockK : row;
+              if constexpr (PAIR)
+                tma_box_pair(sa + h * kBoxBytes, ma, bar, x, y);
+              else
+                tma_box(sa + h * kBoxBytes, ma, bar, x, y);
+            }
+#pragma unroll
+            for (int h = 0; h < (b_rows(BN) + kBoxRows - 1) / kBoxRows; ++h) {
+              const int row = pl.col0 + my_rows + h * kBoxRows;
+              const int x = P.b_mn ? row : kb * kBlockK, y = P.b_mn ? kb * kBlockK : row;
+              if constexpr (PAIR)
+                tma_box_pair(sb + h * kBoxBytes, mb, bar, x, y);
+              else
+                tma_box(sb + h * kBoxBytes, mb, bar, x, y);
             }
           }
         }
       }
-      // loads in flight end before the CTA does
-      for (uint32_t k = it > (uint32_t)kStages ? it - kStages : 0; k < it; ++k)
-        if (!bar_wait(full + 8 * (k % kStages), k / kStages & 1u)) break;
+      if (!ok) atomicOr(p.err, kErrProductWait);
+      // Loads in flight end before the CTA does.  The odd CTA of a pair has no barrier of its own for them: its
+      // loads are done when the pair's last sums are (below), and after a wait that ran out it gives them 10 ms.
+      if (PAIR && rank != 0) {
+        if (!ok)
+          for (const uint64_t t0 = now_ns(); now_ns() - t0 < 10000000ull;) {
+          }
+      } else {
+        for (uint32_t k = it > (uint32_t)kStages ? it - kStages : 0; k < it; ++k)
+          if (!bar_wait(full + 8 * (k % kStages), k / kStages & 1u)) break;
+      }
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0) {
+    if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
       uint32_t it = 0, cc = 0;
       bool ok = true;
       for (int t = first; t < p.n_tiles && ok; t += step) {
         const Place pl = place<BN, GROUPED>(p, t);
         const Product& P = *pl.P;
         const int nkb = (P.K + kBlockK - 1) / kBlockK, kb0 = nkb * q / S, kb1 = nkb * (q + 1) / S;
-        const uint32_t idesc = instr_desc(p.bf16, P.a_mn, P.b_mn, kTileM, BN);
+        const uint32_t idesc = instr_desc(p.bf16, P.a_mn, P.b_mn, PAIR ? 2 * kTileM : kTileM, BN);
         // K-major: 8-row groups 1024 bytes apart, 32 bytes per K step.  Rows contiguous: 64-row
         // boxes 8 KB apart, 8-k groups 1024 bytes apart, 16 k rows (2048 bytes) per K step.
         const uint32_t lead_a = P.a_mn ? kBoxBytes : 16, lead_b = P.b_mn ? kBoxBytes : 16;
@@ -374,195 +530,112 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
               const uint64_t da = smem_desc(sa, lead_a, 1024), db = smem_desc(sa + kABytes, lead_b, 1024);
 #pragma unroll
               for (int k = 0; k < kBlockK / 16; ++k)
-                mma_f16(acc, da + k * step_a, db + k * step_b, idesc, kb > k0 || k > 0);
-              mma_commit(empty + 8 * s);
+                mma_f16<PAIR>(acc, da + k * step_a, db + k * step_b, idesc, kb > k0 || k > 0);
+              mma_commit<PAIR>(empty + 8 * s);
             }
             if (!ok) break;
-            mma_commit(tfull + 8 * (cc & 1u));
+            mma_commit<PAIR>(tfull + 8 * (cc & 1u));
           }
         }
       }
       if (!ok) {
         atomicOr(p.err, kErrProductWait);
-        mma_commit(drain);  // products in flight end before the CTA does
+        mma_commit<PAIR>(drain);  // products in flight end before the CTA does
         bar_wait(drain, 0);
       }
     }
     __syncwarp();
+    if (S > 1) cluster_sync();  // the epilogue warps' first one
   } else {
-    constexpr int kHalf = BN / 2;
-    const int ew = warp - 2;
-    const int quad = warp & 3;            // the TMEM lanes this warp may read
-    const int colbase = ew < 4 ? 0 : kHalf;  // warps 2-5 and 6-9 cover each quadrant once
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    const int ew = warp - 4;
+    const int quad = warp & 3;    // the TMEM lanes this warp may read
+    const int half = ew >> 2;     // warps 4-7 and 8-11 cover each quadrant once: half of every slab's columns each
     const int row = quad * 32 + lane;
     uint32_t cc = 0;
     bool ok = true;
     for (int t = first; t < p.n_tiles; t += step) {
       const Place pl = place<BN, GROUPED>(p, t);
-      const Product& P = *pl.P;
+      const Product P = *pl.P;  // in registers (no indexed access)
       const int nkb = (P.K + kBlockK - 1) / kBlockK, kb0 = nkb * q / S, kb1 = nkb * (q + 1) / S;
-      float acc[kHalf];
+      float acc[BN / 2];
 #pragma unroll
-      for (int k = 0; k < kHalf; ++k) acc[k] = 0.f;
+      for (int k = 0; k < BN / 2; ++k) acc[k] = 0.f;
       for (int ps = 0; ps < P.n_pass; ++ps) {
-        const float scale = P.scale[ps];
+        const float scale = pl.P->scale[ps];
         for (int k0 = kb0; k0 < kb1; k0 += P.chunk, ++cc) {
           if (ok && !bar_wait(tfull + 8 * (cc & 1u), cc >> 1 & 1u)) ok = false;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;  // the error word is set below; the tile's values are not written
           fence_after();
-          const uint32_t at = tmem + (cc & 1u) * BN + colbase + ((uint32_t)(quad * 32) << 16);
-          if constexpr (kHalf >= 32) {
+          const uint32_t at = tmem + (cc & 1u) * BN + half * kHalf + ((uint32_t)(quad * 32) << 16);
 #pragma unroll
-            for (int c = 0; c < kHalf; c += 32) {
-              float v[32];
-              tmem_ld32(at + c, v);
+          for (int sl = 0; sl < kSlabs; ++sl) {
+            float v[kHalf];
+            if constexpr (kHalf == 32)
+              tmem_ld32(at + sl * kSlab, v);
+            else
+              tmem_ld16(at + sl * kSlab, v);
 #pragma unroll
-              for (int k = 0; k < 32; ++k) acc[c + k] += scale * v[k];
-            }
-          } else {
-            float v[16];
-            tmem_ld16(at, v);
-#pragma unroll
-            for (int k = 0; k < 16; ++k) acc[k] += scale * v[k];
+            for (int k = 0; k < kHalf; ++k) acc[sl * kHalf + k] += scale * v[k];
           }
           fence_before();
           __syncwarp();
-          if (lane == 0) bar_arrive(tempty + 8 * (cc & 1u));
-        }
-      }
-      // the sums to shared memory; the previous tile's have been read
-      asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
-#pragma unroll
-      for (int k = 0; k < kHalf; k += 4)
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(staging + (row * kPitch + colbase + k) * 4),
-                     "f"(acc[k]), "f"(acc[k + 1]), "f"(acc[k + 2]), "f"(acc[k + 3])
-                     : "memory");
-      asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
-      if (S > 1) break;  // one tile per cluster; its sums are joined below
-      if (!ok) continue;
-      const int M = P.M, N = P.N;
-      if (!P.swap) {
-        const bool vec = wide_access<GROUPED>(P, p);
-        constexpr int kLanes = BN / 4, kRows = 32 / kLanes;  // lanes on a row, rows at a time
-        for (int r = ew * kRows + (vec ? lane / kLanes : 0); r < kTileM; r += kEpiWarps * kRows) {
-          if (vec) {
-            const int m = pl.row0 + r, c = lane % kLanes * 4, n = pl.col0 + c;
-            if (m >= M || n >= N) continue;
-            float v[4];
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                         : "r"(staging + (r * kPitch + c) * 4));
-            if (n + 4 <= N) {
-              emit<4, GROUPED>(P, p, m, n, v);
-            } else {
-              for (int k = 0; k < 4 && n + k < N; ++k) {
-                float u[1] = {v[k]};
-                emit<1, GROUPED>(P, p, m, n + k, u);
-              }
-            }
-          } else {
-            for (int rr = r; rr < r + kRows; ++rr) {
-              const int m = pl.row0 + rr;
-              for (int c = lane; c < BN; c += 32) {
-                const int n = pl.col0 + c;
-                if (m >= M || n >= N) continue;
-                float u[1];
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(u[0]) : "r"(staging + (rr * kPitch + c) * 4));
-                emit<1, GROUPED>(P, p, m, n, u);
-              }
-            }
+          if (lane == 0) {
+            if constexpr (PAIR)
+              bar_arrive_cluster(peer_addr(tempty + 8 * (cc & 1u), 0));
+            else
+              bar_arrive(tempty + 8 * (cc & 1u));
           }
         }
       }
-      if (P.swap || pl.mirror) {
-        // D(i, j) at output row j, column i: a warp takes 32 rows i, so its stores run along output rows
-        for (int u = ew; u < BN; u += kEpiWarps) {
-          const int i = (u & 3) * 32 + lane, c = (u >> 2) * 4, n = pl.row0 + i;
-          if (n >= M) continue;
-          float v[4];
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
-                       : "r"(staging + (i * kPitch + c) * 4));
+      if (S > 1) {
+        // one tile per cluster: the whole tile's sums go where the operands were, and are joined below
+        if (ok) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (pl.col0 + c + k < N) {
-              float w[1] = {v[k]};
-              emit<1, GROUPED>(P, p, pl.col0 + c + k, n, w);
-            }
+          for (int sl = 0; sl < kSlabs; ++sl)
+#pragma unroll
+            for (int k = 0; k < kHalf; k += 4)
+              st_shared4(ring + (row * pitch(BN) + sl * kSlab + half * kHalf + k) * 4, &acc[sl * kHalf + k]);
         }
+        break;
+      }
+#pragma unroll
+      for (int sl = 0; sl < kSlabs; ++sl) {
+        bar_sync_epilogue();  // the slab before has been read
+#pragma unroll
+        for (int k = 0; k < kHalf; k += 4)
+          st_shared4(staging + (row * kSlabPitch + half * kHalf + k) * 4, &acc[sl * kHalf + k]);
+        bar_sync_epilogue();
+        const int row0 = pl.row0 + my_rows, col0 = pl.col0 + sl * kSlab;
+        const OwnSums sums{staging};
+        if (ok && !P.swap) write_rows<kSlab, GROUPED>(P, p, row0, col0, lane, ew, 0, kTileM, pl.mirror, sums);
+        if (GROUPED && pl.mirror) bar_sync_epilogue();
+        if (ok && (P.swap || pl.mirror))
+          write_transposed<kSlab, GROUPED>(P, p, row0, col0, lane, ew, kEpiWarps, pl.mirror, sums);
       }
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrProductWait);
-  }
-
-  if (S > 1) {
-    __syncwarp();
-    cluster_sync();  // every CTA's sums are in its shared memory
-    if (warp >= 2 && first < p.n_tiles) {
-      const Place pl = place<BN, GROUPED>(p, first);
-      const Product& P = *pl.P;
-      const int ew = warp - 2, M = P.M, N = P.N, share = kTileM / S;
-      const bool failed = *reinterpret_cast<volatile uint32_t*>(p.err) != 0;
-      if (!failed && !P.swap) {
-        const bool vec = wide_access<GROUPED>(P, p);
-        for (int r = q * share + ew; r < (q + 1) * share; r += kEpiWarps) {
-          const int m = pl.row0 + r;
-          if (m >= M) continue;
-          if (vec) {
-            for (int c = lane * 4; c < BN; c += 128) {
-              const int n = pl.col0 + c;
-              if (n >= N) continue;
-              float v[4] = {0.f, 0.f, 0.f, 0.f};
-              for (int k = 0; k < S; ++k) {
-                const float4 u = ld_peer4(peer_addr(staging + (r * kPitch + c) * 4, k));
-                v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
-              }
-              if (n + 4 <= N) {
-                emit<4, GROUPED>(P, p, m, n, v);
-              } else {
-                for (int k = 0; k < 4 && n + k < N; ++k) {
-                  float u[1] = {v[k]};
-                  emit<1, GROUPED>(P, p, m, n + k, u);
-                }
-              }
-            }
-          } else {
-            for (int c = lane; c < BN; c += 32) {
-              const int n = pl.col0 + c;
-              if (n >= N) continue;
-              float u[1] = {0.f};
-              for (int k = 0; k < S; ++k) u[0] += ld_peer(peer_addr(staging + (r * kPitch + c) * 4, k));
-              emit<1, GROUPED>(P, p, m, n, u);
-            }
-          }
-        }
-      }
-      if (!failed && (P.swap || pl.mirror)) {
-        for (int u = q * kEpiWarps + ew; u < BN; u += S * kEpiWarps) {
-          const int i = (u & 3) * 32 + lane, c = (u >> 2) * 4, n = pl.row0 + i;
-          if (n >= M) continue;
-          float v[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int k = 0; k < S; ++k) {
-            const float4 w = ld_peer4(peer_addr(staging + (i * kPitch + c) * 4, k));
-            v[0] += w.x, v[1] += w.y, v[2] += w.z, v[3] += w.w;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (pl.col0 + c + k < N) {
-              float w[1] = {v[k]};
-              emit<1, GROUPED>(P, p, pl.col0 + c + k, n, w);
-            }
-        }
+    if (S > 1) {
+      __syncwarp();
+      cluster_sync();  // every CTA's sums are in its shared memory
+      if (*reinterpret_cast<volatile uint32_t*>(p.err) == 0) {
+        const Place pl = place<BN, GROUPED>(p, first);
+        const int share = kTileM / S;
+        const ClusterSums sums{ring, S};
+        const Product P = *pl.P;
+        if (!P.swap)
+          write_rows<BN, GROUPED>(P, p, pl.row0, pl.col0, lane, ew, q * share, (q + 1) * share, false, sums);
+        if (P.swap || pl.mirror)
+          write_transposed<BN, GROUPED>(P, p, pl.row0, pl.col0, lane, q * kEpiWarps + ew, S * kEpiWarps, false, sums);
       }
     }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while a peer reads its shared memory
   }
   __syncthreads();
+  if (PAIR || S > 1) cluster_sync();  // no CTA leaves while a peer's products or sums need it
   if (warp == 1) {
     fence_after();
-    tmem_free(tmem, kCols);
+    tmem_free<PAIR>(tmem, kCols);
   }
 }
 
@@ -578,7 +651,10 @@ cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
     if (dev <= 63) sized.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  const int ctas = p.splits > 1 ? p.n_tiles * p.splits : (p.n_tiles < sms ? p.n_tiles : sms);
+  // a pair per tile, or a cluster per tile, or persistent CTAs
+  const int cluster = BN == 256 ? 2 : p.splits;
+  const int64_t whole = (int64_t)p.n_tiles * cluster;
+  const int64_t ctas = BN != 256 && p.splits > 1 ? whole : std::min<int64_t>(whole, sms / cluster * cluster);
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes(BN);
@@ -588,9 +664,9 @@ cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (p.splits > 1) {
+  if (cluster > 1) {
     at[1].id = cudaLaunchAttributeClusterDimension;
-    at[1].val.clusterDim.x = (unsigned)p.splits;
+    at[1].val.clusterDim.x = (unsigned)cluster;
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
@@ -629,7 +705,8 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
 
 cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream) {
   if (p.n_tiles <= 0) return cudaSuccess;
-  if (grouped) return tile_n == 64 ? launch_one<64, true>(p, sms, stream) : launch_one<128, true>(p, sms, stream);
+  if (grouped) return tile_n == 256 ? launch_one<256, true>(p, sms, stream) : launch_one<128, true>(p, sms, stream);
+  if (tile_n == 256) return launch_one<256, false>(p, sms, stream);
   if (tile_n == 32) return launch_one<32, false>(p, sms, stream);
   if (tile_n == 64) return launch_one<64, false>(p, sms, stream);
   return launch_one<128, false>(p, sms, stream);
