@@ -74,6 +74,7 @@ struct Mat {
     return Range(p, p && rows ? ((uint64_t)(rows - 1) * (uint64_t)ld + (uint64_t)cols) * (uint64_t)esize : 0);
   }
   bool tma() const { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0; }
+  bool tma32() const { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 4 == 0; }
   bool vec4(int esize) const { return reinterpret_cast<uintptr_t>(p) % (4 * (size_t)esize) == 0 && ld % 4 == 0; }
 };
 
@@ -94,6 +95,10 @@ ddl_status_t aligned(const Mat& m, int64_t max_rows, Buffer* b, cudaStream_t s, 
 
 bool map_of(ddl::ProductLaunch* L, int k, const Mat& m, int box_rows) {
   return ddl::make_map(&L->maps[k], m.p, (uint64_t)m.rows, (uint64_t)m.cols, (uint64_t)m.ld, box_rows, L->bf16 != 0);
+}
+
+bool map32_of(ddl::ProductLaunch* L, int k, const Mat& m) {
+  return ddl::make_map32(&L->maps[k], m.p, (uint64_t)m.rows, (uint64_t)m.cols, (uint64_t)m.ld);
 }
 
 int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
@@ -207,6 +212,18 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   L.n_tiles = (int32_t)tiles;
   L.splits = tile_n == 256 ? 1 : ddl::choose_splits(tiles, P.chunk, h->sms);
   L.err = h->d_err;
+  P.in0 = P.in1 = P.out0 = P.out1 = -1;
+  // rows that TMA can address, of whole 16-byte pieces, let the epilogue move whole boxes
+  L.boxes = !swap && L.splits == 1 && N % 8 == 0 && my.tma() && (!z || mz.tma()) && (!residual || mr.tma()) &&
+            reinterpret_cast<uintptr_t>(bias) % 16 == 0;
+  if (L.boxes) {
+    P.out0 = 2;
+    if (!map_of(&L, 2, my, ddl::kBoxRows)) return DDL_ERR_CUDA;
+    if (z) P.out1 = 3;
+    if (z && !map_of(&L, 3, mz, ddl::kBoxRows)) return DDL_ERR_CUDA;
+    if (residual) P.in0 = 4;
+    if (residual && !map_of(&L, 4, mr, ddl::kBoxRows)) return DDL_ERR_CUDA;
+  }
   return ddl::status_of(ddl::launch_product(L, tile_n, false, h->sms, s));
 }
 
@@ -321,6 +338,9 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.out_type = grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16;
     P.accumulate = accumulate ? 1 : 0;
     P.vec = mdw.vec4(ge);
+    P.in0 = accumulate ? 5 : -1;
+    P.out0 = 5;
+    P.in1 = P.out1 = -1;
     P.out = dw;
     P.ldo = mdw.ld;
     L.inl_tiles[L.n_inl++] = (int32_t)dw_tiles;
@@ -339,6 +359,8 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.epi = ddl::kEpiStore;
     P.out_type = h->type;
     P.vec = mdx.vec4(2);
+    P.out0 = 6;
+    P.in0 = P.in1 = P.out1 = -1;
     P.out = dx;
     P.ldo = mdx.ld;
     L.inl_tiles[L.n_inl++] = (int32_t)dx_tiles;
@@ -346,6 +368,13 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   }
   L.n_tiles = L.inl_tiles[0] + L.inl_tiles[1];
   L.splits = tile_n == 256 ? 1 : ddl::choose_splits(L.n_tiles, longest, h->sms);
+  L.boxes = L.splits == 1 && (!dw || (ge == 4 ? mdw.tma32() : mdw.tma())) && (!dx || mdx.tma()) &&
+            K % 8 == 0;
+  if (L.boxes) {
+    // a binary16 gradient's map takes the operands' element type: TMA moves its bits only
+    if (dw && !(ge == 4 ? map32_of(&L, 5, mdw) : map_of(&L, 5, mdw, ddl::kBoxRows))) return DDL_ERR_CUDA;
+    if (dx && !map_of(&L, 6, mdx, ddl::kBoxRows)) return DDL_ERR_CUDA;
+  }
   return ddl::status_of(ddl::launch_product(L, tile_n, false, h->sms, s));
 }
 

@@ -215,6 +215,10 @@ ddl_status_t build(ddl_ortho* o) {
       P.p_hi = base + (k == kPoly ? p.b[0] : k == kApply0 || k == kApply1 ? p.x[1 - xi][0] : p.a[0]);
       P.p_lo = base + (k == kPoly ? p.b[1] : k == kApply0 || k == kApply1 ? p.x[1 - xi][1] : p.a[1]);
       P.ldp = k == kApply0 || k == kApply1 ? p.ldx : p.lds;
+      P.in0 = k == kGram0 || k == kGram1 ? -1 : k == kPoly ? map + 4 : map + 2 * xi;
+      P.in1 = P.in0 < 0 ? -1 : P.in0 + 1;
+      P.out0 = k == kPoly ? map + 6 : k == kApply0 || k == kApply1 ? map + 2 * (1 - xi) : map + 4;
+      P.out1 = P.out0 + 1;
       // planes always allow 4-element accesses; the flat buffers' rows do where the offset and ld do
       P.vec = k >= kLast0 ? (m.offset % 4 == 0 && m.ld % 4 == 0) : 1;
       o->stage[k].products.push_back(P);
@@ -289,6 +293,7 @@ ddl_status_t products(ddl_ortho* o, ddl::ProductLaunch* L, int last, bool vec, c
       L->g_tiles = st.d_tiles;
       L->n_tiles = (int32_t)st.tiles.size();
       L->splits = st.splits;
+      L->boxes = st.splits == 1 && kind < kLast0;  // the last product goes to the caller's buffers
       const cudaError_t e = ddl::launch_product(*L, st.tile, true, o->sms, s);
       if (e != cudaSuccess) return ddl::status_of(e);
     }

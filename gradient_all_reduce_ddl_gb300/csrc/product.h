@@ -48,6 +48,8 @@ struct Product {
   int32_t act;
   int32_t out_type;
   int32_t accumulate;
+  int32_t in0, in1;    // launches with box epilogues: maps of what the epilogue reads (residual, old output, C's
+  int32_t out0, out1;  // planes) and writes (output, z, the result's planes); -1: none
   int32_t vec;     // every pointer and row stride of the epilogue allows 4-element accesses
   const void* bias;
   const void* add;   // residual
@@ -83,6 +85,7 @@ struct ProductLaunch {
   const Tile* g_tiles;
   int32_t n_tiles;
   int32_t splits;           // CTAs of a cluster that share a tile's contraction
+  int32_t boxes;            // tiles of 128 or 256 columns, splits 1: the epilogue moves boxes by TMA (in0 ... out1)
   int32_t bf16;             // operands are bfloat16, else binary16
   uint32_t* err;
   // Newton-Schulz coefficients and the flat buffers of its last product
@@ -103,6 +106,9 @@ cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int
 // Tensor map of a row-major 16-bit matrix (rows x cols, ld elements between
 // rows; 16-byte aligned base and row stride), boxes of 64 columns x box_rows.
 bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_rows, bool bf16);
+
+// The same of a binary32 matrix, boxes of 32 columns x 64 rows (kEpiStore's output).
+bool make_map32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld);
 
 // Error word bits of these kernels.
 enum : uint32_t { kErrProductWait = 16u };

@@ -49,8 +49,10 @@ __host__ __device__ constexpr int stages(int bn) { return bn >= 128 ? 5 : 6; }
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + b_rows(bn) * kBlockK * 2; }
 __host__ __device__ constexpr int slab(int bn) { return bn < 64 ? bn : 64; }  // columns passed on at a time
 __host__ __device__ constexpr int pitch(int cols) { return cols + 4; }        // floats; rows 4 banks apart
+constexpr int kPlaneBytes = kTileM * 64 * 2;  // 64 columns of 16 bits: two boxes
+constexpr int kSlabBytes = 2 * kPlaneBytes;   // what a box epilogue keeps of 64 columns: two planes, or binary32
 __host__ __device__ constexpr int smem_bytes(int bn) {
-  return 1024 + stages(bn) * stage_bytes(bn) + kTileM * pitch(slab(bn)) * 4;
+  return 1024 + stages(bn) * stage_bytes(bn) + (bn >= 128 ? 2 * kSlabBytes : kTileM * pitch(slab(bn)) * 4);
 }
 
 // -- element access -------------------------------------------------------------
@@ -144,6 +146,52 @@ __device__ __forceinline__ void load_planes(const uint16_t* hi, const uint16_t* 
 
 // -- epilogues ---------------------------------------------------------------------
 
+template <int V, int R, int ACT>
+__device__ __forceinline__ void activate_all(float (&v)[R][V]) {
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int k = 0; k < V; ++k) v[i][k] = activate(v[i][k], ACT);
+}
+
+template <int V, int R, int TYPE>
+__device__ __forceinline__ void emit_linear(const Product& P, const int (&m)[R], const bool (&in)[R], int n,
+                                            float (&v)[R][V]) {
+  float t[V], add[R][V];
+  if (P.add) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (in[i]) load16(P.add, (int64_t)m[i] * P.ld_add + n, TYPE, add[i]);
+  }
+  if (P.bias) {
+    load16(P.bias, n, TYPE, t);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i][k] += t[k];
+  }
+  if (P.z) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      if (in[i]) store16(P.z, (int64_t)m[i] * P.ldz + n, TYPE, v[i]);
+  }
+  switch (P.act) {
+    case kActRelu: activate_all<V, R, kActRelu>(v); break;
+    case kActGelu: activate_all<V, R, kActGelu>(v); break;
+    case kActSilu: activate_all<V, R, kActSilu>(v); break;
+    default: break;
+  }
+  if (P.add) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i][k] += add[i][k];
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (in[i]) store16(P.out, (int64_t)m[i] * P.ldo + n, TYPE, v[i]);
+}
+
 // V values of D in each of R rows: rows m[i] of the output (where in[i]), columns n...  Every load of the R rows is
 // issued before the first is used.  v becomes what was stored (before the flat buffers' rounding).
 template <int V, int R, bool GROUPED>
@@ -151,31 +199,11 @@ __device__ __forceinline__ void emit(const Product& P, const ProductLaunch& p, c
                                      int n, float (&v)[R][V]) {
   if constexpr (!GROUPED) {
     if (P.epi == kEpiLinear) {
-      float t[V], add[R][V];
-      if (P.add) {
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (in[i]) load16(P.add, (int64_t)m[i] * P.ld_add + n, P.type, add[i]);
-      }
-      if (P.bias) {
-        load16(P.bias, n, P.type, t);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[i][k] += t[k];
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i) {
-        if (!in[i]) continue;
-        if (P.z) store16(P.z, (int64_t)m[i] * P.ldz + n, P.type, v[i]);
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[i][k] = activate(v[i][k], P.act);
-        if (P.add) {
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[i][k] += add[i][k];
-        }
-        store16(P.out, (int64_t)m[i] * P.ldo + n, P.type, v[i]);
-      }
+      // one branch on the type and one on the activation for all R x V values
+      if (P.type == kBF16)
+        emit_linear<V, R, kBF16>(P, m, in, n, v);
+      else
+        emit_linear<V, R, kF16>(P, m, in, n, v);
     } else {
       if (P.accumulate) {
         float t[R][V];
@@ -239,13 +267,13 @@ __device__ __forceinline__ void emit(const Product& P, const ProductLaunch& p, c
   }
 }
 
-// One element.
+// One element (edges, unaligned rows, transposed outputs): out of line, so that the code of the wide path stays small.
 template <bool GROUPED>
-__device__ __forceinline__ float emit_one(const Product& P, const ProductLaunch& p, int m, int n, float x) {
+__device__ __noinline__ float emit_one(const Product* P, const ProductLaunch* p, int m, int n, float x) {
   const int mm[1] = {m};
   const bool in[1] = {true};
   float v[1][1] = {{x}};
-  emit<1, 1, GROUPED>(P, p, mm, in, n, v);
+  emit<1, 1, GROUPED>(*P, *p, mm, in, n, v);
   return v[0][0];
 }
 
@@ -253,6 +281,26 @@ __device__ __forceinline__ float emit_one(const Product& P, const ProductLaunch&
 __device__ __forceinline__ void bar_sync_epilogue() {
   asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory");
 }
+
+// What the loops over a tile's contraction read of its product, in registers: a load from the product's own memory
+// would be repeated after every wait.
+struct Shape {
+  int kb0, kb1, chunk, n_pass, a_mn, b_mn;
+  float scale0, scale1, scale2;
+  __device__ __forceinline__ Shape(const Product& P, int part, int parts)
+      : chunk(P.chunk),
+        n_pass(P.n_pass),
+        a_mn(P.a_mn),
+        b_mn(P.b_mn),
+        scale0(P.scale[0]),
+        scale1(P.scale[1]),
+        scale2(P.scale[2]) {
+    const int nkb = (P.K + kBlockK - 1) / kBlockK;
+    kb0 = nkb * part / parts;
+    kb1 = nkb * (part + 1) / parts;
+  }
+  __device__ __forceinline__ float scale(int pass) const { return pass == 0 ? scale0 : pass == 1 ? scale1 : scale2; }
+};
 
 struct Place {
   const Product* P;
@@ -311,50 +359,70 @@ struct ClusterSums {
   }
 };
 
+// `from` is the product that P is a copy of.
 // Writes rows [r0, r1) of 128 x COLS sums that begin at D(row0, col0), along rows of D.  back: the finished values
 // also replace the sums in this CTA's shared memory.
-template <int COLS, bool GROUPED, class Sums>
-__device__ __forceinline__ void write_rows(const Product& P, const ProductLaunch& p, int row0, int col0, int lane, int ew,
-                                           int r0, int r1, bool back, const Sums sums) {
+template <int COLS, bool GROUPED, bool WHOLE, class Sums>
+__device__ __forceinline__ void write_rows_wide(const Product& P, const Product* from, const ProductLaunch& p, int row0,
+                                                int col0, int lane, int ew, int r0, int r1, bool back, const Sums sums) {
   constexpr int kPitch = pitch(COLS), kBatch = 4;
   constexpr int kLanes = COLS / 4 < 32 ? COLS / 4 : 32, kRows = 32 / kLanes;  // lanes on a row, rows at a time
-  const int M = P.M, N = P.N;
-  if (wide_access<GROUPED>(P, p)) {
-    for (int c = lane % kLanes * 4; c < COLS; c += kLanes * 4) {
-      const int n = col0 + c;
-      if (n >= N) continue;
-      for (int rr = r0 + ew * kRows + lane / kLanes; rr < r1; rr += kEpiWarps * kRows * kBatch) {
-        int m[kBatch];
-        bool in[kBatch];
-        float v[kBatch][4];
+  for (int c = lane % kLanes * 4; c < COLS; c += kLanes * 4) {
+    const int n = col0 + c;
+    if (!WHOLE && n >= P.N) continue;
+#pragma unroll 1
+    for (int rr = r0 + ew * kRows + lane / kLanes; rr < r1; rr += kEpiWarps * kRows * kBatch) {
+      int m[kBatch];
+      bool in[kBatch];
+      float v[kBatch][4];
 #pragma unroll
-        for (int i = 0; i < kBatch; ++i) {
-          const int r = rr + i * kEpiWarps * kRows;
-          m[i] = row0 + r;
-          in[i] = r < r1 && m[i] < M;
-          if (in[i]) sums.four((r * kPitch + c) * 4, v[i]);
-        }
-        if (n + 4 <= N) {
-          emit<4, kBatch, GROUPED>(P, p, m, in, n, v);
-        } else {
+      for (int i = 0; i < kBatch; ++i) {
+        const int r = rr + i * kEpiWarps * kRows;
+        m[i] = row0 + r;
+        in[i] = WHOLE || (r < r1 && m[i] < P.M);
+        if (in[i]) sums.four((r * kPitch + c) * 4, v[i]);
+      }
+      if (WHOLE || n + 4 <= P.N) {
+        emit<4, kBatch, GROUPED>(P, p, m, in, n, v);
+      } else {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k)
+#pragma unroll 1
+          for (int i = 0; i < kBatch; ++i) {
+            const int r = rr + i * kEpiWarps * kRows;
+            if (r >= r1 || row0 + r >= P.M || n + k >= P.N) continue;
+            const uint32_t at = (r * kPitch + c + k) * 4;
+            const float x = emit_one<GROUPED>(from, &p, row0 + r, n + k, sums.one(at));
+            if (back) st_shared(sums.base + at, x);
+          }
+        continue;
+      }
+      if (back) {
 #pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (in[i] && n + k < N) v[i][k] = emit_one<GROUPED>(P, p, m[i], n + k, v[i][k]);
-        }
-        if (back) {
-#pragma unroll
-          for (int i = 0; i < kBatch; ++i)
-            if (in[i]) st_shared4(sums.base + ((rr + i * kEpiWarps * kRows) * kPitch + c) * 4, v[i]);
-        }
+        for (int i = 0; i < kBatch; ++i)
+          if (in[i]) st_shared4(sums.base + ((rr + i * kEpiWarps * kRows) * kPitch + c) * 4, v[i]);
       }
     }
+  }
+}
+
+template <int COLS, bool GROUPED, class Sums>
+__device__ __forceinline__ void write_rows(const Product& P, const Product* from, const ProductLaunch& p, int row0,
+                                           int col0, int lane, int ew, int r0, int r1, bool back, const Sums sums) {
+  constexpr int kStride = kEpiWarps * 4 * (COLS / 4 < 32 ? 128 / COLS : 1);  // rows a pass of all warps covers
+  if (wide_access<GROUPED>(P, p)) {
+    // tiles that lie wholly inside need no predicate anywhere
+    if (row0 + r1 <= P.M && col0 + COLS <= P.N && (r1 - r0) % kStride == 0)
+      write_rows_wide<COLS, GROUPED, true>(P, from, p, row0, col0, lane, ew, r0, r1, back, sums);
+    else
+      write_rows_wide<COLS, GROUPED, false>(P, from, p, row0, col0, lane, ew, r0, r1, back, sums);
   } else {  // rows at any alignment: a warp along a row, element by element
+#pragma unroll 1
     for (int r = r0 + ew; r < r1; r += kEpiWarps) {
-      if (row0 + r >= M) break;
+      if (row0 + r >= P.M) break;
+#pragma unroll 1
       for (int c = lane; c < COLS; c += 32)
-        if (col0 + c < N) emit_one<GROUPED>(P, p, row0 + r, col0 + c, sums.one((r * kPitch + c) * 4));
+        if (col0 + c < P.N) emit_one<GROUPED>(from, &p, row0 + r, col0 + c, sums.one((r * (COLS + 4) + c) * 4));
     }
   }
 }
@@ -362,8 +430,8 @@ __device__ __forceinline__ void write_rows(const Product& P, const ProductLaunch
 // Writes the sums with D(i, j) at output row j, column i.  A warp takes 32 rows i, so that its stores run along
 // output rows.  finished: the values are final (symmetric products' mirror images).
 template <int COLS, bool GROUPED, class Sums>
-__device__ __forceinline__ void write_transposed(const Product& P, const ProductLaunch& p, int row0, int col0, int lane,
-                                                 int first, int step, bool finished, const Sums sums) {
+__device__ __forceinline__ void write_transposed(const Product& P, const Product* from, const ProductLaunch& p, int row0,
+                                                 int col0, int lane, int first, int step, bool finished, const Sums sums) {
   constexpr int kPitch = pitch(COLS);
   for (int u = first; u < COLS; u += step) {
     const int i = (u & 3) * 32 + lane, c = (u >> 2) * 4, n = row0 + i;
@@ -378,11 +446,176 @@ __device__ __forceinline__ void write_transposed(const Product& P, const Product
         float w[1] = {v[k]};
         store_planes(P.p_hi, P.p_lo, (int64_t)m * P.ldp + n, w);
       } else {
-        emit_one<GROUPED>(P, p, m, n, v[k]);
+        emit_one<GROUPED>(from, &p, m, n, v[k]);
       }
     }
   }
 }
+
+// -- box epilogues ------------------------------------------------------------------
+//
+// 64 columns of a tile at a time.  A thread has 32 columns of one row; what it reads (residual, old output, C's
+// planes) TMA has put into a slab of shared memory, the results replace it there in place, and TMA stores the slab.
+// A box that the matrix's edge cuts is stored in whole 16-byte pieces, so a caller's rows end on one where boxes are used.
+// The slab's planes are boxes with the 128-byte swizzle: 16-byte piece c of row r lies at piece c ^ (r & 7).
+
+__device__ __forceinline__ uint32_t piece(uint32_t plane, int row, int c) {
+  return plane + row * 128 + ((c ^ (row & 7)) << 4);
+}
+
+__device__ __forceinline__ void unpack8(uint4 u, int type, float (&v)[8]) {
+  const float2 a = from16x2(u.x, type), b = from16x2(u.y, type), c = from16x2(u.z, type), d = from16x2(u.w, type);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y, v[4] = c.x, v[5] = c.y, v[6] = d.x, v[7] = d.y;
+}
+
+__device__ __forceinline__ uint4 pack8(const float* v, int type) {
+  return make_uint4(to16x2(v[0], v[1], type), to16x2(v[2], v[3], type), to16x2(v[4], v[5], type), to16x2(v[6], v[7], type));
+}
+
+// The planes of 8 values.
+__device__ __forceinline__ void split8(const float* v, uint4* hi, uint4* lo) {
+  *hi = pack8(v, kF16);
+  float h[8], l[8];
+  unpack8(*hi, kF16, h);
+#pragma unroll
+  for (int k = 0; k < 8; ++k) l[k] = fabsf(h[k]) <= 65504.f ? (v[k] - h[k]) * kLoScale : 0.f;
+  *lo = pack8(l, kF16);
+}
+
+template <int TYPE, int ACT>
+__device__ __forceinline__ void slab_linear(const Product& P, float* v, uint32_t buf, int row, int half, int n0) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    float* x = v + 8 * g;
+    const int n = n0 + 8 * g;
+    if (P.bias) {
+      const uint16_t* b = static_cast<const uint16_t*>(P.bias) + n;
+      if (n + 8 <= P.N) {
+        float t[8];
+        unpack8(*reinterpret_cast<const uint4*>(b), TYPE, t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] += t[k];
+      } else {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (n + k < P.N) x[k] += from16(b[k], TYPE);
+      }
+    }
+    const uint32_t at = piece(buf, row, 4 * half + g);
+    if (P.out1 >= 0) st_shared16(at + kPlaneBytes, pack8(x, TYPE));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = activate(x[k], ACT);
+    if (P.in0 >= 0) {
+      float t[8];
+      unpack8(ld_shared16(at), TYPE, t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] += t[k];
+    }
+    st_shared16(at, pack8(x, TYPE));
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ void slab_linear_act(const Product& P, float* v, uint32_t buf, int row, int half, int n0) {
+  switch (P.act) {
+    case kActRelu: slab_linear<TYPE, kActRelu>(P, v, buf, row, half, n0); break;
+    case kActGelu: slab_linear<TYPE, kActGelu>(P, v, buf, row, half, n0); break;
+    case kActSilu: slab_linear<TYPE, kActSilu>(P, v, buf, row, half, n0); break;
+    default: slab_linear<TYPE, kActNone>(P, v, buf, row, half, n0); break;
+  }
+}
+
+template <bool GROUPED>
+__device__ __forceinline__ void slab_values(const Product& P, const ProductLaunch& p, float* v, uint32_t buf, int row,
+                                            int half, int row0, int n0, bool mirror) {
+  if constexpr (GROUPED) {
+    const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = P.epi == kEpiPoly ? p.cc : 1.f;
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      float* x = v + 8 * g;
+      const uint32_t at = piece(buf, row, 4 * half + g);
+      if (P.in0 >= 0) {
+        float h[8], l[8];
+        unpack8(ld_shared16(at), kF16, h);
+        unpack8(ld_shared16(at + kPlaneBytes), kF16, l);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = cd * x[k] + cc * (h[k] + l[k] * (1.f / kLoScale));
+      }
+      uint4 hi, lo;
+      split8(x, &hi, &lo);
+      st_shared16(at, hi);
+      st_shared16(at + kPlaneBytes, lo);
+      if (mirror && row0 + row < P.M) {  // D(i, j) also at (j, i): the warp's 32 rows i lie side by side there
+        const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (n0 + 8 * g + k < P.N) {
+            const int64_t to = (int64_t)(n0 + 8 * g + k) * P.ldp + row0 + row;
+            P.p_hi[to] = (uint16_t)(h[k >> 1] >> (k & 1) * 16);
+            P.p_lo[to] = (uint16_t)(l[k >> 1] >> (k & 1) * 16);
+          }
+      }
+    }
+  } else if (P.epi == kEpiLinear) {
+    if (P.type == kBF16)
+      slab_linear_act<kBF16>(P, v, buf, row, half, n0);
+    else
+      slab_linear_act<kF16>(P, v, buf, row, half, n0);
+  } else if (P.out_type == kF32) {
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+      const uint32_t at = piece(buf + half * kPlaneBytes, row, g);
+      float* x = v + 4 * g;
+      if (P.in0 >= 0) {
+        float t[4];
+        ld_shared4(at, t);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] += t[k];
+      }
+      st_shared4(at, x);
+    }
+  } else {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const uint32_t at = piece(buf, row, 4 * half + g);
+      float* x = v + 8 * g;
+      if (P.in0 >= 0) {
+        float t[8];
+        unpack8(ld_shared16(at), P.out_type, t);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] += t[k];
+      }
+      st_shared16(at, pack8(x, P.out_type));
+    }
+  }
+}
+
+// One walk over the slabs of a CTA's tiles: the warp that moves the boxes has two, for what it prepares and for what
+// it stores.
+template <int BN, bool GROUPED>
+struct Slabs {
+  int t, step, sl, n_sl;
+  Place pl;
+  int in0, in1, out0, out1, f32, rows, cols;
+  __device__ __forceinline__ Slabs(const ProductLaunch& p, int first, int by) : t(first), step(by), sl(0) { load(p); }
+  __device__ __forceinline__ void load(const ProductLaunch& p) {
+    if (t >= p.n_tiles) return;
+    pl = place<BN, GROUPED>(p, t);
+    const Product& P = *pl.P;
+    in0 = P.in0, in1 = P.in1, out0 = P.out0, out1 = P.out1;
+    f32 = !GROUPED && P.epi == kEpiStore && P.out_type == kF32;
+    rows = P.M, cols = P.N;
+    const int left = (P.N - pl.col0 + 63) / 64;
+    n_sl = left < BN / 64 ? left : BN / 64;
+  }
+  __device__ __forceinline__ bool more(const ProductLaunch& p) const { return t < p.n_tiles; }
+  __device__ __forceinline__ void next(const ProductLaunch& p) {
+    if (++sl < n_sl) return;
+    sl = 0;
+    t += step;
+    load(p);
+  }
+};
 
 // BN 256: a cluster of two CTAs makes a 256 x 256 tile, each CTA 128 of its rows, from one stream of products that
 // the even CTA issues for both.
@@ -393,12 +626,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   constexpr uint32_t kCols = 2 * BN;
   constexpr int kSlab = slab(BN), kSlabPitch = pitch(kSlab), kHalf = kSlab / 2, kSlabs = BN / kSlab;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kStages + 5];
+  __shared__ uint64_t bars[2 * kStages + 9];
   __shared__ uint32_t tmem_slot;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t staging = ring + kStages * stage_bytes(BN);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
-                 drain = tempty + 16;
+                 drain = tempty + 16, ready = drain + 8, written = ready + 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -409,6 +642,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int b = 0; b < 2; ++b) {
       bar_init(tfull + 8 * b, 1);
       bar_init(tempty + 8 * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
+      bar_init(ready + 8 * b, 1);
+      bar_init(written + 8 * b, kEpiWarps);
     }
     bar_init(drain, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -441,15 +676,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       for (int t = first; t < p.n_tiles && ok; t += step) {
         const Place pl = place<BN, GROUPED>(p, t);
         const Product& P = *pl.P;
-        const int nkb = (P.K + kBlockK - 1) / kBlockK, kb0 = nkb * q / S, kb1 = nkb * (q + 1) / S;
-        for (int ps = 0; ps < P.n_pass && ok; ++ps) {
+        const Shape sh(P, q, S);
+        for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
           const CUtensorMap* ma = maps + P.a[ps];
           const CUtensorMap* mb = maps + P.b[ps];
           if constexpr (GROUPED) {  // written by the host before this launch
             asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
             asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
           }
-          for (int kb = kb0; kb < kb1; ++kb, ++it) {
+          for (int kb = sh.kb0; kb < sh.kb1; ++kb, ++it) {
             const uint32_t s = it % kStages;
             if (!bar_wait(empty + 8 * s, (it / kStages & 1u) ^ 1u)) {
               ok = false;
@@ -468,7 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
             for (int h = 0; h < kTileM / kBoxRows; ++h) {
               const int row = pl.row0 + my_rows + h * kBoxRows;
-              const int x = P.a_mn ? row : kb * kBlockK, y = P.a_mn ? kb * kBlockK : row;
+              const int x = sh.a_mn ? row : kb * kBlockK, y = sh.a_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
                 tma_box_pair(sa + h * kBoxBytes, ma, bar, x, y);
               else
@@ -477,7 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
             for (int h = 0; h < (b_rows(BN) + kBoxRows - 1) / kBoxRows; ++h) {
               const int row = pl.col0 + my_rows + h * kBoxRows;
-              const int x = P.b_mn ? row : kb * kBlockK, y = P.b_mn ? kb * kBlockK : row;
+              const int x = sh.b_mn ? row : kb * kBlockK, y = sh.b_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
                 tma_box_pair(sb + h * kBoxBytes, mb, bar, x, y);
               else
@@ -503,16 +738,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bool ok = true;
       for (int t = first; t < p.n_tiles && ok; t += step) {
         const Place pl = place<BN, GROUPED>(p, t);
-        const Product& P = *pl.P;
-        const int nkb = (P.K + kBlockK - 1) / kBlockK, kb0 = nkb * q / S, kb1 = nkb * (q + 1) / S;
-        const uint32_t idesc = instr_desc(p.bf16, P.a_mn, P.b_mn, PAIR ? 2 * kTileM : kTileM, BN);
+        const Shape sh(*pl.P, q, S);
+        const uint32_t idesc = instr_desc(p.bf16, sh.a_mn, sh.b_mn, PAIR ? 2 * kTileM : kTileM, BN);
         // K-major: 8-row groups 1024 bytes apart, 32 bytes per K step.  Rows contiguous: 64-row
         // boxes 8 KB apart, 8-k groups 1024 bytes apart, 16 k rows (2048 bytes) per K step.
-        const uint32_t lead_a = P.a_mn ? kBoxBytes : 16, lead_b = P.b_mn ? kBoxBytes : 16;
-        const uint64_t step_a = (P.a_mn ? 2048 : 32) >> 4, step_b = (P.b_mn ? 2048 : 32) >> 4;
-        for (int ps = 0; ps < P.n_pass && ok; ++ps) {
-          for (int k0 = kb0; k0 < kb1 && ok; k0 += P.chunk, ++cc) {
-            const int k1 = k0 + P.chunk < kb1 ? k0 + P.chunk : kb1;
+        const uint32_t lead_a = sh.a_mn ? kBoxBytes : 16, lead_b = sh.b_mn ? kBoxBytes : 16;
+        const uint64_t step_a = (sh.a_mn ? 2048 : 32) >> 4, step_b = (sh.b_mn ? 2048 : 32) >> 4;
+        for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
+          for (int k0 = sh.kb0; k0 < sh.kb1 && ok; k0 += sh.chunk, ++cc) {
+            const int k1 = k0 + sh.chunk < sh.kb1 ? k0 + sh.chunk : sh.kb1;
             const uint32_t acc = tmem + (cc & 1u) * BN;
             if (!bar_wait(tempty + 8 * (cc & 1u), (cc >> 1 & 1u) ^ 1u)) {
               ok = false;
@@ -544,6 +778,59 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         bar_wait(drain, 0);
       }
     }
+    if constexpr (BN >= 128) {
+      if (warp == 2 && lane == 0 && p.boxes) {
+        // Slab u of this CTA's tiles uses buffer u & 1: filled (or declared free) here, worked on by the epilogue
+        // warps, stored here; then slab u + 2 may have the buffer.
+        Slabs<BN, GROUPED> fill(p, first, step), store(p, first, step);
+        uint32_t u = 0, w = 0;
+        bool ok = true;
+        while (ok && store.more(p)) {
+          while (u < w + 2 && fill.more(p)) {
+            if (u >= 2) store_wait_read();  // slab u - 2 has been read
+            const uint32_t buf = staging + (u & 1u) * kSlabBytes, bar = ready + 8 * (u & 1u);
+            if (fill.in0 >= 0) {
+              bar_expect(bar, fill.f32 || fill.in1 >= 0 ? kSlabBytes : kPlaneBytes);
+              const int x = fill.pl.col0 + fill.sl * 64, y = fill.pl.row0 + my_rows;
+              for (int h = 0; h < 2; ++h) {
+                tma_box(buf + h * kBoxBytes, maps + fill.in0, bar, x, y + h * kBoxRows);
+                if (fill.f32)
+                  tma_box(buf + kPlaneBytes + h * kBoxBytes, maps + fill.in0, bar, x + 32, y + h * kBoxRows);
+                else if (fill.in1 >= 0)
+                  tma_box(buf + kPlaneBytes + h * kBoxBytes, maps + fill.in1, bar, x, y + h * kBoxRows);
+              }
+            } else {
+              bar_arrive(bar);
+            }
+            fill.next(p);
+            ++u;
+          }
+          const uint32_t buf = staging + (w & 1u) * kSlabBytes;
+          if (!bar_wait(written + 8 * (w & 1u), w >> 1 & 1u)) {
+            ok = false;
+            break;
+          }
+          const int x = store.pl.col0 + store.sl * 64;
+          for (int h = 0; h < 2; ++h) {
+            const int y = store.pl.row0 + my_rows + h * kBoxRows;
+            if (y >= store.rows) break;
+            tma_store(maps + store.out0, buf + h * kBoxBytes, x, y);
+            if (store.f32) {
+              if (x + 32 < store.cols) tma_store(maps + store.out0, buf + kPlaneBytes + h * kBoxBytes, x + 32, y);
+            } else if (store.out1 >= 0)
+              tma_store(maps + store.out1, buf + kPlaneBytes + h * kBoxBytes, x, y);
+          }
+          store_commit();
+          store.next(p);
+          ++w;
+        }
+        if (!ok) {
+          atomicOr(p.err, kErrProductWait);
+          for (uint32_t k = w; k < u; ++k) bar_wait(ready + 8 * (k & 1u), k >> 1 & 1u);  // loads in flight
+        }
+        store_wait();
+      }
+    }
     __syncwarp();
     if (S > 1) cluster_sync();  // the epilogue warps' first one
   } else {
@@ -552,18 +839,39 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     const int quad = warp & 3;    // the TMEM lanes this warp may read
     const int half = ew >> 2;     // warps 4-7 and 8-11 cover each quadrant once: half of every slab's columns each
     const int row = quad * 32 + lane;
-    uint32_t cc = 0;
+    uint32_t cc = 0, use = 0;
     bool ok = true;
     for (int t = first; t < p.n_tiles; t += step) {
       const Place pl = place<BN, GROUPED>(p, t);
-      const Product P = *pl.P;  // in registers (no indexed access)
-      const int nkb = (P.K + kBlockK - 1) / kBlockK, kb0 = nkb * q / S, kb1 = nkb * (q + 1) / S;
+      const Product& G = *pl.P;
+      const Shape sh(G, q, S);
+      // what the epilogue reads from HBM comes to L2 while the products run
+      if constexpr (!GROUPED) {
+        if (S == 1 && !G.swap && !p.boxes) {
+          const int m = pl.row0 + my_rows + row;
+          if (m < G.M) {
+            const char* from = nullptr;
+            int bytes = 2;
+            if (G.epi == kEpiLinear && G.add)
+              from = static_cast<const char*>(G.add) + ((int64_t)m * G.ld_add + pl.col0) * 2;
+            else if (G.epi == kEpiStore && G.accumulate) {
+              bytes = G.out_type == kF32 ? 4 : 2;
+              from = static_cast<const char*>(G.out) + ((int64_t)m * G.ldo + pl.col0) * bytes;
+            }
+            if (from) {
+              const int cols = G.N - pl.col0 < BN ? G.N - pl.col0 : BN;
+              for (int c = half * 128; c < cols * bytes; c += 256)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(from + c));
+            }
+          }
+        }
+      }
       float acc[BN / 2];
 #pragma unroll
       for (int k = 0; k < BN / 2; ++k) acc[k] = 0.f;
-      for (int ps = 0; ps < P.n_pass; ++ps) {
-        const float scale = pl.P->scale[ps];
-        for (int k0 = kb0; k0 < kb1; k0 += P.chunk, ++cc) {
+      for (int ps = 0; ps < sh.n_pass; ++ps) {
+        const float scale = sh.scale(ps);
+        for (int k0 = sh.kb0; k0 < sh.kb1; k0 += sh.chunk, ++cc) {
           if (ok && !bar_wait(tfull + 8 * (cc & 1u), cc >> 1 & 1u)) ok = false;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) continue;  // the error word is set below; the tile's values are not written
@@ -589,6 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           }
         }
       }
+      const Product P = *pl.P;  // in registers (no indexed access)
       if (S > 1) {
         // one tile per cluster: the whole tile's sums go where the operands were, and are joined below
         if (ok) {
@@ -600,19 +909,38 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         break;
       }
+      if constexpr (BN >= 128) {
+        if (p.boxes) {
+#pragma unroll 1
+          for (int sl = 0; sl < kSlabs && pl.col0 + sl * kSlab < P.N; ++sl, ++use) {
+            if (ok && !bar_wait(ready + 8 * (use & 1u), use >> 1 & 1u)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            slab_values<GROUPED>(P, p, acc, staging + (use & 1u) * kSlabBytes, row, half, pl.row0 + my_rows,
+                                 pl.col0 + sl * kSlab + half * kHalf, pl.mirror);
+            fence_async();
+            __syncwarp();
+            if (lane == 0) bar_arrive(written + 8 * (use & 1u));
 #pragma unroll
-      for (int sl = 0; sl < kSlabs; ++sl) {
+            for (int k = 0; k + kHalf < BN / 2; ++k) acc[k] = acc[k + kHalf];  // the next slab's sums come first
+          }
+          continue;
+        }
+      }
+#pragma unroll 1
+      for (int sl = 0; sl < kSlabs; ++sl) {  // one copy of the code: it has to stay in the instruction cache
         bar_sync_epilogue();  // the slab before has been read
 #pragma unroll
-        for (int k = 0; k < kHalf; k += 4)
-          st_shared4(staging + (row * kSlabPitch + half * kHalf + k) * 4, &acc[sl * kHalf + k]);
+        for (int k = 0; k < kHalf; k += 4) st_shared4(staging + (row * kSlabPitch + half * kHalf + k) * 4, &acc[k]);
+#pragma unroll
+        for (int k = 0; k + kHalf < BN / 2; ++k) acc[k] = acc[k + kHalf];
         bar_sync_epilogue();
         const int row0 = pl.row0 + my_rows, col0 = pl.col0 + sl * kSlab;
         const OwnSums sums{staging};
-        if (ok && !P.swap) write_rows<kSlab, GROUPED>(P, p, row0, col0, lane, ew, 0, kTileM, pl.mirror, sums);
+        if (ok && !P.swap) write_rows<kSlab, GROUPED>(P, pl.P, p, row0, col0, lane, ew, 0, kTileM, pl.mirror, sums);
         if (GROUPED && pl.mirror) bar_sync_epilogue();
         if (ok && (P.swap || pl.mirror))
-          write_transposed<kSlab, GROUPED>(P, p, row0, col0, lane, ew, kEpiWarps, pl.mirror, sums);
+          write_transposed<kSlab, GROUPED>(P, pl.P, p, row0, col0, lane, ew, kEpiWarps, pl.mirror, sums);
       }
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrProductWait);
@@ -625,9 +953,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const ClusterSums sums{ring, S};
         const Product P = *pl.P;
         if (!P.swap)
-          write_rows<BN, GROUPED>(P, p, pl.row0, pl.col0, lane, ew, q * share, (q + 1) * share, false, sums);
+          write_rows<BN, GROUPED>(P, pl.P, p, pl.row0, pl.col0, lane, ew, q * share, (q + 1) * share, false, sums);
         if (P.swap || pl.mirror)
-          write_transposed<BN, GROUPED>(P, p, pl.row0, pl.col0, lane, q * kEpiWarps + ew, S * kEpiWarps, false, sums);
+          write_transposed<BN, GROUPED>(P, pl.P, p, pl.row0, pl.col0, lane, q * kEpiWarps + ew, S * kEpiWarps, false, sums);
       }
     }
   }
@@ -701,6 +1029,18 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
             dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_map32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {ld * 4};
+  const cuuint32_t box[2] = {32, (cuuint32_t)kBoxRows};
+  const cuuint32_t unit[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, unit,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream) {
