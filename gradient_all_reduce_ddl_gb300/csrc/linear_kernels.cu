@@ -4,12 +4,15 @@
 #include "activation.cuh"
 #include "linear_kernels.h"
 #include "product.h"
+#include "tc_ptx.cuh"
 
 namespace ddl {
 namespace {
 
 __global__ void pack16_kernel(const uint16_t* __restrict__ src, int64_t ld, uint16_t* __restrict__ dst, int64_t ldp,
                               int64_t rows, int64_t cols) {
+  tc::griddep_launch();
+  tc::griddep_wait();
   const int64_t col0 = (int64_t)blockIdx.x * 256 + (threadIdx.x & 31);
   for (int64_t r = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); r < rows; r += (int64_t)gridDim.y * 8) {
     uint16_t v[8];
@@ -53,6 +56,8 @@ __device__ __forceinline__ void planes_of(float v, int type, int n, uint16_t (&o
 // A CTA takes 128 columns x kDzRows rows; warp w the rows w, w + 8, ...
 template <bool VEC>
 __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
+  tc::griddep_launch();
+  tc::griddep_wait();
   __shared__ float sums[8][128];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c0 = (int64_t)blockIdx.y * 128, r0 = (int64_t)blockIdx.x * kDzRows;
@@ -113,6 +118,8 @@ __global__ void __launch_bounds__(256) dz_kernel(const DzParams p) {
 // 32 columns a CTA; warp w adds the row blocks w, w + 8, ..., then the warps' sums are added in order.
 __global__ void __launch_bounds__(256) db_kernel(const float* __restrict__ partial, int64_t blocks, int64_t cols,
                                                  void* db, int type, int accumulate) {
+  tc::griddep_launch();
+  tc::griddep_wait();
   __shared__ float sums[8][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
@@ -144,24 +151,19 @@ cudaError_t launch_pack16(const void* src, int64_t ld, void* dst, int64_t ldp, i
                           cudaStream_t stream) {
   const int64_t by = (rows + 7) / 8;
   const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)(by < 65535 ? by : 65535));
-  pack16_kernel<<<grid, 256, 0, stream>>>(static_cast<const uint16_t*>(src), ld, static_cast<uint16_t*>(dst), ldp, rows,
-                                          cols);
-  return cudaGetLastError();
+  return tc::launch_early(pack16_kernel, grid, 256, stream, static_cast<const uint16_t*>(src), ld,
+                          static_cast<uint16_t*>(dst), ldp, rows, cols);
 }
 
 cudaError_t launch_dz(const DzParams& p, cudaStream_t stream) {
   const dim3 grid((unsigned)((p.rows + kDzRows - 1) / kDzRows), (unsigned)((p.cols + 127) / 128));
-  if (p.vec)
-    dz_kernel<true><<<grid, 256, 0, stream>>>(p);
-  else
-    dz_kernel<false><<<grid, 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  return tc::launch_early(p.vec ? dz_kernel<true> : dz_kernel<false>, grid, 256, stream, p);
 }
 
 cudaError_t launch_db(const float* partial, int64_t blocks, int64_t cols, void* db, int type, int accumulate,
                       cudaStream_t stream) {
-  db_kernel<<<(unsigned)((cols + 31) / 32), 256, 0, stream>>>(partial, blocks, cols, db, type, accumulate);
-  return cudaGetLastError();
+  return tc::launch_early(db_kernel, dim3((unsigned)((cols + 31) / 32)), 256, stream, partial, blocks, cols, db, type,
+                          accumulate);
 }
 
 }  // namespace ddl

@@ -29,7 +29,7 @@ struct Stage {
   int splits = 1;
 };
 
-enum { kGram0, kGram1, kPoly, kApply0, kApply1, kLast0, kLast1, kStages };  // 0/1: the X iterate read
+enum { kGram0, kGram1, kPoly, kApply0, kApply1, kStages };  // 0/1: the X iterate read
 
 }  // namespace
 
@@ -168,23 +168,28 @@ ddl_status_t build(ddl_ortho* o) {
     ddl::OrthoMatrix& d = mats[i];
     d.offset = (int64_t)m.offset;
     d.ld = (int64_t)m.ld;
-    d.rows = (int64_t)m.rows;
-    d.cols = (int64_t)m.cols;
-    d.hi = base + p.x[0][0];
-    d.lo = base + p.x[0][1];
+    const bool wide = m.rows <= m.cols;
+    d.rows = (int32_t)m.rows;
+    d.cols = (int32_t)m.cols;
+    for (int k = 0; k < 2; ++k) {
+      d.hi[k] = base + p.x[k][0];
+      d.lo[k] = base + p.x[k][1];
+    }
     d.ldp = p.ldx;
+    d.shape_scale = wide ? 1.f : (float)std::sqrt((double)m.rows / (double)m.cols);
+    d.vec = m.offset % 4 == 0 && m.ld % 4 == 0 && m.cols % 4 == 0;
     d.item0 = (int32_t)items.size();
-    const int64_t elems = d.rows * d.cols;
-    for (int64_t b = 0; b < elems; b += ddl::kOrthoItemElems)
-      items.push_back({i, 0, b, std::min<int64_t>(elems, b + ddl::kOrthoItemElems)});
+    const int32_t cols = std::min(d.cols, ddl::kOrthoItemElems), rows = std::max(1, ddl::kOrthoItemElems / cols);
+    for (int32_t r = 0; r < d.rows; r += rows)
+      for (int32_t c = 0; c < d.cols; c += cols)
+        items.push_back({i, r, std::min(d.rows, r + rows), c, std::min(d.cols, c + cols)});
     d.n_items = (int32_t)items.size() - d.item0;
 
-    const bool wide = m.rows <= m.cols;
     const int map = 8 * i;
     for (int k = 0; k < kStages; ++k) {
       ddl::Product P;
       std::memset(&P, 0, sizeof(P));
-      const int xi = k == kGram1 || k == kApply1 || k == kLast1 ? 1 : 0;  // the iterate read
+      const int xi = k == kGram1 || k == kApply1 ? 1 : 0;  // the iterate read
       if (k == kGram0 || k == kGram1) {  // A = X X^T, or X^T X when X is tall
         P.M = P.N = (int32_t)s;
         P.K = (int32_t)(wide ? m.cols : m.rows);
@@ -204,13 +209,10 @@ ddl_status_t build(ddl_ortho* o) {
         P.K = (int32_t)s;
         P.b_mn = wide ? 1 : 0;  // X as [K][N]; B is its own transpose
         split_passes(&P, wide ? map + 6 : map + 2 * xi, wide ? map + 2 * xi : map + 6);
-        P.epi = k == kApply0 || k == kApply1 ? ddl::kEpiApply : ddl::kEpiOrtho;
+        P.epi = ddl::kEpiApply;
         P.c_hi = base + p.x[xi][0];
         P.c_lo = base + p.x[xi][1];
         P.ldc = p.ldx;
-        P.ldo = (int64_t)m.ld;
-        P.offset = (int64_t)m.offset;
-        P.shape_scale = wide ? 1.f : (float)std::sqrt((double)m.rows / (double)m.cols);
       }
       P.p_hi = base + (k == kPoly ? p.b[0] : k == kApply0 || k == kApply1 ? p.x[1 - xi][0] : p.a[0]);
       P.p_lo = base + (k == kPoly ? p.b[1] : k == kApply0 || k == kApply1 ? p.x[1 - xi][1] : p.a[1]);
@@ -219,8 +221,7 @@ ddl_status_t build(ddl_ortho* o) {
       P.in1 = P.in0 < 0 ? -1 : P.in0 + 1;
       P.out0 = k == kPoly ? map + 6 : k == kApply0 || k == kApply1 ? map + 2 * (1 - xi) : map + 4;
       P.out1 = P.out0 + 1;
-      // planes always allow 4-element accesses; the flat buffers' rows do where the offset and ld do
-      P.vec = k >= kLast0 ? (m.offset % 4 == 0 && m.ld % 4 == 0) : 1;
+      P.vec = 1;  // planes always allow 4-element accesses
       o->stage[k].products.push_back(P);
     }
   }
@@ -274,27 +275,25 @@ ddl_status_t bind(ddl_ortho* o) {
   return DDL_OK;
 }
 
-// The products of every step; `last` is the kind of the final epilogue.
-ddl_status_t products(ddl_ortho* o, ddl::ProductLaunch* L, int last, bool vec, cudaStream_t s) {
-  L->g_maps = o->d_maps;
-  L->err = o->d_err;
-  L->ca = o->coeff[0];
-  L->cb = o->coeff[1];
-  L->cc = o->coeff[2];
-  L->last_epi = last;
-  L->flat_vec = vec;
-  int x = 0;
-  for (int k = 0; k < o->steps; ++k, x ^= 1) {
-    const int order[3] = {x ? kGram1 : kGram0, kPoly,
-                          k + 1 < o->steps ? (x ? kApply1 : kApply0) : (x ? kLast1 : kLast0)};
+// The products of every step; the result is iterate steps & 1.
+ddl_status_t products(ddl_ortho* o, cudaStream_t s) {
+  ddl::ProductLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  L.g_maps = o->d_maps;
+  L.err = o->d_err;
+  L.ca = o->coeff[0];
+  L.cb = o->coeff[1];
+  L.cc = o->coeff[2];
+  for (int k = 0; k < o->steps; ++k) {
+    const int order[3] = {k & 1 ? kGram1 : kGram0, kPoly, k & 1 ? kApply1 : kApply0};
     for (int kind : order) {
       const Stage& st = o->stage[kind];
-      L->g_products = st.d_products;
-      L->g_tiles = st.d_tiles;
-      L->n_tiles = (int32_t)st.tiles.size();
-      L->splits = st.splits;
-      L->boxes = st.splits == 1 && kind < kLast0;  // the last product goes to the caller's buffers
-      const cudaError_t e = ddl::launch_product(*L, st.tile, true, o->sms, s);
+      L.g_products = st.d_products;
+      L.g_tiles = st.d_tiles;
+      L.n_tiles = (int32_t)st.tiles.size();
+      L.splits = st.splits;
+      L.boxes = st.splits == 1;
+      const cudaError_t e = ddl::launch_product(L, st.tile, true, o->sms, s);
       if (e != cudaSuccess) return ddl::status_of(e);
     }
   }
@@ -304,6 +303,20 @@ ddl_status_t products(ddl_ortho* o, ddl::ProductLaunch* L, int last, bool vec, c
 int elem_size(int type) { return type == ddl::kF32 ? 4 : 2; }
 
 bool aligned4(const void* p, int esize) { return reinterpret_cast<uintptr_t>(p) % (4 * (size_t)esize) == 0; }
+
+// Preparation, products and the finishing pass.
+ddl_status_t update(ddl_ortho* o, const ddl::OrthoPrep& p, ddl::OrthoFinish* f, cudaStream_t s) {
+  cudaError_t e = ddl::launch_ortho_norms(p, s);
+  if (e == cudaSuccess) e = ddl::launch_ortho_planes(p, s);
+  if (e != cudaSuccess) return ddl::status_of(e);
+  const ddl_status_t st = products(o, s);
+  if (st != DDL_OK) return st;
+  f->matrices = o->d_mats;
+  f->items = o->d_items;
+  f->n_items = o->n_items;
+  f->iterate = o->steps & 1;
+  return ddl::status_of(ddl::launch_ortho_finish(*f, s));
+}
 
 }  // namespace
 
@@ -327,7 +340,7 @@ ddl_status_t ddl_ortho_create(int n_matrices, const ddl_matrix_t* matrices, ddl_
     }
     extent = std::max<uint64_t>(extent, m.offset + (m.rows - 1) * m.ld + m.cols);
     tiles += (uint64_t)blocks_of((int64_t)m.rows, 128) * (uint64_t)blocks_of((int64_t)m.cols, 128);
-    items += m.rows * m.cols / ddl::kOrthoItemElems + 1;
+    items += m.rows * m.cols / (ddl::kOrthoItemElems / 2) + m.rows + 1;
   }
   if (unsupported || tiles > (1ull << 27) || items > (1ull << 27)) return DDL_ERR_UNSUPPORTED;
   ddl_ortho* o = new (std::nothrow) ddl_ortho();
@@ -373,15 +386,14 @@ ddl_status_t ddl_ortho_run(ddl_ortho_t o, const void* in, void* out, void* strea
   if (st != DDL_OK) return st;
   if (!ddl::device_pointer(in, o->device) || !ddl::device_pointer(out, o->device)) return DDL_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  ddl::OrthoPrep p = {o->d_mats, o->d_items, o->d_partial, in, o->type, nullptr, 0.f, 0, o->eps, o->n_items};
-  cudaError_t e = ddl::launch_ortho_norms(p, s);
-  if (e == cudaSuccess) e = ddl::launch_ortho_planes(p, s);
-  if (e != cudaSuccess) return ddl::status_of(e);
-  ddl::ProductLaunch L;
-  std::memset(&L, 0, sizeof(L));
-  L.flat_out = out;
-  L.flat_type = o->type;
-  return products(o, &L, ddl::kEpiOrtho, aligned4(out, es), s);
+  ddl::OrthoPrep p = {o->d_mats, o->d_items, o->d_partial, in,     o->type,          nullptr,
+                      0.f,       0,          o->eps,       o->n_items, aligned4(in, es)};
+  ddl::OrthoFinish f;
+  std::memset(&f, 0, sizeof(f));
+  f.out = out;
+  f.type = o->type;
+  f.vec = aligned4(out, es);
+  return update(o, p, &f, s);
 }
 
 ddl_status_t ddl_ortho_muon(ddl_ortho_t o, const void* grad, int n_copies, float* const* param_bufs, float* mom, float lr,
@@ -390,8 +402,8 @@ ddl_status_t ddl_ortho_muon(ddl_ortho_t o, const void* grad, int n_copies, float
   if (n_copies > ddl::kMaxCopies || o->type == ddl::kBF16) return DDL_ERR_UNSUPPORTED;
   const int es = elem_size(o->type);
   if (reinterpret_cast<uintptr_t>(grad) % es || reinterpret_cast<uintptr_t>(mom) % 4) return DDL_ERR_INVALID_ARG;
-  ddl::ProductLaunch L;
-  std::memset(&L, 0, sizeof(L));
+  ddl::OrthoFinish f;
+  std::memset(&f, 0, sizeof(f));
   bool vec = true;
   uintptr_t at[ddl::kMaxCopies + 1];
   const uint64_t bytes = o->extent * 4;
@@ -401,7 +413,7 @@ ddl_status_t ddl_ortho_muon(ddl_ortho_t o, const void* grad, int n_copies, float
     const ddl::Range rp(p, bytes);
     if (!p || reinterpret_cast<uintptr_t>(p) % 4 || rp.wraps() || rg.wraps() || rp.overlaps(rg)) return DDL_ERR_INVALID_ARG;
     if (r < n_copies) {
-      L.copies[r] = p;
+      f.copies[r] = p;
       vec = vec && aligned4(p, 4);
     }
     at[r] = reinterpret_cast<uintptr_t>(p);
@@ -415,15 +427,13 @@ ddl_status_t ddl_ortho_muon(ddl_ortho_t o, const void* grad, int n_copies, float
   for (int r = 0; r < n_copies; ++r)
     if (!ddl::device_pointer(param_bufs[r], o->device)) return DDL_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  ddl::OrthoPrep p = {o->d_mats, o->d_items, o->d_partial, grad, o->type, mom, momentum, nesterov ? 1 : 0, o->eps,
-                      o->n_items};
-  cudaError_t e = ddl::launch_ortho_norms(p, s);
-  if (e == cudaSuccess) e = ddl::launch_ortho_planes(p, s);
-  if (e != cudaSuccess) return ddl::status_of(e);
-  L.lr = lr;
-  L.decay = 1.f - lr * weight_decay;
-  L.n_copies = n_copies;
-  return products(o, &L, ddl::kEpiMuon, vec, s);
+  ddl::OrthoPrep p = {o->d_mats, o->d_items,       o->d_partial, grad,       o->type,                              mom,
+                      momentum,  nesterov ? 1 : 0, o->eps,       o->n_items, aligned4(grad, es) && aligned4(mom, 4)};
+  f.lr = lr;
+  f.decay = 1.f - lr * weight_decay;
+  f.n_copies = n_copies;
+  f.vec = vec;
+  return update(o, p, &f, s);
 }
 
 ddl_status_t ddl_ortho_check(ddl_ortho_t o, void* stream) {

@@ -19,7 +19,6 @@ constexpr int kBlockK = 64;      // contraction elements per stage (one 128-byte
 constexpr int kBoxRows = 64;     // rows of a TMA box
 constexpr int kMaxPasses = 3;
 constexpr int kMaxMaps = 8;      // tensor maps carried in the launch record
-constexpr int kMaxCopies = 256;  // parameter copies of the Muon step
 
 enum ElemType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
 enum ActKind : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
@@ -28,9 +27,7 @@ enum EpilogueKind : int {
   kEpiStore = 1,   // out = D (+ out)
   kEpiGram = 2,    // planes of D, and of its transpose
   kEpiPoly = 3,    // planes of b C + c D (C, D symmetric), and of the transpose
-  kEpiApply = 4,   // planes of a C + D
-  kEpiOrtho = 5,   // out = a C + D, in the matrix's place of a flat buffer
-  kEpiMuon = 6     // p = p (1 - lr wd) - lr s (a C + D) in every parameter copy
+  kEpiApply = 4    // planes of a C + D
 };
 
 // One product.  A is M x K, B is N x K; a_mn / b_mn: stored with the rows
@@ -56,7 +53,7 @@ struct Product {
   int64_t ld_add;
   void* z;
   int64_t ldz;
-  void* out;         // kEpiOrtho: element offset added to the launch's buffer
+  void* out;
   int64_t ldo;
   // Newton-Schulz: C's planes, the result's planes (row strides ldc, ldp)
   const uint16_t* c_hi;
@@ -65,8 +62,6 @@ struct Product {
   uint16_t* p_hi;
   uint16_t* p_lo;
   int64_t ldp;
-  int64_t offset;    // the matrix's first element in the flat buffers
-  float shape_scale; // s of the Muon step
 };
 
 struct Tile {
@@ -88,15 +83,7 @@ struct ProductLaunch {
   int32_t boxes;            // tiles of 128 or 256 columns, splits 1: the epilogue moves boxes by TMA (in0 ... out1)
   int32_t bf16;             // operands are bfloat16, else binary16
   uint32_t* err;
-  // Newton-Schulz coefficients and the flat buffers of its last product
-  float ca, cb, cc;
-  int32_t last_epi;         // kEpiOrtho or kEpiMuon, where a product's own is kEpiOrtho
-  int32_t flat_vec;         // those buffers allow 4-element accesses
-  void* flat_out;
-  int32_t flat_type;
-  float lr, decay;          // decay = 1 - lr * weight_decay
-  int32_t n_copies;
-  float* copies[kMaxCopies];
+  float ca, cb, cc;         // Newton-Schulz coefficients
 };
 
 // tile_n: 128, 64 or 32 output columns per 128-row tile; 256: 256 x 256 tiles on CTA pairs (splits 1).  Grouped

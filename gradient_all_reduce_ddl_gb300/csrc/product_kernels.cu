@@ -193,7 +193,7 @@ __device__ __forceinline__ void emit_linear(const Product& P, const int (&m)[R],
 }
 
 // V values of D in each of R rows: rows m[i] of the output (where in[i]), columns n...  Every load of the R rows is
-// issued before the first is used.  v becomes what was stored (before the flat buffers' rounding).
+// issued before the first is used.  v becomes what was stored.
 template <int V, int R, bool GROUPED>
 __device__ __forceinline__ void emit(const Product& P, const ProductLaunch& p, const int (&m)[R], const bool (&in)[R],
                                      int n, float (&v)[R][V]) {
@@ -231,39 +231,9 @@ __device__ __forceinline__ void emit(const Product& P, const ProductLaunch& p, c
 #pragma unroll
         for (int k = 0; k < V; ++k) v[i][k] = cc * c[i][k] + cd * v[i][k];
     }
-    if (P.epi != kEpiOrtho) {
 #pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (in[i]) store_planes(P.p_hi, P.p_lo, (int64_t)m[i] * P.ldp + n, v[i]);
-      return;
-    }
-    if (p.last_epi == kEpiOrtho) {
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (in[i]) store_any(p.flat_out, P.offset + (int64_t)m[i] * P.ldo + n, p.flat_type, v[i]);
-      return;
-    }
-    const float step = p.lr * P.shape_scale;
-    constexpr int kFlight = R >= 4 ? 2 : 4;  // copies loaded at once
-    for (int r = 0; r < p.n_copies; r += kFlight) {
-      float t[kFlight][R][V];
-#pragma unroll
-      for (int j = 0; j < kFlight; ++j)
-        if (r + j < p.n_copies)
-#pragma unroll
-          for (int i = 0; i < R; ++i)
-            if (in[i]) load32(p.copies[r + j] + P.offset + (int64_t)m[i] * P.ldo + n, t[j][i]);
-#pragma unroll
-      for (int j = 0; j < kFlight; ++j)
-        if (r + j < p.n_copies)
-#pragma unroll
-          for (int i = 0; i < R; ++i) {
-            if (!in[i]) continue;
-#pragma unroll
-            for (int k = 0; k < V; ++k) t[j][i][k] = t[j][i][k] * p.decay - step * v[i][k];
-            store32(p.copies[r + j] + P.offset + (int64_t)m[i] * P.ldo + n, t[j][i]);
-          }
-    }
+    for (int i = 0; i < R; ++i)
+      if (in[i]) store_planes(P.p_hi, P.p_lo, (int64_t)m[i] * P.ldp + n, v[i]);
   }
 }
 
@@ -306,12 +276,6 @@ struct Place {
   const Product* P;
   int row0, col0, mirror;
 };
-
-// Whether a product's epilogue may take 4 elements at a time.
-template <bool GROUPED>
-__device__ __forceinline__ bool wide_access(const Product& P, const ProductLaunch& p) {
-  return P.vec && (!GROUPED || P.epi != kEpiOrtho || p.flat_vec);
-}
 
 template <int BN, bool GROUPED>
 __device__ __forceinline__ Place place(const ProductLaunch& p, int t) {
@@ -410,7 +374,7 @@ template <int COLS, bool GROUPED, class Sums>
 __device__ __forceinline__ void write_rows(const Product& P, const Product* from, const ProductLaunch& p, int row0,
                                            int col0, int lane, int ew, int r0, int r1, bool back, const Sums sums) {
   constexpr int kStride = kEpiWarps * 4 * (COLS / 4 < 32 ? 128 / COLS : 1);  // rows a pass of all warps covers
-  if (wide_access<GROUPED>(P, p)) {
+  if (P.vec) {
     // tiles that lie wholly inside need no predicate anywhere
     if (row0 + r1 <= P.M && col0 + COLS <= P.N && (r1 - r0) % kStride == 0)
       write_rows_wide<COLS, GROUPED, true>(P, from, p, row0, col0, lane, ew, r0, r1, back, sums);

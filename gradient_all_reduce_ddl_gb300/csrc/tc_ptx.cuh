@@ -102,6 +102,22 @@ __device__ __forceinline__ void bar_arrive_cluster(uint32_t bar) {
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Launches a kernel that may start while the one before it on the stream drains; it calls griddep_wait() before it
+// touches what that kernel writes.
+template <class... Args>
+inline cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int threads, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // -- tcgen05 -------------------------------------------------------------------
 
 // PAIR: both CTAs of the pair make the call, for the same columns of each.
