@@ -333,7 +333,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
       P.b[k] = 3;
       P.scale[k] = ddl::plane_scale(h->type, planes, k);
     }
-    P.chunk = grad_dtype == DDL_FP32 ? 4 : (int32_t)blocks_of(T, ddl::kBlockK);
+    P.chunk = grad_dtype == DDL_FP32 ? 8 : (int32_t)blocks_of(T, ddl::kBlockK);
     P.epi = ddl::kEpiStore;
     P.out_type = grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16;
     P.accumulate = accumulate ? 1 : 0;

@@ -104,7 +104,7 @@ void split_passes(ddl::Product* P, int a_hi, int b_hi) {
     P->b[k] = b[k];
     P->scale[k] = k == 0 ? 1.f : 1.f / 2048.f;
   }
-  P->chunk = 4;
+  P->chunk = 8;
 }
 
 // The tiles of every product of a stage, longest contractions first so that the last to start are short.

@@ -308,7 +308,15 @@ struct OwnSums {
 };
 struct ClusterSums {
   uint32_t base;
-  int parts;
+  int parts;  // 2, 4 or 8
+  template <int PARTS>
+  __device__ __forceinline__ void add4(uint32_t at, float (&v)[4]) const {
+    float4 u[PARTS];
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) u[k] = ld_peer4(peer_addr(base + at, k));
+#pragma unroll
+    for (int k = 0; k < PARTS; ++k) v[0] += u[k].x, v[1] += u[k].y, v[2] += u[k].z, v[3] += u[k].w;
+  }
   __device__ __forceinline__ float one(uint32_t at) const {
     float v = 0.f;
     for (int k = 0; k < parts; ++k) v += ld_peer(peer_addr(base + at, k));
@@ -316,10 +324,12 @@ struct ClusterSums {
   }
   __device__ __forceinline__ void four(uint32_t at, float (&v)[4]) const {
     v[0] = v[1] = v[2] = v[3] = 0.f;
-    for (int k = 0; k < parts; ++k) {
-      const float4 u = ld_peer4(peer_addr(base + at, k));
-      v[0] += u.x, v[1] += u.y, v[2] += u.z, v[3] += u.w;
-    }
+    if (parts == 2)
+      add4<2>(at, v);
+    else if (parts == 4)
+      add4<4>(at, v);
+    else
+      add4<8>(at, v);
   }
 };
 
@@ -391,27 +401,34 @@ __device__ __forceinline__ void write_rows(const Product& P, const Product* from
   }
 }
 
-// Writes the sums with D(i, j) at output row j, column i.  A warp takes 32 rows i, so that its stores run along
-// output rows.  finished: the values are final (symmetric products' mirror images).
+// Writes rows [r0, r0 + rows) of the sums with D(i, j) at output row j, column i: neighbouring lanes take neighbouring
+// rows i, so that stores run along output rows, and four columns j.  rows is 16, 32, 64 or 128.  finished: the values
+// are final (symmetric products' mirror images).
 template <int COLS, bool GROUPED, class Sums>
-__device__ __forceinline__ void write_transposed(const Product& P, const Product* from, const ProductLaunch& p, int row0,
-                                                 int col0, int lane, int first, int step, bool finished, const Sums sums) {
+__device__ __forceinline__ void write_transposed(const Product& P, const ProductLaunch& p, int row0, int col0, int thread,
+                                                 int r0, int rows, bool finished, const Sums sums) {
   constexpr int kPitch = pitch(COLS);
-  for (int u = first; u < COLS; u += step) {
-    const int i = (u & 3) * 32 + lane, c = (u >> 2) * 4, n = row0 + i;
-    if (n >= P.M) continue;
+#pragma unroll 1
+  for (int u = thread; u < rows * (COLS / 4); u += kEpiWarps * 32) {
+    const int i = r0 + u % rows, c = u / rows * 4, n = row0 + i;
+    if (n >= P.M || col0 + c >= P.N) continue;
     float v[4];
     sums.four((i * kPitch + c) * 4, v);
+    int m[4];
+    bool in[4];
+    float w[4][1];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const int m = col0 + c + k;
-      if (m >= P.N) continue;
-      if (finished) {
-        float w[1] = {v[k]};
-        store_planes(P.p_hi, P.p_lo, (int64_t)m * P.ldp + n, w);
-      } else {
-        emit_one<GROUPED>(from, &p, m, n, v[k]);
-      }
+      m[k] = col0 + c + k;
+      in[k] = m[k] < P.N;
+      w[k][0] = v[k];
+    }
+    if (finished) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (in[k]) store_planes(P.p_hi, P.p_lo, (int64_t)m[k] * P.ldp + n, w[k]);
+    } else {
+      emit<1, 4, GROUPED>(P, p, m, in, n, w);
     }
   }
 }
@@ -621,6 +638,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   fence_after();
   const uint32_t tmem = tmem_slot;
   griddep_launch();
+  if constexpr (GROUPED) {
+    // the first tile's records are the handle's own: to L1 and L2 while the kernel before still runs
+    const int t = blockIdx.x / (PAIR ? 2 : p.splits);
+    if (warp == 3 && t < p.n_tiles) {
+      const Place pl = place<BN, GROUPED>(p, t);
+      const int ps = lane & 3;
+      if (lane < 3 && ps < pl.P->n_pass)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(p.g_maps + pl.P->a[ps]) : "memory");
+      else if (lane >= 4 && lane < 7 && ps < pl.P->n_pass)
+        asm volatile("prefetch.tensormap [%0];" ::"l"(p.g_maps + pl.P->b[ps]) : "memory");
+    }
+  } else if (warp == 3 && lane < 2) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(p.maps + (lane ? p.inl[0].b[0] : p.inl[0].a[0])) : "memory");
+  }
   griddep_wait();
 
   const int S = PAIR ? 1 : p.splits;
@@ -904,22 +935,26 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if (ok && !P.swap) write_rows<kSlab, GROUPED>(P, pl.P, p, row0, col0, lane, ew, 0, kTileM, pl.mirror, sums);
         if (GROUPED && pl.mirror) bar_sync_epilogue();
         if (ok && (P.swap || pl.mirror))
-          write_transposed<kSlab, GROUPED>(P, pl.P, p, row0, col0, lane, ew, kEpiWarps, pl.mirror, sums);
+          write_transposed<kSlab, GROUPED>(P, p, row0, col0, ew * 32 + lane, 0, kTileM, pl.mirror, sums);
       }
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrProductWait);
     if (S > 1) {
       __syncwarp();
       cluster_sync();  // every CTA's sums are in its shared memory
-      if (*reinterpret_cast<volatile uint32_t*>(p.err) == 0) {
+      {  // also after a failed wait (every warp has to reach the same barriers); the values are void then
         const Place pl = place<BN, GROUPED>(p, first);
         const int share = kTileM / S;
         const ClusterSums sums{ring, S};
         const Product P = *pl.P;
+        // this CTA finishes its share of the rows; nobody else reads them, so its own copy can take the results
         if (!P.swap)
-          write_rows<BN, GROUPED>(P, pl.P, p, pl.row0, pl.col0, lane, ew, q * share, (q + 1) * share, false, sums);
-        if (P.swap || pl.mirror)
-          write_transposed<BN, GROUPED>(P, pl.P, p, pl.row0, pl.col0, lane, q * kEpiWarps + ew, S * kEpiWarps, false, sums);
+          write_rows<BN, GROUPED>(P, pl.P, p, pl.row0, pl.col0, lane, ew, q * share, (q + 1) * share, pl.mirror, sums);
+        if (GROUPED && pl.mirror) bar_sync_epilogue();
+        if (P.swap)
+          write_transposed<BN, GROUPED>(P, p, pl.row0, pl.col0, ew * 32 + lane, q * share, share, false, sums);
+        else if (pl.mirror)
+          write_transposed<BN, GROUPED>(P, p, pl.row0, pl.col0, ew * 32 + lane, q * share, share, true, OwnSums{ring});
       }
     }
   }
