@@ -25,7 +25,7 @@ struct ddl_linear {
   int device = -1;
   int sms = 0;
   uint32_t* d_err = nullptr;
-  Buffer x, w, dz[ddl::kMaxPlanes], partial;
+  Buffer x, w, dz[ddl::kMaxPlanes], partial, done;
 };
 
 namespace {
@@ -45,6 +45,7 @@ ddl_status_t bind(ddl_linear* h) {
   uint32_t* err = nullptr;
   e = ddl::device_alloc(reinterpret_cast<void**>(&err), sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaMemset(err, 0, sizeof(uint32_t));
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);  // the caller's stream may not wait for that one
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) {
     cudaFree(err);
@@ -82,15 +83,16 @@ bool fits(int64_t rows, int64_t ld, int64_t cols) {
   return ld >= cols && ld <= (1ll << 31) && rows <= (1ll << 60) / ld;
 }
 
-// The matrix itself, or its copy with 16-byte aligned rows.
-ddl_status_t aligned(const Mat& m, int64_t max_rows, Buffer* b, cudaStream_t s, Mat* out) {
+// The matrix itself, or where the preparing launch copies it with 16-byte aligned rows.
+ddl_status_t aligned(const Mat& m, int64_t max_rows, Buffer* b, ddl::LinearPrep* prep, Mat* out) {
   *out = m;
   if (m.tma()) return DDL_OK;
   const int64_t ldp = (int64_t)ddl::round8((uint64_t)m.cols);
   const ddl_status_t st = need(b, (size_t)max_rows * (size_t)ldp * 2);
   if (st != DDL_OK) return st;
   *out = Mat{b->p, m.rows, m.cols, ldp};
-  return ddl::status_of(ddl::launch_pack16(m.p, m.ld, b->p, ldp, m.rows, m.cols, s));
+  prep->pack[prep->n_packs++] = {static_cast<const uint16_t*>(m.p), m.ld, static_cast<uint16_t*>(b->p), ldp, m.rows, m.cols};
+  return DDL_OK;
 }
 
 bool map_of(ddl::ProductLaunch* L, int k, const Mat& m, int box_rows) {
@@ -178,8 +180,12 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
     if (p && !ddl::device_pointer(p, h->device)) return DDL_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   Mat ax, aw;
-  if ((st = aligned(mx, h->max_tokens, &h->x, s, &ax)) != DDL_OK) return st;
-  if ((st = aligned(mw, N, &h->w, s, &aw)) != DDL_OK) return st;
+  ddl::LinearPrep prep;
+  std::memset(&prep, 0, sizeof(prep));
+  prep.type = h->type;
+  if ((st = aligned(mx, h->max_tokens, &h->x, &prep, &ax)) != DDL_OK) return st;
+  if ((st = aligned(mw, N, &h->w, &prep, &aw)) != DDL_OK) return st;
+  if (prep.n_packs && (st = ddl::status_of(ddl::launch_linear_prep(prep, s))) != DDL_OK) return st;
 
   ddl::ProductLaunch L;
   std::memset(&L, 0, sizeof(L));
@@ -277,32 +283,40 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   const int64_t ldp = own_dz ? (int64_t)ddl::round8((uint64_t)N) : mdy.ld;
   for (int k = 0; k < n_planes; ++k)
     if ((st = need(&h->dz[k], (size_t)h->max_tokens * (size_t)ldp * 2)) != DDL_OK) return st;
-  const int64_t row_blocks = blocks_of(T, ddl::kDzRows);
-  if (db && (st = need(&h->partial, (size_t)blocks_of(h->max_tokens, ddl::kDzRows) * (size_t)N * 4)) != DDL_OK) return st;
+  ddl::LinearPrep prep;
+  std::memset(&prep, 0, sizeof(prep));
+  prep.type = h->type;
   Mat ax, aw;
-  if (dw && (st = aligned(mx, h->max_tokens, &h->x, s, &ax)) != DDL_OK) return st;
-  if (dx && (st = aligned(mw, N, &h->w, s, &aw)) != DDL_OK) return st;
+  if (dw && (st = aligned(mx, h->max_tokens, &h->x, &prep, &ax)) != DDL_OK) return st;
+  if (dx && (st = aligned(mw, N, &h->w, &prep, &aw)) != DDL_OK) return st;
   if (n_planes || db) {
-    ddl::DzParams d;
-    std::memset(&d, 0, sizeof(d));
-    d.dy = dy;
-    d.ldy = mdy.ld;
-    d.z = mz.p;
-    d.ldz = mz.ld;
-    d.rows = T;
-    d.cols = N;
-    d.type = h->type;
-    d.act = h->act;
-    d.n_planes = n_planes;
-    for (int k = 0; k < n_planes; ++k) d.planes[k] = static_cast<uint16_t*>(h->dz[k].p);
-    d.ldp = ldp;
-    d.partial = db ? static_cast<float*>(h->partial.p) : nullptr;
-    d.vec = mdy.vec4(2) && (!has_z || mz.vec4(2)) && N % 4 == 0;
-    cudaError_t e = ddl::launch_dz(d, s);
-    if (e == cudaSuccess && db)
-      e = ddl::launch_db(d.partial, row_blocks, N, db, grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16, accumulate, s);
-    if (e != cudaSuccess) return ddl::status_of(e);
+    prep.has_dz = 1;
+    prep.dy = dy;
+    prep.ldy = mdy.ld;
+    prep.z = mz.p;
+    prep.ldz = mz.ld;
+    prep.rows = T;
+    prep.cols = N;
+    prep.act = h->act;
+    prep.n_planes = n_planes;
+    for (int k = 0; k < n_planes; ++k) prep.planes[k] = static_cast<uint16_t*>(h->dz[k].p);
+    prep.ldp = ldp;
+    prep.vec = mdy.tma() && (!has_z || mz.tma()) && N % 8 == 0;
   }
+  if (db) {
+    const size_t done = (size_t)blocks_of(N, ddl::kDzCols) * 4;
+    if ((st = need(&h->partial, (size_t)blocks_of(h->max_tokens, ddl::kDzRows) * (size_t)N * 4)) != DDL_OK) return st;
+    if (!h->done.p) {
+      if ((st = need(&h->done, done)) != DDL_OK) return st;
+      if ((st = ddl::status_of(cudaMemsetAsync(h->done.p, 0, done, s))) != DDL_OK) return st;
+    }
+    prep.db = db;
+    prep.db_f32 = grad_dtype == DDL_FP32;
+    prep.accumulate = accumulate ? 1 : 0;
+    prep.partial = static_cast<float*>(h->partial.p);
+    prep.done = static_cast<uint32_t*>(h->done.p);
+  }
+  if ((st = ddl::status_of(ddl::launch_linear_prep(prep, s))) != DDL_OK) return st;
   if (!dx && !dw) return DDL_OK;
 
   ddl::ProductLaunch L;
@@ -396,7 +410,7 @@ ddl_status_t ddl_linear_check(ddl_linear_t h, void* stream) {
 ddl_status_t ddl_linear_destroy(ddl_linear_t h) {
   if (!h) return DDL_OK;
   cudaError_t e = cudaSuccess;
-  for (void* p : {(void*)h->d_err, h->x.p, h->w.p, h->dz[0].p, h->dz[1].p, h->dz[2].p, h->partial.p})
+  for (void* p : {(void*)h->d_err, h->x.p, h->w.p, h->dz[0].p, h->dz[1].p, h->dz[2].p, h->partial.p, h->done.p})
     if (p) {
       const cudaError_t f = cudaFree(p);  // waits for the device
       if (e == cudaSuccess) e = f;

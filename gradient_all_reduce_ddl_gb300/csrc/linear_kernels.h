@@ -1,4 +1,4 @@
-// linear_kernels.h -- launches of the linear layers' element-wise kernels (internal).
+// linear_kernels.h -- the launch before a linear layer's products (internal).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -7,34 +7,41 @@
 
 namespace ddl {
 
-constexpr int kDzRows = 64;   // rows of dz whose column sums one CTA makes
+constexpr int kDzRows = 64, kDzCols = 256;  // what a CTA makes of dz
 constexpr int kMaxPlanes = 3;
 
-// Copies a rows x cols 16-bit matrix to rows padded to ldp elements.
-cudaError_t launch_pack16(const void* src, int64_t ld, void* dst, int64_t ldp, int64_t rows, int64_t cols,
-                          cudaStream_t stream);
+// A copy of a rows x cols 16-bit matrix with rows padded to ldp elements.
+struct Pack {
+  const uint16_t* src;
+  int64_t ld;
+  uint16_t* dst;
+  int64_t ldp, rows, cols;
+};
 
-struct DzParams {
+// What the products need first: up to two operand copies, and dz = dy act'(z) as planes with its column sums.
+struct LinearPrep {
+  int32_t n_packs;
+  Pack pack[2];
+  int32_t has_dz;
   const void* dy;
   int64_t ldy;
   const void* z;  // NULL: dz = dy
   int64_t ldz;
   int64_t rows, cols;
   int32_t type, act;
-  int32_t n_planes;   // 0: column sums only
-  int32_t split;      // more planes than one: binary16 halves (see plane_scale), bfloat16 thirds
+  int32_t n_planes;  // 0: column sums only
   uint16_t* planes[kMaxPlanes];
   int64_t ldp;
-  float* partial;     // [ceil(rows / kDzRows)][cols] column sums, or NULL
-  int32_t vec;        // rows and pointers allow 4-element accesses
+  int32_t vec;       // rows and pointers allow 16-byte accesses
+  // the bias gradient: NULL, or db (+)= the column sums; partial has a row per kDzRows rows, done a zero per kDzCols
+  void* db;
+  int32_t db_f32, accumulate;
+  float* partial;
+  uint32_t* done;
 };
-cudaError_t launch_dz(const DzParams& p, cudaStream_t stream);
+cudaError_t launch_linear_prep(const LinearPrep& p, cudaStream_t stream);
 
 // What plane k of n of dz is multiplied by.
 float plane_scale(int type, int n, int k);
-
-// db (+)= the column sums' sum, in row-block order.
-cudaError_t launch_db(const float* partial, int64_t blocks, int64_t cols, void* db, int type, int accumulate,
-                      cudaStream_t stream);
 
 }  // namespace ddl

@@ -249,6 +249,7 @@ ddl_status_t build(ddl_ortho* o) {
   if (e == cudaSuccess) e = ddl::device_alloc(reinterpret_cast<void**>(&o->d_partial), items.size() * sizeof(double));
   const uint32_t zero = 0;
   if (e == cudaSuccess) e = upload(&o->d_err, &zero, 1);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);  // the caller's stream may not wait for that one
   return ddl::status_of(e);
 }
 

@@ -390,13 +390,24 @@ __device__ __forceinline__ void write_rows(const Product& P, const Product* from
       write_rows_wide<COLS, GROUPED, true>(P, from, p, row0, col0, lane, ew, r0, r1, back, sums);
     else
       write_rows_wide<COLS, GROUPED, false>(P, from, p, row0, col0, lane, ew, r0, r1, back, sums);
-  } else {  // rows at any alignment: a warp along a row, element by element
+  } else {  // rows at any alignment: a warp along a row, element by element, four rows at a time
 #pragma unroll 1
-    for (int r = r0 + ew; r < r1; r += kEpiWarps) {
-      if (row0 + r >= P.M) break;
+    for (int c = lane; c < COLS; c += 32) {
+      if (col0 + c >= P.N) break;
 #pragma unroll 1
-      for (int c = lane; c < COLS; c += 32)
-        if (col0 + c < P.N) emit_one<GROUPED>(from, &p, row0 + r, col0 + c, sums.one((r * (COLS + 4) + c) * 4));
+      for (int rr = r0 + ew; rr < r1; rr += kEpiWarps * 4) {
+        int m[4];
+        bool in[4];
+        float v[4][1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = rr + i * kEpiWarps;
+          m[i] = row0 + r;
+          in[i] = r < r1 && m[i] < P.M;
+          v[i][0] = in[i] ? sums.one((r * (COLS + 4) + c) * 4) : 0.f;
+        }
+        emit<1, 4, GROUPED>(P, p, m, in, col0 + c, v);
+      }
     }
   }
 }

@@ -130,14 +130,33 @@ def _dev_ptrs(bufs):
     return [b.data_ptr() if hasattr(b, "data_ptr") else int(b) for b in bufs]
 
 
+_raw_stream = None  # torch's lookup of the current stream's handle, once found
+
+
 def _stream_handle(stream):
+    global _raw_stream
     if stream is None:
         try:
-            import torch
-            return torch.cuda.current_stream().cuda_stream
+            if _raw_stream is not None:
+                return _raw_stream(_current_device())
+            return _find_raw_stream()
         except Exception:  # noqa: BLE001 - no torch / no GPU: the legacy default stream
             return 0
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _find_raw_stream():
+    """The current stream's handle by torch's public call; keeps the direct lookups it is made of for later calls."""
+    global _raw_stream, _current_device
+    import torch
+    handle = torch.cuda.current_stream().cuda_stream
+    try:
+        raw, device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        if raw(device()) == handle:
+            _raw_stream, _current_device = raw, device
+    except AttributeError:
+        pass
+    return handle
 
 
 # -- thin wrappers with the C names ------------------------------------------
@@ -533,29 +552,38 @@ def _matrix(t, rows, cols, dtype, name):
     """(pointer, row stride) of a rows x cols tensor with contiguous rows; (None, 0) for None."""
     if t is None:
         return None, 0
-    if tuple(t.shape) != (rows, cols):
+    if t.shape != (rows, cols):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(rows, cols)}")
-    if str(t.dtype) != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if not t.is_cuda or (cols > 1 and t.stride(1) != 1) or (rows > 1 and t.stride(0) < cols):
+    ld, unit = t.stride()
+    if not t.is_cuda or (unit != 1 and cols > 1) or (ld < cols and rows > 1):
         raise ValueError(f"{name}: expected a CUDA tensor with contiguous, non-overlapping rows, strides {t.stride()}")
-    return t.data_ptr(), t.stride(0) if rows > 1 else cols
+    return t.data_ptr(), ld if rows > 1 else cols
 
 
 def _vector(t, n, dtype, name):
     if t is None:
         return None
-    if tuple(t.shape) != (n,):
+    if t.shape != (n,):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n,)}")
-    if str(t.dtype) != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
     if not t.is_cuda or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{name}: expected a contiguous CUDA vector")
     return t.data_ptr()
 
 
-_TORCH_NAMES = {"f32": "torch.float32", "f16": "torch.float16", "bf16": "torch.bfloat16"}
-_GRAD_DTYPES = {"torch.float32": DDL_FP32, "torch.float16": DDL_FP16}
+def _torch_dtype(name):
+    import torch
+    return {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[name]
+
+
+def _grad_dtype(t):
+    name = str(t.dtype)
+    if name not in ("torch.float32", "torch.float16"):
+        raise ValueError(f"gradients: dtype {name}, expected torch.float32 or torch.float16")
+    return DDL_FP32 if name == "torch.float32" else DDL_FP16
 
 
 class Linear:
@@ -566,13 +594,13 @@ class Linear:
 
     def __init__(self, in_features, out_features, max_tokens, dtype="f16", act="none"):
         self.n_in, self.n_out, self.max_tokens, self.dtype, self.act = in_features, out_features, max_tokens, dtype, act
-        self._name = _TORCH_NAMES[dtype]
+        self._dtype = _torch_dtype(dtype)
         self.handle = None
         self.handle = ddl_linear_create(max_tokens, in_features, out_features, OPERAND_DTYPES[dtype], ACTIVATIONS[act])
 
     def forward(self, x, w, y, bias=None, residual=None, z=None, stream=None):
         """Writes y (and the pre-activations z, where given); returns y."""
-        t, d = x.shape[0], self._name
+        t, d = x.shape[0], self._dtype
         px, ldx = _matrix(x, t, self.n_in, d, "x")
         pw, ldw = _matrix(w, self.n_out, self.n_in, d, "w")
         pr, ldr = _matrix(residual, t, self.n_out, d, "residual")
@@ -584,10 +612,9 @@ class Linear:
 
     def backward(self, dy, x=None, w=None, z=None, dx=None, dw=None, db=None, accumulate=False, stream=None):
         """Writes dx; writes dw and db, or adds to them."""
-        t, d = dy.shape[0], self._name
-        g = str((dw if dw is not None else db).dtype) if dw is not None or db is not None else "torch.float32"
-        if g not in _GRAD_DTYPES:
-            raise ValueError(f"gradients: dtype {g}, expected torch.float32 or torch.float16")
+        t, d = dy.shape[0], self._dtype
+        some = dw if dw is not None else db
+        g, grad_dtype = (None, DDL_FP32) if some is None else (some.dtype, _grad_dtype(some))
         pdy, ldy = _matrix(dy, t, self.n_out, d, "dy")
         px, ldx = _matrix(x, t, self.n_in, d, "x")
         pw, ldw = _matrix(w, self.n_out, self.n_in, d, "w")
@@ -595,7 +622,7 @@ class Linear:
         pdx, lddx = _matrix(dx, t, self.n_in, d, "dx")
         pdw, lddw = _matrix(dw, self.n_out, self.n_in, g, "dw")
         ddl_linear_backward(self.handle, t, pdy, ldy, px, ldx, pw, ldw, pz, ldz, pdx, lddx, pdw, lddw,
-                            _vector(db, self.n_out, g, "db"), _GRAD_DTYPES[g], accumulate, stream)
+                            _vector(db, self.n_out, g, "db"), grad_dtype, accumulate, stream)
 
     def check(self, stream=None):
         ddl_linear_check(self.handle, stream)
@@ -627,27 +654,27 @@ class Ortho:
         self.matrices = [tuple(int(v) for v in m) for m in matrices]
         self.dtype = dtype
         self.extent = max((m[0] + (m[1] - 1) * (m[3] if len(m) > 3 else m[2]) + m[2] for m in self.matrices), default=0)
-        self._name = _TORCH_NAMES[dtype]
+        self._dtype, self._f32 = _torch_dtype(dtype), _torch_dtype("f32")
         self.handle = None
         self.handle = ddl_ortho_create(self.matrices, OPERAND_DTYPES[dtype])
         ddl_ortho_set_polynomial(self.handle, steps, *coefficients, eps)
 
     def _flat(self, t, dtype, name):
-        if t.dim() != 1 or t.numel() < self.extent or str(t.dtype) != dtype or not t.is_cuda or (
+        if t.dim() != 1 or t.numel() < self.extent or t.dtype is not dtype or not t.is_cuda or (
                 t.numel() > 1 and t.stride(0) != 1):
             raise ValueError(f"{name}: expected a contiguous CUDA vector of {dtype} with at least {self.extent} elements")
         return t
 
     def run(self, inp, out, stream=None):
         """Orthogonalises every matrix of inp into out; returns out."""
-        ddl_ortho_run(self.handle, self._flat(inp, self._name, "inp"), self._flat(out, self._name, "out"), stream)
+        ddl_ortho_run(self.handle, self._flat(inp, self._dtype, "inp"), self._flat(out, self._dtype, "out"), stream)
         return out
 
     def muon(self, grad, params, mom, lr, momentum=0.95, weight_decay=0.0, nesterov=True, stream=None):
         """Updates mom and every copy in params (a list, one per rank) in place."""
-        ddl_ortho_muon(self.handle, self._flat(grad, self._name, "grad"),
-                       [self._flat(p, "torch.float32", "params") for p in params],
-                       self._flat(mom, "torch.float32", "mom"), lr, momentum, weight_decay, nesterov, stream)
+        ddl_ortho_muon(self.handle, self._flat(grad, self._dtype, "grad"),
+                       [self._flat(p, self._f32, "params") for p in params],
+                       self._flat(mom, self._f32, "mom"), lr, momentum, weight_decay, nesterov, stream)
 
     def check(self, stream=None):
         ddl_ortho_check(self.handle, stream)
