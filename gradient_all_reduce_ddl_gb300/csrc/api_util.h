@@ -4,6 +4,7 @@
 
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <cstdlib>
 
@@ -44,21 +45,36 @@ struct Range {
 
 inline uint64_t round8(uint64_t n) { return (n + 7) / 8 * 8; }
 
-// CTAs per cluster for `tiles` tiles of a contraction of `blocks` K blocks:
-// doubled while the doubled clusters still fit on the SMs and leave each CTA
-// two K blocks.
-inline int choose_splits(int64_t tiles, int64_t blocks, int sms) {
-  int s = 1;
-  while (s < 8 && tiles * s * 2 <= sms && blocks >= 4 * s) s *= 2;
-  return s;
-}
+// How a product is laid on the SMs: tiles of 128 x 128 on a CTA or 256 x 256 on a pair, and how many parts of the
+// contraction a cluster shares out.
+struct Layout {
+  int tile, splits;
+  double us;
+};
 
-// Whether a product of `tiles128` 128 x 128 tiles runs faster as `tiles256` 256 x 256 tiles on CTA pairs: both sides'
-// rounds over the SMs, a pair's tile being twice a CTA's work at 1 / kPairGain of its time.
-constexpr double kPairGain = 1.7;
-inline bool prefer_pairs(int64_t tiles128, int64_t tiles256, int sms) {
-  const int64_t rounds128 = (tiles128 + sms - 1) / sms, rounds256 = (tiles256 + sms / 2 - 1) / (sms / 2);
-  return tiles128 > sms / 2 && (double)rounds256 * 2.0 < (double)rounds128 * kPairGain;
+// The layout with the least estimated time.  rounds(tile, workers): contraction steps (64-element blocks times passes)
+// of the busiest of `workers` CTAs or pairs taking that tile size's tiles in turn; count(tile): tiles.  The constants are
+// measured on a GB300: a step of a CTA's 128 x 128 tile 0.33 us (its shared memory is the bound), of a pair's 256 x 256
+// tile 0.28 us; an epilogue about 5 us, 9 for a pair's tile, and 3 more where a cluster joins parts.  Clusters of 8 reach
+// 128 of the SMs, of 4 144.
+template <class Rounds, class Count>
+Layout choose_layout(const Rounds& rounds, const Count& count, int64_t longest, int sms) {
+  Layout best{128, 1, 1e30};
+  for (int tile = 128; tile <= 256; tile += 128) {
+    const int width = tile / 128;
+    for (int s = 1; s * width <= 8; s *= 2) {
+      if (s > 1 && longest < 2 * s) break;  // two steps each at least
+      const int cluster = s * width;
+      const int room = cluster == 8 ? sms * 16 / 19 : cluster == 4 ? sms * 18 / 19 : sms;
+      const int workers = std::max(1, room / cluster);
+      if (s > 1 && count(tile) > 2 * (int64_t)workers) break;  // many tiles: splitting only adds joins
+      const double waves = s > 1 ? (double)((count(tile) + workers - 1) / workers) : 1.0;
+      const double us = (double)rounds(tile, workers) / s * (tile == 128 ? 0.33 : 0.28) +
+                        waves * ((tile == 128 ? 5.0 : 9.0) + (s > 1 ? 3.0 : 0.0));
+      if (us < best.us) best = {tile, s, us};
+    }
+  }
+  return best;
 }
 
 }  // namespace ddl

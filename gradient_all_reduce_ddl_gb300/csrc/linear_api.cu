@@ -1,6 +1,7 @@
 // linear_api.cu -- the C entry points of the linear layers (include/ddl.h).
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstring>
 #include <new>
 
@@ -171,10 +172,18 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
 
   ddl_status_t st = bind(h);
   if (st != DDL_OK) return st;
-  const int64_t tiles256 = blocks_of(T, 256) * blocks_of(N, 256);
-  if (!swap && ddl::prefer_pairs(tiles, tiles256, h->sms)) {
-    tile_n = 256;
-    tiles = tiles256;
+  const int64_t steps = blocks_of(K, ddl::kBlockK);
+  int splits = 1;
+  if (swap) {
+    // the weights come from HBM at the SMs' joint rate: as many CTAs as there are SMs, two blocks each at least
+    while (splits < 8 && tiles * splits * 2 <= h->sms && steps >= 4 * splits) splits *= 2;
+  } else {
+    const auto count = [&](int tile) { return blocks_of(T, tile) * blocks_of(N, tile); };
+    const ddl::Layout l = ddl::choose_layout(
+        [&](int tile, int workers) { return blocks_of(count(tile), workers) * steps; }, count, steps, h->sms);
+    tile_n = l.tile;
+    splits = l.splits;
+    tiles = count(tile_n);
   }
   for (const void* p : {x, w, bias, residual, (const void*)z, (const void*)y})
     if (p && !ddl::device_pointer(p, h->device)) return DDL_ERR_INVALID_ARG;
@@ -200,7 +209,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   P.a[0] = swap ? 1 : 0;
   P.b[0] = swap ? 0 : 1;
   P.scale[0] = 1.f;
-  P.chunk = (int32_t)blocks_of(K, ddl::kBlockK);
+  P.chunk = (int32_t)steps;
   P.epi = ddl::kEpiLinear;
   P.swap = swap;
   P.type = h->type;
@@ -216,7 +225,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   L.n_inl = 1;
   L.inl_tiles[0] = (int32_t)tiles;
   L.n_tiles = (int32_t)tiles;
-  L.splits = tile_n == 256 ? 1 : ddl::choose_splits(tiles, P.chunk, h->sms);
+  L.splits = splits;
   L.err = h->d_err;
   P.in0 = P.in1 = P.out0 = P.out1 = -1;
   // rows that TMA can address, of whole 16-byte pieces, let the epilogue move whole boxes
@@ -327,14 +336,21 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   for (int k = 0; k < planes; ++k)
     if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBoxRows)) return DDL_ERR_CUDA;
   if ((dw && !map_of(&L, 3, ax, ddl::kBoxRows)) || (dx && !map_of(&L, 4, aw, ddl::kBoxRows))) return DDL_ERR_CUDA;
-  int64_t longest = 0;
-  const int64_t dx256 = dx ? blocks_of(T, 256) * blocks_of(K, 256) : 0;
-  const int64_t dw256 = dw ? blocks_of(N, 256) * blocks_of(K, 256) : 0;
-  const int tile_n = ddl::prefer_pairs(dx_tiles + dw_tiles, dx256 + dw256, h->sms) ? 256 : 128;
-  if (tile_n == 256) {
-    dx_tiles = dx256;
-    dw_tiles = dw256;
-  }
+  // dw's tiles come first, then dx's; the workers take them in turn
+  const auto dw_count = [&](int tile) { return dw ? blocks_of(N, tile) * blocks_of(K, tile) : 0; };
+  const auto dx_count = [&](int tile) { return dx ? blocks_of(T, tile) * blocks_of(K, tile) : 0; };
+  const int64_t dw_steps = blocks_of(T, ddl::kBlockK) * planes, dx_steps = blocks_of(N, ddl::kBlockK);
+  const ddl::Layout l = ddl::choose_layout(
+      [&](int tile, int workers) {
+        const int64_t all = dw_count(tile) + dx_count(tile), mine = blocks_of(all, workers);
+        const int64_t long_ones = std::min(mine, blocks_of(dw_count(tile), workers));
+        return long_ones * dw_steps + (mine - long_ones) * dx_steps;
+      },
+      [&](int tile) { return dw_count(tile) + dx_count(tile); },
+      std::min(dw ? blocks_of(T, ddl::kBlockK) : dx_steps, dx ? dx_steps : blocks_of(T, ddl::kBlockK)), h->sms);
+  const int tile_n = l.tile;
+  dw_tiles = dw_count(tile_n);
+  dx_tiles = dx_count(tile_n);
   if (dw) {  // dw[n][k] = sum_t dz[t][n] x[t][k]: both operands with their rows contiguous
     ddl::Product& P = L.inl[L.n_inl];
     P.M = (int32_t)N;
@@ -358,7 +374,6 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.out = dw;
     P.ldo = mdw.ld;
     L.inl_tiles[L.n_inl++] = (int32_t)dw_tiles;
-    longest = blocks_of(T, ddl::kBlockK);
   }
   if (dx) {  // dx[t][k] = sum_n dz[t][n] w[n][k]
     ddl::Product& P = L.inl[L.n_inl];
@@ -378,10 +393,9 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.out = dx;
     P.ldo = mdx.ld;
     L.inl_tiles[L.n_inl++] = (int32_t)dx_tiles;
-    if (P.chunk > longest) longest = P.chunk;
   }
   L.n_tiles = L.inl_tiles[0] + L.inl_tiles[1];
-  L.splits = tile_n == 256 ? 1 : ddl::choose_splits(L.n_tiles, longest, h->sms);
+  L.splits = l.splits;
   L.boxes = L.splits == 1 && (!dw || (ge == 4 ? mdw.tma32() : mdw.tma())) && (!dx || mdx.tma()) &&
             K % 8 == 0;
   if (L.boxes) {

@@ -228,17 +228,15 @@ ddl_status_t build(ddl_ortho* o) {
   for (int k = 0; k < kStages; ++k) {
     Stage& st = o->stage[k];
     const bool symmetric = k == kGram0 || k == kGram1 || k == kPoly;
-    st.tiles = tiles_of(st, 128, symmetric);
-    std::vector<ddl::Tile> pairs = tiles_of(st, 256, symmetric);
-    // a pair's tile is twice a CTA's work at 1 / kPairGain of its time
-    if ((int64_t)st.tiles.size() > o->sms / 2 &&
-        2.0 * (double)busiest(st, pairs, o->sms / 2) < ddl::kPairGain * (double)busiest(st, st.tiles, o->sms)) {
-      st.tiles = std::move(pairs);
-      st.tile = 256;
-    }
-    st.splits = st.tile == 256 ? 1
-                               : ddl::choose_splits((int64_t)st.tiles.size(),
-                                                    blocks_of(st.products[st.tiles[0].product].K, ddl::kBlockK), o->sms);
+    std::vector<ddl::Tile> tiles[2] = {tiles_of(st, 128, symmetric), tiles_of(st, 256, symmetric)};
+    int64_t shortest = INT64_MAX;
+    for (const ddl::Product& P : st.products) shortest = std::min(shortest, blocks_of(P.K, ddl::kBlockK));
+    const ddl::Layout l = ddl::choose_layout(
+        [&](int tile, int workers) { return busiest(st, tiles[tile / 256], workers) * ddl::kMaxPasses; },
+        [&](int tile) { return (int64_t)tiles[tile / 256].size(); }, shortest, o->sms);
+    st.tile = l.tile;
+    st.splits = l.splits;
+    st.tiles = std::move(tiles[l.tile / 256]);
     if (e == cudaSuccess) e = upload(&st.d_products, st.products.data(), st.products.size());
     if (e == cudaSuccess) e = upload(&st.d_tiles, st.tiles.data(), st.tiles.size());
   }

@@ -112,38 +112,6 @@ __device__ __forceinline__ void store_any(void* base, int64_t at, int type, cons
     store16(base, at, type, v);
 }
 
-// x ~ hi + 2^-11 lo, 22 bits of x while hi is a normal binary16 (below that the
-// error stays under 2^-36); an infinite or NaN hi carries the value alone.
-__device__ __forceinline__ void split(float x, uint16_t* hi, uint16_t* lo) {
-  const __half h = __float2half_rn(x);
-  const float hf = __half2float(h);
-  *hi = __half_as_ushort(h);
-  *lo = isfinite(hf) ? __half_as_ushort(__float2half_rn((x - hf) * kLoScale)) : (uint16_t)0;
-}
-
-template <int V>
-__device__ __forceinline__ void store_planes(uint16_t* hi, uint16_t* lo, int64_t at, const float (&v)[V]) {
-  uint16_t h[V], l[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) split(v[k], &h[k], &l[k]);
-  if constexpr (V == 4) {
-    *reinterpret_cast<ushort4*>(hi + at) = make_ushort4(h[0], h[1], h[2], h[3]);
-    *reinterpret_cast<ushort4*>(lo + at) = make_ushort4(l[0], l[1], l[2], l[3]);
-  } else {
-    hi[at] = h[0];
-    lo[at] = l[0];
-  }
-}
-
-template <int V>
-__device__ __forceinline__ void load_planes(const uint16_t* hi, const uint16_t* lo, int64_t at, float (&v)[V]) {
-  float l[V];
-  load16(hi, at, kF16, v);
-  load16(lo, at, kF16, l);
-#pragma unroll
-  for (int k = 0; k < V; ++k) v[k] += l[k] * (1.f / kLoScale);
-}
-
 // -- epilogues ---------------------------------------------------------------------
 
 template <int V, int R, int ACT>
@@ -192,59 +160,40 @@ __device__ __forceinline__ void emit_linear(const Product& P, const int (&m)[R],
     if (in[i]) store16(P.out, (int64_t)m[i] * P.ldo + n, TYPE, v[i]);
 }
 
-// V values of D in each of R rows: rows m[i] of the output (where in[i]), columns n...  Every load of the R rows is
-// issued before the first is used.  v becomes what was stored.
-template <int V, int R, bool GROUPED>
-__device__ __forceinline__ void emit(const Product& P, const ProductLaunch& p, const int (&m)[R], const bool (&in)[R],
-                                     int n, float (&v)[R][V]) {
-  if constexpr (!GROUPED) {
-    if (P.epi == kEpiLinear) {
-      // one branch on the type and one on the activation for all R x V values
-      if (P.type == kBF16)
-        emit_linear<V, R, kBF16>(P, m, in, n, v);
-      else
-        emit_linear<V, R, kF16>(P, m, in, n, v);
-    } else {
-      if (P.accumulate) {
-        float t[R][V];
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-          if (in[i]) load_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, t[i]);
-#pragma unroll
-        for (int i = 0; i < R; ++i)
-#pragma unroll
-          for (int k = 0; k < V; ++k) v[i][k] += t[i][k];
-      }
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (in[i]) store_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, v[i]);
-    }
-  } else {
-    if (P.epi != kEpiGram) {
-      float c[R][V];
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-        if (in[i]) load_planes(P.c_hi, P.c_lo, (int64_t)m[i] * P.ldc + n, c[i]);
-      const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = P.epi == kEpiPoly ? p.cc : 1.f;
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int k = 0; k < V; ++k) v[i][k] = cc * c[i][k] + cd * v[i][k];
-    }
+// V values of D in each of R rows of a linear layer's result: rows m[i] of the output (where in[i]), columns n...
+// Every load of the R rows is issued before the first is used.
+template <int V, int R>
+__device__ __forceinline__ void emit(const Product& P, const int (&m)[R], const bool (&in)[R], int n, float (&v)[R][V]) {
+  if (P.epi == kEpiLinear) {
+    // one branch on the type and one on the activation for all R x V values
+    if (P.type == kBF16)
+      emit_linear<V, R, kBF16>(P, m, in, n, v);
+    else
+      emit_linear<V, R, kF16>(P, m, in, n, v);
+    return;
+  }
+  if (P.accumulate) {
+    float t[R][V];
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (in[i]) store_planes(P.p_hi, P.p_lo, (int64_t)m[i] * P.ldp + n, v[i]);
+      if (in[i]) load_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, t[i]);
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[i][k] += t[i][k];
   }
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+    if (in[i]) store_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, v[i]);
 }
 
-// One element (edges, unaligned rows, transposed outputs): out of line, so that the code of the wide path stays small.
-template <bool GROUPED>
-__device__ __noinline__ float emit_one(const Product* P, const ProductLaunch* p, int m, int n, float x) {
+// One element at the edge of the wide path, out of line so that the code around it stays small.  `P` is the launch's own
+// record.
+__device__ __noinline__ void emit_one(const Product* P, int m, int n, float x) {
   const int mm[1] = {m};
   const bool in[1] = {true};
   float v[1][1] = {{x}};
-  emit<1, 1, GROUPED>(*P, *p, mm, in, n, v);
-  return v[0][0];
+  emit<1, 1>(*P, mm, in, n, v);
 }
 
 // The epilogue warps' own barrier.
@@ -270,6 +219,18 @@ struct Shape {
     kb1 = nkb * (part + 1) / parts;
   }
   __device__ __forceinline__ float scale(int pass) const { return pass == 0 ? scale0 : pass == 1 ? scale1 : scale2; }
+};
+
+// A place in the ring of stages, and the parity of its next use.
+struct Slot {
+  uint32_t s = 0, phase = 0;
+  template <int STAGES>
+  __device__ __forceinline__ void next() {
+    if (++s == STAGES) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
 };
 
 struct Place {
@@ -308,18 +269,19 @@ struct OwnSums {
 };
 struct ClusterSums {
   uint32_t base;
-  int parts;  // 2, 4 or 8
+  int parts;         // 2, 4 or 8
+  int first, apart;  // their CTAs' ranks
   template <int PARTS>
   __device__ __forceinline__ void add4(uint32_t at, float (&v)[4]) const {
     float4 u[PARTS];
 #pragma unroll
-    for (int k = 0; k < PARTS; ++k) u[k] = ld_peer4(peer_addr(base + at, k));
+    for (int k = 0; k < PARTS; ++k) u[k] = ld_peer4(peer_addr(base + at, first + k * apart));
 #pragma unroll
     for (int k = 0; k < PARTS; ++k) v[0] += u[k].x, v[1] += u[k].y, v[2] += u[k].z, v[3] += u[k].w;
   }
   __device__ __forceinline__ float one(uint32_t at) const {
     float v = 0.f;
-    for (int k = 0; k < parts; ++k) v += ld_peer(peer_addr(base + at, k));
+    for (int k = 0; k < parts; ++k) v += ld_peer(peer_addr(base + at, first + k * apart));
     return v;
   }
   __device__ __forceinline__ void four(uint32_t at, float (&v)[4]) const {
@@ -333,12 +295,11 @@ struct ClusterSums {
   }
 };
 
-// `from` is the product that P is a copy of.
-// Writes rows [r0, r1) of 128 x COLS sums that begin at D(row0, col0), along rows of D.  back: the finished values
-// also replace the sums in this CTA's shared memory.
-template <int COLS, bool GROUPED, bool WHOLE, class Sums>
-__device__ __forceinline__ void write_rows_wide(const Product& P, const Product* from, const ProductLaunch& p, int row0,
-                                                int col0, int lane, int ew, int r0, int r1, bool back, const Sums sums) {
+// Writes rows [r0, r1) of 128 x COLS sums that begin at D(row0, col0), along rows of D.  `from` is the record that P is a
+// copy of.
+template <int COLS, bool WHOLE, class Sums>
+__device__ __forceinline__ void write_rows_wide(const Product& P, const Product* from, int row0, int col0, int lane, int ew,
+                                                int r0, int r1, const Sums sums) {
   constexpr int kPitch = pitch(COLS), kBatch = 4;
   constexpr int kLanes = COLS / 4 < 32 ? COLS / 4 : 32, kRows = 32 / kLanes;  // lanes on a row, rows at a time
   for (int c = lane % kLanes * 4; c < COLS; c += kLanes * 4) {
@@ -357,39 +318,30 @@ __device__ __forceinline__ void write_rows_wide(const Product& P, const Product*
         if (in[i]) sums.four((r * kPitch + c) * 4, v[i]);
       }
       if (WHOLE || n + 4 <= P.N) {
-        emit<4, kBatch, GROUPED>(P, p, m, in, n, v);
+        emit<4, kBatch>(P, m, in, n, v);
       } else {
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; n + k < P.N; ++k)
 #pragma unroll 1
           for (int i = 0; i < kBatch; ++i) {
             const int r = rr + i * kEpiWarps * kRows;
-            if (r >= r1 || row0 + r >= P.M || n + k >= P.N) continue;
-            const uint32_t at = (r * kPitch + c + k) * 4;
-            const float x = emit_one<GROUPED>(from, &p, row0 + r, n + k, sums.one(at));
-            if (back) st_shared(sums.base + at, x);
+            if (r < r1 && row0 + r < P.M) emit_one(from, row0 + r, n + k, sums.one((r * kPitch + c + k) * 4));
           }
-        continue;
-      }
-      if (back) {
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i)
-          if (in[i]) st_shared4(sums.base + ((rr + i * kEpiWarps * kRows) * kPitch + c) * 4, v[i]);
       }
     }
   }
 }
 
-template <int COLS, bool GROUPED, class Sums>
-__device__ __forceinline__ void write_rows(const Product& P, const Product* from, const ProductLaunch& p, int row0,
-                                           int col0, int lane, int ew, int r0, int r1, bool back, const Sums sums) {
+template <int COLS, class Sums>
+__device__ __forceinline__ void write_rows(const Product& P, const Product* from, int row0, int col0, int lane, int ew, int r0,
+                                           int r1, const Sums sums) {
   constexpr int kStride = kEpiWarps * 4 * (COLS / 4 < 32 ? 128 / COLS : 1);  // rows a pass of all warps covers
   if (P.vec) {
     // tiles that lie wholly inside need no predicate anywhere
     if (row0 + r1 <= P.M && col0 + COLS <= P.N && (r1 - r0) % kStride == 0)
-      write_rows_wide<COLS, GROUPED, true>(P, from, p, row0, col0, lane, ew, r0, r1, back, sums);
+      write_rows_wide<COLS, true>(P, from, row0, col0, lane, ew, r0, r1, sums);
     else
-      write_rows_wide<COLS, GROUPED, false>(P, from, p, row0, col0, lane, ew, r0, r1, back, sums);
+      write_rows_wide<COLS, false>(P, from, row0, col0, lane, ew, r0, r1, sums);
   } else {  // rows at any alignment: a warp along a row, element by element, four rows at a time
 #pragma unroll 1
     for (int c = lane; c < COLS; c += 32) {
@@ -404,20 +356,19 @@ __device__ __forceinline__ void write_rows(const Product& P, const Product* from
           const int r = rr + i * kEpiWarps;
           m[i] = row0 + r;
           in[i] = r < r1 && m[i] < P.M;
-          v[i][0] = in[i] ? sums.one((r * (COLS + 4) + c) * 4) : 0.f;
+          v[i][0] = in[i] ? sums.one((r * pitch(COLS) + c) * 4) : 0.f;
         }
-        emit<1, 4, GROUPED>(P, p, m, in, col0 + c, v);
+        emit<1, 4>(P, m, in, col0 + c, v);
       }
     }
   }
 }
 
 // Writes rows [r0, r0 + rows) of the sums with D(i, j) at output row j, column i: neighbouring lanes take neighbouring
-// rows i, so that stores run along output rows, and four columns j.  rows is 16, 32, 64 or 128.  finished: the values
-// are final (symmetric products' mirror images).
-template <int COLS, bool GROUPED, class Sums>
-__device__ __forceinline__ void write_transposed(const Product& P, const ProductLaunch& p, int row0, int col0, int thread,
-                                                 int r0, int rows, bool finished, const Sums sums) {
+// rows i, so that stores run along output rows, and four columns j.  rows is 16, 32, 64 or 128.
+template <int COLS, class Sums>
+__device__ __forceinline__ void write_transposed(const Product& P, int row0, int col0, int thread, int r0, int rows,
+                                                 const Sums sums) {
   constexpr int kPitch = pitch(COLS);
 #pragma unroll 1
   for (int u = thread; u < rows * (COLS / 4); u += kEpiWarps * 32) {
@@ -434,13 +385,7 @@ __device__ __forceinline__ void write_transposed(const Product& P, const Product
       in[k] = m[k] < P.N;
       w[k][0] = v[k];
     }
-    if (finished) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (in[k]) store_planes(P.p_hi, P.p_lo, (int64_t)m[k] * P.ldp + n, w[k]);
-    } else {
-      emit<1, 4, GROUPED>(P, p, m, in, n, w);
-    }
+    emit<1, 4>(P, m, in, n, w);
   }
 }
 
@@ -472,6 +417,22 @@ __device__ __forceinline__ void split8(const float* v, uint4* hi, uint4* lo) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) l[k] = fabsf(h[k]) <= 65504.f ? (v[k] - h[k]) * kLoScale : 0.f;
   *lo = pack8(l, kF16);
+}
+
+// Stores 8 columns n.. of the warp's 32 rows at their mirror images.  Lanes 2k and 2k + 1 trade halves, so that each has
+// two neighbouring rows of one column, and 16 lanes write 64 bytes of an image row.  row0 + row is even on even lanes; the
+// row after the last, if a lane pair has one, falls into the padding.
+__device__ __forceinline__ void store_mirror8(uint16_t* plane, int64_t ld, uint4 u, int row, int rows, int n, int cols,
+                                              int lane) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  const int odd = lane & 1;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t other = __shfl_xor_sync(0xffffffffu, w[k], 1);
+    const uint32_t pair = odd ? __byte_perm(other, w[k], 0x7632) : __byte_perm(w[k], other, 0x5410);
+    const int c = n + 2 * k + odd, r = row - odd;
+    if (r < rows && c < cols) *reinterpret_cast<uint32_t*>(plane + (int64_t)c * ld + r) = pair;
+  }
 }
 
 template <int TYPE, int ACT>
@@ -537,15 +498,9 @@ __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunc
       split8(x, &hi, &lo);
       st_shared16(at, hi);
       st_shared16(at + kPlaneBytes, lo);
-      if (mirror && row0 + row < P.M) {  // D(i, j) also at (j, i): the warp's 32 rows i lie side by side there
-        const uint32_t h[4] = {hi.x, hi.y, hi.z, hi.w}, l[4] = {lo.x, lo.y, lo.z, lo.w};
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (n0 + 8 * g + k < P.N) {
-            const int64_t to = (int64_t)(n0 + 8 * g + k) * P.ldp + row0 + row;
-            P.p_hi[to] = (uint16_t)(h[k >> 1] >> (k & 1) * 16);
-            P.p_lo[to] = (uint16_t)(l[k >> 1] >> (k & 1) * 16);
-          }
+      if (mirror) {  // D(i, j) also at (j, i): the warp's 32 rows i lie side by side there
+        store_mirror8(P.p_hi, P.ldp, hi, row0 + row, P.M, n0 + 8 * g, P.N, row & 31);
+        store_mirror8(P.p_lo, P.ldp, lo, row0 + row, P.M, n0 + 8 * g, P.N, row & 31);
       }
     }
   } else if (P.epi == kEpiLinear) {
@@ -582,6 +537,47 @@ __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunc
   }
 }
 
+// 8 columns n.. of output row m where the contraction was split: `sum` holds D.  Rows of the planes are padded to 8 columns,
+// so a piece that begins inside the matrix is whole.
+template <int PIECES>
+__device__ __forceinline__ void joined_planes(const Product& P, const ProductLaunch& p, float (&sum)[PIECES][8], int m, int n,
+                                              bool mirror, int lane) {
+  const bool in = m < P.M;
+  if (P.epi != kEpiGram) {
+    uint4 h[PIECES], l[PIECES];
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      h[i] = l[i] = make_uint4(0, 0, 0, 0);
+      if (!in || n + 8 * i >= P.N) continue;
+      h[i] = *reinterpret_cast<const uint4*>(P.c_hi + (int64_t)m * P.ldc + n + 8 * i);
+      l[i] = *reinterpret_cast<const uint4*>(P.c_lo + (int64_t)m * P.ldc + n + 8 * i);
+    }
+    const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = P.epi == kEpiPoly ? p.cc : 1.f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      float a[8], b[8];
+      unpack8(h[i], kF16, a);
+      unpack8(l[i], kF16, b);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[i][k] = cd * sum[i][k] + cc * (a[k] + b[k] * (1.f / kLoScale));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) {
+    if (n + 8 * i >= P.N) continue;
+    uint4 hi, lo;
+    split8(sum[i], &hi, &lo);
+    if (in) {
+      *reinterpret_cast<uint4*>(P.p_hi + (int64_t)m * P.ldp + n + 8 * i) = hi;
+      *reinterpret_cast<uint4*>(P.p_lo + (int64_t)m * P.ldp + n + 8 * i) = lo;
+    }
+    if (mirror) {
+      store_mirror8(P.p_hi, P.ldp, hi, m, P.M, n + 8 * i, P.N, lane);
+      store_mirror8(P.p_lo, P.ldp, lo, m, P.M, n + 8 * i, P.N, lane);
+    }
+  }
+}
+
 // One walk over the slabs of a CTA's tiles: the warp that moves the boxes has two, for what it prepares and for what
 // it stores.
 template <int BN, bool GROUPED>
@@ -609,8 +605,8 @@ struct Slabs {
   }
 };
 
-// BN 256: a cluster of two CTAs makes a 256 x 256 tile, each CTA 128 of its rows, from one stream of products that
-// the even CTA issues for both.
+// BN 256: a pair of CTAs makes a 256 x 256 tile, each CTA 128 of its rows, from one stream of products that the even
+// CTA issues for both.
 template <int BN, bool GROUPED>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductLaunch p) {
   constexpr bool PAIR = BN == 256;
@@ -651,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   griddep_launch();
   if constexpr (GROUPED) {
     // the first tile's records are the handle's own: to L1 and L2 while the kernel before still runs
-    const int t = blockIdx.x / (PAIR ? 2 : p.splits);
+    const int t = blockIdx.x / (PAIR ? 2 * p.splits : p.splits);
     if (warp == 3 && t < p.n_tiles) {
       const Place pl = place<BN, GROUPED>(p, t);
       const int ps = lane & 3;
@@ -665,19 +661,21 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   }
   griddep_wait();
 
-  const int S = PAIR ? 1 : p.splits;
+  // a cluster has S parts of a tile's contraction, each a CTA's or a pair's
+  const int S = p.splits;
   const int rank = PAIR || S > 1 ? (int)cluster_rank() : 0;
-  const int q = PAIR ? 0 : rank;
-  const int ctas = PAIR ? 2 : S;
+  const int odd = PAIR ? rank & 1 : 0, lead = rank - odd;
+  const int q = PAIR ? rank >> 1 : rank;
+  const int ctas = PAIR ? 2 * S : S;
   const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
-  const int my_rows = PAIR ? rank * kTileM : 0;  // this CTA's part of the tile's rows
+  const int my_rows = odd * kTileM;  // this CTA's part of the tile's rows
   const CUtensorMap* maps = GROUPED ? p.g_maps : p.maps;
 
   // The epilogue's sums want registers: 384 threads of 168 become 128 of 40 and 256 of 232 (64,512 either way).
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
-      uint32_t it = 0;
+      Slot at;
       bool ok = true;
       for (int t = first; t < p.n_tiles && ok; t += step) {
         const Place pl = place<BN, GROUPED>(p, t);
@@ -690,19 +688,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
             asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
           }
-          for (int kb = sh.kb0; kb < sh.kb1; ++kb, ++it) {
-            const uint32_t s = it % kStages;
-            if (!bar_wait(empty + 8 * s, (it / kStages & 1u) ^ 1u)) {
+          for (int kb = sh.kb0; kb < sh.kb1; ++kb, at.next<kStages>()) {
+            const uint32_t s = at.s;
+            if (!bar_wait(empty + 8 * s, at.phase ^ 1u)) {
               ok = false;
               break;
             }
             const uint32_t sa = ring + s * stage_bytes(BN), sb = sa + kABytes;
             uint32_t bar = full + 8 * s;
             if constexpr (PAIR) {  // both CTAs' loads count on the even one's barrier
-              if (rank == 0)
+              if (!odd)
                 bar_expect(bar, 2 * stage_bytes(BN));
               else
-                bar = peer_addr(bar, 0);
+                bar = peer_addr(bar, lead);
             } else {
               bar_expect(bar, stage_bytes(BN));
             }
@@ -730,17 +728,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!ok) atomicOr(p.err, kErrProductWait);
       // Loads in flight end before the CTA does.  The odd CTA of a pair has no barrier of its own for them: its
       // loads are done when the pair's last sums are (below), and after a wait that ran out it gives them 10 ms.
-      if (PAIR && rank != 0) {
+      if (PAIR && odd) {
         if (!ok)
           for (const uint64_t t0 = now_ns(); now_ns() - t0 < 10000000ull;) {
           }
       } else {
-        for (uint32_t k = it > (uint32_t)kStages ? it - kStages : 0; k < it; ++k)
-          if (!bar_wait(full + 8 * (k % kStages), k / kStages & 1u)) break;
+        // every slot's last use (one without any counts as done)
+        for (int k = 0; k < kStages; ++k, at.next<kStages>())
+          if (!bar_wait(full + 8 * at.s, at.phase ^ 1u)) break;
       }
     }
-    if (warp == 1 && lane == 0 && (!PAIR || rank == 0)) {
-      uint32_t it = 0, cc = 0;
+    if (warp == 1 && lane == 0 && !odd) {
+      uint32_t cc = 0;
+      Slot at;
       bool ok = true;
       for (int t = first; t < p.n_tiles && ok; t += step) {
         const Place pl = place<BN, GROUPED>(p, t);
@@ -748,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint32_t idesc = instr_desc(p.bf16, sh.a_mn, sh.b_mn, PAIR ? 2 * kTileM : kTileM, BN);
         // K-major: 8-row groups 1024 bytes apart, 32 bytes per K step.  Rows contiguous: 64-row
         // boxes 8 KB apart, 8-k groups 1024 bytes apart, 16 k rows (2048 bytes) per K step.
-        const uint32_t lead_a = sh.a_mn ? kBoxBytes : 16, lead_b = sh.b_mn ? kBoxBytes : 16;
+        const uint64_t desc_a = smem_desc(ring, sh.a_mn ? kBoxBytes : 16, 1024);
+        const uint64_t desc_b = smem_desc(ring + kABytes, sh.b_mn ? kBoxBytes : 16, 1024);
         const uint64_t step_a = (sh.a_mn ? 2048 : 32) >> 4, step_b = (sh.b_mn ? 2048 : 32) >> 4;
         for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
           for (int k0 = sh.kb0; k0 < sh.kb1 && ok; k0 += sh.chunk, ++cc) {
@@ -759,28 +760,27 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
               break;
             }
             fence_after();
-            for (int kb = k0; kb < k1; ++kb, ++it) {
-              const uint32_t s = it % kStages;
-              if (!bar_wait(full + 8 * s, it / kStages & 1u)) {
+            for (int kb = k0; kb < k1; ++kb, at.next<kStages>()) {
+              const uint32_t s = at.s;
+              if (!bar_wait(full + 8 * s, at.phase)) {
                 ok = false;
                 break;
               }
               fence_after();
-              const uint32_t sa = ring + s * stage_bytes(BN);
-              const uint64_t da = smem_desc(sa, lead_a, 1024), db = smem_desc(sa + kABytes, lead_b, 1024);
+              const uint64_t da = desc_a + s * (stage_bytes(BN) >> 4), db = desc_b + s * (stage_bytes(BN) >> 4);
 #pragma unroll
               for (int k = 0; k < kBlockK / 16; ++k)
                 mma_f16<PAIR>(acc, da + k * step_a, db + k * step_b, idesc, kb > k0 || k > 0);
-              mma_commit<PAIR>(empty + 8 * s);
+              mma_commit<PAIR>(empty + 8 * s, lead);
             }
             if (!ok) break;
-            mma_commit<PAIR>(tfull + 8 * (cc & 1u));
+            mma_commit<PAIR>(tfull + 8 * (cc & 1u), lead);
           }
         }
       }
       if (!ok) {
         atomicOr(p.err, kErrProductWait);
-        mma_commit<PAIR>(drain);  // products in flight end before the CTA does
+        mma_commit<PAIR>(drain, lead);  // products in flight end before the CTA does
         bar_wait(drain, 0);
       }
     }
@@ -897,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           __syncwarp();
           if (lane == 0) {
             if constexpr (PAIR)
-              bar_arrive_cluster(peer_addr(tempty + 8 * (cc & 1u), 0));
+              bar_arrive_cluster(peer_addr(tempty + 8 * (cc & 1u), lead));
             else
               bar_arrive(tempty + 8 * (cc & 1u));
           }
@@ -933,20 +933,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           continue;
         }
       }
+      if constexpr (!GROUPED) {
 #pragma unroll 1
-      for (int sl = 0; sl < kSlabs; ++sl) {  // one copy of the code: it has to stay in the instruction cache
-        bar_sync_epilogue();  // the slab before has been read
+        for (int sl = 0; sl < kSlabs; ++sl) {  // one copy of the code: it has to stay in the instruction cache
+          bar_sync_epilogue();                 // the slab before has been read
 #pragma unroll
-        for (int k = 0; k < kHalf; k += 4) st_shared4(staging + (row * kSlabPitch + half * kHalf + k) * 4, &acc[k]);
+          for (int k = 0; k < kHalf; k += 4) st_shared4(staging + (row * kSlabPitch + half * kHalf + k) * 4, &acc[k]);
 #pragma unroll
-        for (int k = 0; k + kHalf < BN / 2; ++k) acc[k] = acc[k + kHalf];
-        bar_sync_epilogue();
-        const int row0 = pl.row0 + my_rows, col0 = pl.col0 + sl * kSlab;
-        const OwnSums sums{staging};
-        if (ok && !P.swap) write_rows<kSlab, GROUPED>(P, pl.P, p, row0, col0, lane, ew, 0, kTileM, pl.mirror, sums);
-        if (GROUPED && pl.mirror) bar_sync_epilogue();
-        if (ok && (P.swap || pl.mirror))
-          write_transposed<kSlab, GROUPED>(P, p, row0, col0, ew * 32 + lane, 0, kTileM, pl.mirror, sums);
+          for (int k = 0; k + kHalf < BN / 2; ++k) acc[k] = acc[k + kHalf];
+          bar_sync_epilogue();
+          const int row0 = pl.row0 + my_rows, col0 = pl.col0 + sl * kSlab;
+          const OwnSums sums{staging};
+          if (ok && !P.swap) write_rows<kSlab>(P, pl.P, row0, col0, lane, ew, 0, kTileM, sums);
+          if (ok && P.swap) write_transposed<kSlab>(P, row0, col0, ew * 32 + lane, 0, kTileM, sums);
+        }
       }
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrProductWait);
@@ -955,17 +955,35 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       cluster_sync();  // every CTA's sums are in its shared memory
       {  // also after a failed wait (every warp has to reach the same barriers); the values are void then
         const Place pl = place<BN, GROUPED>(p, first);
-        const int share = kTileM / S;
-        const ClusterSums sums{ring, S};
+        const ClusterSums sums{ring, S, odd, PAIR ? 2 : 1};
         const Product P = *pl.P;
-        // this CTA finishes its share of the rows; nobody else reads them, so its own copy can take the results
-        if (!P.swap)
-          write_rows<BN, GROUPED>(P, pl.P, p, pl.row0, pl.col0, lane, ew, q * share, (q + 1) * share, pl.mirror, sums);
-        if (GROUPED && pl.mirror) bar_sync_epilogue();
-        if (P.swap)
-          write_transposed<BN, GROUPED>(P, p, pl.row0, pl.col0, ew * 32 + lane, q * share, share, false, sums);
-        else if (pl.mirror)
-          write_transposed<BN, GROUPED>(P, p, pl.row0, pl.col0, ew * 32 + lane, q * share, share, true, OwnSums{ring});
+        if constexpr (GROUPED) {
+          // this CTA finishes BN / S columns, a thread half of them of one row, two pieces of 8 at a time (one where S is 8)
+          const int cols = BN / (2 * S), c0 = q * (BN / S) + half * cols;
+          if (cols >= 16) {
+#pragma unroll 1
+            for (int c = c0; c < c0 + cols; c += 16) {
+              float v[2][8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                sums.four((row * pitch(BN) + c + 4 * k) * 4, *reinterpret_cast<float(*)[4]>(&v[k >> 1][k & 1 ? 4 : 0]));
+              joined_planes<2>(P, p, v, pl.row0 + my_rows + row, pl.col0 + c, pl.mirror, lane);
+            }
+          } else {
+            float v[1][8];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              sums.four((row * pitch(BN) + c0 + 4 * k) * 4, *reinterpret_cast<float(*)[4]>(&v[0][4 * k]));
+            joined_planes<1>(P, p, v, pl.row0 + my_rows + row, pl.col0 + c0, pl.mirror, lane);
+          }
+        } else {
+          // this CTA finishes its share of the rows
+          const int share = kTileM / S;
+          if (!P.swap)
+            write_rows<BN>(P, pl.P, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, sums);
+          else
+            write_transposed<BN>(P, pl.row0 + my_rows, pl.col0, ew * 32 + lane, q * share, share, sums);
+        }
       }
     }
   }
@@ -989,10 +1007,10 @@ cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
     if (dev <= 63) sized.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t cfg = {};
-  // a pair per tile, or a cluster per tile, or persistent CTAs
-  const int cluster = BN == 256 ? 2 : p.splits;
+  // a cluster per tile, or persistent CTAs or pairs
+  const int cluster = (BN == 256 ? 2 : 1) * p.splits;
   const int64_t whole = (int64_t)p.n_tiles * cluster;
-  const int64_t ctas = BN != 256 && p.splits > 1 ? whole : std::min<int64_t>(whole, sms / cluster * cluster);
+  const int64_t ctas = p.splits > 1 ? whole : std::min<int64_t>(whole, sms / cluster * cluster);
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes(BN);
