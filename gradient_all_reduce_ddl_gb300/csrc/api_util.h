@@ -9,6 +9,7 @@
 #include <cstdlib>
 
 #include "ddl.h"
+#include "product.h"
 
 namespace ddl {
 
@@ -53,24 +54,25 @@ struct Layout {
 };
 
 // The layout with the least estimated time.  rounds(tile, workers): contraction steps (64-element blocks times passes)
-// of the busiest of `workers` CTAs or pairs taking that tile size's tiles in turn; count(tile): tiles.  The constants are
-// measured on a GB300: a step of a CTA's 128 x 128 tile 0.33 us (its shared memory is the bound), of a pair's 256 x 256
-// tile 0.28 us; an epilogue about 5 us, 9 for a pair's tile, and 3 more where a cluster joins parts.  Clusters of 8 reach
-// 128 of the SMs, of 4 144.
+// of the busiest of `workers` CTAs or pairs taking that tile size's tiles in turn; count(tile): tiles; shortest: blocks of
+// the shortest contraction.  Measured on a GB300, in sequences of dependent launches: a step of a CTA's 128 x 128 tile
+// takes 0.31 us whether one SM or all are busy (its shared memory is the bound), of a pair's 256 x 256 tile 0.28 us; the
+// rest of a launch 4.3 us, 8.8 for pairs; a further tile of the same worker adds 3 and 5; joining two, four, eight parts
+// 3, 3.7, 5.
 template <class Rounds, class Count>
-Layout choose_layout(const Rounds& rounds, const Count& count, int64_t longest, int sms) {
+Layout choose_layout(const Rounds& rounds, const Count& count, int64_t shortest, const Residency& room) {
   Layout best{128, 1, 1e30};
   for (int tile = 128; tile <= 256; tile += 128) {
     const int width = tile / 128;
     for (int s = 1; s * width <= 8; s *= 2) {
-      if (s > 1 && longest < 2 * s) break;  // two steps each at least
-      const int cluster = s * width;
-      const int room = cluster == 8 ? sms * 16 / 19 : cluster == 4 ? sms * 18 / 19 : sms;
-      const int workers = std::max(1, room / cluster);
-      if (s > 1 && count(tile) > 2 * (int64_t)workers) break;  // many tiles: splitting only adds joins
-      const double waves = s > 1 ? (double)((count(tile) + workers - 1) / workers) : 1.0;
-      const double us = (double)rounds(tile, workers) / s * (tile == 128 ? 0.33 : 0.28) +
-                        waves * ((tile == 128 ? 5.0 : 9.0) + (s > 1 ? 3.0 : 0.0));
+      if (s > 1 && shortest < 2 * s) break;  // two steps each at least
+      const int workers = room.clusters[s * width == 8 ? 3 : s * width / 2];
+      if (workers < 1) continue;
+      const int64_t waves = (count(tile) + workers - 1) / workers;
+      if (s > 1 && waves > 2) break;  // many tiles: splitting only adds joins
+      const double join = s == 1 ? 0.0 : s == 2 ? 3.0 : s == 4 ? 3.7 : 5.0;
+      const double us = tile == 128 ? (double)rounds(128, workers) / s * 0.31 + 4.3 + join + (double)(waves - 1) * (3.0 + join)
+                                    : (double)rounds(256, workers) / s * 0.28 + 8.8 + join + (double)(waves - 1) * (5.0 + join);
       if (us < best.us) best = {tile, s, us};
     }
   }

@@ -25,6 +25,7 @@ struct ddl_linear {
   int act;
   int device = -1;
   int sms = 0;
+  ddl::Residency room = {};
   uint32_t* d_err = nullptr;
   Buffer x, w, dz[ddl::kMaxPlanes], partial, done;
 };
@@ -48,6 +49,7 @@ ddl_status_t bind(ddl_linear* h) {
   if (e == cudaSuccess) e = cudaMemset(err, 0, sizeof(uint32_t));
   if (e == cudaSuccess) e = cudaStreamSynchronize(cudaStreamLegacy);  // the caller's stream may not wait for that one
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = ddl::product_residency(h->sms, &h->room);
   if (e != cudaSuccess) {
     cudaFree(err);
     return ddl::status_of(e);
@@ -180,7 +182,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   } else {
     const auto count = [&](int tile) { return blocks_of(T, tile) * blocks_of(N, tile); };
     const ddl::Layout l = ddl::choose_layout(
-        [&](int tile, int workers) { return blocks_of(count(tile), workers) * steps; }, count, steps, h->sms);
+        [&](int tile, int workers) { return blocks_of(count(tile), workers) * steps; }, count, steps, h->room);
     tile_n = l.tile;
     splits = l.splits;
     tiles = count(tile_n);
@@ -347,7 +349,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
         return long_ones * dw_steps + (mine - long_ones) * dx_steps;
       },
       [&](int tile) { return dw_count(tile) + dx_count(tile); },
-      std::min(dw ? blocks_of(T, ddl::kBlockK) : dx_steps, dx ? dx_steps : blocks_of(T, ddl::kBlockK)), h->sms);
+      std::min(dw ? blocks_of(T, ddl::kBlockK) : dx_steps, dx ? dx_steps : blocks_of(T, ddl::kBlockK)), h->room);
   const int tile_n = l.tile;
   dw_tiles = dw_count(tile_n);
   dx_tiles = dx_count(tile_n);

@@ -42,6 +42,7 @@ struct ddl_ortho {
   uint64_t extent = 0;  // elements of the flat buffers that the matrices reach
   int device = -1;
   int sms = 0;
+  ddl::Residency room = {};
   bool ready = false;
   uint32_t* d_err = nullptr;
   void* d_planes = nullptr;  // one block: every plane
@@ -233,7 +234,7 @@ ddl_status_t build(ddl_ortho* o) {
     for (const ddl::Product& P : st.products) shortest = std::min(shortest, blocks_of(P.K, ddl::kBlockK));
     const ddl::Layout l = ddl::choose_layout(
         [&](int tile, int workers) { return busiest(st, tiles[tile / 256], workers) * ddl::kMaxPasses; },
-        [&](int tile) { return (int64_t)tiles[tile / 256].size(); }, shortest, o->sms);
+        [&](int tile) { return (int64_t)tiles[tile / 256].size(); }, shortest, o->room);
     st.tile = l.tile;
     st.splits = l.splits;
     st.tiles = std::move(tiles[l.tile / 256]);
@@ -258,6 +259,7 @@ ddl_status_t bind(ddl_ortho* o) {
   if (e != cudaSuccess) return ddl::status_of(e);
   if (o->ready) return o->device == dev ? DDL_OK : DDL_ERR_INVALID_ARG;
   e = cudaDeviceGetAttribute(&o->sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess) e = ddl::product_residency(o->sms, &o->room);
   if (e != cudaSuccess) return ddl::status_of(e);
   ddl_status_t st;
   try {

@@ -86,7 +86,13 @@ struct ProductLaunch {
   float ca, cb, cc;         // Newton-Schulz coefficients
 };
 
-// tile_n: 128, 64 or 32 output columns per 128-row tile; 256: 256 x 256 tiles on CTA pairs (splits 1).  Grouped
+// Clusters of 1, 2, 4 and 8 CTAs of the product kernel that the current device holds at a time.
+struct Residency {
+  int clusters[4];
+};
+cudaError_t product_residency(int sms, Residency* r);
+
+// tile_n: 128, 64 or 32 output columns per 128-row tile; 256: 256 x 256 tiles on CTA pairs.  Grouped
 // launches take 128 or 256.
 cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream);
 

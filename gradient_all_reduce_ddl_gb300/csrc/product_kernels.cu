@@ -1029,6 +1029,23 @@ cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, product_kernel<BN, GROUPED>, p);
 }
 
+template <int BN>
+cudaError_t residency(int cluster, int* n) {
+  cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(BN);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = (unsigned)cluster;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaOccupancyMaxActiveClusters(n, product_kernel<BN, true>, &cfg);
+}
+
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                               const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                               CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -1069,6 +1086,14 @@ bool make_map32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, unit,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t product_residency(int sms, Residency* r) {
+  r->clusters[0] = sms;
+  cudaError_t e = residency<256>(2, &r->clusters[1]);
+  if (e == cudaSuccess) e = residency<256>(4, &r->clusters[2]);
+  if (e == cudaSuccess) e = residency<256>(8, &r->clusters[3]);
+  return e;
 }
 
 cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream) {
