@@ -98,8 +98,9 @@ ddl_status_t aligned(const Mat& m, int64_t max_rows, Buffer* b, ddl::LinearPrep*
   return DDL_OK;
 }
 
-bool map_of(ddl::ProductLaunch* L, int k, const Mat& m, int box_rows) {
-  return ddl::make_map(&L->maps[k], m.p, (uint64_t)m.rows, (uint64_t)m.cols, (uint64_t)m.ld, box_rows, L->bf16 != 0);
+bool map_of(ddl::ProductLaunch* L, int k, const Mat& m, int box_cols, int box_rows = ddl::kBoxRows) {
+  return ddl::make_map(&L->maps[k], m.p, (uint64_t)m.rows, (uint64_t)m.cols, (uint64_t)m.ld, box_cols, box_rows,
+                       L->bf16 != 0);
 }
 
 bool map32_of(ddl::ProductLaunch* L, int k, const Mat& m) {
@@ -201,7 +202,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   ddl::ProductLaunch L;
   std::memset(&L, 0, sizeof(L));
   L.bf16 = h->type == ddl::kBF16;
-  if (!map_of(&L, 0, ax, swap && tile_n == 32 ? 32 : ddl::kBoxRows) || !map_of(&L, 1, aw, ddl::kBoxRows))
+  if (!map_of(&L, 0, ax, ddl::kBlockK, swap && tile_n == 32 ? 32 : ddl::kBoxRows) || !map_of(&L, 1, aw, ddl::kBlockK))
     return DDL_ERR_CUDA;
   ddl::Product& P = L.inl[0];
   P.M = (int32_t)(swap ? N : T);
@@ -235,13 +236,13 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
             reinterpret_cast<uintptr_t>(bias) % 16 == 0;
   if (L.boxes) {
     P.out0 = 2;
-    if (!map_of(&L, 2, my, ddl::kBoxRows)) return DDL_ERR_CUDA;
+    if (!map_of(&L, 2, my, ddl::kSlabCols)) return DDL_ERR_CUDA;
     if (z) P.out1 = 3;
-    if (z && !map_of(&L, 3, mz, ddl::kBoxRows)) return DDL_ERR_CUDA;
+    if (z && !map_of(&L, 3, mz, ddl::kSlabCols)) return DDL_ERR_CUDA;
     if (residual) P.in0 = 4;
-    if (residual && !map_of(&L, 4, mr, ddl::kBoxRows)) return DDL_ERR_CUDA;
+    if (residual && !map_of(&L, 4, mr, ddl::kSlabCols)) return DDL_ERR_CUDA;
   }
-  return ddl::status_of(ddl::launch_product(L, tile_n, false, h->sms, s));
+  return ddl::status_of(ddl::launch_product(L, tile_n, h->sms, s));
 }
 
 ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, size_t ldy, const void* x, size_t ldx,
@@ -336,8 +337,8 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   L.err = h->d_err;
   const int planes = n_planes ? n_planes : 1;
   for (int k = 0; k < planes; ++k)
-    if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBoxRows)) return DDL_ERR_CUDA;
-  if ((dw && !map_of(&L, 3, ax, ddl::kBoxRows)) || (dx && !map_of(&L, 4, aw, ddl::kBoxRows))) return DDL_ERR_CUDA;
+    if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBlockK)) return DDL_ERR_CUDA;
+  if ((dw && !map_of(&L, 3, ax, ddl::kBlockK)) || (dx && !map_of(&L, 4, aw, ddl::kBlockK))) return DDL_ERR_CUDA;
   // dw's tiles come first, then dx's; the workers take them in turn
   const auto dw_count = [&](int tile) { return dw ? blocks_of(N, tile) * blocks_of(K, tile) : 0; };
   const auto dx_count = [&](int tile) { return dx ? blocks_of(T, tile) * blocks_of(K, tile) : 0; };
@@ -402,10 +403,10 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
             K % 8 == 0;
   if (L.boxes) {
     // a binary16 gradient's map takes the operands' element type: TMA moves its bits only
-    if (dw && !(ge == 4 ? map32_of(&L, 5, mdw) : map_of(&L, 5, mdw, ddl::kBoxRows))) return DDL_ERR_CUDA;
-    if (dx && !map_of(&L, 6, mdx, ddl::kBoxRows)) return DDL_ERR_CUDA;
+    if (dw && !(ge == 4 ? map32_of(&L, 5, mdw) : map_of(&L, 5, mdw, ddl::kSlabCols))) return DDL_ERR_CUDA;
+    if (dx && !map_of(&L, 6, mdx, ddl::kSlabCols)) return DDL_ERR_CUDA;
   }
-  return ddl::status_of(ddl::launch_product(L, tile_n, false, h->sms, s));
+  return ddl::status_of(ddl::launch_product(L, tile_n, h->sms, s));
 }
 
 ddl_status_t ddl_linear_check(ddl_linear_t h, void* stream) {

@@ -153,19 +153,20 @@ ddl_status_t build(ddl_ortho* o) {
   if (e != cudaSuccess) return ddl::status_of(e);
   uint16_t* base = static_cast<uint16_t*>(o->d_planes);
 
-  std::vector<CUtensorMap> maps((size_t)n * 8);
+  std::vector<CUtensorMap> maps((size_t)n * 16);
   std::vector<ddl::OrthoMatrix> mats(n);
   std::vector<ddl::OrthoItem> items;
   for (int i = 0; i < n; ++i) {
     const ddl_matrix_t& m = o->mats[i];
     const uint64_t s = std::min(m.rows, m.cols);
     const Planes& p = pl[i];
-    // maps 8 i + {0, 1}: X0, {2, 3}: X1, {4, 5}: A, {6, 7}: B
+    // maps 16 i + {0, 1}: X0, {2, 3}: X1, {4, 5}: A, {6, 7}: B as operands; 8 more: the same as the epilogue moves them
     const uint64_t where[8] = {p.x[0][0], p.x[0][1], p.x[1][0], p.x[1][1], p.a[0], p.a[1], p.b[0], p.b[1]};
     for (int k = 0; k < 8; ++k)
-      if (!ddl::make_map(&maps[(size_t)i * 8 + k], base + where[k], k < 4 ? m.rows : s, k < 4 ? m.cols : s,
-                         (uint64_t)(k < 4 ? p.ldx : p.lds), ddl::kBoxRows, false))
-        return DDL_ERR_CUDA;
+      for (int slab = 0; slab < 2; ++slab)
+        if (!ddl::make_map(&maps[(size_t)i * 16 + 8 * slab + k], base + where[k], k < 4 ? m.rows : s, k < 4 ? m.cols : s,
+                           (uint64_t)(k < 4 ? p.ldx : p.lds), slab ? ddl::kSlabCols : ddl::kBlockK, ddl::kBoxRows, false))
+          return DDL_ERR_CUDA;
     ddl::OrthoMatrix& d = mats[i];
     d.offset = (int64_t)m.offset;
     d.ld = (int64_t)m.ld;
@@ -186,7 +187,7 @@ ddl_status_t build(ddl_ortho* o) {
         items.push_back({i, r, std::min(d.rows, r + rows), c, std::min(d.cols, c + cols)});
     d.n_items = (int32_t)items.size() - d.item0;
 
-    const int map = 8 * i;
+    const int map = 16 * i;
     for (int k = 0; k < kStages; ++k) {
       ddl::Product P;
       std::memset(&P, 0, sizeof(P));
@@ -218,9 +219,9 @@ ddl_status_t build(ddl_ortho* o) {
       P.p_hi = base + (k == kPoly ? p.b[0] : k == kApply0 || k == kApply1 ? p.x[1 - xi][0] : p.a[0]);
       P.p_lo = base + (k == kPoly ? p.b[1] : k == kApply0 || k == kApply1 ? p.x[1 - xi][1] : p.a[1]);
       P.ldp = k == kApply0 || k == kApply1 ? p.ldx : p.lds;
-      P.in0 = k == kGram0 || k == kGram1 ? -1 : k == kPoly ? map + 4 : map + 2 * xi;
+      P.in0 = k == kGram0 || k == kGram1 ? -1 : k == kPoly ? map + 12 : map + 8 + 2 * xi;
       P.in1 = P.in0 < 0 ? -1 : P.in0 + 1;
-      P.out0 = k == kPoly ? map + 6 : k == kApply0 || k == kApply1 ? map + 2 * (1 - xi) : map + 4;
+      P.out0 = k == kPoly ? map + 14 : k == kApply0 || k == kApply1 ? map + 8 + 2 * (1 - xi) : map + 12;
       P.out1 = P.out0 + 1;
       P.vec = 1;  // planes always allow 4-element accesses
       o->stage[k].products.push_back(P);
@@ -294,7 +295,7 @@ ddl_status_t products(ddl_ortho* o, cudaStream_t s) {
       L.n_tiles = (int32_t)st.tiles.size();
       L.splits = st.splits;
       L.boxes = st.splits == 1;
-      const cudaError_t e = ddl::launch_product(L, st.tile, true, o->sms, s);
+      const cudaError_t e = ddl::launch_product(L, st.tile, o->sms, s);
       if (e != cudaSuccess) return ddl::status_of(e);
     }
   }

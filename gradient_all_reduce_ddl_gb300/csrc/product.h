@@ -17,6 +17,7 @@ namespace ddl {
 constexpr int kTileM = 128;      // output rows per tile
 constexpr int kBlockK = 64;      // contraction elements per stage (one 128-byte swizzle row)
 constexpr int kBoxRows = 64;     // rows of a TMA box
+constexpr int kSlabCols = 32;    // columns that the epilogue moves at a time
 constexpr int kMaxPasses = 3;
 constexpr int kMaxMaps = 8;      // tensor maps carried in the launch record
 
@@ -80,7 +81,8 @@ struct ProductLaunch {
   const Tile* g_tiles;
   int32_t n_tiles;
   int32_t splits;           // CTAs of a cluster that share a tile's contraction
-  int32_t boxes;            // tiles of 128 or 256 columns, splits 1: the epilogue moves boxes by TMA (in0 ... out1)
+  int32_t boxes;            // single launches, tiles of 128 or 256 columns, splits 1: the epilogue moves boxes by TMA (in0
+                            // ... out1); grouped ones with splits 1 always do
   int32_t bf16;             // operands are bfloat16, else binary16
   uint32_t* err;
   float ca, cb, cc;         // Newton-Schulz coefficients
@@ -93,12 +95,13 @@ struct Residency {
 cudaError_t product_residency(int sms, Residency* r);
 
 // tile_n: 128, 64 or 32 output columns per 128-row tile; 256: 256 x 256 tiles on CTA pairs.  Grouped
-// launches take 128 or 256.
-cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream);
+// launches and kEpiStore take 128 or 256.
+cudaError_t launch_product(const ProductLaunch& p, int tile_n, int sms, cudaStream_t stream);
 
-// Tensor map of a row-major 16-bit matrix (rows x cols, ld elements between
-// rows; 16-byte aligned base and row stride), boxes of 64 columns x box_rows.
-bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_rows, bool bf16);
+// Tensor map of a row-major 16-bit matrix (rows x cols, ld elements between rows; 16-byte aligned base and row stride):
+// boxes of 64 columns (operands, 128-byte swizzle) or 32 (the epilogue's slabs, 64-byte swizzle) x box_rows.
+bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_cols, int box_rows,
+              bool bf16);
 
 // The same of a binary32 matrix, boxes of 32 columns x 64 rows (kEpiStore's output).
 bool make_map32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld);

@@ -43,16 +43,21 @@ constexpr int kBoxBytes = kBoxRows * kBlockK * 2;
 constexpr int kABytes = kTileM * kBlockK * 2;
 constexpr float kLoScale = 2048.f;  // lo planes hold (x - hi) * 2^11
 
+// What a launch is for; each has its own epilogues (and registers: one that spilled would go to L2 for it, since shared
+// memory leaves no L1).
+enum : int { kForward, kBackward, kSteps };
+
 // Per CTA: a pair (tile_n 256) splits both operands' rows between its CTAs.
 __host__ __device__ constexpr int b_rows(int bn) { return bn == 256 ? 128 : bn; }
 __host__ __device__ constexpr int stages(int bn) { return bn >= 128 ? 5 : 6; }
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + b_rows(bn) * kBlockK * 2; }
-__host__ __device__ constexpr int slab(int bn) { return bn < 64 ? bn : 64; }  // columns passed on at a time
+constexpr int kSlab = kSlabCols;
 __host__ __device__ constexpr int pitch(int cols) { return cols + 4; }        // floats; rows 4 banks apart
-constexpr int kPlaneBytes = kTileM * 64 * 2;  // 64 columns of 16 bits: two boxes
-constexpr int kSlabBytes = 2 * kPlaneBytes;   // what a box epilogue keeps of 64 columns: two planes, or binary32
+constexpr int kPlaneBytes = kTileM * kSlab * 2;  // a slab of 16 bits: two boxes of 64 rows
+constexpr int kSlabBytes = 2 * kPlaneBytes;      // what a box epilogue keeps of a slab: two planes, or binary32
+constexpr int kBufs = 4;                         // slabs on their way in, in work and on their way out
 __host__ __device__ constexpr int smem_bytes(int bn) {
-  return 1024 + stages(bn) * stage_bytes(bn) + (bn >= 128 ? 2 * kSlabBytes : kTileM * pitch(slab(bn)) * 4);
+  return 1024 + stages(bn) * stage_bytes(bn) + (bn >= 128 ? kBufs * kSlabBytes : kTileM * pitch(kSlab) * 4);
 }
 
 // -- element access -------------------------------------------------------------
@@ -162,38 +167,39 @@ __device__ __forceinline__ void emit_linear(const Product& P, const int (&m)[R],
 
 // V values of D in each of R rows of a linear layer's result: rows m[i] of the output (where in[i]), columns n...
 // Every load of the R rows is issued before the first is used.
-template <int V, int R>
+template <int V, int R, int MODE>
 __device__ __forceinline__ void emit(const Product& P, const int (&m)[R], const bool (&in)[R], int n, float (&v)[R][V]) {
-  if (P.epi == kEpiLinear) {
+  if constexpr (MODE == kForward) {
     // one branch on the type and one on the activation for all R x V values
     if (P.type == kBF16)
       emit_linear<V, R, kBF16>(P, m, in, n, v);
     else
       emit_linear<V, R, kF16>(P, m, in, n, v);
-    return;
-  }
-  if (P.accumulate) {
-    float t[R][V];
+  } else {
+    if (P.accumulate) {
+      float t[R][V];
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (in[i]) load_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, t[i]);
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+#pragma unroll
+        for (int k = 0; k < V; ++k) v[i][k] += t[i][k];
+    }
 #pragma unroll
     for (int i = 0; i < R; ++i)
-      if (in[i]) load_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, t[i]);
-#pragma unroll
-    for (int i = 0; i < R; ++i)
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[i][k] += t[i][k];
+      if (in[i]) store_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, v[i]);
   }
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-    if (in[i]) store_any(P.out, (int64_t)m[i] * P.ldo + n, P.out_type, v[i]);
 }
 
 // One element at the edge of the wide path, out of line so that the code around it stays small.  `P` is the launch's own
 // record.
+template <int MODE>
 __device__ __noinline__ void emit_one(const Product* P, int m, int n, float x) {
   const int mm[1] = {m};
   const bool in[1] = {true};
   float v[1][1] = {{x}};
-  emit<1, 1>(*P, mm, in, n, v);
+  emit<1, 1, MODE>(*P, mm, in, n, v);
 }
 
 // The epilogue warps' own barrier.
@@ -238,10 +244,10 @@ struct Place {
   int row0, col0, mirror;
 };
 
-template <int BN, bool GROUPED>
+template <int BN, int MODE>
 __device__ __forceinline__ Place place(const ProductLaunch& p, int t) {
   constexpr int BM = BN == 256 ? 2 * kTileM : kTileM;
-  if constexpr (GROUPED) {
+  if constexpr (MODE == kSteps) {
     const int4 u = __ldg(reinterpret_cast<const int4*>(p.g_tiles) + t);
     return {p.g_products + u.x, u.y * BM, u.z * BN, u.w};
   } else {
@@ -297,7 +303,7 @@ struct ClusterSums {
 
 // Writes rows [r0, r1) of 128 x COLS sums that begin at D(row0, col0), along rows of D.  `from` is the record that P is a
 // copy of.
-template <int COLS, bool WHOLE, class Sums>
+template <int COLS, int MODE, bool WHOLE, class Sums>
 __device__ __forceinline__ void write_rows_wide(const Product& P, const Product* from, int row0, int col0, int lane, int ew,
                                                 int r0, int r1, const Sums sums) {
   constexpr int kPitch = pitch(COLS), kBatch = 4;
@@ -318,30 +324,30 @@ __device__ __forceinline__ void write_rows_wide(const Product& P, const Product*
         if (in[i]) sums.four((r * kPitch + c) * 4, v[i]);
       }
       if (WHOLE || n + 4 <= P.N) {
-        emit<4, kBatch>(P, m, in, n, v);
+        emit<4, kBatch, MODE>(P, m, in, n, v);
       } else {
 #pragma unroll 1
         for (int k = 0; n + k < P.N; ++k)
 #pragma unroll 1
           for (int i = 0; i < kBatch; ++i) {
             const int r = rr + i * kEpiWarps * kRows;
-            if (r < r1 && row0 + r < P.M) emit_one(from, row0 + r, n + k, sums.one((r * kPitch + c + k) * 4));
+            if (r < r1 && row0 + r < P.M) emit_one<MODE>(from, row0 + r, n + k, sums.one((r * kPitch + c + k) * 4));
           }
       }
     }
   }
 }
 
-template <int COLS, class Sums>
+template <int COLS, int MODE, class Sums>
 __device__ __forceinline__ void write_rows(const Product& P, const Product* from, int row0, int col0, int lane, int ew, int r0,
                                            int r1, const Sums sums) {
   constexpr int kStride = kEpiWarps * 4 * (COLS / 4 < 32 ? 128 / COLS : 1);  // rows a pass of all warps covers
   if (P.vec) {
     // tiles that lie wholly inside need no predicate anywhere
     if (row0 + r1 <= P.M && col0 + COLS <= P.N && (r1 - r0) % kStride == 0)
-      write_rows_wide<COLS, true>(P, from, row0, col0, lane, ew, r0, r1, sums);
+      write_rows_wide<COLS, MODE, true>(P, from, row0, col0, lane, ew, r0, r1, sums);
     else
-      write_rows_wide<COLS, false>(P, from, row0, col0, lane, ew, r0, r1, sums);
+      write_rows_wide<COLS, MODE, false>(P, from, row0, col0, lane, ew, r0, r1, sums);
   } else {  // rows at any alignment: a warp along a row, element by element, four rows at a time
 #pragma unroll 1
     for (int c = lane; c < COLS; c += 32) {
@@ -358,7 +364,7 @@ __device__ __forceinline__ void write_rows(const Product& P, const Product* from
           in[i] = r < r1 && m[i] < P.M;
           v[i][0] = in[i] ? sums.one((r * pitch(COLS) + c) * 4) : 0.f;
         }
-        emit<1, 4>(P, m, in, col0 + c, v);
+        emit<1, 4, MODE>(P, m, in, col0 + c, v);
       }
     }
   }
@@ -366,7 +372,7 @@ __device__ __forceinline__ void write_rows(const Product& P, const Product* from
 
 // Writes rows [r0, r0 + rows) of the sums with D(i, j) at output row j, column i: neighbouring lanes take neighbouring
 // rows i, so that stores run along output rows, and four columns j.  rows is 16, 32, 64 or 128.
-template <int COLS, class Sums>
+template <int COLS, int MODE, class Sums>
 __device__ __forceinline__ void write_transposed(const Product& P, int row0, int col0, int thread, int r0, int rows,
                                                  const Sums sums) {
   constexpr int kPitch = pitch(COLS);
@@ -385,19 +391,23 @@ __device__ __forceinline__ void write_transposed(const Product& P, int row0, int
       in[k] = m[k] < P.N;
       w[k][0] = v[k];
     }
-    emit<1, 4>(P, m, in, n, w);
+    emit<1, 4, MODE>(P, m, in, n, w);
   }
 }
 
 // -- box epilogues ------------------------------------------------------------------
 //
-// 64 columns of a tile at a time.  A thread has 32 columns of one row; what it reads (residual, old output, C's
+// 32 columns of a tile at a time.  A thread has 16 columns of one row; what it reads (residual, old output, C's
 // planes) TMA has put into a slab of shared memory, the results replace it there in place, and TMA stores the slab.
 // A box that the matrix's edge cuts is stored in whole 16-byte pieces, so a caller's rows end on one where boxes are used.
-// The slab's planes are boxes with the 128-byte swizzle: 16-byte piece c of row r lies at piece c ^ (r & 7).
+// A plane's rows are 64 bytes with the 64-byte swizzle: 16-byte piece c of row r lies at piece c ^ (r / 2 & 3).  Binary32
+// rows are 128 bytes with the 128-byte swizzle: at piece c ^ (r & 7).
 
 __device__ __forceinline__ uint32_t piece(uint32_t plane, int row, int c) {
-  return plane + row * 128 + ((c ^ (row & 7)) << 4);
+  return plane + row * 64 + ((c ^ (row >> 1 & 3)) << 4);
+}
+__device__ __forceinline__ uint32_t piece32(uint32_t slab, int row, int c) {
+  return slab + row * 128 + ((c ^ (row & 7)) << 4);
 }
 
 __device__ __forceinline__ void unpack8(uint4 u, int type, float (&v)[8]) {
@@ -437,35 +447,38 @@ __device__ __forceinline__ void store_mirror8(uint16_t* plane, int64_t ld, uint4
 
 template <int TYPE, int ACT>
 __device__ __forceinline__ void slab_linear(const Product& P, float* v, uint32_t buf, int row, int half, int n0) {
+  const uint32_t at[2] = {piece(buf, row, 2 * half), piece(buf, row, 2 * half + 1)};
+  uint4 add[2];
+  if (P.in0 >= 0) add[0] = ld_shared16(at[0]), add[1] = ld_shared16(at[1]);
+  if (P.bias) {
+    const uint16_t* b = static_cast<const uint16_t*>(P.bias) + n0;
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    float* x = v + 8 * g;
-    const int n = n0 + 8 * g;
-    if (P.bias) {
-      const uint16_t* b = static_cast<const uint16_t*>(P.bias) + n;
-      if (n + 8 <= P.N) {
+    for (int g = 0; g < 2; ++g) {
+      if (n0 + 8 * g + 8 <= P.N) {
         float t[8];
-        unpack8(*reinterpret_cast<const uint4*>(b), TYPE, t);
+        unpack8(*reinterpret_cast<const uint4*>(b + 8 * g), TYPE, t);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] += t[k];
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (n + k < P.N) x[k] += from16(b[k], TYPE);
-      }
+        for (int k = 0; k < 8; ++k) v[8 * g + k] += t[k];
+      }  // rows are whole pieces: the other columns are outside
     }
-    const uint32_t at = piece(buf, row, 4 * half + g);
-    if (P.out1 >= 0) st_shared16(at + kPlaneBytes, pack8(x, TYPE));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] = activate(x[k], ACT);
-    if (P.in0 >= 0) {
-      float t[8];
-      unpack8(ld_shared16(at), TYPE, t);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] += t[k];
-    }
-    st_shared16(at, pack8(x, TYPE));
   }
+  if (P.out1 >= 0) {
+    st_shared16(at[0] + kPlaneBytes, pack8(v, TYPE));
+    st_shared16(at[1] + kPlaneBytes, pack8(v + 8, TYPE));
+  }
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = activate(v[k], ACT);
+  if (P.in0 >= 0) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float t[8];
+      unpack8(add[g], TYPE, t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[8 * g + k] += t[k];
+    }
+  }
+  st_shared16(at[0], pack8(v, TYPE));
+  st_shared16(at[1], pack8(v + 8, TYPE));
 }
 
 template <int TYPE>
@@ -478,53 +491,59 @@ __device__ __forceinline__ void slab_linear_act(const Product& P, float* v, uint
   }
 }
 
-template <bool GROUPED>
+template <int MODE>
 __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunch& p, float* v, uint32_t buf, int row,
                                             int half, int row0, int n0, bool mirror) {
-  if constexpr (GROUPED) {
+  if constexpr (MODE == kSteps) {
     const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = P.epi == kEpiPoly ? p.cc : 1.f;
+    const uint32_t at[2] = {piece(buf, row, 2 * half), piece(buf, row, 2 * half + 1)};
+    if (P.in0 >= 0) {
+      uint4 h[2], l[2];
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float* x = v + 8 * g;
-      const uint32_t at = piece(buf, row, 4 * half + g);
-      if (P.in0 >= 0) {
-        float h[8], l[8];
-        unpack8(ld_shared16(at), kF16, h);
-        unpack8(ld_shared16(at + kPlaneBytes), kF16, l);
+      for (int g = 0; g < 2; ++g) h[g] = ld_shared16(at[g]), l[g] = ld_shared16(at[g] + kPlaneBytes);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = cd * x[k] + cc * (h[k] + l[k] * (1.f / kLoScale));
-      }
-      uint4 hi, lo;
-      split8(x, &hi, &lo);
-      st_shared16(at, hi);
-      st_shared16(at + kPlaneBytes, lo);
-      if (mirror) {  // D(i, j) also at (j, i): the warp's 32 rows i lie side by side there
-        store_mirror8(P.p_hi, P.ldp, hi, row0 + row, P.M, n0 + 8 * g, P.N, row & 31);
-        store_mirror8(P.p_lo, P.ldp, lo, row0 + row, P.M, n0 + 8 * g, P.N, row & 31);
+      for (int g = 0; g < 2; ++g) {
+        float a[8], b[8];
+        unpack8(h[g], kF16, a);
+        unpack8(l[g], kF16, b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[8 * g + k] = cd * v[8 * g + k] + cc * (a[k] + b[k] * (1.f / kLoScale));
       }
     }
-  } else if (P.epi == kEpiLinear) {
+    uint4 hi[2], lo[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) split8(v + 8 * g, &hi[g], &lo[g]);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      st_shared16(at[g], hi[g]);
+      st_shared16(at[g] + kPlaneBytes, lo[g]);
+    }
+    if (mirror) {  // D(i, j) also at (j, i): the warp's 32 rows i lie side by side there
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        store_mirror8(P.p_hi, P.ldp, hi[g], row0 + row, P.M, n0 + 8 * g, P.N, row & 31);
+        store_mirror8(P.p_lo, P.ldp, lo[g], row0 + row, P.M, n0 + 8 * g, P.N, row & 31);
+      }
+    }
+  } else if constexpr (MODE == kForward) {
     if (P.type == kBF16)
       slab_linear_act<kBF16>(P, v, buf, row, half, n0);
     else
       slab_linear_act<kF16>(P, v, buf, row, half, n0);
   } else if (P.out_type == kF32) {
+    float t[4][4];
+    if (P.in0 >= 0) {
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      const uint32_t at = piece(buf + half * kPlaneBytes, row, g);
-      float* x = v + 4 * g;
-      if (P.in0 >= 0) {
-        float t[4];
-        ld_shared4(at, t);
+      for (int g = 0; g < 4; ++g) ld_shared4(piece32(buf, row, 4 * half + g), t[g]);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] += t[k];
-      }
-      st_shared4(at, x);
+      for (int k = 0; k < 16; ++k) v[k] += t[k >> 2][k & 3];
     }
+#pragma unroll
+    for (int g = 0; g < 4; ++g) st_shared4(piece32(buf, row, 4 * half + g), v + 4 * g);
   } else {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const uint32_t at = piece(buf, row, 4 * half + g);
+    for (int g = 0; g < 2; ++g) {
+      const uint32_t at = piece(buf, row, 2 * half + g);
       float* x = v + 8 * g;
       if (P.in0 >= 0) {
         float t[8];
@@ -580,21 +599,21 @@ __device__ __forceinline__ void joined_planes(const Product& P, const ProductLau
 
 // One walk over the slabs of a CTA's tiles: the warp that moves the boxes has two, for what it prepares and for what
 // it stores.
-template <int BN, bool GROUPED>
+template <int BN, int MODE>
 struct Slabs {
   int t, step, sl, n_sl;
   Place pl;
-  int in0, in1, out0, out1, f32, rows, cols;
+  int in0, in1, out0, out1, f32, rows;
   __device__ __forceinline__ Slabs(const ProductLaunch& p, int first, int by) : t(first), step(by), sl(0) { load(p); }
   __device__ __forceinline__ void load(const ProductLaunch& p) {
     if (t >= p.n_tiles) return;
-    pl = place<BN, GROUPED>(p, t);
+    pl = place<BN, MODE>(p, t);
     const Product& P = *pl.P;
     in0 = P.in0, in1 = P.in1, out0 = P.out0, out1 = P.out1;
-    f32 = !GROUPED && P.epi == kEpiStore && P.out_type == kF32;
-    rows = P.M, cols = P.N;
-    const int left = (P.N - pl.col0 + 63) / 64;
-    n_sl = left < BN / 64 ? left : BN / 64;
+    f32 = MODE == kBackward && P.out_type == kF32;
+    rows = P.M;
+    const int left = (P.N - pl.col0 + kSlab - 1) / kSlab;
+    n_sl = left < BN / kSlab ? left : BN / kSlab;
   }
   __device__ __forceinline__ bool more(const ProductLaunch& p) const { return t < p.n_tiles; }
   __device__ __forceinline__ void next(const ProductLaunch& p) {
@@ -607,19 +626,20 @@ struct Slabs {
 
 // BN 256: a pair of CTAs makes a 256 x 256 tile, each CTA 128 of its rows, from one stream of products that the even
 // CTA issues for both.
-template <int BN, bool GROUPED>
+template <int BN, int MODE>
 __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_constant__ ProductLaunch p) {
   constexpr bool PAIR = BN == 256;
+  constexpr bool DIRECT = MODE == kForward;  // one chunk: sums go from TMEM to the epilogue
   constexpr int kStages = stages(BN);
   constexpr uint32_t kCols = 2 * BN;
-  constexpr int kSlab = slab(BN), kSlabPitch = pitch(kSlab), kHalf = kSlab / 2, kSlabs = BN / kSlab;
+  constexpr int kSlabPitch = pitch(kSlab), kHalf = kSlab / 2, kSlabs = BN / kSlab;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2 * kStages + 9];
+  __shared__ uint64_t bars[2 * kStages + 5 + 2 * kBufs];
   __shared__ uint32_t tmem_slot;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t staging = ring + kStages * stage_bytes(BN);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
-                 drain = tempty + 16, ready = drain + 8, written = ready + 16;
+                 drain = tempty + 16, ready = drain + 8, written = ready + 8 * kBufs;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
@@ -630,6 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int b = 0; b < 2; ++b) {
       bar_init(tfull + 8 * b, 1);
       bar_init(tempty + 8 * b, PAIR ? 2 * kEpiWarps : kEpiWarps);
+    }
+    for (int b = 0; b < kBufs; ++b) {
       bar_init(ready + 8 * b, 1);
       bar_init(written + 8 * b, kEpiWarps);
     }
@@ -645,11 +667,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   fence_after();
   const uint32_t tmem = tmem_slot;
   griddep_launch();
-  if constexpr (GROUPED) {
+  if constexpr (MODE == kSteps) {
     // the first tile's records are the handle's own: to L1 and L2 while the kernel before still runs
     const int t = blockIdx.x / (PAIR ? 2 * p.splits : p.splits);
     if (warp == 3 && t < p.n_tiles) {
-      const Place pl = place<BN, GROUPED>(p, t);
+      const Place pl = place<BN, MODE>(p, t);
       const int ps = lane & 3;
       if (lane < 3 && ps < pl.P->n_pass)
         asm volatile("prefetch.tensormap [%0];" ::"l"(p.g_maps + pl.P->a[ps]) : "memory");
@@ -669,22 +691,22 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const int ctas = PAIR ? 2 * S : S;
   const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
   const int my_rows = odd * kTileM;  // this CTA's part of the tile's rows
-  const CUtensorMap* maps = GROUPED ? p.g_maps : p.maps;
+  const CUtensorMap* maps = MODE == kSteps ? p.g_maps : p.maps;
 
-  // The epilogue's sums want registers: 384 threads of 168 become 128 of 40 and 256 of 232 (64,512 either way).
+  // The epilogue's sums want registers: 384 threads of 168 become 128 of 56 and 256 of 224 (64,512 either way).
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {
       Slot at;
       bool ok = true;
       for (int t = first; t < p.n_tiles && ok; t += step) {
-        const Place pl = place<BN, GROUPED>(p, t);
+        const Place pl = place<BN, MODE>(p, t);
         const Product& P = *pl.P;
         const Shape sh(P, q, S);
         for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
           const CUtensorMap* ma = maps + P.a[ps];
           const CUtensorMap* mb = maps + P.b[ps];
-          if constexpr (GROUPED) {  // written by the host before this launch
+          if constexpr (MODE == kSteps) {  // written by the host before this launch
             asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
             asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
           }
@@ -743,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       Slot at;
       bool ok = true;
       for (int t = first; t < p.n_tiles && ok; t += step) {
-        const Place pl = place<BN, GROUPED>(p, t);
+        const Place pl = place<BN, MODE>(p, t);
         const Shape sh(*pl.P, q, S);
         const uint32_t idesc = instr_desc(p.bf16, sh.a_mn, sh.b_mn, PAIR ? 2 * kTileM : kTileM, BN);
         // K-major: 8-row groups 1024 bytes apart, 32 bytes per K step.  Rows contiguous: 64-row
@@ -786,53 +808,51 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
     if constexpr (BN >= 128) {
       if (warp == 2 && lane == 0 && p.boxes) {
-        // Slab u of this CTA's tiles uses buffer u & 1: filled (or declared free) here, worked on by the epilogue
-        // warps, stored here; then slab u + 2 may have the buffer.
-        Slabs<BN, GROUPED> fill(p, first, step), store(p, first, step);
-        uint32_t u = 0, w = 0;
+        // The slabs of this CTA's tiles take the four buffers in turn: one is filled (or declared free) here, worked on by
+        // the epilogue warps, stored here, and can be filled again once the store has read it.  Three are filled ahead,
+        // which leaves the store before last time to be read.
+        Slabs<BN, MODE> fill(p, first, step), store(p, first, step);
+        uint32_t ahead = 0, filled = 0;
+        Slot fu, wu;
         bool ok = true;
         while (ok && store.more(p)) {
-          while (u < w + 2 && fill.more(p)) {
-            if (u >= 2) store_wait_read();  // slab u - 2 has been read
-            const uint32_t buf = staging + (u & 1u) * kSlabBytes, bar = ready + 8 * (u & 1u);
+          for (; ahead < kBufs - 1 && fill.more(p); ++ahead, ++filled) {
+            if (filled >= kBufs) store_wait_read<1>();
+            const uint32_t buf = staging + fu.s * kSlabBytes, bar = ready + 8 * fu.s;
             if (fill.in0 >= 0) {
               bar_expect(bar, fill.f32 || fill.in1 >= 0 ? kSlabBytes : kPlaneBytes);
-              const int x = fill.pl.col0 + fill.sl * 64, y = fill.pl.row0 + my_rows;
+              const int x = fill.pl.col0 + fill.sl * kSlab, y = fill.pl.row0 + my_rows;
+              const int box = fill.f32 ? kPlaneBytes : kPlaneBytes / 2;
               for (int h = 0; h < 2; ++h) {
-                tma_box(buf + h * kBoxBytes, maps + fill.in0, bar, x, y + h * kBoxRows);
-                if (fill.f32)
-                  tma_box(buf + kPlaneBytes + h * kBoxBytes, maps + fill.in0, bar, x + 32, y + h * kBoxRows);
-                else if (fill.in1 >= 0)
-                  tma_box(buf + kPlaneBytes + h * kBoxBytes, maps + fill.in1, bar, x, y + h * kBoxRows);
+                tma_box(buf + h * box, maps + fill.in0, bar, x, y + h * kBoxRows);
+                if (fill.in1 >= 0) tma_box(buf + kPlaneBytes + h * box, maps + fill.in1, bar, x, y + h * kBoxRows);
               }
             } else {
               bar_arrive(bar);
             }
             fill.next(p);
-            ++u;
+            fu.next<kBufs>();
           }
-          const uint32_t buf = staging + (w & 1u) * kSlabBytes;
-          if (!bar_wait(written + 8 * (w & 1u), w >> 1 & 1u)) {
+          const uint32_t buf = staging + wu.s * kSlabBytes;
+          if (!bar_wait(written + 8 * wu.s, wu.phase)) {
             ok = false;
             break;
           }
-          const int x = store.pl.col0 + store.sl * 64;
+          const int x = store.pl.col0 + store.sl * kSlab, box = store.f32 ? kPlaneBytes : kPlaneBytes / 2;
           for (int h = 0; h < 2; ++h) {
             const int y = store.pl.row0 + my_rows + h * kBoxRows;
             if (y >= store.rows) break;
-            tma_store(maps + store.out0, buf + h * kBoxBytes, x, y);
-            if (store.f32) {
-              if (x + 32 < store.cols) tma_store(maps + store.out0, buf + kPlaneBytes + h * kBoxBytes, x + 32, y);
-            } else if (store.out1 >= 0)
-              tma_store(maps + store.out1, buf + kPlaneBytes + h * kBoxBytes, x, y);
+            tma_store(maps + store.out0, buf + h * box, x, y);
+            if (store.out1 >= 0) tma_store(maps + store.out1, buf + kPlaneBytes + h * box, x, y);
           }
           store_commit();
           store.next(p);
-          ++w;
+          wu.next<kBufs>();
+          --ahead;
         }
         if (!ok) {
           atomicOr(p.err, kErrProductWait);
-          for (uint32_t k = w; k < u; ++k) bar_wait(ready + 8 * (k & 1u), k >> 1 & 1u);  // loads in flight
+          for (; ahead > 0; --ahead, wu.next<kBufs>()) bar_wait(ready + 8 * wu.s, wu.phase);  // loads in flight
         }
         store_wait();
       }
@@ -840,27 +860,28 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     __syncwarp();
     if (S > 1) cluster_sync();  // the epilogue warps' first one
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
     const int ew = warp - 4;
     const int quad = warp & 3;    // the TMEM lanes this warp may read
     const int half = ew >> 2;     // warps 4-7 and 8-11 cover each quadrant once: half of every slab's columns each
     const int row = quad * 32 + lane;
-    uint32_t cc = 0, use = 0;
+    uint32_t cc = 0;
+    Slot use;
     bool ok = true;
     for (int t = first; t < p.n_tiles; t += step) {
-      const Place pl = place<BN, GROUPED>(p, t);
+      const Place pl = place<BN, MODE>(p, t);
       const Product& G = *pl.P;
       const Shape sh(G, q, S);
       // what the epilogue reads from HBM comes to L2 while the products run
-      if constexpr (!GROUPED) {
+      if constexpr (MODE != kSteps) {
         if (S == 1 && !G.swap && !p.boxes) {
           const int m = pl.row0 + my_rows + row;
           if (m < G.M) {
             const char* from = nullptr;
             int bytes = 2;
-            if (G.epi == kEpiLinear && G.add)
+            if (MODE == kForward && G.add)
               from = static_cast<const char*>(G.add) + ((int64_t)m * G.ld_add + pl.col0) * 2;
-            else if (G.epi == kEpiStore && G.accumulate) {
+            else if (MODE == kBackward && G.accumulate) {
               bytes = G.out_type == kF32 ? 4 : 2;
               from = static_cast<const char*>(G.out) + ((int64_t)m * G.ldo + pl.col0) * bytes;
             }
@@ -872,81 +893,115 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           }
         }
       }
-      float acc[BN / 2];
+      const Product P = *pl.P;  // in registers (no indexed access)
+      const uint32_t lanes = (uint32_t)(quad * 32) << 16;
+      // The sums of this thread's 16 columns of the slabs in turn: from TMEM, or added up in registers chunk by chunk.
+      float acc[DIRECT ? kHalf : BN / 2];
+      const auto wait_sums = [&]() {
+        if (ok && !bar_wait(tfull + 8 * (cc & 1u), cc >> 1 & 1u)) ok = false;
+        ok = __all_sync(0xffffffffu, ok);  // if not: the error word is set below, and the tile's values are not written
+        fence_after();
+        return ok;
+      };
+      const auto release_sums = [&]() {
+        fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (PAIR)
+            bar_arrive_cluster(peer_addr(tempty + 8 * (cc & 1u), lead));
+          else
+            bar_arrive(tempty + 8 * (cc & 1u));
+        }
+        ++cc;
+      };
+      uint32_t from = 0;  // TMEM column of the slab's sums (DIRECT)
+      if constexpr (DIRECT) {
+        wait_sums();
+        from = tmem + (cc & 1u) * BN + half * kHalf + lanes;
+      } else {
 #pragma unroll
-      for (int k = 0; k < BN / 2; ++k) acc[k] = 0.f;
-      for (int ps = 0; ps < sh.n_pass; ++ps) {
-        const float scale = sh.scale(ps);
-        for (int k0 = sh.kb0; k0 < sh.kb1; k0 += sh.chunk, ++cc) {
-          if (ok && !bar_wait(tfull + 8 * (cc & 1u), cc >> 1 & 1u)) ok = false;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) continue;  // the error word is set below; the tile's values are not written
-          fence_after();
-          const uint32_t at = tmem + (cc & 1u) * BN + half * kHalf + ((uint32_t)(quad * 32) << 16);
+        for (int k = 0; k < BN / 2; ++k) acc[k] = 0.f;
+        for (int ps = 0; ps < sh.n_pass; ++ps) {
+          const float scale = sh.scale(ps);
+          for (int k0 = sh.kb0; k0 < sh.kb1; k0 += sh.chunk) {
+            if (!wait_sums()) {
+              ++cc;
+              continue;
+            }
+            const uint32_t at = tmem + (cc & 1u) * BN + half * kHalf + lanes;
 #pragma unroll
-          for (int sl = 0; sl < kSlabs; ++sl) {
-            float v[kHalf];
-            if constexpr (kHalf == 32)
-              tmem_ld32(at + sl * kSlab, v);
-            else
-              tmem_ld16(at + sl * kSlab, v);
+            for (int sl = 0; sl < kSlabs; sl += 2) {
+              float v[2 * kHalf];
+              tmem_ld16x2(at + sl * kSlab, at + (sl + 1) * kSlab, v);
 #pragma unroll
-            for (int k = 0; k < kHalf; ++k) acc[sl * kHalf + k] += scale * v[k];
-          }
-          fence_before();
-          __syncwarp();
-          if (lane == 0) {
-            if constexpr (PAIR)
-              bar_arrive_cluster(peer_addr(tempty + 8 * (cc & 1u), lead));
-            else
-              bar_arrive(tempty + 8 * (cc & 1u));
+              for (int k = 0; k < 2 * kHalf; ++k) acc[sl * kHalf + k] += scale * v[k];
+            }
+            release_sums();
           }
         }
       }
-      const Product P = *pl.P;  // in registers (no indexed access)
+      const auto load_slab = [&](int sl) {
+        if constexpr (DIRECT) tmem_ld16(from + sl * kSlab, acc);
+      };
+      const auto next_slab = [&]() {
+        if constexpr (!DIRECT) {
+#pragma unroll
+          for (int k = 0; k + kHalf < BN / 2; ++k) acc[k] = acc[k + kHalf];
+        }
+      };
       if (S > 1) {
         // one tile per cluster: the whole tile's sums go where the operands were, and are joined below
         if (ok) {
-#pragma unroll
-          for (int sl = 0; sl < kSlabs; ++sl)
+#pragma unroll 1
+          for (int sl = 0; sl < kSlabs; ++sl) {
+            load_slab(sl);
 #pragma unroll
             for (int k = 0; k < kHalf; k += 4)
-              st_shared4(ring + (row * pitch(BN) + sl * kSlab + half * kHalf + k) * 4, &acc[sl * kHalf + k]);
+              st_shared4(ring + (row * pitch(BN) + sl * kSlab + half * kHalf + k) * 4, &acc[k]);
+            next_slab();
+          }
         }
         break;
       }
-      if constexpr (BN >= 128) {
-        if (p.boxes) {
+      bool boxes = false;
+      if constexpr (BN >= 128) boxes = MODE == kSteps || p.boxes;
+      if (boxes) {
+        if constexpr (BN >= 128) {
 #pragma unroll 1
-          for (int sl = 0; sl < kSlabs && pl.col0 + sl * kSlab < P.N; ++sl, ++use) {
-            if (ok && !bar_wait(ready + 8 * (use & 1u), use >> 1 & 1u)) ok = false;
+          for (int sl = 0; sl < kSlabs && pl.col0 + sl * kSlab < P.N; ++sl, use.next<kBufs>()) {  // one copy of the code:
+            // it has to stay in the instruction cache
+            if (ok && !bar_wait(ready + 8 * use.s, use.phase)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
-            slab_values<GROUPED>(P, p, acc, staging + (use & 1u) * kSlabBytes, row, half, pl.row0 + my_rows,
-                                 pl.col0 + sl * kSlab + half * kHalf, pl.mirror);
+            load_slab(sl);
+            slab_values<MODE>(P, p, acc, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
+                              pl.col0 + sl * kSlab + half * kHalf, pl.mirror);
             fence_async();
             __syncwarp();
-            if (lane == 0) bar_arrive(written + 8 * (use & 1u));
-#pragma unroll
-            for (int k = 0; k + kHalf < BN / 2; ++k) acc[k] = acc[k + kHalf];  // the next slab's sums come first
+            if (lane == 0) bar_arrive(written + 8 * use.s);
+            next_slab();
           }
-          continue;
         }
-      }
-      if constexpr (!GROUPED) {
+      } else if constexpr (MODE != kSteps) {
 #pragma unroll 1
-        for (int sl = 0; sl < kSlabs; ++sl) {  // one copy of the code: it has to stay in the instruction cache
-          bar_sync_epilogue();                 // the slab before has been read
+        for (int sl = 0; sl < kSlabs; ++sl) {
+          if (ok) load_slab(sl);
+          bar_sync_epilogue();  // the slab before has been read
 #pragma unroll
           for (int k = 0; k < kHalf; k += 4) st_shared4(staging + (row * kSlabPitch + half * kHalf + k) * 4, &acc[k]);
-#pragma unroll
-          for (int k = 0; k + kHalf < BN / 2; ++k) acc[k] = acc[k + kHalf];
+          next_slab();
           bar_sync_epilogue();
           const int row0 = pl.row0 + my_rows, col0 = pl.col0 + sl * kSlab;
           const OwnSums sums{staging};
-          if (ok && !P.swap) write_rows<kSlab>(P, pl.P, row0, col0, lane, ew, 0, kTileM, sums);
-          if (ok && P.swap) write_transposed<kSlab>(P, row0, col0, ew * 32 + lane, 0, kTileM, sums);
+          if (ok && !P.swap) write_rows<kSlab, MODE>(P, pl.P, row0, col0, lane, ew, 0, kTileM, sums);
+          if (ok && P.swap) write_transposed<kSlab, MODE>(P, row0, col0, ew * 32 + lane, 0, kTileM, sums);
         }
+      }
+      if constexpr (DIRECT) {
+        if (ok)
+          release_sums();
+        else
+          ++cc;
       }
     }
     if (!ok && lane == 0) atomicOr(p.err, kErrProductWait);
@@ -954,10 +1009,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       __syncwarp();
       cluster_sync();  // every CTA's sums are in its shared memory
       {  // also after a failed wait (every warp has to reach the same barriers); the values are void then
-        const Place pl = place<BN, GROUPED>(p, first);
+        const Place pl = place<BN, MODE>(p, first);
         const ClusterSums sums{ring, S, odd, PAIR ? 2 : 1};
         const Product P = *pl.P;
-        if constexpr (GROUPED) {
+        if constexpr (MODE == kSteps) {
           // this CTA finishes BN / S columns, a thread half of them of one row, two pieces of 8 at a time (one where S is 8)
           const int cols = BN / (2 * S), c0 = q * (BN / S) + half * cols;
           if (cols >= 16) {
@@ -980,9 +1035,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           // this CTA finishes its share of the rows
           const int share = kTileM / S;
           if (!P.swap)
-            write_rows<BN>(P, pl.P, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, sums);
+            write_rows<BN, MODE>(P, pl.P, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, sums);
           else
-            write_transposed<BN>(P, pl.row0 + my_rows, pl.col0, ew * 32 + lane, q * share, share, sums);
+            write_transposed<BN, MODE>(P, pl.row0 + my_rows, pl.col0, ew * 32 + lane, q * share, share, sums);
         }
       }
     }
@@ -995,14 +1050,14 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   }
 }
 
-template <int BN, bool GROUPED>
+template <int BN, int MODE>
 cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
   static std::atomic<uint64_t> sized{0};  // devices whose copy of the kernel may use this much shared memory
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev > 63 || !(sized.load(std::memory_order_relaxed) >> dev & 1)) {
-    e = cudaFuncSetAttribute(product_kernel<BN, GROUPED>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
+    e = cudaFuncSetAttribute(product_kernel<BN, MODE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
     if (e != cudaSuccess) return e;
     if (dev <= 63) sized.fetch_or(1ull << dev, std::memory_order_relaxed);
   }
@@ -1026,12 +1081,12 @@ cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.numAttrs = 2;
   }
-  return cudaLaunchKernelEx(&cfg, product_kernel<BN, GROUPED>, p);
+  return cudaLaunchKernelEx(&cfg, product_kernel<BN, MODE>, p);
 }
 
 template <int BN>
 cudaError_t residency(int cluster, int* n) {
-  cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
+  cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)cluster);
@@ -1043,7 +1098,7 @@ cudaError_t residency(int cluster, int* n) {
   at.val.clusterDim.y = at.val.clusterDim.z = 1;
   cfg.attrs = &at;
   cfg.numAttrs = 1;
-  return cudaOccupancyMaxActiveClusters(n, product_kernel<BN, true>, &cfg);
+  return cudaOccupancyMaxActiveClusters(n, product_kernel<BN, kSteps>, &cfg);
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
@@ -1064,15 +1119,17 @@ EncodeFn encode_fn() {
 
 }  // namespace
 
-bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_rows, bool bf16) {
+bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_cols, int box_rows,
+              bool bf16) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {ld * 2};
-  const cuuint32_t box[2] = {(cuuint32_t)kBlockK, (cuuint32_t)box_rows};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
   const cuuint32_t unit[2] = {1, 1};
   return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base),
-            dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1096,13 +1153,14 @@ cudaError_t product_residency(int sms, Residency* r) {
   return e;
 }
 
-cudaError_t launch_product(const ProductLaunch& p, int tile_n, bool grouped, int sms, cudaStream_t stream) {
+cudaError_t launch_product(const ProductLaunch& p, int tile_n, int sms, cudaStream_t stream) {
   if (p.n_tiles <= 0) return cudaSuccess;
-  if (grouped) return tile_n == 256 ? launch_one<256, true>(p, sms, stream) : launch_one<128, true>(p, sms, stream);
-  if (tile_n == 256) return launch_one<256, false>(p, sms, stream);
-  if (tile_n == 32) return launch_one<32, false>(p, sms, stream);
-  if (tile_n == 64) return launch_one<64, false>(p, sms, stream);
-  return launch_one<128, false>(p, sms, stream);
+  if (p.g_products) return tile_n == 256 ? launch_one<256, kSteps>(p, sms, stream) : launch_one<128, kSteps>(p, sms, stream);
+  if (p.inl[0].epi == kEpiStore)
+    return tile_n == 256 ? launch_one<256, kBackward>(p, sms, stream) : launch_one<128, kBackward>(p, sms, stream);
+  if (tile_n == 256) return launch_one<256, kForward>(p, sms, stream);
+  if (tile_n == 128) return launch_one<128, kForward>(p, sms, stream);
+  return tile_n == 64 ? launch_one<64, kForward>(p, sms, stream) : launch_one<32, kForward>(p, sms, stream);
 }
 
 }  // namespace ddl
