@@ -96,14 +96,14 @@ struct Planes {
 
 int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
-// x = hi + 2^-11 lo, so a product of two such operands is three passes; lo lo is below the last bit kept.
+// x ~ hi + lo, so a product of two such operands is three passes; lo lo is below the last bit kept.
 void split_passes(ddl::Product* P, int a_hi, int b_hi) {
   P->n_pass = 3;
   const int a[3] = {a_hi, a_hi, a_hi + 1}, b[3] = {b_hi, b_hi + 1, b_hi};
   for (int k = 0; k < 3; ++k) {
     P->a[k] = a[k];
     P->b[k] = b[k];
-    P->scale[k] = k == 0 ? 1.f : 1.f / 2048.f;
+    P->scale[k] = 1.f / (ddl::kPlaneScale * ddl::kPlaneScale);
   }
   P->chunk = 8;
 }

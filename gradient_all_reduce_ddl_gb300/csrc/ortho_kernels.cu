@@ -182,7 +182,7 @@ __device__ __forceinline__ void planes_item(const OrthoPrep& p, const OrthoMatri
         const float w = !p.mom ? u[k][j] : p.nesterov ? u[k][j] + p.mu * v[k][j] : v[k][j];
         x[j] = w * scale;
         h[j] = __half2float(__float2half_rn(x[j]));
-        l[j] = fabsf(h[j]) <= 65504.f ? (x[j] - h[j]) * 2048.f : 0.f;
+        l[j] = x[j] - h[j];
       }
       store_any(m.hi[0], plane[k], kF16, h);
       store_any(m.lo[0], plane[k], kF16, l);
@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(kThreads) planes_kernel(const __grid_constant_
   double s = 0;
   for (int i = threadIdx.x; i < m.n_items; i += kThreads) s += p.partial[m.item0 + i];
   s = block_sum(s);
-  if (threadIdx.x == 0) inv = (float)(1.0 / (sqrt(s) + (double)p.eps));
+  if (threadIdx.x == 0) inv = (float)((double)kPlaneScale / (sqrt(s) + (double)p.eps));
   __syncthreads();
   if (m.vec && p.vec)
     planes_item<4>(p, m, it, inv);
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads) planes_kernel(const __grid_constant_
 template <int V>
 __device__ __forceinline__ void finish_item(const OrthoFinish& p, const OrthoMatrix& m, const OrthoItem& it) {
   const Walk walk = Walk::of<V>(it);
-  const float step = p.lr * m.shape_scale;
+  const float step = p.lr * m.shape_scale * (1.f / kPlaneScale);
   for (uint32_t i = threadIdx.x; i < walk.total; i += kThreads) {
     int64_t at, plane;
     walk.place<V>(m, i, &at, &plane);
@@ -228,13 +228,13 @@ __device__ __forceinline__ void finish_item(const OrthoFinish& p, const OrthoMat
         for (int k = 0; k < 4; ++k) {
           if (c + k >= p.n_copies) break;
 #pragma unroll
-          for (int j = 0; j < V; ++j) t[k][j] = t[k][j] * p.decay - step * (x[j] + l[j] * (1.f / 2048.f));
+          for (int j = 0; j < V; ++j) t[k][j] = t[k][j] * p.decay - step * (x[j] + l[j]);
           store_any(p.copies[c + k], at, kF32, t[k]);
         }
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < V; ++j) x[j] += l[j] * (1.f / 2048.f);
+      for (int j = 0; j < V; ++j) x[j] = (x[j] + l[j]) * (1.f / kPlaneScale);
       store_any(p.out, at, p.type, x);
     }
   }

@@ -19,6 +19,9 @@ constexpr int kBlockK = 64;      // contraction elements per stage (one 128-byte
 constexpr int kBoxRows = 64;     // rows of a TMA box
 constexpr int kSlabCols = 32;    // columns that the epilogue moves at a time
 constexpr int kMaxPasses = 3;
+// Planes of the Newton-Schulz iterates: hi = binary16(x 2^12), lo = binary16(x 2^12 - hi).  The iterates and their
+// polynomials stay below 16 in magnitude (a polynomial that lets them grow past it gives NaN); the smallest lo is 2^-36.
+constexpr float kPlaneScale = 4096.f;
 constexpr int kMaxMaps = 8;      // tensor maps carried in the launch record
 
 enum ElemType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };

@@ -41,7 +41,6 @@ constexpr int kThreads = 384;  // warps 2 and 3 only fill the first warpgroup
 constexpr int kEpiWarps = 8;
 constexpr int kBoxBytes = kBoxRows * kBlockK * 2;
 constexpr int kABytes = kTileM * kBlockK * 2;
-constexpr float kLoScale = 2048.f;  // lo planes hold (x - hi) * 2^11
 
 // What a launch is for; each has its own epilogues (and registers: one that spilled would go to L2 for it, since shared
 // memory leaves no L1).
@@ -419,13 +418,13 @@ __device__ __forceinline__ uint4 pack8(const float* v, int type) {
   return make_uint4(to16x2(v[0], v[1], type), to16x2(v[2], v[3], type), to16x2(v[4], v[5], type), to16x2(v[6], v[7], type));
 }
 
-// The planes of 8 values.
-__device__ __forceinline__ void split8(const float* v, uint4* hi, uint4* lo) {
-  *hi = pack8(v, kF16);
+// The planes of 8 values x kPlaneScale.
+__device__ __forceinline__ void split8(const float* x, uint4* hi, uint4* lo) {
   float h[8], l[8];
+  *hi = pack8(x, kF16);
   unpack8(*hi, kF16, h);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) l[k] = fabsf(h[k]) <= 65504.f ? (v[k] - h[k]) * kLoScale : 0.f;
+  for (int k = 0; k < 8; ++k) l[k] = x[k] - h[k];
   *lo = pack8(l, kF16);
 }
 
@@ -495,7 +494,8 @@ template <int MODE>
 __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunch& p, float* v, uint32_t buf, int row,
                                             int half, int row0, int n0, bool mirror) {
   if constexpr (MODE == kSteps) {
-    const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = P.epi == kEpiPoly ? p.cc : 1.f;
+    // v is D in binary32, C's planes hold kPlaneScale times its values, as the result's will
+    const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = (P.epi == kEpiPoly ? p.cc : 1.f) * kPlaneScale;
     const uint32_t at[2] = {piece(buf, row, 2 * half), piece(buf, row, 2 * half + 1)};
     if (P.in0 >= 0) {
       uint4 h[2], l[2];
@@ -507,8 +507,11 @@ __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunc
         unpack8(h[g], kF16, a);
         unpack8(l[g], kF16, b);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[8 * g + k] = cd * v[8 * g + k] + cc * (a[k] + b[k] * (1.f / kLoScale));
+        for (int k = 0; k < 8; ++k) v[8 * g + k] = cd * v[8 * g + k] + cc * (a[k] + b[k]);
       }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] *= kPlaneScale;
     }
     uint4 hi[2], lo[2];
 #pragma unroll
@@ -571,15 +574,20 @@ __device__ __forceinline__ void joined_planes(const Product& P, const ProductLau
       h[i] = *reinterpret_cast<const uint4*>(P.c_hi + (int64_t)m * P.ldc + n + 8 * i);
       l[i] = *reinterpret_cast<const uint4*>(P.c_lo + (int64_t)m * P.ldc + n + 8 * i);
     }
-    const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = P.epi == kEpiPoly ? p.cc : 1.f;
+    const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = (P.epi == kEpiPoly ? p.cc : 1.f) * kPlaneScale;
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       float a[8], b[8];
       unpack8(h[i], kF16, a);
       unpack8(l[i], kF16, b);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) sum[i][k] = cd * sum[i][k] + cc * (a[k] + b[k] * (1.f / kLoScale));
+      for (int k = 0; k < 8; ++k) sum[i][k] = cd * sum[i][k] + cc * (a[k] + b[k]);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) sum[i][k] *= kPlaneScale;
   }
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) {
@@ -694,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const CUtensorMap* maps = MODE == kSteps ? p.g_maps : p.maps;
 
   // The epilogue's sums want registers: 384 threads of 168 become 128 of 56 and 256 of 224 (64,512 either way).
+  __syncwarp();
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     if (warp == 0 && lane == 0) {

@@ -122,10 +122,14 @@ inline cudaError_t launch_early(void (*kernel)(Args...), dim3 grid, int threads,
 }
 
 // -- tcgen05 -------------------------------------------------------------------
+//
+// The .sync.aligned forms want the whole warp at the same instruction, which a branch or a loop before them does not
+// promise: each wrapper converges the warp first.
 
 // PAIR: both CTAs of the pair make the call, for the same columns of each.
 template <bool PAIR>
 __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
+  __syncwarp();
   if constexpr (PAIR) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_dst), "r"(cols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -137,6 +141,7 @@ __device__ __forceinline__ void tmem_alloc(uint32_t smem_dst, uint32_t cols) {
 
 template <bool PAIR>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
+  __syncwarp();
   if constexpr (PAIR)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
   else
@@ -194,6 +199,7 @@ __device__ __forceinline__ uint32_t instr_desc(bool bf16, bool a_mn, bool b_mn, 
 
 // Twice 16 columns of this warp's 32 lanes, complete on return.
 __device__ __forceinline__ void tmem_ld16x2(uint32_t addr, uint32_t addr2, float (&v)[32]) {
+  __syncwarp();
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -211,6 +217,7 @@ __device__ __forceinline__ void tmem_ld16x2(uint32_t addr, uint32_t addr2, float
 
 // 16 columns of this warp's 32 lanes, complete on return.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float (&v)[16]) {
+  __syncwarp();
   uint32_t* u = reinterpret_cast<uint32_t*>(v);
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
@@ -244,6 +251,7 @@ __device__ __forceinline__ void ld_shared4(uint32_t addr, float (&v)[4]) {
 // -- clusters --------------------------------------------------------------------
 
 __device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
