@@ -559,48 +559,92 @@ __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunc
   }
 }
 
-// 8 columns n.. of output row m where the contraction was split: `sum` holds D.  Rows of the planes are padded to 8 columns,
-// so a piece that begins inside the matrix is whole.
-template <int PIECES>
-__device__ __forceinline__ void joined_planes(const Product& P, const ProductLaunch& p, float (&sum)[PIECES][8], int m, int n,
-                                              bool mirror, int lane) {
-  const bool in = m < P.M;
-  if (P.epi != kEpiGram) {
-    uint4 h[PIECES], l[PIECES];
+__device__ __forceinline__ void unpack4(uint2 u, float (&v)[4]) {
+  const float2 a = from16x2(u.x, kF16), b = from16x2(u.y, kF16);
+  v[0] = a.x, v[1] = a.y, v[2] = b.x, v[3] = b.y;
+}
+
+// The planes of 4 values x kPlaneScale.
+__device__ __forceinline__ void split4(const float (&x)[4], uint2* hi, uint2* lo) {
+  float h[4];
+  *hi = make_uint2(to16x2(x[0], x[1], kF16), to16x2(x[2], x[3], kF16));
+  unpack4(*hi, h);
+  *lo = make_uint2(to16x2(x[0] - h[0], x[1] - h[1], kF16), to16x2(x[2] - h[2], x[3] - h[3], kF16));
+}
+
+// Where the contraction was split: finishes rows [r0, r0 + rows) of the BN columns at D(row0, col0), along rows of the
+// planes (padded to 8 columns, so that a group of 4 that begins inside the matrix is whole).  back: the finished values,
+// x kPlaneScale, also replace the sums in this CTA's shared memory.
+template <int BN>
+__device__ __forceinline__ void joined_rows(const Product& P, const ProductLaunch& p, const ClusterSums sums, int row0,
+                                            int col0, int r0, int rows, int ew, int lane, bool back) {
+  constexpr int kBatch = 4;
+  const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = (P.epi == kEpiPoly ? p.cc : 1.f) * kPlaneScale;
+#pragma unroll 1
+  for (int c = lane * 4; c < BN; c += 128) {
+    const int n = col0 + c;
+    if (n >= P.N) continue;
+#pragma unroll 1
+    for (int rr = ew; rr < rows; rr += kEpiWarps * kBatch) {
+      uint2 h[kBatch], l[kBatch];
+      float v[kBatch][4];
+      bool in[kBatch];
 #pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      h[i] = l[i] = make_uint4(0, 0, 0, 0);
-      if (!in || n + 8 * i >= P.N) continue;
-      h[i] = *reinterpret_cast<const uint4*>(P.c_hi + (int64_t)m * P.ldc + n + 8 * i);
-      l[i] = *reinterpret_cast<const uint4*>(P.c_lo + (int64_t)m * P.ldc + n + 8 * i);
+      for (int i = 0; i < kBatch; ++i) {
+        const int m = row0 + r0 + rr + i * kEpiWarps;
+        in[i] = rr + i * kEpiWarps < rows && m < P.M;
+        if (in[i] && P.epi != kEpiGram) {
+          h[i] = *reinterpret_cast<const uint2*>(P.c_hi + (int64_t)m * P.ldc + n);
+          l[i] = *reinterpret_cast<const uint2*>(P.c_lo + (int64_t)m * P.ldc + n);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (in[i]) sums.four(((r0 + rr + i * kEpiWarps) * pitch(BN) + c) * 4, v[i]);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (!in[i]) continue;
+        if (P.epi != kEpiGram) {
+          float a[4], b[4];
+          unpack4(h[i], a);
+          unpack4(l[i], b);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[i][k] = cd * v[i][k] + cc * (a[k] + b[k]);
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[i][k] *= kPlaneScale;
+        }
+        uint2 hi, lo;
+        split4(v[i], &hi, &lo);
+        const int64_t to = (int64_t)(row0 + r0 + rr + i * kEpiWarps) * P.ldp + n;
+        *reinterpret_cast<uint2*>(P.p_hi + to) = hi;
+        *reinterpret_cast<uint2*>(P.p_lo + to) = lo;
+        if (back) st_shared4(sums.base + ((r0 + rr + i * kEpiWarps) * pitch(BN) + c) * 4, v[i]);
+      }
     }
-    const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = (P.epi == kEpiPoly ? p.cc : 1.f) * kPlaneScale;
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i) {
-      float a[8], b[8];
-      unpack8(h[i], kF16, a);
-      unpack8(l[i], kF16, b);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum[i][k] = cd * sum[i][k] + cc * (a[k] + b[k]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < PIECES; ++i)
-#pragma unroll
-      for (int k = 0; k < 8; ++k) sum[i][k] *= kPlaneScale;
   }
+}
+
+// The mirror image of what joined_rows finished: neighbouring lanes take neighbouring rows of D, so that the stores run
+// along the image's rows.  rows is 16, 32 or 64.
+template <int BN>
+__device__ __forceinline__ void joined_mirror(const Product& P, uint32_t base, int row0, int col0, int r0, int rows,
+                                              int thread) {
+#pragma unroll 2
+  for (int u = thread; u < rows * (BN / 4); u += kEpiWarps * 32) {
+    const int i = r0 + u % rows, c = u / rows * 4, n = row0 + i;
+    if (n >= P.M || col0 + c >= P.N) continue;
+    float v[4];
+    ld_shared4(base + (i * pitch(BN) + c) * 4, v);
+    uint2 hi, lo;
+    split4(v, &hi, &lo);
+    const uint32_t h[2] = {hi.x, hi.y}, l[2] = {lo.x, lo.y};
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) {
-    if (n + 8 * i >= P.N) continue;
-    uint4 hi, lo;
-    split8(sum[i], &hi, &lo);
-    if (in) {
-      *reinterpret_cast<uint4*>(P.p_hi + (int64_t)m * P.ldp + n + 8 * i) = hi;
-      *reinterpret_cast<uint4*>(P.p_lo + (int64_t)m * P.ldp + n + 8 * i) = lo;
-    }
-    if (mirror) {
-      store_mirror8(P.p_hi, P.ldp, hi, m, P.M, n + 8 * i, P.N, lane);
-      store_mirror8(P.p_lo, P.ldp, lo, m, P.M, n + 8 * i, P.N, lane);
+    for (int k = 0; k < 4; ++k) {
+      if (col0 + c + k >= P.N) continue;
+      const int64_t to = (int64_t)(col0 + c + k) * P.ldp + n;
+      P.p_hi[to] = (uint16_t)(h[k >> 1] >> (k & 1) * 16);
+      P.p_lo[to] = (uint16_t)(l[k >> 1] >> (k & 1) * 16);
     }
   }
 }
@@ -1022,23 +1066,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const ClusterSums sums{ring, S, odd, PAIR ? 2 : 1};
         const Product P = *pl.P;
         if constexpr (MODE == kSteps) {
-          // this CTA finishes BN / S columns, a thread half of them of one row, two pieces of 8 at a time (one where S is 8)
-          const int cols = BN / (2 * S), c0 = q * (BN / S) + half * cols;
-          if (cols >= 16) {
-#pragma unroll 1
-            for (int c = c0; c < c0 + cols; c += 16) {
-              float v[2][8];
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                sums.four((row * pitch(BN) + c + 4 * k) * 4, *reinterpret_cast<float(*)[4]>(&v[k >> 1][k & 1 ? 4 : 0]));
-              joined_planes<2>(P, p, v, pl.row0 + my_rows + row, pl.col0 + c, pl.mirror, lane);
-            }
-          } else {
-            float v[1][8];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              sums.four((row * pitch(BN) + c0 + 4 * k) * 4, *reinterpret_cast<float(*)[4]>(&v[0][4 * k]));
-            joined_planes<1>(P, p, v, pl.row0 + my_rows + row, pl.col0 + c0, pl.mirror, lane);
+          // this CTA finishes its share of the rows; nobody else reads those sums, so its own copy can take the results
+          const int share = kTileM / S;
+          joined_rows<BN>(P, p, sums, pl.row0 + my_rows, pl.col0, q * share, share, ew, lane, pl.mirror);
+          if (pl.mirror) {
+            bar_sync_epilogue();
+            joined_mirror<BN>(P, ring, pl.row0 + my_rows, pl.col0, q * share, share, ew * 32 + lane);
           }
         } else {
           // this CTA finishes its share of the rows
