@@ -238,6 +238,11 @@ struct Slot {
   }
 };
 
+// Makes a tensor map that the host wrote into device memory usable by this thread's TMA operations.
+__device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
+  asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(map) : "memory");
+}
+
 struct Place {
   const Product* P;
   int row0, col0, mirror;
@@ -664,6 +669,12 @@ struct Slabs {
     in0 = P.in0, in1 = P.in1, out0 = P.out0, out1 = P.out1;
     f32 = MODE == kBackward && P.out_type == kF32;
     rows = P.M;
+    if constexpr (MODE == kSteps) {  // of the walks, the one that fills and the one that stores each use their own
+      if (in0 >= 0) acquire_map(p.g_maps + in0);
+      if (in1 >= 0) acquire_map(p.g_maps + in1);
+      acquire_map(p.g_maps + out0);
+      acquire_map(p.g_maps + out1);
+    }
     const int left = (P.N - pl.col0 + kSlab - 1) / kSlab;
     n_sl = left < BN / kSlab ? left : BN / kSlab;
   }
@@ -719,21 +730,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   fence_after();
   const uint32_t tmem = tmem_slot;
   griddep_launch();
-  if constexpr (MODE == kSteps) {
-    // the first tile's records are the handle's own: to L1 and L2 while the kernel before still runs
-    const int t = blockIdx.x / (PAIR ? 2 * p.splits : p.splits);
-    if (warp == 3 && t < p.n_tiles) {
-      const Place pl = place<BN, MODE>(p, t);
-      const int ps = lane & 3;
-      if (lane < 3 && ps < pl.P->n_pass)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(p.g_maps + pl.P->a[ps]) : "memory");
-      else if (lane >= 4 && lane < 7 && ps < pl.P->n_pass)
-        asm volatile("prefetch.tensormap [%0];" ::"l"(p.g_maps + pl.P->b[ps]) : "memory");
-    }
-  } else if (warp == 3 && lane < 2) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(p.maps + (lane ? p.inl[0].b[0] : p.inl[0].a[0])) : "memory");
-  }
-  griddep_wait();
+  // Every role reads its first tile's records (the handle's own, or this launch's) before it waits for the kernel
+  // before this one, whose results only then may be touched.
 
   // a cluster has S parts of a tile's contraction, each a CTA's or a pair's
   const int S = p.splits;
@@ -756,13 +754,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const Place pl = place<BN, MODE>(p, t);
         const Product& P = *pl.P;
         const Shape sh(P, q, S);
+        const CUtensorMap *ma0 = maps + P.a[0], *ma1 = maps + P.a[1], *ma2 = maps + P.a[2];
+        const CUtensorMap *mb0 = maps + P.b[0], *mb1 = maps + P.b[1], *mb2 = maps + P.b[2];
+        if constexpr (MODE == kSteps) {
+          // written by the host before this launch; of three passes the first two share A, the outer two B
+          acquire_map(ma0);
+          acquire_map(ma2);
+          acquire_map(mb0);
+          acquire_map(mb1);
+        }
+        if (t == first) griddep_wait();
         for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
-          const CUtensorMap* ma = maps + P.a[ps];
-          const CUtensorMap* mb = maps + P.b[ps];
-          if constexpr (MODE == kSteps) {  // written by the host before this launch
-            asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(ma) : "memory");
-            asm volatile("fence.proxy.tensormap::generic.acquire.gpu [%0], 128;" ::"l"(mb) : "memory");
-          }
+          const CUtensorMap* ma = ps == 0 ? ma0 : ps == 1 ? ma1 : ma2;
+          const CUtensorMap* mb = ps == 0 ? mb0 : ps == 1 ? mb1 : mb2;
           for (int kb = sh.kb0; kb < sh.kb1; ++kb, at.next<kStages>()) {
             const uint32_t s = at.s;
             if (!bar_wait(empty + 8 * s, at.phase ^ 1u)) {
@@ -817,6 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       uint32_t cc = 0;
       Slot at;
       bool ok = true;
+      griddep_wait();
       for (int t = first; t < p.n_tiles && ok; t += step) {
         const Place pl = place<BN, MODE>(p, t);
         const Shape sh(*pl.P, q, S);
@@ -865,6 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // the epilogue warps, stored here, and can be filled again once the store has read it.  Three are filled ahead,
         // which leaves the store before last time to be read.
         Slabs<BN, MODE> fill(p, first, step), store(p, first, step);
+        griddep_wait();
         uint32_t ahead = 0, filled = 0;
         Slot fu, wu;
         bool ok = true;
@@ -925,6 +931,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const Place pl = place<BN, MODE>(p, t);
       const Product& G = *pl.P;
       const Shape sh(G, q, S);
+      if (t == first) griddep_wait();
       // what the epilogue reads from HBM comes to L2 while the products run
       if constexpr (MODE != kSteps) {
         if (S == 1 && !G.swap && !p.boxes) {
