@@ -309,6 +309,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     prep.ldz = mz.ld;
     prep.rows = T;
     prep.cols = N;
+    prep.block_rows = (int32_t)ddl::dz_rows(T);
     prep.act = h->act;
     prep.n_planes = n_planes;
     for (int k = 0; k < n_planes; ++k) prep.planes[k] = static_cast<uint16_t*>(h->dz[k].p);
@@ -317,7 +318,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   }
   if (db) {
     const size_t done = (size_t)blocks_of(N, ddl::kDzCols) * 4;
-    if ((st = need(&h->partial, (size_t)blocks_of(h->max_tokens, ddl::kDzRows) * (size_t)N * 4)) != DDL_OK) return st;
+    if ((st = need(&h->partial, (size_t)std::max<int64_t>(64, blocks_of(h->max_tokens, 64)) * (size_t)N * 4)) != DDL_OK) return st;
     if (!h->done.p) {
       if ((st = need(&h->done, done)) != DDL_OK) return st;
       if ((st = ddl::status_of(cudaMemsetAsync(h->done.p, 0, done, s))) != DDL_OK) return st;
@@ -339,22 +340,28 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   for (int k = 0; k < planes; ++k)
     if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBlockK)) return DDL_ERR_CUDA;
   if ((dw && !map_of(&L, 3, ax, ddl::kBlockK)) || (dx && !map_of(&L, 4, aw, ddl::kBlockK))) return DDL_ERR_CUDA;
-  // dw's tiles come first, then dx's; the workers take them in turn
+  // the product with the longer contraction first; the workers take the tiles in turn
   const auto dw_count = [&](int tile) { return dw ? blocks_of(N, tile) * blocks_of(K, tile) : 0; };
   const auto dx_count = [&](int tile) { return dx ? blocks_of(T, tile) * blocks_of(K, tile) : 0; };
   const int64_t dw_steps = blocks_of(T, ddl::kBlockK) * planes, dx_steps = blocks_of(N, ddl::kBlockK);
+  const bool dw_first = dw && (!dx || dw_steps >= dx_steps);
   const ddl::Layout l = ddl::choose_layout(
       [&](int tile, int workers) {
-        const int64_t all = dw_count(tile) + dx_count(tile), mine = blocks_of(all, workers);
-        const int64_t long_ones = std::min(mine, blocks_of(dw_count(tile), workers));
-        return long_ones * dw_steps + (mine - long_ones) * dx_steps;
+        const int64_t one = dw_first ? dw_count(tile) : dx_count(tile), two = dw_first ? dx_count(tile) : dw_count(tile);
+        const int64_t s1 = dw_first ? dw_steps : dx_steps, s2 = dw_first ? dx_steps : dw_steps;
+        int64_t most = 0;
+        for (int64_t i = 0; i < workers; ++i) {  // worker i's tiles are i, i + workers, ...
+          const int64_t mine = one + two > i ? (one + two - i - 1) / workers + 1 : 0, first = one > i ? (one - i - 1) / workers + 1 : 0;
+          most = std::max(most, first * s1 + (mine - first) * s2);
+        }
+        return most;
       },
       [&](int tile) { return dw_count(tile) + dx_count(tile); },
       std::min(dw ? blocks_of(T, ddl::kBlockK) : dx_steps, dx ? dx_steps : blocks_of(T, ddl::kBlockK)), h->room);
   const int tile_n = l.tile;
   dw_tiles = dw_count(tile_n);
   dx_tiles = dx_count(tile_n);
-  if (dw) {  // dw[n][k] = sum_t dz[t][n] x[t][k]: both operands with their rows contiguous
+  const auto add_dw = [&]() {  // dw[n][k] = sum_t dz[t][n] x[t][k]: both operands with their rows contiguous
     ddl::Product& P = L.inl[L.n_inl];
     P.M = (int32_t)N;
     P.N = (int32_t)K;
@@ -377,8 +384,8 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.out = dw;
     P.ldo = mdw.ld;
     L.inl_tiles[L.n_inl++] = (int32_t)dw_tiles;
-  }
-  if (dx) {  // dx[t][k] = sum_n dz[t][n] w[n][k]
+  };
+  const auto add_dx = [&]() {  // dx[t][k] = sum_n dz[t][n] w[n][k]
     ddl::Product& P = L.inl[L.n_inl];
     P.M = (int32_t)T;
     P.N = (int32_t)K;
@@ -396,7 +403,10 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.out = dx;
     P.ldo = mdx.ld;
     L.inl_tiles[L.n_inl++] = (int32_t)dx_tiles;
-  }
+  };
+  if (dw && dw_first) add_dw();
+  if (dx) add_dx();
+  if (dw && !dw_first) add_dw();
   L.n_tiles = L.inl_tiles[0] + L.inl_tiles[1];
   L.splits = l.splits;
   L.boxes = L.splits == 1 && (!dw || (ge == 4 ? mdw.tma32() : mdw.tma())) && (!dx || mdx.tma()) &&

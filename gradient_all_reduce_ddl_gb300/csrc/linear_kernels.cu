@@ -53,7 +53,7 @@ __device__ __forceinline__ void planes_of(float x, float y, uint32_t (&out)[kMax
   }
 }
 
-// kDzRows x kDzCols of dz; warp w has the rows w, w + 8, ..., a lane 8 columns: neighbours (VEC) or 32 apart.
+// block_rows x kDzCols of dz; warp w has the rows w, w + 8, ..., a lane 8 columns: neighbours (VEC) or 32 apart.
 template <int TYPE, int ACT, int N, bool VEC>
 __device__ __forceinline__ void dz_rows(const LinearPrep& p, int64_t r0, int64_t c0, float (&sum)[8]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -61,7 +61,7 @@ __device__ __forceinline__ void dz_rows(const LinearPrep& p, int64_t r0, int64_t
   const uint16_t* zp = static_cast<const uint16_t*>(p.z);
   if (VEC && c0 + 8 * lane >= p.cols) return;
 #pragma unroll 2
-  for (int i = warp; i < kDzRows; i += kWarps) {
+  for (int i = warp; i < p.block_rows; i += kWarps) {
     const int64_t r = r0 + i;
     if (r >= p.rows) break;
     float v[8], z[8];
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   tc::griddep_launch();
   tc::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t across = (p.cols + kDzCols - 1) / kDzCols, down = (p.rows + kDzRows - 1) / kDzRows;
+  const int64_t across = (p.cols + kDzCols - 1) / kDzCols, down = (p.rows + p.block_rows - 1) / p.block_rows;
   int64_t block = blockIdx.x;
   const int64_t dz_blocks = p.has_dz ? across * down : 0;
   if (block >= dz_blocks) {
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   }
   const int64_t cb = block / down, rb = block % down, c0 = cb * kDzCols;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  dz_act<TYPE, VEC>(p, rb * kDzRows, c0, sum);
+  dz_act<TYPE, VEC>(p, rb * p.block_rows, c0, sum);
   if (!p.db) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) sums[warp][VEC ? 8 * lane + j : lane + 32 * j] = sum[j];
@@ -195,7 +195,7 @@ float plane_scale(int type, int n, int k) {
 }
 
 cudaError_t launch_linear_prep(const LinearPrep& p, cudaStream_t stream) {
-  int64_t blocks = p.has_dz ? ((p.cols + kDzCols - 1) / kDzCols) * ((p.rows + kDzRows - 1) / kDzRows) : 0;
+  int64_t blocks = p.has_dz ? ((p.cols + kDzCols - 1) / kDzCols) * ((p.rows + p.block_rows - 1) / p.block_rows) : 0;
   for (int k = 0; k < p.n_packs; ++k)
     blocks += ((p.pack[k].rows + kPackRows - 1) / kPackRows) * ((p.pack[k].cols + kPackCols - 1) / kPackCols);
   if (blocks == 0) return cudaSuccess;
