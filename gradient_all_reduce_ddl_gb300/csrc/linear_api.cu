@@ -35,7 +35,10 @@ namespace {
 using ddl::Range;
 
 constexpr int64_t kMaxFeatures = 1 << 22;
-constexpr int64_t kMaxTokens = (1ll << 31) - 256;
+// Longest sums over tokens: a tile's takes 2^20 blocks x 3 planes x 0.35 us, about half of what a kernel's waits allow.
+constexpr int64_t kMaxTokens = 1 << 26;
+// K blocks that stay in the tensor core's accumulator for 16-bit results.
+constexpr int64_t kLongChunk = 4096;
 // What a tensor map and a tile index can address.
 constexpr int64_t kMaxTiles = (1ll << 31) - 1;
 
@@ -109,13 +112,30 @@ bool map32_of(ddl::ProductLaunch* L, int k, const Mat& m) {
 
 int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
-bool distinct(const Range* out, int n_out, const Range* in, int n_in) {
+// Whether two matrices (element sizes ea, eb) have a byte in common.  Matrices of one row pitch may interleave: column
+// blocks of the same wider buffer.
+bool overlap(const Mat& a, int ea, const Mat& b, int eb) {
+  if (!a.range(ea).overlaps(b.range(eb))) return false;
+  const uint64_t pitch = (uint64_t)a.ld * (uint64_t)ea;
+  if (pitch != (uint64_t)b.ld * (uint64_t)eb) return true;
+  const uintptr_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const uint64_t off = pb >= pa ? (pb - pa) % pitch : (pitch - (pa - pb) % pitch) % pitch;  // b's columns in a's rows
+  return off < (uint64_t)a.cols * (uint64_t)ea || off + (uint64_t)b.cols * (uint64_t)eb > pitch;
+}
+
+struct Operand {
+  Mat m;
+  int esize;
+};
+
+// Nothing written meets anything else, and no range wraps around.
+bool distinct(const Operand* out, int n_out, const Operand* in, int n_in) {
   for (int i = 0; i < n_out; ++i) {
-    if (out[i].wraps()) return false;
+    if (out[i].m.range(out[i].esize).wraps()) return false;
     for (int j = i + 1; j < n_out; ++j)
-      if (out[i].overlaps(out[j])) return false;
+      if (overlap(out[i].m, out[i].esize, out[j].m, out[j].esize)) return false;
     for (int j = 0; j < n_in; ++j)
-      if (in[j].wraps() || out[i].overlaps(in[j])) return false;
+      if (in[j].m.range(in[j].esize).wraps() || overlap(out[i].m, out[i].esize, in[j].m, in[j].esize)) return false;
   }
   return true;
 }
@@ -161,10 +181,8 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
     if (reinterpret_cast<uintptr_t>(m->p) % 2) return DDL_ERR_INVALID_ARG;
   // y may be the residual itself (each element is read before it is written, by the same thread)
   const bool in_place = residual && residual == y && ldr == ldy;
-  const Range outs[2] = {my.range(2), mz.range(2)};
-  const Range ins[4] = {mx.range(2), mw.range(2), mb.range(2), in_place ? Range(nullptr, 0) : mr.range(2)};
+  const Operand outs[2] = {{my, 2}, {mz, 2}}, ins[4] = {{mx, 2}, {mw, 2}, {mb, 2}, {in_place ? Mat{nullptr, 0, 0, 1} : mr, 2}};
   if (!distinct(outs, 2, ins, 4)) return DDL_ERR_INVALID_ARG;
-  if (in_place && mr.range(2).overlaps(mz.range(2))) return DDL_ERR_INVALID_ARG;
 
   // Few tokens: their side becomes the narrow side of the tiles, 32 or 64 wide, and the 128-row side
   // walks the weights, which are the traffic then.
@@ -264,8 +282,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   for (const Mat* m : {&mdy, &mx, &mw, &mz, &mdx})
     if (reinterpret_cast<uintptr_t>(m->p) % 2) return DDL_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(dw) % ge || reinterpret_cast<uintptr_t>(db) % ge) return DDL_ERR_INVALID_ARG;
-  const Range outs[3] = {mdx.range(2), mdw.range(ge), mdb.range(ge)};
-  const Range ins[4] = {mdy.range(2), mx.range(2), mw.range(2), mz.range(2)};
+  const Operand outs[3] = {{mdx, 2}, {mdw, ge}, {mdb, ge}}, ins[4] = {{mdy, 2}, {mx, 2}, {mw, 2}, {mz, 2}};
   if (!distinct(outs, 3, ins, 4)) return DDL_ERR_INVALID_ARG;
 
   int64_t dx_tiles = dx ? blocks_of(T, ddl::kTileM) * blocks_of(K, 128) : 0;
@@ -285,13 +302,16 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   }
 
   // dz: dy itself where it can be; else planes of dy act'(z).  GELU's and SiLU's slopes are not
-  // 16-bit numbers: a binary32 gradient sums 22 (binary16) or 24 (bfloat16) bits of dz, while 16-bit
-  // results take dz rounded to 16 bits, as they are rounded themselves.
+  // 16-bit numbers: a binary32 gradient sums 22 (binary16) or 24 (bfloat16) bits of dz.  16-bit results
+  // take dz rounded to 16 bits, as they are rounded themselves; where one round of the SMs does all of
+  // them, launches and not products are what costs, and they take two planes.
   const bool curved = h->act == ddl::kActGelu || h->act == ddl::kActSilu;
   const bool f16 = h->type == ddl::kF16;
-  const int dw_planes = dw && curved && grad_dtype == DDL_FP32 ? (f16 ? 2 : 3) : 1;
+  const int planes16 = curved && dx_tiles + dw_tiles <= h->sms ? 2 : 1;
+  const int dw_planes = !dw ? 0 : grad_dtype == DDL_FP32 && curved ? (f16 ? 2 : 3) : planes16;
+  const int dx_planes = dx ? planes16 : 0;
   const bool own_dz = (dx || dw) && (has_z || !mdy.tma());
-  const int n_planes = own_dz ? dw_planes : 0;
+  const int n_planes = own_dz ? std::max(dw_planes, dx_planes) : 0;
   const int64_t ldp = own_dz ? (int64_t)ddl::round8((uint64_t)N) : mdy.ld;
   for (int k = 0; k < n_planes; ++k)
     if ((st = need(&h->dz[k], (size_t)h->max_tokens * (size_t)ldp * 2)) != DDL_OK) return st;
@@ -336,14 +356,14 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   std::memset(&L, 0, sizeof(L));
   L.bf16 = !f16;
   L.err = h->d_err;
-  const int planes = n_planes ? n_planes : 1;
-  for (int k = 0; k < planes; ++k)
+  const int maps = std::max(1, n_planes);
+  for (int k = 0; k < maps; ++k)
     if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBlockK)) return DDL_ERR_CUDA;
   if ((dw && !map_of(&L, 3, ax, ddl::kBlockK)) || (dx && !map_of(&L, 4, aw, ddl::kBlockK))) return DDL_ERR_CUDA;
   // the product with the longer contraction first; the workers take the tiles in turn
   const auto dw_count = [&](int tile) { return dw ? blocks_of(N, tile) * blocks_of(K, tile) : 0; };
   const auto dx_count = [&](int tile) { return dx ? blocks_of(T, tile) * blocks_of(K, tile) : 0; };
-  const int64_t dw_steps = blocks_of(T, ddl::kBlockK) * planes, dx_steps = blocks_of(N, ddl::kBlockK);
+  const int64_t dw_steps = blocks_of(T, ddl::kBlockK) * dw_planes, dx_steps = blocks_of(N, ddl::kBlockK) * dx_planes;
   const bool dw_first = dw && (!dx || dw_steps >= dx_steps);
   const ddl::Layout l = ddl::choose_layout(
       [&](int tile, int workers) {
@@ -357,7 +377,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
         return most;
       },
       [&](int tile) { return dw_count(tile) + dx_count(tile); },
-      std::min(dw ? blocks_of(T, ddl::kBlockK) : dx_steps, dx ? dx_steps : blocks_of(T, ddl::kBlockK)), h->room);
+      std::min(dw ? blocks_of(T, ddl::kBlockK) : INT64_MAX, dx ? blocks_of(N, ddl::kBlockK) : INT64_MAX), h->room);
   const int tile_n = l.tile;
   dw_tiles = dw_count(tile_n);
   dx_tiles = dx_count(tile_n);
@@ -367,13 +387,13 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.N = (int32_t)K;
     P.K = (int32_t)T;
     P.a_mn = P.b_mn = 1;
-    P.n_pass = planes;
-    for (int k = 0; k < planes; ++k) {
+    P.n_pass = dw_planes;
+    for (int k = 0; k < dw_planes; ++k) {
       P.a[k] = k;
       P.b[k] = 3;
-      P.scale[k] = ddl::plane_scale(h->type, planes, k);
+      P.scale[k] = ddl::plane_scale(h->type, maps, k);
     }
-    P.chunk = grad_dtype == DDL_FP32 ? 8 : (int32_t)blocks_of(T, ddl::kBlockK);
+    P.chunk = grad_dtype == DDL_FP32 ? 8 : (int32_t)std::min(kLongChunk, blocks_of(T, ddl::kBlockK));
     P.epi = ddl::kEpiStore;
     P.out_type = grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16;
     P.accumulate = accumulate ? 1 : 0;
@@ -391,10 +411,13 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     P.N = (int32_t)K;
     P.K = (int32_t)N;
     P.b_mn = 1;
-    P.n_pass = 1;
-    P.b[0] = 4;
-    P.scale[0] = ddl::plane_scale(h->type, planes, 0);
-    P.chunk = (int32_t)blocks_of(N, ddl::kBlockK);
+    P.n_pass = dx_planes;
+    for (int k = 0; k < dx_planes; ++k) {
+      P.a[k] = k;
+      P.b[k] = 4;
+      P.scale[k] = ddl::plane_scale(h->type, maps, k);
+    }
+    P.chunk = (int32_t)std::min(kLongChunk, blocks_of(N, ddl::kBlockK));
     P.epi = ddl::kEpiStore;
     P.out_type = h->type;
     P.vec = mdx.vec4(2);

@@ -113,12 +113,15 @@ __device__ __forceinline__ void dz_rows(const LinearPrep& p, int64_t r0, int64_t
 
 template <int TYPE, int ACT, bool VEC>
 __device__ __forceinline__ void dz_planes(const LinearPrep& p, int64_t r0, int64_t c0, float (&sum)[8]) {
-  // GELU and SiLU take as many planes as the gradient's type asks for; the others one, or none
-  constexpr int kMost = ACT == kActGelu || ACT == kActSilu ? (TYPE == kBF16 ? 3 : 2) : 1;
+  // GELU and SiLU take as many planes as the results ask for, up to three of bfloat16; the others one, or none
+  constexpr bool kCurved = ACT == kActGelu || ACT == kActSilu;
+  constexpr int kTwo = kCurved ? 2 : 1, kMost = kCurved && TYPE == kBF16 ? 3 : kTwo;
   if (p.n_planes == 0)
     dz_rows<TYPE, ACT, 0, VEC>(p, r0, c0, sum);
   else if (p.n_planes == 1)
     dz_rows<TYPE, ACT, 1, VEC>(p, r0, c0, sum);
+  else if (p.n_planes == 2)
+    dz_rows<TYPE, ACT, kTwo, VEC>(p, r0, c0, sum);
   else
     dz_rows<TYPE, ACT, kMost, VEC>(p, r0, c0, sum);
 }

@@ -385,7 +385,7 @@ ddl_status_t ddl_selftest_wait_timeout(ddl_plan_t plan, uint32_t limit_us, void*
  * x is tokens x in_features, w out_features x in_features, y, z, residual and
  * dy tokens x out_features, all of the handle's 16-bit type (DDL_FP16 or
  * DDL_BF16), rows at a stride of ld elements (ld >= columns, at most 2^31), at
- * any 2-byte address; bias has out_features elements of that type.  Sums run in
+ * any 2-byte address (column blocks of one wider buffer among them); bias has out_features elements of that type.  Sums run in
  * binary32 and are rounded once.  Rows that do not start at 16-byte boundaries
  * (base and stride) are copied to the handle's workspace first; results do not
  * change.
@@ -406,7 +406,7 @@ typedef enum {
 
 typedef struct ddl_linear* ddl_linear_t;
 
-/* max_tokens: the most tokens of any call (sizes the workspace).
+/* max_tokens: the most tokens of any call, 1..2^26 (sizes the workspace).
  * in_features, out_features: 1..2^22.  dtype DDL_FP32 returns
  * DDL_ERR_UNSUPPORTED.  Host-only. */
 ddl_status_t ddl_linear_create(size_t max_tokens, size_t in_features, size_t out_features, ddl_dtype_t dtype,
@@ -414,8 +414,8 @@ ddl_status_t ddl_linear_create(size_t max_tokens, size_t in_features, size_t out
 
 /* bias, residual, z: NULL = absent.  z, if given, receives the
  * pre-activations that ddl_linear_backward reads.  y may be the residual
- * itself (same pointer and stride).  tokens = 0 queues nothing.  One launch
- * (and a copy per operand with unaligned rows). */
+ * itself (same pointer and stride).  tokens = 0 queues nothing.  One launch,
+ * and one before it where an operand's rows are unaligned. */
 ddl_status_t ddl_linear_forward(ddl_linear_t layer, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
                                 const void* bias, const void* residual, size_t ldr, void* z, size_t ldz, void* y,
                                 size_t ldy, void* stream);
@@ -425,10 +425,12 @@ ddl_status_t ddl_linear_forward(ddl_linear_t layer, size_t tokens, const void* x
  * activation is not DDL_ACT_NONE; the others may be NULL.  accumulate != 0
  * adds to dw and db (earlier micro-batches); 0 overwrites them; dx is always
  * overwritten.  dw and db need their type's alignment only.  tokens = 0 gives
- * empty sums.
+ * empty sums.  One launch for both products, and one before it for dz, the
+ * bias gradient and copies of unaligned operands, as far as there are any.
+ * Repeated calls give the same bits.
  * Rounding: binary32 gradients sum dz to 22 bits (DDL_FP16) or 24 bits
- * (DDL_BF16); dx and binary16 gradients sum dz rounded to the layer's type
- * (exact for DDL_ACT_NONE and DDL_ACT_RELU). */
+ * (DDL_BF16); dx and binary16 gradients sum dz rounded to the layer's type, or
+ * twice its bits in small calls (exact for DDL_ACT_NONE and DDL_ACT_RELU). */
 ddl_status_t ddl_linear_backward(ddl_linear_t layer, size_t tokens, const void* dy, size_t ldy, const void* x,
                                  size_t ldx, const void* w, size_t ldw, const void* z, size_t ldz, void* dx, size_t lddx,
                                  void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate, void* stream);
@@ -445,7 +447,7 @@ ddl_status_t ddl_linear_destroy(ddl_linear_t layer);
  * Orthogonalised updates (Muon).  After the all-reduce every rank holds the
  * same averaged gradient; a layer's matrix is then stepped along the nearest
  * orthogonal matrix to its momentum instead of along the momentum itself.  The
- * orthogonalisation is Newton-Schulz: X = G / (|G|_F + eps), then `steps` times
+ * orthogonalisation is a Newton-Schulz iteration: X = G / (|G|_F + eps), then `steps` times
  *   A = X X^T (X^T X where rows > cols),   X = a X + (b A + c A A) X,
  * which drives the singular values towards one.  Operands are kept as pairs of
  * binary16 numbers (22 bits) and sums in binary32: the polynomial's slope at zero
@@ -455,7 +457,7 @@ ddl_status_t ddl_linear_destroy(ddl_linear_t layer);
  * A handle covers the matrices of one flat buffer (the rank buffers' layout);
  * all of them go through each product in one launch.  Elements outside every
  * matrix are neither read nor written.  Ownership, device binding and threads
- * as for the linear layers; all device memory (about 16 bytes per element) is
+ * as for the linear layers; all device memory (8 to 16 bytes per element) is
  * allocated by the first GPU call. */
 
 typedef struct {
@@ -472,7 +474,9 @@ typedef struct ddl_ortho* ddl_ortho_t;
  * (3.4445, -4.7750, 2.0315) with eps = 1e-7.  The array is copied.  Host-only. */
 ddl_status_t ddl_ortho_create(int n_matrices, const ddl_matrix_t* matrices, ddl_dtype_t dtype, ddl_ortho_t* out);
 
-/* Other coefficients a, b, c, step count (1..32) or eps (>= 0).  Host-only. */
+/* Other coefficients a, b, c, step count (1..32) or eps (>= 0).  The iterates
+ * and b A + c A A have to stay below 16 in magnitude (the default's stay below
+ * 3); a polynomial that lets them grow past that gives NaN.  Host-only. */
 ddl_status_t ddl_ortho_set_polynomial(ddl_ortho_t ortho, int steps, float a, float b, float c, float eps);
 
 /* Orthogonalises every matrix of the flat buffer `in` into `out` (both of the

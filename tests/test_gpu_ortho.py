@@ -67,7 +67,8 @@ def _check(got, g, dtype, **kw):
 
 
 SHAPES = [(1, 1), (1, 100), (100, 1), (2, 3), (16, 16), (64, 147), (147, 64), (127, 129), (129, 127), (128, 128),
-          (128, 512), (33, 4608), (4608, 33), (257, 300), (300, 257), (512, 512), (640, 1000), (1000, 2048), (1025, 769)]
+          (128, 512), (33, 4608), (4608, 33), (257, 300), (300, 257), (512, 512), (640, 1000), (1000, 2048), (1025, 769),
+          (2304, 2304), (1280, 5000), (3000, 1100)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -130,6 +131,26 @@ def test_many_matrices(ddl, dtype, shift):
     for m in MIXED:
         _check(_view(out, m), _view(flat, m), dtype)
     assert bool((out[~_inside()] == 7.0).all())
+
+
+def test_large_and_small_together(ddl):
+    """Matrices that fill 256 x 256 tiles on CTA pairs beside ones that do not."""
+    shapes = [(2048, 2048), (64, 147), (2048, 1024), (1000, 2048), (33, 20), (2048, 2050)]
+    mats, at = [], 0
+    for r, c in shapes:
+        mats.append((at, r, c))
+        at += r * c + 3
+    flat = torch.zeros(at, device="cuda")
+    for k, m in enumerate(mats):
+        _view(flat, m).copy_(_gradient(m[1], m[2], k))
+    out = torch.full_like(flat, 7.0)
+    with ddl.Ortho(mats) as o:
+        o.run(flat, out)
+        again = o.run(flat, torch.full_like(flat, 7.0))
+        o.check()
+    assert torch.equal(out, again)
+    for m in mats:
+        _check(_view(out, m), _view(flat, m), "f32")
 
 
 def test_in_place_and_repeats(ddl):

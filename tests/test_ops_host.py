@@ -31,7 +31,7 @@ def _status(ddl, fn, *args):
     ((8, 8, 8, "DDL_FP32", 0), "DDL_ERR_UNSUPPORTED"),
     ((8, (1 << 22) + 1, 8, "DDL_BF16", 0), "DDL_ERR_UNSUPPORTED"),
     ((8, 8, (1 << 22) + 1, "DDL_BF16", 0), "DDL_ERR_UNSUPPORTED"),
-    ((1 << 31, 8, 8, "DDL_BF16", 0), "DDL_ERR_UNSUPPORTED"),
+    (((1 << 26) + 1, 8, 8, "DDL_BF16", 0), "DDL_ERR_UNSUPPORTED"),
 ])
 def test_linear_create_refuses(ddl, args, want):
     t, i, o, dt, act = args
@@ -52,6 +52,8 @@ A, B, C, D = (1 << 20, 2 << 20, 3 << 20, 4 << 20)
     dict(x=A + 1), dict(y=C + 1), dict(residual=D, ldr=23), dict(z=D, ldz=23), dict(ldx=(1 << 31) + 1),
     dict(y=A), dict(y=B + 100), dict(y=A + 15 * 2), dict(z=C, ldz=24), dict(z=A, ldz=24), dict(residual=C, ldr=25),
     dict(residual=C + 2, ldr=24), dict(bias=C), dict(residual=C, ldr=24, z=C, ldz=24),
+    # column blocks of one buffer that share a column, of other pitches, or that run over the pitch
+    dict(x=A, ldx=64, y=A + 15 * 2, ldy=64), dict(x=A, ldx=64, y=A + 32, ldy=65), dict(x=A, ldx=64, y=A + 41 * 2, ldy=64),
 ])
 def test_linear_forward_refuses(ddl, change):
     a = dict(tokens=8, x=A, ldx=16, w=B, ldw=16, bias=None, residual=None, ldr=0, z=None, ldz=0, y=C, ldy=24)
