@@ -338,10 +338,15 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   }
   if (db) {
     const size_t done = (size_t)blocks_of(N, ddl::kDzCols) * 4;
-    if ((st = need(&h->partial, (size_t)std::max<int64_t>(64, blocks_of(h->max_tokens, 64)) * (size_t)N * 4)) != DDL_OK) return st;
+    if ((st = need(&h->partial, (size_t)ddl::dz_row_blocks(h->max_tokens) * (size_t)N * 4)) != DDL_OK) return st;
     if (!h->done.p) {
       if ((st = need(&h->done, done)) != DDL_OK) return st;
-      if ((st = ddl::status_of(cudaMemsetAsync(h->done.p, 0, done, s))) != DDL_OK) return st;
+      if ((st = ddl::status_of(cudaMemsetAsync(h->done.p, 0, done, s))) != DDL_OK) {
+        cudaFree(h->done.p);
+        h->done.p = nullptr;
+        h->done.bytes = 0;
+        return st;
+      }
     }
     prep.db = db;
     prep.db_f32 = grad_dtype == DDL_FP32;

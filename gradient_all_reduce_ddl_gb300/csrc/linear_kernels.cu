@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
     for (int w = 0; w < kWarps; ++w) s += sums[w][threadIdx.x];
     p.partial[rb * p.cols + c] = s;
   }
-  // the last CTA of these columns adds the row blocks' sums, in their order
+  // the last CTA of these columns adds the row blocks' sums: a warp every eighth of them, then the warps, always in this
+  // order
   __threadfence();
   __syncthreads();
   if (threadIdx.x == 0) last = atomicAdd(p.done + cb, 1u) == (uint32_t)(down - 1);
@@ -177,10 +178,23 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   if (!last) return;
   __threadfence();
   if (threadIdx.x == 0) p.done[cb] = 0;  // for the next call
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sum[j] = 0.f;
+#pragma unroll 2
+  for (int64_t b = warp; b < down; b += kWarps) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t at = c0 + lane + 32 * j;
+      sum[j] += at < p.cols ? __ldcg(p.partial + b * p.cols + at) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sums[warp][lane + 32 * j] = sum[j];
+  __syncthreads();
   if (c >= p.cols) return;
   float s = 0.f;
-#pragma unroll 8
-  for (int64_t b = 0; b < down; ++b) s += __ldcg(p.partial + b * p.cols + c);
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) s += sums[w][threadIdx.x];
   if (p.db_f32) {
     float* o = static_cast<float*>(p.db) + c;
     *o = p.accumulate ? *o + s : s;

@@ -628,9 +628,9 @@ class Linear:
         ddl_linear_check(self.handle, stream)
 
     def close(self):
-        if self.handle is not None:
-            ddl_linear_destroy(self.handle)
-            self.handle = None
+        handle, self.handle = self.handle, None  # destroyed once, also where that reports an error
+        if handle is not None:
+            ddl_linear_destroy(handle)
 
     def __del__(self):
         try:
@@ -680,9 +680,9 @@ class Ortho:
         ddl_ortho_check(self.handle, stream)
 
     def close(self):
-        if self.handle is not None:
-            ddl_ortho_destroy(self.handle)
-            self.handle = None
+        handle, self.handle = self.handle, None  # destroyed once, also where that reports an error
+        if handle is not None:
+            ddl_ortho_destroy(handle)
 
     def __del__(self):
         try:

@@ -440,7 +440,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t layer, size_t tokens, const void* 
  * the calls since the last check are not valid). */
 ddl_status_t ddl_linear_check(ddl_linear_t layer, void* stream);
 
-/* Frees the handle and its workspace.  NULL is accepted. */
+/* Frees the handle and its workspace, whatever it returns.  NULL is accepted. */
 ddl_status_t ddl_linear_destroy(ddl_linear_t layer);
 
 /* ---------------------------------------------------------------------------

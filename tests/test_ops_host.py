@@ -161,3 +161,22 @@ def test_binding_checks_tensors(ddl):
     with ddl.Ortho([(0, 4, 4)]) as o:
         with pytest.raises(ValueError):
             o.run(torch.zeros(16), torch.zeros(16))
+
+
+@pytest.mark.parametrize("kind", ["linear", "ortho"])
+def test_a_failing_destroy_is_not_repeated(ddl, monkeypatch, kind):
+    """The handle is gone whatever destroy returns; closing again must not pass it on a second time."""
+    handle = ddl.Linear(4, 4, 4) if kind == "linear" else ddl.Ortho([(0, 2, 2)])
+    name, calls = f"ddl_{kind}_destroy", []
+    real = getattr(ddl, name)
+
+    def failing(h):
+        calls.append(h)
+        real(h)
+        raise ddl.DDLError(ddl.DDL_ERR_CUDA, name)
+    monkeypatch.setattr(ddl, name, failing)
+    with pytest.raises(ddl.DDLError):
+        handle.close()
+    handle.close()
+    del handle
+    assert len(calls) == 1
