@@ -22,7 +22,9 @@ namespace {
 // A launch of one kind of product over all matrices: products, tiles.
 struct Stage {
   std::vector<ddl::Product> products;
-  std::vector<ddl::Tile> tiles;
+  std::vector<ddl::Tile> tiles;  // the workers' first ones, then the others, linked worker by worker
+  int workers = 0;
+  int slots = 0, counts = 0;     // parts of tiles, tiles in parts
   ddl::Product* d_products = nullptr;
   ddl::Tile* d_tiles = nullptr;
   int tile = 128;  // rows and columns of a tile: 128, or 256 on CTA pairs
@@ -50,6 +52,8 @@ struct ddl_ortho {
   ddl::OrthoMatrix* d_mats = nullptr;
   ddl::OrthoItem* d_items = nullptr;
   double* d_partial = nullptr;
+  float* d_parts = nullptr;      // sums of the stages' parts of tiles
+  uint32_t* d_counts = nullptr;  // their counters, zero between launches
   int n_items = 0;
   Stage stage[kStages];
 };
@@ -78,11 +82,12 @@ cudaError_t release(ddl_ortho* o) {
   drop(&o->d_mats);
   drop(&o->d_items);
   drop(&o->d_partial);
+  drop(&o->d_parts);
+  drop(&o->d_counts);
   for (Stage& s : o->stage) {
     drop(&s.d_products);
     drop(&s.d_tiles);
-    s.products.clear();
-    s.tiles.clear();
+    s = Stage();
   }
   o->ready = false;
   return e;
@@ -114,7 +119,9 @@ std::vector<ddl::Tile> tiles_of(const Stage& st, int tile, bool symmetric) {
   for (int k = 0; k < (int)st.products.size(); ++k) {
     const int tm = (int)blocks_of(st.products[k].M, tile), tn = (int)blocks_of(st.products[k].N, tile);
     for (int i = 0; i < tm; ++i)
-      for (int j = 0; j < (symmetric ? i + 1 : tn); ++j) tiles.push_back({k, i, j, symmetric && j < i});
+      for (int j = 0; j < (symmetric ? i + 1 : tn); ++j)
+        tiles.push_back({k, i, j, symmetric && j < i, 0, (int32_t)blocks_of(st.products[k].K, ddl::kBlockK), 0, 1, 0, 0,
+                         ddl::kNoTile, 0});
   }
   std::stable_sort(tiles.begin(), tiles.end(), [&st](const ddl::Tile& x, const ddl::Tile& y) {
     return st.products[x.product].K > st.products[y.product].K;
@@ -127,6 +134,124 @@ int64_t busiest(const Stage& st, const std::vector<ddl::Tile>& tiles, int worker
   std::vector<int64_t> load(workers, 0);
   for (size_t t = 0; t < tiles.size(); ++t) load[t % workers] += blocks_of(st.products[tiles[t].product].K, ddl::kBlockK);
   return *std::max_element(load.begin(), load.end());
+}
+
+using Lists = std::vector<std::vector<ddl::Tile>>;  // each worker's tiles
+
+// What a tile or a part of one costs a worker, in microseconds: per K block (of all passes), and besides; a part's sums
+// read back.  The blocks, a whole tile's epilogue and a launch are choose_layout's; a part and a join were chosen by the
+// fit to whole runs (of (5, 2), (5, 0), (7, 0), (9, 0) and (9, 2) us for pairs the last was the fastest or within 1 %).
+struct Cost {
+  double block, whole, part, join;
+};
+constexpr int kMostParts = 8, kLeastBlocks = 4;
+
+// Gives the workers the tiles one after the other, each up to `limit`; a tile that does not fit is cut along its
+// contraction and goes on with the next worker (McNaughton's wrap-around rule).  False: they do not hold them all.
+bool fill(const std::vector<ddl::Tile>& tiles, int workers, double limit, const Cost& cost, Lists* lists, int* slots,
+          int* counts, int* most) {
+  lists->assign(workers, {});
+  *slots = *counts = *most = 0;
+  int w = 0;
+  double load = 0;
+  for (const ddl::Tile& tile : tiles) {
+    int parts = 0, in[kMostParts];
+    for (int k = 0; k < tile.k1;) {
+      if (w == workers) return false;
+      ddl::Tile t = tile;
+      t.k0 = k;
+      const double need = (tile.k1 - k) * cost.block + (k ? cost.part : cost.whole);
+      if (load + need <= limit) {
+        load += need;
+      } else {
+        const int room = (int)((limit - load - cost.part) / cost.block), fit = std::min(room, tile.k1 - k - kLeastBlocks);
+        if (fit < kLeastBlocks || parts == kMostParts - 1) {
+          if (load == 0) return false;
+          ++w;
+          load = 0;
+          continue;
+        }
+        t.k1 = k + fit;
+        load = limit;
+      }
+      in[parts] = w;
+      t.part = parts++;
+      t.slot = *slots;
+      t.count = *counts;
+      (*lists)[w].push_back(t);
+      k = t.k1;
+      if (load >= limit) ++w, load = 0;
+    }
+    if (parts > 1) {
+      for (int k = 0; k < parts; ++k) (*lists)[in[k]].back().parts = parts;
+      *slots += parts;
+      *counts += 1;
+      *most = std::max(*most, parts);
+    }
+  }
+  return true;
+}
+
+// Lays a stage's tiles on workers: by choose_layout, or, where the workers' shares would be uneven, cut to even ones.
+// A run without and with cuts: four of 1024 x 4096 1039 and 958 us, ResNet-50's matrices 1187 and 961, one of 2304 x 2304
+// 968 and 880, sets whose shares are even anyway the same.
+void lay(Stage* st, bool symmetric, const ddl::Residency& room) {
+  std::vector<ddl::Tile> tiles[2] = {tiles_of(*st, 128, symmetric), tiles_of(*st, 256, symmetric)};
+  int64_t shortest = INT64_MAX;
+  for (const ddl::Product& P : st->products) shortest = std::min(shortest, blocks_of(P.K, ddl::kBlockK));
+  const ddl::Layout l = ddl::choose_layout(
+      [&](int tile, int workers) { return busiest(*st, tiles[tile / 256], workers) * ddl::kMaxPasses; },
+      [&](int tile) { return (int64_t)tiles[tile / 256].size(); }, shortest, room);
+  st->tile = l.tile;
+  st->splits = l.splits;
+  Lists lists;
+  double best = 0.95 * l.us;  // below 5 % cutting costs more (locality, joins) than the estimate knows
+  for (int k = 0; k < 2; ++k) {
+    const int workers = room.clusters[k];
+    const double launch = k ? 8.8 : 4.3;
+    const Cost cost = {ddl::kMaxPasses * (k ? 0.28 : 0.31), k ? 5.0 : 3.0, k ? 9.0 : 6.0, k ? 2.0 : 1.2};
+    if (workers < 1 || (int64_t)tiles[k].size() > 64ll * workers) continue;  // many tiles are even enough
+    double all = 0;
+    for (const ddl::Tile& t : tiles[k]) all += t.k1 * cost.block + cost.whole;
+    Lists trial;
+    int slots, counts, most;
+    double lo = all / workers, hi = best - launch;
+    for (double limit = lo; hi - lo > 0.25; limit = 0.5 * (lo + hi)) {
+      if (!fill(tiles[k], workers, limit, cost, &trial, &slots, &counts, &most)) {
+        lo = limit;
+        continue;
+      }
+      hi = limit;
+      if (limit + launch + most * cost.join >= best) continue;
+      best = limit + launch + most * cost.join;
+      lists = trial;
+      st->tile = k ? 256 : 128;
+      st->splits = 1;
+      st->slots = slots;
+      st->counts = counts;
+    }
+  }
+  if (lists.empty()) {
+    const std::vector<ddl::Tile>& all = tiles[st->tile / 256];
+    const int cluster = st->tile / 128 * st->splits;
+    const size_t workers = st->splits > 1 ? all.size() : std::min<size_t>(all.size(), (size_t)room.clusters[cluster / 2]);
+    lists.assign(workers, {});
+    for (size_t t = 0; t < all.size(); ++t) lists[t % workers].push_back(all[t]);
+  }
+  lists.erase(std::remove_if(lists.begin(), lists.end(), [](const auto& list) { return list.empty(); }), lists.end());
+  st->workers = (int)lists.size();
+  for (std::vector<ddl::Tile>& list : lists) {
+    // parts first: their joins then run under other tiles' products
+    std::stable_partition(list.begin(), list.end(), [](const ddl::Tile& t) { return t.parts > 1; });
+    st->tiles.push_back(list[0]);
+  }
+  for (size_t w = 0; w < lists.size(); ++w) {
+    if (lists[w].size() > 1) st->tiles[w].next = (int32_t)st->tiles.size();
+    for (size_t k = 1; k < lists[w].size(); ++k) {
+      st->tiles.push_back(lists[w][k]);
+      if (k + 1 < lists[w].size()) st->tiles.back().next = (int32_t)st->tiles.size();
+    }
+  }
 }
 
 // Builds the device side: planes, maps, products and tiles.
@@ -227,21 +352,19 @@ ddl_status_t build(ddl_ortho* o) {
       o->stage[k].products.push_back(P);
     }
   }
+  size_t parts = 0, counts = 0;
   for (int k = 0; k < kStages; ++k) {
     Stage& st = o->stage[k];
-    const bool symmetric = k == kGram0 || k == kGram1 || k == kPoly;
-    std::vector<ddl::Tile> tiles[2] = {tiles_of(st, 128, symmetric), tiles_of(st, 256, symmetric)};
-    int64_t shortest = INT64_MAX;
-    for (const ddl::Product& P : st.products) shortest = std::min(shortest, blocks_of(P.K, ddl::kBlockK));
-    const ddl::Layout l = ddl::choose_layout(
-        [&](int tile, int workers) { return busiest(st, tiles[tile / 256], workers) * ddl::kMaxPasses; },
-        [&](int tile) { return (int64_t)tiles[tile / 256].size(); }, shortest, o->room);
-    st.tile = l.tile;
-    st.splits = l.splits;
-    st.tiles = std::move(tiles[l.tile / 256]);
+    lay(&st, k == kGram0 || k == kGram1 || k == kPoly, o->room);
     if (e == cudaSuccess) e = upload(&st.d_products, st.products.data(), st.products.size());
     if (e == cudaSuccess) e = upload(&st.d_tiles, st.tiles.data(), st.tiles.size());
+    const size_t ctas = st.tile / 128;
+    parts = std::max(parts, st.slots * ctas * ddl::kTileM * (size_t)st.tile);
+    counts = std::max(counts, st.counts * ctas);
   }
+  if (e == cudaSuccess && parts) e = ddl::device_alloc(reinterpret_cast<void**>(&o->d_parts), parts * sizeof(float));
+  const std::vector<uint32_t> none(counts, 0);
+  if (e == cudaSuccess && counts) e = upload(&o->d_counts, none.data(), counts);
   o->n_items = (int)items.size();
   if (e == cudaSuccess) e = upload(&o->d_maps, maps.data(), maps.size());
   if (e == cudaSuccess) e = upload(&o->d_mats, mats.data(), mats.size());
@@ -292,7 +415,9 @@ ddl_status_t products(ddl_ortho* o, cudaStream_t s) {
       const Stage& st = o->stage[kind];
       L.g_products = st.d_products;
       L.g_tiles = st.d_tiles;
-      L.n_tiles = (int32_t)st.tiles.size();
+      L.g_parts = o->d_parts;
+      L.g_counts = o->d_counts;
+      L.n_tiles = st.workers;
       L.splits = st.splits;
       L.boxes = st.splits == 1;
       const cudaError_t e = ddl::launch_product(L, st.tile, o->sms, s);

@@ -68,9 +68,16 @@ struct Product {
   int64_t ldp;
 };
 
-struct Tile {
+// A worker's tile of a grouped launch, or a part of its contraction.
+struct alignas(16) Tile {
   int32_t product, ti, tj, mirror;
+  int32_t k0, k1;       // K blocks
+  int32_t part, parts;  // parts > 1: the other workers' parts are added through memory
+  int32_t slot, count;  // the parts' first place there, and their counter
+  int32_t next;         // the worker's next tile, or kNoTile
+  int32_t pad;
 };
+constexpr int32_t kNoTile = 0x7FFFFFFF;
 
 // Launch record.  Grouped launches read products, tiles and maps from device
 // memory; single launches carry up to two products and their maps here.
@@ -82,7 +89,9 @@ struct ProductLaunch {
   const CUtensorMap* g_maps;
   const Product* g_products;
   const Tile* g_tiles;
-  int32_t n_tiles;
+  float* g_parts;           // grouped: sums of parts, 128 x tile columns a CTA
+  uint32_t* g_counts;       // grouped: a counter per tile in parts and CTA; zero between launches
+  int32_t n_tiles;          // grouped: workers (CTAs, pairs or clusters); worker i begins with tile i
   int32_t splits;           // CTAs of a cluster that share a tile's contraction
   int32_t boxes;            // single launches, tiles of 128 or 256 columns, splits 1: the epilogue moves boxes by TMA (in0
                             // ... out1); grouped ones with splits 1 always do

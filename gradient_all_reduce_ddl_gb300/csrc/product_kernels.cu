@@ -211,7 +211,8 @@ __device__ __forceinline__ void bar_sync_epilogue() {
 struct Shape {
   int kb0, kb1, chunk, n_pass, a_mn, b_mn;
   float scale0, scale1, scale2;
-  __device__ __forceinline__ Shape(const Product& P, int part, int parts)
+  // part `part` of `parts` of K blocks [k0, k1)
+  __device__ __forceinline__ Shape(const Product& P, int k0, int k1, int part, int parts)
       : chunk(P.chunk),
         n_pass(P.n_pass),
         a_mn(P.a_mn),
@@ -219,9 +220,8 @@ struct Shape {
         scale0(P.scale[0]),
         scale1(P.scale[1]),
         scale2(P.scale[2]) {
-    const int nkb = (P.K + kBlockK - 1) / kBlockK;
-    kb0 = nkb * part / parts;
-    kb1 = nkb * (part + 1) / parts;
+    kb0 = k0 + (k1 - k0) * part / parts;
+    kb1 = k0 + (k1 - k0) * (part + 1) / parts;
   }
   __device__ __forceinline__ float scale(int pass) const { return pass == 0 ? scale0 : pass == 1 ? scale1 : scale2; }
 };
@@ -246,15 +246,20 @@ __device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
 struct Place {
   const Product* P;
   int row0, col0, mirror;
+  int k0, k1;
+  int part, parts, slot, count;
+  int next;  // the worker's next tile
 };
 
 template <int BN, int MODE>
-__device__ __forceinline__ Place place(const ProductLaunch& p, int t) {
+__device__ __forceinline__ Place place(const ProductLaunch& p, int t, int step) {
   constexpr int BM = BN == 256 ? 2 * kTileM : kTileM;
   if constexpr (MODE == kSteps) {
-    const int4 u = __ldg(reinterpret_cast<const int4*>(p.g_tiles) + t);
-    return {p.g_products + u.x, u.y * BM, u.z * BN, u.w};
+    const int4* tile = reinterpret_cast<const int4*>(p.g_tiles + t);
+    const int4 u = __ldg(tile), k = __ldg(tile + 1), w = __ldg(tile + 2);
+    return {p.g_products + u.x, u.y * BM, u.z * BN, u.w, k.x, k.y, k.z, k.w, w.x, w.y, w.z};
   } else {
+    const int next = t + step;
     int k = 0;
     if (t >= p.inl_tiles[0]) {
       k = 1;
@@ -266,7 +271,7 @@ __device__ __forceinline__ Place place(const ProductLaunch& p, int t) {
     const int band = t / (16 * cols), first = band * 16;
     const int height = rows - first < 16 ? rows - first : 16;
     const int in = t - band * 16 * cols;
-    return {P, (first + in % height) * BM, in / height * BN, 0};
+    return {P, (first + in % height) * BM, in / height * BN, 0, 0, (P->K + kBlockK - 1) / kBlockK, 0, 1, 0, 0, next};
   }
 }
 
@@ -658,13 +663,16 @@ __device__ __forceinline__ void joined_mirror(const Product& P, uint32_t base, i
 // it stores.
 template <int BN, int MODE>
 struct Slabs {
-  int t, step, sl, n_sl;
+  int t, end, step, sl, n_sl;
   Place pl;
   int in0, in1, out0, out1, f32, rows;
-  __device__ __forceinline__ Slabs(const ProductLaunch& p, int first, int by) : t(first), step(by), sl(0) { load(p); }
+  __device__ __forceinline__ Slabs(const ProductLaunch& p, int first, int last, int by)
+      : t(first), end(last), step(by), sl(0) {
+    load(p);
+  }
   __device__ __forceinline__ void load(const ProductLaunch& p) {
-    if (t >= p.n_tiles) return;
-    pl = place<BN, MODE>(p, t);
+    if (t >= end) return;
+    pl = place<BN, MODE>(p, t, step);
     const Product& P = *pl.P;
     in0 = P.in0, in1 = P.in1, out0 = P.out0, out1 = P.out1;
     f32 = MODE == kBackward && P.out_type == kF32;
@@ -678,11 +686,11 @@ struct Slabs {
     const int left = (P.N - pl.col0 + kSlab - 1) / kSlab;
     n_sl = left < BN / kSlab ? left : BN / kSlab;
   }
-  __device__ __forceinline__ bool more(const ProductLaunch& p) const { return t < p.n_tiles; }
+  __device__ __forceinline__ bool more() const { return t < end; }
   __device__ __forceinline__ void next(const ProductLaunch& p) {
     if (++sl < n_sl) return;
     sl = 0;
-    t += step;
+    t = pl.next;
     load(p);
   }
 };
@@ -699,6 +707,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5 + 2 * kBufs];
   __shared__ uint32_t tmem_slot;
+  __shared__ int joins;                  // this CTA's part of a tile was the last: it finishes the tile
+  __shared__ volatile int empty_slab[kBufs];  // a slab of a part whose tile another CTA finishes
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const uint32_t staging = ring + kStages * stage_bytes(BN);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16,
@@ -739,7 +749,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const int odd = PAIR ? rank & 1 : 0, lead = rank - odd;
   const int q = PAIR ? rank >> 1 : rank;
   const int ctas = PAIR ? 2 * S : S;
-  const int first = blockIdx.x / ctas, step = gridDim.x / ctas;
+  // this worker's tiles: a list, or every step-th
+  const int first = blockIdx.x / ctas, step = gridDim.x / ctas, end = MODE == kSteps ? kNoTile : p.n_tiles;
   const int my_rows = odd * kTileM;  // this CTA's part of the tile's rows
   const CUtensorMap* maps = MODE == kSteps ? p.g_maps : p.maps;
 
@@ -750,10 +761,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (warp == 0 && lane == 0) {
       Slot at;
       bool ok = true;
-      for (int t = first; t < p.n_tiles && ok; t += step) {
-        const Place pl = place<BN, MODE>(p, t);
+      for (int t = first, next; t < end && ok; t = next) {
+        const Place pl = place<BN, MODE>(p, t, step);
+        next = pl.next;
         const Product& P = *pl.P;
-        const Shape sh(P, q, S);
+        const Shape sh(P, pl.k0, pl.k1, q, S);
         const CUtensorMap *ma0 = maps + P.a[0], *ma1 = maps + P.a[1], *ma2 = maps + P.a[2];
         const CUtensorMap *mb0 = maps + P.b[0], *mb1 = maps + P.b[1], *mb2 = maps + P.b[2];
         if constexpr (MODE == kSteps) {
@@ -822,9 +834,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       Slot at;
       bool ok = true;
       griddep_wait();
-      for (int t = first; t < p.n_tiles && ok; t += step) {
-        const Place pl = place<BN, MODE>(p, t);
-        const Shape sh(*pl.P, q, S);
+      for (int t = first, next; t < end && ok; t = next) {
+        const Place pl = place<BN, MODE>(p, t, step);
+        next = pl.next;
+        const Shape sh(*pl.P, pl.k0, pl.k1, q, S);
         const uint32_t idesc = instr_desc(p.bf16, sh.a_mn, sh.b_mn, PAIR ? 2 * kTileM : kTileM, BN);
         // K-major: 8-row groups 1024 bytes apart, 32 bytes per K step.  Rows contiguous: 64-row
         // boxes 8 KB apart, 8-k groups 1024 bytes apart, 16 k rows (2048 bytes) per K step.
@@ -869,13 +882,13 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         // The slabs of this CTA's tiles take the four buffers in turn: one is filled (or declared free) here, worked on by
         // the epilogue warps, stored here, and can be filled again once the store has read it.  Three are filled ahead,
         // which leaves the store before last time to be read.
-        Slabs<BN, MODE> fill(p, first, step), store(p, first, step);
+        Slabs<BN, MODE> fill(p, first, end, step), store(p, first, end, step);
         griddep_wait();
         uint32_t ahead = 0, filled = 0;
         Slot fu, wu;
         bool ok = true;
-        while (ok && store.more(p)) {
-          for (; ahead < kBufs - 1 && fill.more(p); ++ahead, ++filled) {
+        while (ok && store.more()) {
+          for (; ahead < kBufs - 1 && fill.more(); ++ahead, ++filled) {
             if (filled >= kBufs) store_wait_read<1>();
             const uint32_t buf = staging + fu.s * kSlabBytes, bar = ready + 8 * fu.s;
             if (fill.in0 >= 0) {
@@ -900,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           const int x = store.pl.col0 + store.sl * kSlab, box = store.f32 ? kPlaneBytes : kPlaneBytes / 2;
           for (int h = 0; h < 2; ++h) {
             const int y = store.pl.row0 + my_rows + h * kBoxRows;
-            if (y >= store.rows) break;
+            if (y >= store.rows || (MODE == kSteps && empty_slab[wu.s])) break;
             tma_store(maps + store.out0, buf + h * box, x, y);
             if (store.out1 >= 0) tma_store(maps + store.out1, buf + kPlaneBytes + h * box, x, y);
           }
@@ -927,10 +940,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     uint32_t cc = 0;
     Slot use;
     bool ok = true;
-    for (int t = first; t < p.n_tiles; t += step) {
-      const Place pl = place<BN, MODE>(p, t);
+    for (int t = first, next; t < end; t = next) {
+      const Place pl = place<BN, MODE>(p, t, step);
+      next = pl.next;
       const Product& G = *pl.P;
-      const Shape sh(G, q, S);
+      const Shape sh(G, pl.k0, pl.k1, q, S);
       if (t == first) griddep_wait();
       // what the epilogue reads from HBM comes to L2 while the products run
       if constexpr (MODE != kSteps) {
@@ -1023,6 +1037,54 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         break;
       }
+      bool skip = false;
+      if constexpr (MODE == kSteps) {
+        if (pl.parts > 1) {
+          // Every part's sums go to memory, each thread's values in the thread's own place; the CTA whose part comes last
+          // adds them in their order (so the result does not depend on which that is) and finishes the tile.  Nobody
+          // waits for anybody.
+          constexpr int kFours = BN / 8;
+          float4* place4 = reinterpret_cast<float4*>(p.g_parts) + ew * 32 + lane;
+          const int64_t apart = (PAIR ? 2 : 1) * kFours * (kEpiWarps * 32);
+          float4* at = place4 + (pl.slot + pl.part) * apart + odd * (kFours * kEpiWarps * 32);
+#pragma unroll
+          for (int k = 0; k < kFours; ++k)
+            __stcg(at + k * (kEpiWarps * 32), make_float4(acc[4 * k], acc[4 * k + 1], acc[4 * k + 2], acc[4 * k + 3]));
+          __threadfence();
+          bar_sync_epilogue();
+          if (ew == 0 && lane == 0) {  // also after a failed wait: the counters return to zero
+            uint32_t* count = p.g_counts + pl.count * (PAIR ? 2 : 1) + odd;
+            joins = atomicAdd(count, 1u) == (uint32_t)(pl.parts - 1);
+            if (joins) *count = 0;
+            __threadfence();
+          }
+          bar_sync_epilogue();
+          skip = !joins;
+          if (!skip) {
+            at = place4 + pl.slot * apart + odd * (kFours * kEpiWarps * 32);
+#pragma unroll
+            for (int k = 0; k < kFours; ++k) {
+              const float4 u = __ldcg(at + k * (kEpiWarps * 32));
+              acc[4 * k] = u.x, acc[4 * k + 1] = u.y, acc[4 * k + 2] = u.z, acc[4 * k + 3] = u.w;
+            }
+#pragma unroll 1
+            for (int part = 1; part < pl.parts; ++part) {
+              at += apart;
+#pragma unroll
+              for (int k0 = 0; k0 < kFours; k0 += 8) {
+                float4 u[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) u[k] = __ldcg(at + (k0 + k) * (kEpiWarps * 32));
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                  const int i = 4 * (k0 + k);
+                  acc[i] += u[k].x, acc[i + 1] += u[k].y, acc[i + 2] += u[k].z, acc[i + 3] += u[k].w;
+                }
+              }
+            }
+          }
+        }
+      }
       bool boxes = false;
       if constexpr (BN >= 128) boxes = MODE == kSteps || p.boxes;
       if (boxes) {
@@ -1034,11 +1096,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             load_slab(sl);
-            slab_values<MODE>(P, p, acc, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
-                              pl.col0 + sl * kSlab + half * kHalf, pl.mirror);
+            if (!skip)
+              slab_values<MODE>(P, p, acc, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
+                                pl.col0 + sl * kSlab + half * kHalf, pl.mirror);
             fence_async();
             __syncwarp();
-            if (lane == 0) bar_arrive(written + 8 * use.s);
+            if (lane == 0) {
+              if (MODE == kSteps) empty_slab[use.s] = skip;
+              bar_arrive(written + 8 * use.s);
+            }
             next_slab();
           }
         }
@@ -1069,7 +1135,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       __syncwarp();
       cluster_sync();  // every CTA's sums are in its shared memory
       {  // also after a failed wait (every warp has to reach the same barriers); the values are void then
-        const Place pl = place<BN, MODE>(p, first);
+        const Place pl = place<BN, MODE>(p, first, step);
         const ClusterSums sums{ring, S, odd, PAIR ? 2 : 1};
         const Product P = *pl.P;
         if constexpr (MODE == kSteps) {
@@ -1114,7 +1180,7 @@ cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
   // a cluster per tile, or persistent CTAs or pairs
   const int cluster = (BN == 256 ? 2 : 1) * p.splits;
   const int64_t whole = (int64_t)p.n_tiles * cluster;
-  const int64_t ctas = p.splits > 1 ? whole : std::min<int64_t>(whole, sms / cluster * cluster);
+  const int64_t ctas = p.splits > 1 || p.g_products ? whole : std::min<int64_t>(whole, sms / cluster * cluster);
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem_bytes(BN);

@@ -457,8 +457,9 @@ ddl_status_t ddl_linear_destroy(ddl_linear_t layer);
  * A handle covers the matrices of one flat buffer (the rank buffers' layout);
  * all of them go through each product in one launch.  Elements outside every
  * matrix are neither read nor written.  Ownership, device binding and threads
- * as for the linear layers; all device memory (8 to 16 bytes per element) is
- * allocated by the first GPU call. */
+ * as for the linear layers; all device memory (8 to 16 bytes per element, and
+ * up to 40 MB for sums where long products are shared out) is allocated by the
+ * first GPU call. */
 
 typedef struct {
   size_t offset;  /* first element in the flat buffers */
