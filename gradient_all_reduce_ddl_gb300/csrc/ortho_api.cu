@@ -281,6 +281,10 @@ ddl_status_t build(ddl_ortho* o) {
   std::vector<CUtensorMap> maps((size_t)n * 16);
   std::vector<ddl::OrthoMatrix> mats(n);
   std::vector<ddl::OrthoItem> items;
+  uint64_t elems = 0;
+  for (const ddl_matrix_t& m : o->mats) elems += m.rows * m.cols;
+  int32_t item = ddl::kOrthoItemElems;
+  while (item > ddl::kOrthoLeastElems && elems / (uint64_t)item < (uint64_t)(ddl::kOrthoItemsPerSm * o->sms)) item /= 2;
   for (int i = 0; i < n; ++i) {
     const ddl_matrix_t& m = o->mats[i];
     const uint64_t s = std::min(m.rows, m.cols);
@@ -306,7 +310,7 @@ ddl_status_t build(ddl_ortho* o) {
     d.shape_scale = wide ? 1.f : (float)std::sqrt((double)m.rows / (double)m.cols);
     d.vec = m.offset % 4 == 0 && m.ld % 4 == 0 && m.cols % 4 == 0;
     d.item0 = (int32_t)items.size();
-    const int32_t cols = std::min(d.cols, ddl::kOrthoItemElems), rows = std::max(1, ddl::kOrthoItemElems / cols);
+    const int32_t cols = std::min(d.cols, item), rows = std::max(1, item / cols);
     for (int32_t r = 0; r < d.rows; r += rows)
       for (int32_t c = 0; c < d.cols; c += cols)
         items.push_back({i, r, std::min(d.rows, r + rows), c, std::min(d.cols, c + cols)});

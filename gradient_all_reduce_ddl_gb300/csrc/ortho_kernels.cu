@@ -2,7 +2,7 @@
 // momentum step, the matrices' Frobenius norms and the first iterate's planes;
 // the result or the parameter step from the last iterate's planes.
 //
-// All are bound by HBM (or L2) traffic.  A CTA takes an item of about 8192
+// All are bound by HBM (or L2) traffic.  A CTA takes an item of 1024 to 8192
 // elements, four to a thread at a time where the layout allows it, with the
 // loads of four such groups issued together (the parameter step: of four copies).
 // The parameter step is a pass of its own rather than the last product's epilogue:

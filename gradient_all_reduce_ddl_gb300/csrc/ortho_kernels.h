@@ -26,7 +26,10 @@ struct OrthoItem {
   int32_t matrix, r0, r1, c0, c1;
 };
 
-constexpr int kOrthoItemElems = 8192;
+// Elements of an item: from the largest down to the smallest, until there are two items for every SM.  A whole run of
+// 64 x 147 takes 96 us (115 with the largest alone), of 2049 x 1023 276 (287), of 1000 x 2048 257 (261); with eight items
+// an SM the last two take 291 and 281, since every CTA of the second pass adds all of its matrix's sums.
+constexpr int kOrthoItemElems = 8192, kOrthoLeastElems = 1024, kOrthoItemsPerSm = 2;
 
 struct OrthoPrep {
   const OrthoMatrix* matrices;
