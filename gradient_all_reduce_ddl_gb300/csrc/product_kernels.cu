@@ -120,10 +120,13 @@ __device__ __forceinline__ void store_any(void* base, int64_t at, int type, cons
 
 template <int V, int R, int ACT>
 __device__ __forceinline__ void activate_all(float (&v)[R][V]) {
+  constexpr int N = (R * V + 1) / 2 * 2;
+  float u[N] = {};
 #pragma unroll
-  for (int i = 0; i < R; ++i)
+  for (int k = 0; k < R * V; ++k) u[k] = v[k / V][k % V];
+  activate<ACT>(u);
 #pragma unroll
-    for (int k = 0; k < V; ++k) v[i][k] = activate(v[i][k], ACT);
+  for (int k = 0; k < R * V; ++k) v[k / V][k % V] = u[k];
 }
 
 template <int V, int R, int TYPE>
@@ -455,54 +458,59 @@ __device__ __forceinline__ void store_mirror8(uint16_t* plane, int64_t ld, uint4
 }
 
 template <int TYPE, int ACT>
-__device__ __forceinline__ void slab_linear(const Product& P, float* v, uint32_t buf, int row, int half, int n0) {
+__device__ __forceinline__ void slab_linear(const Product& P, float* v, const uint4 (&bias)[2], uint32_t buf, int row,
+                                            int half) {
   const uint32_t at[2] = {piece(buf, row, 2 * half), piece(buf, row, 2 * half + 1)};
   uint4 add[2];
   if (P.in0 >= 0) add[0] = ld_shared16(at[0]), add[1] = ld_shared16(at[1]);
-  if (P.bias) {
-    const uint16_t* b = static_cast<const uint16_t*>(P.bias) + n0;
+  float u[16];
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      if (n0 + 8 * g + 8 <= P.N) {
-        float t[8];
-        unpack8(*reinterpret_cast<const uint4*>(b + 8 * g), TYPE, t);
+  for (int g = 0; g < 2; ++g) {
+    float t[8];
+    unpack8(bias[g], TYPE, t);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[8 * g + k] += t[k];
-      }  // rows are whole pieces: the other columns are outside
-    }
+    for (int k = 0; k < 8; ++k) u[8 * g + k] = v[8 * g + k] + t[k];
   }
   if (P.out1 >= 0) {
-    st_shared16(at[0] + kPlaneBytes, pack8(v, TYPE));
-    st_shared16(at[1] + kPlaneBytes, pack8(v + 8, TYPE));
+    st_shared16(at[0] + kPlaneBytes, pack8(u, TYPE));
+    st_shared16(at[1] + kPlaneBytes, pack8(u + 8, TYPE));
   }
-#pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = activate(v[k], ACT);
+  activate<ACT>(u);
   if (P.in0 >= 0) {
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
       float t[8];
       unpack8(add[g], TYPE, t);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[8 * g + k] += t[k];
+      for (int k = 0; k < 8; ++k) u[8 * g + k] += t[k];
     }
   }
-  st_shared16(at[0], pack8(v, TYPE));
-  st_shared16(at[1], pack8(v + 8, TYPE));
+  st_shared16(at[0], pack8(u, TYPE));
+  st_shared16(at[1], pack8(u + 8, TYPE));
 }
 
 template <int TYPE>
-__device__ __forceinline__ void slab_linear_act(const Product& P, float* v, uint32_t buf, int row, int half, int n0) {
+__device__ __forceinline__ void slab_linear_act(const Product& P, float* v, const uint4 (&bias)[2], uint32_t buf, int row,
+                                                int half) {
   switch (P.act) {
-    case kActRelu: slab_linear<TYPE, kActRelu>(P, v, buf, row, half, n0); break;
-    case kActGelu: slab_linear<TYPE, kActGelu>(P, v, buf, row, half, n0); break;
-    case kActSilu: slab_linear<TYPE, kActSilu>(P, v, buf, row, half, n0); break;
-    default: slab_linear<TYPE, kActNone>(P, v, buf, row, half, n0); break;
+    case kActRelu: slab_linear<TYPE, kActRelu>(P, v, bias, buf, row, half); break;
+    case kActGelu: slab_linear<TYPE, kActGelu>(P, v, bias, buf, row, half); break;
+    case kActSilu: slab_linear<TYPE, kActSilu>(P, v, bias, buf, row, half); break;
+    default: slab_linear<TYPE, kActNone>(P, v, bias, buf, row, half); break;
   }
 }
 
+// 16 columns n.. of the bias (zeros without one, or outside: rows are whole pieces).
+__device__ __forceinline__ void load_bias(const Product& P, int n, uint4 (&bias)[2]) {
+#pragma unroll
+  for (int g = 0; g < 2; ++g)
+    bias[g] = P.bias && n + 8 * g < P.N ? __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.bias) + n + 8 * g))
+                                        : make_uint4(0, 0, 0, 0);
+}
+
 template <int MODE>
-__device__ __forceinline__ void slab_values(const Product& P, const ProductLaunch& p, float* v, uint32_t buf, int row,
-                                            int half, int row0, int n0, bool mirror) {
+__device__ __forceinline__ void slab_values(const Product& P, const ProductLaunch& p, float* v, const uint4 (&bias)[2],
+                                            uint32_t buf, int row, int half, int row0, int n0, bool mirror) {
   if constexpr (MODE == kSteps) {
     // v is D in binary32, C's planes hold kPlaneScale times its values, as the result's will
     const float cc = P.epi == kEpiPoly ? p.cb : p.ca, cd = (P.epi == kEpiPoly ? p.cc : 1.f) * kPlaneScale;
@@ -540,9 +548,9 @@ __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunc
     }
   } else if constexpr (MODE == kForward) {
     if (P.type == kBF16)
-      slab_linear_act<kBF16>(P, v, buf, row, half, n0);
+      slab_linear_act<kBF16>(P, v, bias, buf, row, half);
     else
-      slab_linear_act<kF16>(P, v, buf, row, half, n0);
+      slab_linear_act<kF16>(P, v, bias, buf, row, half);
   } else if (P.out_type == kF32) {
     float t[4][4];
     if (P.in0 >= 0) {
@@ -1089,15 +1097,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if constexpr (BN >= 128) boxes = MODE == kSteps || p.boxes;
       if (boxes) {
         if constexpr (BN >= 128) {
+          uint4 bias_ahead[2] = {};
+          if constexpr (MODE == kForward) load_bias(P, pl.col0 + half * kHalf, bias_ahead);
 #pragma unroll 1
           for (int sl = 0; sl < kSlabs && pl.col0 + sl * kSlab < P.N; ++sl, use.next<kBufs>()) {  // one copy of the code:
             // it has to stay in the instruction cache
+            uint4 bias[2] = {bias_ahead[0], bias_ahead[1]};
+            if (MODE == kForward && sl + 1 < kSlabs) load_bias(P, pl.col0 + (sl + 1) * kSlab + half * kHalf, bias_ahead);
             if (ok && !bar_wait(ready + 8 * use.s, use.phase)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             load_slab(sl);
             if (!skip)
-              slab_values<MODE>(P, p, acc, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
+              slab_values<MODE>(P, p, acc, bias, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
                                 pl.col0 + sl * kSlab + half * kHalf, pl.mirror);
             fence_async();
             __syncwarp();

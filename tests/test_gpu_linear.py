@@ -408,3 +408,23 @@ def test_refuses_host_memory_and_failed_allocation(ddl, monkeypatch):
         layer.check()
     z = x.double() @ w.double().t()
     _within(y, z, _forward_bound(x, w, None, z, None, z, "f16")[1])
+
+
+@pytest.mark.parametrize("n_out", [8, 1])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_activations_of_every_number(ddl, dtype, n_out):
+    """Every 16-bit number as a pre-activation: 2^-20 of its size for the activation, and the result's rounding."""
+    x = torch.arange(1 << 16, device="cuda").to(torch.int32).to(torch.int16).view(TYPES[dtype]).view(-1, 1)
+    w = torch.ones(n_out, 1, dtype=TYPES[dtype], device="cuda")
+    z64 = x.double()
+    for act in ("none", "relu", "gelu", "silu"):
+        y = _blank(1 << 16, n_out, dtype)[0]
+        with ddl.Linear(1, n_out, 1 << 16, dtype, act) as layer:
+            layer.forward(x, w, y)
+            layer.check()
+        assert torch.equal(torch.nan_to_num(y), torch.nan_to_num(y[:, :1]).expand_as(y))
+        want, got = _act(z64, act)[:, 0], y[:, 0].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.isinf(got), torch.isinf(want))
+        ok = torch.isfinite(want)
+        _within(got[ok], want[ok], 2.0 ** -20 * z64[ok, 0].abs() + U[dtype] * want[ok].abs() + TINY[dtype])
