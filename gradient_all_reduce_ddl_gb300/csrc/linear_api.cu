@@ -101,7 +101,8 @@ ddl_status_t aligned(const Mat& m, int64_t max_rows, Buffer* b, ddl::LinearPrep*
   return DDL_OK;
 }
 
-bool map_of(ddl::ProductLaunch* L, int k, const Mat& m, int box_cols, int box_rows = ddl::kBoxRows) {
+bool map_of(ddl::ProductLaunch* L, int k, const Mat& m, int box_cols, int box_rows = 0) {
+  if (!box_rows) box_rows = box_cols == ddl::kSlabCols ? ddl::kTileM : ddl::kBoxRows;
   return ddl::make_map(&L->maps[k], m.p, (uint64_t)m.rows, (uint64_t)m.cols, (uint64_t)m.ld, box_cols, box_rows,
                        L->bf16 != 0);
 }

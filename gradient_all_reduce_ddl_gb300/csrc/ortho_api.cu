@@ -294,7 +294,8 @@ ddl_status_t build(ddl_ortho* o) {
     for (int k = 0; k < 8; ++k)
       for (int slab = 0; slab < 2; ++slab)
         if (!ddl::make_map(&maps[(size_t)i * 16 + 8 * slab + k], base + where[k], k < 4 ? m.rows : s, k < 4 ? m.cols : s,
-                           (uint64_t)(k < 4 ? p.ldx : p.lds), slab ? ddl::kSlabCols : ddl::kBlockK, ddl::kBoxRows, false))
+                           (uint64_t)(k < 4 ? p.ldx : p.lds), slab ? ddl::kSlabCols : ddl::kBlockK,
+                           slab ? ddl::kTileM : ddl::kBoxRows, false))
           return DDL_ERR_CUDA;
     ddl::OrthoMatrix& d = mats[i];
     d.offset = (int64_t)m.offset;

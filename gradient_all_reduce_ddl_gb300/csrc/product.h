@@ -16,7 +16,7 @@ namespace ddl {
 
 constexpr int kTileM = 128;      // output rows per tile
 constexpr int kBlockK = 64;      // contraction elements per stage (one 128-byte swizzle row)
-constexpr int kBoxRows = 64;     // rows of a TMA box
+constexpr int kBoxRows = 64;     // rows of an operand's TMA box
 constexpr int kSlabCols = 32;    // columns that the epilogue moves at a time
 constexpr int kMaxPasses = 3;
 // Planes of the Newton-Schulz iterates: hi = binary16(x 2^12), lo = binary16(x 2^12 - hi).  The iterates and their
@@ -115,7 +115,7 @@ cudaError_t launch_product(const ProductLaunch& p, int tile_n, int sms, cudaStre
 bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_cols, int box_rows,
               bool bf16);
 
-// The same of a binary32 matrix, boxes of 32 columns x 64 rows (kEpiStore's output).
+// The same of a binary32 matrix, boxes of 32 columns x 128 rows (kEpiStore's output).
 bool make_map32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld);
 
 // Error word bits of these kernels.

@@ -52,7 +52,7 @@ __host__ __device__ constexpr int stages(int bn) { return bn >= 128 ? 5 : 6; }
 __host__ __device__ constexpr int stage_bytes(int bn) { return kABytes + b_rows(bn) * kBlockK * 2; }
 constexpr int kSlab = kSlabCols;
 __host__ __device__ constexpr int pitch(int cols) { return cols + 4; }        // floats; rows 4 banks apart
-constexpr int kPlaneBytes = kTileM * kSlab * 2;  // a slab of 16 bits: two boxes of 64 rows
+constexpr int kPlaneBytes = kTileM * kSlab * 2;  // a slab of 16 bits
 constexpr int kSlabBytes = 2 * kPlaneBytes;      // what a box epilogue keeps of a slab: two planes, or binary32
 constexpr int kBufs = 4;                         // slabs on their way in, in work and on their way out
 __host__ __device__ constexpr int smem_bytes(int bn) {
@@ -264,7 +264,7 @@ __device__ __forceinline__ Place place(const ProductLaunch& p, int t, int step) 
   } else {
     const int next = t + step;
     int k = 0;
-    if (t >= p.inl_tiles[0]) {
+    if (MODE == kBackward && t >= p.inl_tiles[0]) {  // forward launches have one product
       k = 1;
       t -= p.inl_tiles[0];
     }
@@ -672,7 +672,7 @@ __device__ __forceinline__ void joined_mirror(const Product& P, uint32_t base, i
 template <int BN, int MODE>
 struct Slabs {
   int t, end, step, sl, n_sl;
-  Place pl;
+  int row0, col0, following;
   int in0, in1, out0, out1, f32, rows;
   __device__ __forceinline__ Slabs(const ProductLaunch& p, int first, int last, int by)
       : t(first), end(last), step(by), sl(0) {
@@ -680,8 +680,9 @@ struct Slabs {
   }
   __device__ __forceinline__ void load(const ProductLaunch& p) {
     if (t >= end) return;
-    pl = place<BN, MODE>(p, t, step);
-    const Product& P = *pl.P;
+    const Place pl = place<BN, MODE>(p, t, step);
+    row0 = pl.row0, col0 = pl.col0, following = pl.next;
+    const Product& P = MODE == kForward ? p.inl[0] : *pl.P;
     in0 = P.in0, in1 = P.in1, out0 = P.out0, out1 = P.out1;
     f32 = MODE == kBackward && P.out_type == kF32;
     rows = P.M;
@@ -698,7 +699,7 @@ struct Slabs {
   __device__ __forceinline__ void next(const ProductLaunch& p) {
     if (++sl < n_sl) return;
     sl = 0;
-    t = pl.next;
+    t = following;
     load(p);
   }
 };
@@ -901,12 +902,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             const uint32_t buf = staging + fu.s * kSlabBytes, bar = ready + 8 * fu.s;
             if (fill.in0 >= 0) {
               bar_expect(bar, fill.f32 || fill.in1 >= 0 ? kSlabBytes : kPlaneBytes);
-              const int x = fill.pl.col0 + fill.sl * kSlab, y = fill.pl.row0 + my_rows;
-              const int box = fill.f32 ? kPlaneBytes : kPlaneBytes / 2;
-              for (int h = 0; h < 2; ++h) {
-                tma_box(buf + h * box, maps + fill.in0, bar, x, y + h * kBoxRows);
-                if (fill.in1 >= 0) tma_box(buf + kPlaneBytes + h * box, maps + fill.in1, bar, x, y + h * kBoxRows);
-              }
+              const int x = fill.col0 + fill.sl * kSlab, y = fill.row0 + my_rows;
+              tma_box(buf, maps + fill.in0, bar, x, y);
+              if (fill.in1 >= 0) tma_box(buf + kPlaneBytes, maps + fill.in1, bar, x, y);
             } else {
               bar_arrive(bar);
             }
@@ -918,12 +916,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             ok = false;
             break;
           }
-          const int x = store.pl.col0 + store.sl * kSlab, box = store.f32 ? kPlaneBytes : kPlaneBytes / 2;
-          for (int h = 0; h < 2; ++h) {
-            const int y = store.pl.row0 + my_rows + h * kBoxRows;
-            if (y >= store.rows || (MODE == kSteps && empty_slab[wu.s])) break;
-            tma_store(maps + store.out0, buf + h * box, x, y);
-            if (store.out1 >= 0) tma_store(maps + store.out1, buf + kPlaneBytes + h * box, x, y);
+          const int x = store.col0 + store.sl * kSlab, y = store.row0 + my_rows;
+          if (y < store.rows && !(MODE == kSteps && empty_slab[wu.s])) {
+            tma_store(maps + store.out0, buf, x, y);
+            if (store.out1 >= 0) tma_store(maps + store.out1, buf + kPlaneBytes, x, y);
           }
           store_commit();
           store.next(p);
@@ -951,7 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first, next; t < end; t = next) {
       const Place pl = place<BN, MODE>(p, t, step);
       next = pl.next;
-      const Product& G = *pl.P;
+      const Product& G = MODE == kForward ? p.inl[0] : *pl.P;
       const Shape sh(G, pl.k0, pl.k1, q, S);
       if (t == first) griddep_wait();
       // what the epilogue reads from HBM comes to L2 while the products run
@@ -975,7 +971,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           }
         }
       }
-      const Product P = *pl.P;  // in registers (no indexed access)
+      // in registers (no indexed access); a forward launch's only product is read as a parameter
+      const Product copy = MODE == kForward ? Product{} : G;
+      const Product& P = MODE == kForward ? p.inl[0] : copy;
       const uint32_t lanes = (uint32_t)(quad * 32) << 16;
       // The sums of this thread's 16 columns of the slabs in turn: from TMEM, or added up in registers chunk by chunk.
       float acc[DIRECT ? kHalf : BN / 2];
@@ -1265,7 +1263,7 @@ bool make_map32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols
   if (!fn) return false;
   const cuuint64_t dims[2] = {cols, rows};
   const cuuint64_t strides[1] = {ld * 4};
-  const cuuint32_t box[2] = {32, (cuuint32_t)kBoxRows};
+  const cuuint32_t box[2] = {32, (cuuint32_t)kTileM};
   const cuuint32_t unit[2] = {1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void*>(base), dims, strides, box, unit,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
