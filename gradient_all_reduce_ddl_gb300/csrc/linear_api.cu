@@ -221,7 +221,9 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   ddl::ProductLaunch L;
   std::memset(&L, 0, sizeof(L));
   L.bf16 = h->type == ddl::kBF16;
-  if (!map_of(&L, 0, ax, ddl::kBlockK, swap && tile_n == 32 ? 32 : ddl::kBoxRows) || !map_of(&L, 1, aw, ddl::kBlockK))
+  // boxes of a tile's rows
+  const int narrow = std::min(tile_n, ddl::kTileM);
+  if (!map_of(&L, 0, ax, ddl::kBlockK, swap ? narrow : ddl::kTileM) || !map_of(&L, 1, aw, ddl::kBlockK, swap ? ddl::kTileM : narrow))
     return DDL_ERR_CUDA;
   ddl::Product& P = L.inl[0];
   P.M = (int32_t)(swap ? N : T);

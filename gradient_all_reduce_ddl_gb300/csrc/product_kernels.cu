@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
               bar_expect(bar, stage_bytes(BN));
             }
 #pragma unroll
-            for (int h = 0; h < kTileM / kBoxRows; ++h) {
+            for (int h = 0; h < (MODE == kForward ? 1 : kTileM / kBoxRows); ++h) {
               const int row = pl.row0 + my_rows + h * kBoxRows;
               const int x = sh.a_mn ? row : kb * kBlockK, y = sh.a_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 tma_box(sa + h * kBoxBytes, ma, bar, x, y);
             }
 #pragma unroll
-            for (int h = 0; h < (b_rows(BN) + kBoxRows - 1) / kBoxRows; ++h) {
+            for (int h = 0; h < (MODE == kForward ? 1 : (b_rows(BN) + kBoxRows - 1) / kBoxRows); ++h) {
               const int row = pl.col0 + my_rows + h * kBoxRows;
               const int x = sh.b_mn ? row : kb * kBlockK, y = sh.b_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
