@@ -233,7 +233,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   P.a[0] = swap ? 1 : 0;
   P.b[0] = swap ? 0 : 1;
   P.scale[0] = 1.f;
-  P.chunk = (int32_t)steps;
+  P.chunk[0] = P.chunk[1] = (int32_t)steps;
   P.epi = ddl::kEpiLinear;
   P.swap = swap;
   P.type = h->type;
@@ -401,7 +401,8 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
       P.b[k] = 3;
       P.scale[k] = ddl::plane_scale(h->type, maps, k);
     }
-    P.chunk = grad_dtype == DDL_FP32 ? 8 : (int32_t)std::min(kLongChunk, blocks_of(T, ddl::kBlockK));
+    P.chunk[0] = P.chunk[1] = grad_dtype == DDL_FP32 ? 8 : (int32_t)std::min(kLongChunk, blocks_of(T, ddl::kBlockK));
+    if (grad_dtype == DDL_FP32) P.chunk[1] = 32;  // the sums of lower planes are small
     P.epi = ddl::kEpiStore;
     P.out_type = grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16;
     P.accumulate = accumulate ? 1 : 0;
@@ -425,7 +426,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
       P.b[k] = 4;
       P.scale[k] = ddl::plane_scale(h->type, maps, k);
     }
-    P.chunk = (int32_t)std::min(kLongChunk, blocks_of(N, ddl::kBlockK));
+    P.chunk[0] = P.chunk[1] = (int32_t)std::min(kLongChunk, blocks_of(N, ddl::kBlockK));
     P.epi = ddl::kEpiStore;
     P.out_type = h->type;
     P.vec = mdx.vec4(2);

@@ -101,8 +101,19 @@ struct Planes {
 
 int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
 
+// K blocks that the first pass of a stage's products leaves in the tensor core's truncating accumulator.  What counts
+// is A A: its diagonal is one large term among small ones, and all that is added after it truncates it.  For s = 200 to
+// 500 a chunk of 4 blocks there made the result's error 2 to 3.5 times a binary32 evaluation's; with these chunks it is
+// 0.3 to 1.2 times that (1.5 for the longest of the smallest matrices).  One block instead of eight throughout costs
+// 15 % of four 1024 x 4096, this 2 %.
+int chunk_of(int stage, uint64_t s) {
+  if (stage == kPoly) return s <= 1024 ? 1 : 2;
+  if (stage == kGram0 || stage == kGram1) return s <= 128 ? 1 : 4;
+  return 8;
+}
+
 // x ~ hi + lo, so a product of two such operands is three passes; lo lo is below the last bit kept.
-void split_passes(ddl::Product* P, int a_hi, int b_hi) {
+void split_passes(ddl::Product* P, int a_hi, int b_hi, int chunk) {
   P->n_pass = 3;
   const int a[3] = {a_hi, a_hi, a_hi + 1}, b[3] = {b_hi, b_hi + 1, b_hi};
   for (int k = 0; k < 3; ++k) {
@@ -110,7 +121,8 @@ void split_passes(ddl::Product* P, int a_hi, int b_hi) {
     P->b[k] = b[k];
     P->scale[k] = 1.f / (ddl::kPlaneScale * ddl::kPlaneScale);
   }
-  P->chunk = 8;
+  P->chunk[0] = chunk;
+  P->chunk[1] = 32;  // these sums are 2^-11 of the first's
 }
 
 // The tiles of every product of a stage, longest contractions first so that the last to start are short.
@@ -326,11 +338,11 @@ ddl_status_t build(ddl_ortho* o) {
         P.M = P.N = (int32_t)s;
         P.K = (int32_t)(wide ? m.cols : m.rows);
         P.a_mn = P.b_mn = wide ? 0 : 1;
-        split_passes(&P, map + 2 * xi, map + 2 * xi);
+        split_passes(&P, map + 2 * xi, map + 2 * xi, chunk_of(k, s));
         P.epi = ddl::kEpiGram;
       } else if (k == kPoly) {  // B = b A + c A A
         P.M = P.N = P.K = (int32_t)s;
-        split_passes(&P, map + 4, map + 4);
+        split_passes(&P, map + 4, map + 4, chunk_of(k, s));
         P.epi = ddl::kEpiPoly;
         P.c_hi = base + p.a[0];
         P.c_lo = base + p.a[1];
@@ -340,7 +352,7 @@ ddl_status_t build(ddl_ortho* o) {
         P.N = (int32_t)m.cols;
         P.K = (int32_t)s;
         P.b_mn = wide ? 1 : 0;  // X as [K][N]; B is its own transpose
-        split_passes(&P, wide ? map + 6 : map + 2 * xi, wide ? map + 2 * xi : map + 6);
+        split_passes(&P, wide ? map + 6 : map + 2 * xi, wide ? map + 2 * xi : map + 6, chunk_of(k, s));
         P.epi = ddl::kEpiApply;
         P.c_hi = base + p.x[xi][0];
         P.c_lo = base + p.x[xi][1];

@@ -8,7 +8,9 @@
 // The parameter step is a pass of its own rather than the last product's epilogue:
 // with 16 copies it moves 132 bytes an element, which the eight epilogue warps of
 // a persistent product kernel cannot keep in flight (ResNet-50's last product took
-// 972 us with the step in its epilogue, against 105 us without).
+// 972 us with the step in its epilogue, against 105 us without).  ResNet-50, 16 copies:
+// momentum and norms 58 us (5.2 TB/s), planes 53 (5.8), parameter step 511 (6.6 of the
+// measured 6.8).
 #include "activation.cuh"
 #include "ortho_kernels.h"
 #include "product.h"

@@ -3,8 +3,9 @@
 // One kernel carries every product of the linear layers and of the
 // Newton-Schulz steps: D = sum over passes of scale * A B^T on the tensor
 // cores, then an epilogue on the binary32 sums.  Passes let an operand be the
-// sum of several 16-bit planes (x ~ hi + 2^-11 lo), which is how results that
-// are kept in binary32 get products of more than 11 bits.
+// sum of several 16-bit planes (two of binary16 hold x 2^12 = hi + lo to 22
+// bits), which is how results that are kept in binary32 get products of more
+// than 11 bits.
 #pragma once
 
 #include <cuda.h>
@@ -42,7 +43,7 @@ struct Product {
   int32_t n_pass;
   int32_t a[kMaxPasses], b[kMaxPasses];  // tensor map of each pass's operands
   float scale[kMaxPasses];
-  int32_t chunk;   // K blocks summed in the tensor core before they are added in binary32 registers
+  int32_t chunk[2];  // K blocks summed in the tensor core before they are added in binary32 registers: first pass, others
   int32_t epi;     // EpilogueKind
   int32_t swap;    // D is the transpose of the output: D(i, j) belongs at out[j][i]
   int32_t type;    // ElemType of bias, add, z

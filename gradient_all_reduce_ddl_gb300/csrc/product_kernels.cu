@@ -3,20 +3,36 @@
 //
 //   D(i, j) = sum_pass scale_pass sum_k A_pass(i, k) B_pass(j, k)
 //
-// on tcgen05 (128 x tile_n tiles, accumulators in TMEM), then one of the
-// epilogues of product.h.
+// on tcgen05 (128 x tile_n tiles on a CTA, 256 x 256 on a CTA pair; accumulators
+// in TMEM), then one of the epilogues of product.h.
 //
-// Roles of a CTA's warps: warp 0 loads operand boxes by TMA into a ring
-// of shared-memory stages, warp 1 issues the products, warps 4-11 take the
-// finished sums out of TMEM, add them in binary32 registers, pass them through
-// shared memory (so that every global access of the epilogue runs along rows)
-// and write the result.  The two TMEM accumulators alternate, so the epilogue
-// of one chunk or tile runs under the products of the next.
+// Roles of a CTA's warps: warp 0 loads operand boxes by TMA into a ring of
+// shared-memory stages, warp 1 issues the products, warps 4-11 take the finished
+// sums out of TMEM and make the results, warp 2 moves what they read and write,
+// a slab of 32 columns at a time, as TMA boxes between memory and four buffers of
+// shared memory (rows that TMA cannot address go through one such buffer and are
+// written by the warps themselves, along rows).  The two TMEM accumulators
+// alternate, so the epilogue of one chunk or tile runs under the products of the
+// next.
+//
+// What bounds it.  256 x 256 x 64 takes a pair 0.28 us at full clocks and 0.34 under
+// the power cap of long runs: 8192 x 8192 -> 4096 without an epilogue runs at the
+// library's speed (300 us, 1830 TFLOP/s).  A launch adds 4 to 9 us and its last epilogue
+// 3 (no activation) to 10 us (GELU, residual, pre-activations): 8192 x 4096 -> 4096 takes
+// 152 and 173 us against the library's 135 for the product alone.  128 x 128 tiles
+// are bound by shared memory (0.31 us for 128 x 128 x 64, half a pair's rate) and are
+// taken where pairs would leave SMs idle (choose_layout).  An epilogue slab costs its
+// warps 1100 cycles, most of it latency of some 150 instructions, and 800 more with
+// GELU: layers with less than 1024 inputs are bound by that (8192 x 512 -> 4096: 40 and
+// 71 us).  Two groups of epilogue warps on alternate slabs gained 3 us without and lost
+// 4 us with GELU (registers), six stages and two slabs nothing: neither is here.
 //
 // The tensor core adds with truncation: a long sum of one sign loses about
 // half a unit in the last place of each of its K/16 additions.  Results kept in
 // binary32 therefore leave the accumulator every `chunk` K blocks and are added
-// in registers with rounding to nearest; 16-bit results sum all of K in TMEM.
+// in registers with rounding to nearest (the first pass's; the sums of lower planes
+// are 2^-8 or 2^-11 of those and may stay longer); 16-bit results sum all of K in
+// TMEM.
 //
 // A long contraction with few tiles is split over the CTAs of a cluster; each
 // leaves its sums in shared memory and the cluster's CTAs add them in rank order
@@ -212,11 +228,12 @@ __device__ __forceinline__ void bar_sync_epilogue() {
 // What the loops over a tile's contraction read of its product, in registers: a load from the product's own memory
 // would be repeated after every wait.
 struct Shape {
-  int kb0, kb1, chunk, n_pass, a_mn, b_mn;
+  int kb0, kb1, chunk0, chunk1, n_pass, a_mn, b_mn;
   float scale0, scale1, scale2;
   // part `part` of `parts` of K blocks [k0, k1)
   __device__ __forceinline__ Shape(const Product& P, int k0, int k1, int part, int parts)
-      : chunk(P.chunk),
+      : chunk0(P.chunk[0]),
+        chunk1(P.chunk[1]),
         n_pass(P.n_pass),
         a_mn(P.a_mn),
         b_mn(P.b_mn),
@@ -226,6 +243,7 @@ struct Shape {
     kb0 = k0 + (k1 - k0) * part / parts;
     kb1 = k0 + (k1 - k0) * (part + 1) / parts;
   }
+  __device__ __forceinline__ int chunk(int pass) const { return pass ? chunk1 : chunk0; }
   __device__ __forceinline__ float scale(int pass) const { return pass == 0 ? scale0 : pass == 1 ? scale1 : scale2; }
 };
 
@@ -854,8 +872,9 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint64_t desc_b = smem_desc(ring + kABytes, sh.b_mn ? kBoxBytes : 16, 1024);
         const uint64_t step_a = (sh.a_mn ? 2048 : 32) >> 4, step_b = (sh.b_mn ? 2048 : 32) >> 4;
         for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
-          for (int k0 = sh.kb0; k0 < sh.kb1 && ok; k0 += sh.chunk, ++cc) {
-            const int k1 = k0 + sh.chunk < sh.kb1 ? k0 + sh.chunk : sh.kb1;
+          const int chunk = sh.chunk(ps);
+          for (int k0 = sh.kb0; k0 < sh.kb1 && ok; k0 += chunk, ++cc) {
+            const int k1 = k0 + chunk < sh.kb1 ? k0 + chunk : sh.kb1;
             const uint32_t acc = tmem + (cc & 1u) * BN;
             if (!bar_wait(tempty + 8 * (cc & 1u), (cc >> 1 & 1u) ^ 1u)) {
               ok = false;
@@ -1003,7 +1022,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         for (int k = 0; k < BN / 2; ++k) acc[k] = 0.f;
         for (int ps = 0; ps < sh.n_pass; ++ps) {
           const float scale = sh.scale(ps);
-          for (int k0 = sh.kb0; k0 < sh.kb1; k0 += sh.chunk) {
+          const int chunk = sh.chunk(ps);
+          for (int k0 = sh.kb0; k0 < sh.kb1; k0 += chunk) {
             if (!wait_sums()) {
               ++cc;
               continue;
