@@ -305,13 +305,14 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   }
 
   // dz: dy itself where it can be; else planes of dy act'(z).  GELU's and SiLU's slopes are not
-  // 16-bit numbers: a binary32 gradient sums 22 (binary16) or 24 (bfloat16) bits of dz.  16-bit results
-  // take dz rounded to 16 bits, as they are rounded themselves; where one round of the SMs does all of
-  // them, launches and not products are what costs, and they take two planes.
+  // 16-bit numbers: a binary32 gradient sums 22 (binary16) or 24 (bfloat16) bits of dz, a binary16
+  // gradient of a bfloat16 layer 16.  Results of the layer's own type take dz rounded to it, as they are
+  // rounded themselves; where one round of the SMs does all of them, launches and not products are what
+  // costs, and they take two planes.
   const bool curved = h->act == ddl::kActGelu || h->act == ddl::kActSilu;
   const bool f16 = h->type == ddl::kF16;
   const int planes16 = curved && dx_tiles + dw_tiles <= h->sms ? 2 : 1;
-  const int dw_planes = !dw ? 0 : grad_dtype == DDL_FP32 && curved ? (f16 ? 2 : 3) : planes16;
+  const int dw_planes = !dw ? 0 : !curved ? 1 : grad_dtype == DDL_FP32 ? (f16 ? 2 : 3) : f16 ? planes16 : 2;
   const int dx_planes = dx ? planes16 : 0;
   const bool own_dz = (dx || dw) && (has_z || !mdy.tma());
   const int n_planes = own_dz ? std::max(dw_planes, dx_planes) : 0;

@@ -428,3 +428,17 @@ def test_activations_of_every_number(ddl, dtype, n_out):
         assert torch.equal(torch.isinf(got), torch.isinf(want))
         ok = torch.isfinite(want)
         _within(got[ok], want[ok], 2.0 ** -20 * z64[ok, 0].abs() + U[dtype] * want[ok].abs() + TINY[dtype])
+
+
+@pytest.mark.parametrize("tokens, n_in, n_out", [(3, 2240, 5568), (517, 771, 1029), (1834, 1152, 448)])
+def test_binary16_gradient_of_a_bfloat16_layer(ddl, tokens, n_in, n_out):
+    """Its 11 bits are not lost to a bfloat16 dz: at most the result's own rounding (2^-11 of each element) and as
+    much again for the 16 bits of dz and the sum."""
+    dy, x, z = _normal(1, tokens, n_out, "bf16"), _normal(2, tokens, n_in, "bf16"), _normal(4, tokens, n_out, "bf16")
+    dw = _blank(n_out, n_in, "f16")[0]
+    for act in ("gelu", "silu"):
+        with ddl.Linear(n_in, n_out, tokens, "bf16", act) as layer:
+            layer.backward(dy, x, z=z, dw=dw)
+            layer.check()
+        want = (dy.double() * _slope(z.double(), act)).t() @ x.double()
+        assert (dw.double() - want).norm() <= 2.0 ** -10 * want.norm()
