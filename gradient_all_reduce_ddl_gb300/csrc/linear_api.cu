@@ -402,6 +402,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
       P.b[k] = 3;
       P.scale[k] = ddl::plane_scale(h->type, maps, k);
     }
+    // 8 blocks: a one-sign sum ends 9e-7 off, and 4e-7 with 4 blocks, which take 2 to 10 % more time
     P.chunk[0] = P.chunk[1] = grad_dtype == DDL_FP32 ? 8 : (int32_t)std::min(kLongChunk, blocks_of(T, ddl::kBlockK));
     if (grad_dtype == DDL_FP32) P.chunk[1] = 32;  // the sums of lower planes are small
     P.epi = ddl::kEpiStore;
