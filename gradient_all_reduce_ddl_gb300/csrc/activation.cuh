@@ -36,27 +36,6 @@ __device__ __forceinline__ uint32_t to16x2(float x, float y, int type) {
   return u;
 }
 
-// The normal distribution function Phi(z), and in *e exp(-z^2 / 2), without branches:
-// Phi(-|z|) = exp(-z^2 / 2) t Q(t) with t = 1 / (1 + 0.4 |z| / sqrt 2), the form of Abramowitz & Stegun 7.1.26
-// with Q of degree 8 fitted to erfcx for |z| <= 14 (Lawson's minimax iteration; relative error 6e-8, 2.2e-7
-// absolute in binary32 arithmetic).
-__device__ __forceinline__ float normal_cdf(float z, float* e) {
-  const float x = fabsf(z) * 0.70710678118654752f;
-  const float t = __fdividef(1.f, 1.f + 0.4f * x);
-  float q = 0.0206265207f;
-  q = q * t + -0.0701596215f;
-  q = q * t + 0.0419936478f;
-  q = q * t + 0.0439821631f;
-  q = q * t + 0.0398782492f;
-  q = q * t + 0.0966966003f;
-  q = q * t + 0.100943796f;
-  q = q * t + 0.113221556f;
-  q = q * t + 0.112817116f;
-  *e = __expf(-x * x);
-  const float tail = q * t * *e;
-  return z < 0.f ? tail : 1.f - tail;
-}
-
 // Two binary32 numbers in one register pair: half the instructions of what bounds an epilogue.
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
   uint64_t d;
@@ -138,6 +117,27 @@ __device__ __forceinline__ void activate(float (&v)[N], int act) {
   }
 }
 
+// The normal distribution function Phi(z), and in *e exp(-z^2 / 2), without branches:
+// Phi(-|z|) = exp(-z^2 / 2) t Q(t) with t = 1 / (1 + 0.4 |z| / sqrt 2), the form of Abramowitz & Stegun 7.1.26
+// with Q of degree 8 fitted to erfcx for |z| <= 14 (Lawson's minimax iteration; relative error 6e-8, 2.2e-7
+// absolute in binary32 arithmetic).
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+  const float x = fabsf(z) * 0.70710678118654752f;
+  const float t = rcp_fast(1.f + 0.4f * x);
+  float q = 0.0206265207f;
+  q = q * t + -0.0701596215f;
+  q = q * t + 0.0419936478f;
+  q = q * t + 0.0439821631f;
+  q = q * t + 0.0398782492f;
+  q = q * t + 0.0966966003f;
+  q = q * t + 0.100943796f;
+  q = q * t + 0.113221556f;
+  q = q * t + 0.112817116f;
+  *e = exp2_fast(z * z * -0.72134752044448170f);  // -log2(e) / 2
+  const float tail = q * t * *e;
+  return z < 0.f ? tail : 1.f - tail;
+}
+
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
     case kActRelu: return z > 0.f ? 1.f : 0.f;
@@ -147,7 +147,7 @@ __device__ __forceinline__ float act_slope(float z, int act) {
       return phi + z * (e * 0.39894228040143268f);
     }
     case kActSilu: {
-      const float s = __fdividef(1.f, 1.f + __expf(-z));
+      const float s = rcp_fast(1.f + exp2_fast(-1.4426950408889634f * z));
       return s + z * (s * (1.f - s));
     }
     default: return 1.f;
