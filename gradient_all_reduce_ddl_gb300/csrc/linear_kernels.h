@@ -9,8 +9,8 @@ namespace ddl {
 
 constexpr int kDzCols = 256;  // what a CTA makes of dz: columns, and rows by the number of them
 // Few rows: 16 a CTA, whose row loop bounds a small pass; more: 64, which leaves fewer sums to add at the end.  Column
-// sums of a GELU layer's dz, 16 against 64 rows: 1024 x 128 6.7 and 7.8 us, 1024 x 4096 12.0 and 13.9, 2048 x 128 9.5
-// and 8.5, 2048 x 4096 20.2 and 15.6, 8192 x 8192 139 and 91.
+// sums of a GELU layer's dz, 16 against 64 rows: 1024 x 128 6.5 and 7.8 us, 1024 x 4096 11.4 and 12.4, 2048 x 128 9.2
+// and 8.0, 2048 x 4096 19.0 and 13.8, 8192 x 8192 126 and 78.
 constexpr int64_t kDzFewRows = 1024;
 inline int64_t dz_rows(int64_t rows) { return rows > kDzFewRows ? 64 : 16; }
 // The most row blocks of a pass over up to `most` rows, for the workspace of their sums.

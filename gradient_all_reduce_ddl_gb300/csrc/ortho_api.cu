@@ -107,7 +107,7 @@ int64_t blocks_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
 // 0.3 to 1.2 times that (1.5 for the longest of the smallest matrices).  One block instead of eight throughout costs
 // 15 % of four 1024 x 4096, this 2 %.
 int chunk_of(int stage, uint64_t s) {
-  if (stage == kPoly) return s <= 1024 ? 1 : 2;
+  if (stage == kPoly) return s <= 640 ? 1 : 2;
   if (stage == kGram0 || stage == kGram1) return s <= 128 ? 1 : 4;
   return 8;
 }

@@ -36,7 +36,9 @@
 //
 // A long contraction with few tiles is split over the CTAs of a cluster; each
 // leaves its sums in shared memory and the cluster's CTAs add them in rank order
-// through distributed shared memory, so results do not depend on timing.
+// through distributed shared memory, so results do not depend on timing.  In
+// grouped launches a long tile may instead be cut into parts of several workers,
+// which are added through memory by the one that comes last.
 //
 // Every wait is bounded.  One that runs out sets kErrProductWait; the CTA then
 // waits (bounded too) for its own loads and products, frees its TMEM and ends.
@@ -53,7 +55,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;  // warps 2 and 3 only fill the first warpgroup
+constexpr int kThreads = 384;  // warp 3 only fills the first warpgroup
 constexpr int kEpiWarps = 8;
 constexpr int kBoxBytes = kBoxRows * kBlockK * 2;
 constexpr int kABytes = kTileM * kBlockK * 2;
