@@ -275,3 +275,20 @@ def test_refuses_host_memory_and_failed_allocation(ddl, monkeypatch):
         o.run(g.view(-1), out.view(-1))
         o.check()
     _check(out, g, "f32")
+
+
+@pytest.mark.parametrize("rows, cols", [(48, 507), (192, 3265), (256, 832), (1287, 384), (536, 1335), (768, 768), (1024, 3400)])
+def test_no_less_exact_than_binary32(ddl, rows, cols):
+    """22-bit operands and sums that are promoted in time: over several inputs no more than one and a half times a
+    binary32 evaluation's error, and 2^-21 for the operands' and the result's own last bits."""
+    own = plain = 0.0
+    with ddl.Ortho([(0, rows, cols)]) as o:
+        for seed in range(4):
+            g = _gradient(rows, cols, seed)
+            got = torch.empty_like(g)
+            o.run(g.view(-1), got.view(-1))
+            want = _newton_schulz(g.double())
+            own += float((got.double() - want).norm() / want.norm())
+            plain += float((_newton_schulz(g).double() - want).norm() / want.norm())
+        o.check()
+    assert own <= 1.5 * plain + 4 * 2.0 ** -21, (own / 4, plain / 4)
