@@ -429,9 +429,8 @@ ddl_status_t ddl_linear_forward(ddl_linear_t layer, size_t tokens, const void* x
  * bias gradient and copies of unaligned operands, as far as there are any.
  * Repeated calls give the same bits.
  * Rounding: binary32 gradients sum dz to 22 bits (DDL_FP16) or 24 bits
- * (DDL_BF16), binary16 gradients of DDL_BF16 layers to 16 bits; dx and other
- * binary16 gradients sum dz rounded to the layer's type, or twice its bits in
- * small calls (exact for DDL_ACT_NONE and DDL_ACT_RELU). */
+ * (DDL_BF16), dx and binary16 gradients to 22 or 16 bits, whatever the number
+ * of tokens (exact for DDL_ACT_NONE and DDL_ACT_RELU). */
 ddl_status_t ddl_linear_backward(ddl_linear_t layer, size_t tokens, const void* dy, size_t ldy, const void* x,
                                  size_t ldx, const void* w, size_t ldw, const void* z, size_t ldz, void* dx, size_t lddx,
                                  void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate, void* stream);

@@ -442,3 +442,68 @@ def test_binary16_gradient_of_a_bfloat16_layer(ddl, tokens, n_in, n_out):
             layer.check()
         want = (dy.double() * _slope(z.double(), act)).t() @ x.double()
         assert (dw.double() - want).norm() <= 2.0 ** -10 * want.norm()
+
+
+def _close_to_rounding(got, want, dtype, off):
+    """In the Frobenius norm: the exact values' own rounding to the type (5 % for the sample), and `off` before it."""
+    assert torch.isfinite(got.double()).all()
+    rounding = (want.to(TYPES[dtype]).double() - want).norm()
+    err = (got.double() - want).norm()
+    assert err <= 1.05 * rounding + off, f"off by {err / want.norm():.2e}, rounding is {rounding / want.norm():.2e}"
+
+
+@pytest.mark.parametrize("grad", ["f16", "f32"])
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+@pytest.mark.parametrize("scale", [1.0, 1e-4, 1e-5, 1e-6])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_dz_keeps_its_bits_in_large_calls(ddl, dtype, scale, act, grad):
+    """More tiles than SMs, gradients of any size: dx and binary16 dw are off by their own rounding, not by dz's.  Before
+    it: dz to 2^-21 of itself and 2^-34 (binary16) or 2^-16 (bfloat16), the slope's 2^-20 of up to 1.2 |dy|, both as if they
+    added up; and a sum's additions of 16 products at 2^-22 of the result each (its partial sums grow up to it)."""
+    T, K, N = 8192, 1024, 256
+    dy, x = _normal(1, T, N, dtype, scale), _normal(2, T, K, dtype)
+    w, z = _normal(3, N, K, dtype), _normal(4, T, N, dtype)
+    dx, dw = _blank(T, K, dtype)[0], _blank(N, K, grad)[0]
+    with ddl.Linear(K, N, T, dtype, act) as layer:
+        layer.backward(dy, x, w, z=z, dx=dx, dw=dw)
+        layer.check()
+    dz = dy.double() * _slope(z.double(), act)
+    kept = (2.0 ** -21 * dz.abs() + 2.0 ** -34) if dtype == "f16" else 2.0 ** -16 * dz.abs()
+    kept = kept + 2.0 ** -20 * 1.2 * dy.double().abs()
+    want = dz @ w.double()
+    _close_to_rounding(dx, want, dtype, (kept @ w.double().abs()).norm() + (N / 16 + 16) * 2.0 ** -22 * want.norm())
+    if grad == "f16":
+        want = dz.t() @ x.double()
+        _close_to_rounding(dw, want, grad, (kept.t() @ x.double().abs()).norm() + (T / 16 + 16) * 2.0 ** -22 * want.norm())
+
+
+@pytest.mark.parametrize("grad", ["f16", "f32"])
+def test_largest_gradients_in_large_calls(ddl, grad):
+    """dz above binary16's largest number (65504 times a slope of 1.13) with finite dx and dw, more tiles than SMs."""
+    T, K, N = 8192, 1024, 256
+    dy, x, w, z = _normal(1, T, N, "f16"), _normal(2, T, K, "f16"), _normal(3, N, K, "f16", 1e-2), _normal(4, T, N, "f16")
+    dy[77, 5], z[77, 5] = 65504.0, 1.5
+    x[77] *= 0.01
+    dx, dw = _blank(T, K, "f16")[0], _blank(N, K, grad)[0]
+    with ddl.Linear(K, N, T, "f16", "gelu") as layer:
+        layer.backward(dy, x, w, z=z, dx=dx, dw=dw)
+        layer.check()
+    dz = dy.double() * _slope(z.double(), "gelu")
+    for got, want in ((dx, dz @ w.double()), (dw, dz.t() @ x.double())):
+        assert torch.isfinite(got).all()
+        assert (got.double() - want).norm() <= 2.0 ** -10 * want.norm()
+
+
+@pytest.mark.parametrize("dtype, grad", [("f16", "f16"), ("f16", "f32"), ("bf16", "f16"), ("bf16", "f32")])
+def test_fewer_tokens_need_no_more_memory(ddl, monkeypatch, dtype, grad):
+    """What a handle's largest call has allocated is enough for its smaller ones (a stream capture could not allocate)."""
+    K = N = 1024
+    with ddl.Linear(K, N, 8192, dtype, "gelu") as layer:
+        for tokens in (8192, 1024, 64, 1):
+            dy, x, z = _normal(1, tokens, N, dtype), _normal(2, tokens, K, dtype), _normal(4, tokens, N, dtype)
+            w, dx = _normal(3, N, K, dtype, 0.1), _blank(tokens, K, dtype)[0]
+            dw, db = _blank(N, K, grad)[0], _blank(1, N, grad)[0]
+            layer.backward(dy, x, w, z=z, dx=dx, dw=dw, db=db[0])
+            layer.check()
+            monkeypatch.setenv("DDL_INJECT_ALLOC_FAILURE", "1")
+        monkeypatch.delenv("DDL_INJECT_ALLOC_FAILURE")
