@@ -507,3 +507,26 @@ def test_fewer_tokens_need_no_more_memory(ddl, monkeypatch, dtype, grad):
             layer.check()
             monkeypatch.setenv("DDL_INJECT_ALLOC_FAILURE", "1")
         monkeypatch.delenv("DDL_INJECT_ALLOC_FAILURE")
+
+
+@pytest.mark.parametrize("tokens", [90, 3000])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_infinite_operands_of_split_products(ddl, dtype, tokens):
+    """An infinity or NaN in x or w goes where the formula puts it, whatever the lower planes of dz are."""
+    K, N = 136, 200
+    dy, x = _normal(1, tokens, N, dtype), _normal(2, tokens, K, dtype)
+    w, z = _normal(3, N, K, dtype), _normal(4, tokens, N, dtype)
+    x[3, 5], x[60, 40], x[61, 41] = math.inf, -math.inf, math.nan
+    w[7, 9], w[199, 135] = math.inf, -math.inf
+    for act in ("gelu", "silu"):
+        dz = dy.double() * _slope(z.double(), act)
+        for grad in ("f32", "f16"):
+            dx, dw = _blank(tokens, K, dtype)[0], _blank(N, K, grad)[0]
+            with ddl.Linear(K, N, tokens, dtype, act) as layer:
+                layer.backward(dy, x, w, z=z, dx=dx, dw=dw)
+                layer.check()
+            for got, want in ((dx, dz @ w.double()), (dw, dz.t() @ x.double())):
+                assert int((~torch.isfinite(want)).sum()) >= 2 * want.shape[0]
+                assert torch.equal(torch.isnan(got), torch.isnan(want))
+                assert torch.equal(torch.isinf(got), torch.isinf(want))
+                assert torch.equal(got[torch.isinf(got)].sign(), want[torch.isinf(want)].to(got.dtype).sign())
