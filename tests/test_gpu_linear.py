@@ -530,3 +530,26 @@ def test_infinite_operands_of_split_products(ddl, dtype, tokens):
                 assert torch.equal(torch.isnan(got), torch.isnan(want))
                 assert torch.equal(torch.isinf(got), torch.isinf(want))
                 assert torch.equal(got[torch.isinf(got)].sign(), want[torch.isinf(want)].to(got.dtype).sign())
+
+
+@pytest.mark.parametrize("act", ["none", "relu"])
+@pytest.mark.parametrize("tokens, n_in, n_out, dtype", [
+    (64, 200, 136, "f16"), (128, 3759, 72, "bf16"), (256, 2624, 64, "bf16"), (384, 2944, 512, "f16"), (442, 64, 192, "f16"),
+    (512, 2304, 6877, "bf16"), (562, 320, 987, "bf16"), (832, 128, 121, "bf16"), (860, 128, 256, "f16"), (1728, 122, 576, "f16"),
+    (2560, 974, 64, "f16"), (5696, 79, 192, "bf16"), (8192, 1024, 1024, "bf16"), (20000, 136, 264, "f16"),
+])
+def test_binary32_dw_is_no_less_exact_than_binary32(ddl, tokens, n_in, n_out, dtype, act):
+    """dz is exact here, so dw's error is the sum's: over several inputs no more than one and a half times what products
+    in binary32 leave, and half a unit in the last place for the result."""
+    own = plain = 0.0
+    with ddl.Linear(n_in, n_out, tokens, dtype, act) as layer:
+        for seed in range(3):
+            dy, x, z = (_normal(10 * seed + k, tokens, n, dtype) for k, n in ((1, n_out), (2, n_in), (3, n_out)))
+            dw = _blank(n_out, n_in, "f32")[0]
+            layer.backward(dy, x, z=None if act == "none" else z, dw=dw)
+            dz = dy if act == "none" else torch.where(z > 0, dy, torch.zeros_like(dy))
+            want = dz.double().t() @ x.double()
+            own += float((dw.double() - want).norm() / want.norm())
+            plain += float((dz.float().t() @ x.float() - want).norm() / want.norm())
+        layer.check()
+    assert own <= 1.5 * plain + 3 * 2.0 ** -24, (own / 3, plain / 3)
