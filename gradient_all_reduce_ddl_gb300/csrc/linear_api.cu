@@ -37,8 +37,10 @@ using ddl::Range;
 constexpr int64_t kMaxFeatures = 1 << 22;
 // Longest sums over tokens: a tile's takes 2^20 blocks x 3 planes x 0.35 us, about half of what a kernel's waits allow.
 constexpr int64_t kMaxTokens = 1 << 26;
-// K blocks that stay in the tensor core's accumulator for 16-bit results.
-constexpr int64_t kLongChunk = 4096;
+// K blocks that stay in the tensor core's truncating accumulator for 16-bit results.  Each of a block's four additions
+// loses up to half a unit in the last place of the partial sum, 2^-24 of it: 256 blocks 2^-14 of a sum of one sign, a quarter
+// of binary16's half unit (2^-12 at least), 2048 blocks a quarter of bfloat16's.
+int64_t long_chunk(int type) { return type == ddl::kF16 ? 256 : 2048; }
 // K blocks of a binary32 result: what the truncating accumulator loses of a chunk does not average out, while a sum in
 // binary32 loses less the shorter it is.  With these chunks dw's error over the sizes measured (64 to 65,536 tokens,
 // normal inputs, dz exact) is 0.2 to 1.34 times that of products in binary32; with 8 blocks throughout it was up to 5.4
@@ -214,6 +216,12 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
     splits = l.splits;
     tiles = count(tile_n);
   }
+  // a contraction beyond what may stay in the accumulator has a kernel of its own, whose narrowest tile is 64 wide (binary16
+  // with and without chunks: 16 tokens, 524,288 -> 1024 283 and 282 us; 2048, 32,768 -> 4096 with GELU, residual and z 363
+  // and 353)
+  const int64_t chunk = long_chunk(h->type);
+  const bool chunked = blocks_of(steps, splits) > chunk;
+  if (chunked) tile_n = std::max(tile_n, 64);
   for (const void* p : {x, w, bias, residual, (const void*)z, (const void*)y})
     if (p && !ddl::device_pointer(p, h->device)) return DDL_ERR_INVALID_ARG;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -240,7 +248,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   P.a[0] = swap ? 1 : 0;
   P.b[0] = swap ? 0 : 1;
   P.scale[0] = 1.f;
-  P.chunk[0] = P.chunk[1] = (int32_t)steps;
+  P.chunk[0] = P.chunk[1] = (int32_t)(chunked ? chunk : steps);
   P.epi = ddl::kEpiLinear;
   P.swap = swap;
   P.type = h->type;
@@ -257,6 +265,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   L.inl_tiles[0] = (int32_t)tiles;
   L.n_tiles = (int32_t)tiles;
   L.splits = splits;
+  L.chunked = chunked;
   L.err = h->d_err;
   P.in0 = P.in1 = P.out0 = P.out1 = -1;
   // rows that TMA can address, of whole 16-byte pieces, let the epilogue move whole boxes
@@ -409,7 +418,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
       P.b[k] = 3;
       P.scale[k] = ddl::plane_scale(h->type, maps, k);
     }
-    P.chunk[0] = P.chunk[1] = grad_dtype == DDL_FP32 ? f32_chunk(T) : (int32_t)std::min(kLongChunk, blocks_of(T, ddl::kBlockK));
+    P.chunk[0] = P.chunk[1] = grad_dtype == DDL_FP32 ? f32_chunk(T) : (int32_t)long_chunk(ddl::kF16);
     if (grad_dtype == DDL_FP32) P.chunk[1] = 32;  // the sums of lower planes are small
     P.epi = ddl::kEpiStore;
     P.out_type = grad_dtype == DDL_FP32 ? ddl::kF32 : ddl::kF16;
@@ -434,7 +443,7 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
       P.b[k] = 4;
       P.scale[k] = ddl::plane_scale(h->type, maps, k);
     }
-    P.chunk[0] = P.chunk[1] = (int32_t)std::min(kLongChunk, blocks_of(N, ddl::kBlockK));
+    P.chunk[0] = P.chunk[1] = (int32_t)long_chunk(h->type);
     P.epi = ddl::kEpiStore;
     P.out_type = h->type;
     P.vec = mdx.vec4(2);

@@ -96,6 +96,7 @@ struct ProductLaunch {
   int32_t splits;           // CTAs of a cluster that share a tile's contraction
   int32_t boxes;            // single launches, tiles of 128 or 256 columns, splits 1: the epilogue moves boxes by TMA (in0
                             // ... out1); grouped ones with splits 1 always do
+  int32_t chunked;          // kEpiLinear: the contraction is longer than its chunk (tiles of 64 columns or more)
   int32_t bf16;             // operands are bfloat16, else binary16
   uint32_t* err;
   float ca, cb, cc;         // Newton-Schulz coefficients

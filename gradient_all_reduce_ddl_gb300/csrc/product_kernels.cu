@@ -31,8 +31,9 @@
 // half a unit in the last place of each of its K/16 additions.  Results kept in
 // binary32 therefore leave the accumulator every `chunk` K blocks and are added
 // in registers with rounding to nearest (the first pass's; the sums of lower planes
-// are 2^-8 or 2^-11 of those and may stay longer); 16-bit results sum all of K in
-// TMEM.
+// are 2^-8 or 2^-11 of those and may stay longer).  16-bit results may stay much
+// longer; the forward kernel takes its sums straight from TMEM, and contractions that
+// need chunks have a kernel of their own.
 //
 // A long contraction with few tiles is split over the CTAs of a cluster; each
 // leaves its sums in shared memory and the cluster's CTAs add them in rank order
@@ -64,7 +65,8 @@ constexpr int kABytes = kTileM * kBlockK * 2;
 
 // What a launch is for; each has its own epilogues (and registers: one that spilled would go to L2 for it, since shared
 // memory leaves no L1).
-enum : int { kForward, kBackward, kSteps };
+enum : int { kForward, kBackward, kSteps, kForwardLong };
+__host__ __device__ constexpr bool is_forward(int mode) { return mode == kForward || mode == kForwardLong; }
 
 // Per CTA: a pair (tile_n 256) splits both operands' rows between its CTAs.
 __host__ __device__ constexpr int b_rows(int bn) { return bn == 256 ? 128 : bn; }
@@ -191,7 +193,7 @@ __device__ __forceinline__ void emit_linear(const Product& P, const int (&m)[R],
 // Every load of the R rows is issued before the first is used.
 template <int V, int R, int MODE>
 __device__ __forceinline__ void emit(const Product& P, const int (&m)[R], const bool (&in)[R], int n, float (&v)[R][V]) {
-  if constexpr (MODE == kForward) {
+  if constexpr (is_forward(MODE)) {
     // one branch on the type and one on the activation for all R x V values
     if (P.type == kBF16)
       emit_linear<V, R, kBF16>(P, m, in, n, v);
@@ -568,7 +570,7 @@ __device__ __forceinline__ void slab_values(const Product& P, const ProductLaunc
         store_mirror8(P.p_lo, P.ldp, lo[g], row0 + row, P.M, n0 + 8 * g, P.N, row & 31);
       }
     }
-  } else if constexpr (MODE == kForward) {
+  } else if constexpr (is_forward(MODE)) {
     if (P.type == kBF16)
       slab_linear_act<kBF16>(P, v, bias, buf, row, half);
     else
@@ -704,7 +706,7 @@ struct Slabs {
     if (t >= end) return;
     const Place pl = place<BN, MODE>(p, t, step);
     row0 = pl.row0, col0 = pl.col0, following = pl.next;
-    const Product& P = MODE == kForward ? p.inl[0] : *pl.P;
+    const Product& P = is_forward(MODE) ? p.inl[0] : *pl.P;
     in0 = P.in0, in1 = P.in1, out0 = P.out0, out1 = P.out1;
     f32 = MODE == kBackward && P.out_type == kF32;
     rows = P.M;
@@ -827,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
               bar_expect(bar, stage_bytes(BN));
             }
 #pragma unroll
-            for (int h = 0; h < (MODE == kForward ? 1 : kTileM / kBoxRows); ++h) {
+            for (int h = 0; h < (is_forward(MODE) ? 1 : kTileM / kBoxRows); ++h) {
               const int row = pl.row0 + my_rows + h * kBoxRows;
               const int x = sh.a_mn ? row : kb * kBlockK, y = sh.a_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
@@ -836,7 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 tma_box(sa + h * kBoxBytes, ma, bar, x, y);
             }
 #pragma unroll
-            for (int h = 0; h < (MODE == kForward ? 1 : (b_rows(BN) + kBoxRows - 1) / kBoxRows); ++h) {
+            for (int h = 0; h < (is_forward(MODE) ? 1 : (b_rows(BN) + kBoxRows - 1) / kBoxRows); ++h) {
               const int row = pl.col0 + my_rows + h * kBoxRows;
               const int x = sh.b_mn ? row : kb * kBlockK, y = sh.b_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
@@ -970,7 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first, next; t < end; t = next) {
       const Place pl = place<BN, MODE>(p, t, step);
       next = pl.next;
-      const Product& G = MODE == kForward ? p.inl[0] : *pl.P;
+      const Product& G = is_forward(MODE) ? p.inl[0] : *pl.P;
       const Shape sh(G, pl.k0, pl.k1, q, S);
       if (t == first) griddep_wait();
       // what the epilogue reads from HBM comes to L2 while the products run
@@ -980,7 +982,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           if (m < G.M) {
             const char* from = nullptr;
             int bytes = 2;
-            if (MODE == kForward && G.add)
+            if (is_forward(MODE) && G.add)
               from = static_cast<const char*>(G.add) + ((int64_t)m * G.ld_add + pl.col0) * 2;
             else if (MODE == kBackward && G.accumulate) {
               bytes = G.out_type == kF32 ? 4 : 2;
@@ -995,8 +997,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
       }
       // in registers (no indexed access); a forward launch's only product is read as a parameter
-      const Product copy = MODE == kForward ? Product{} : G;
-      const Product& P = MODE == kForward ? p.inl[0] : copy;
+      const Product copy = is_forward(MODE) ? Product{} : G;
+      const Product& P = is_forward(MODE) ? p.inl[0] : copy;
       const uint32_t lanes = (uint32_t)(quad * 32) << 16;
       // The sums of this thread's 16 columns of the slabs in turn: from TMEM, or added up in registers chunk by chunk.
       float acc[DIRECT ? kHalf : BN / 2];
@@ -1131,12 +1133,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (boxes) {
         if constexpr (BN >= 128) {
           uint4 bias_ahead[2] = {};
-          if constexpr (MODE == kForward) load_bias(P, pl.col0 + half * kHalf, bias_ahead);
+          if constexpr (is_forward(MODE)) load_bias(P, pl.col0 + half * kHalf, bias_ahead);
 #pragma unroll 1
           for (int sl = 0; sl < kSlabs && pl.col0 + sl * kSlab < P.N; ++sl, use.next<kBufs>()) {  // one copy of the code:
             // it has to stay in the instruction cache
             uint4 bias[2] = {bias_ahead[0], bias_ahead[1]};
-            if (MODE == kForward && sl + 1 < kSlabs) load_bias(P, pl.col0 + (sl + 1) * kSlab + half * kHalf, bias_ahead);
+            if (is_forward(MODE) && sl + 1 < kSlabs) load_bias(P, pl.col0 + (sl + 1) * kSlab + half * kHalf, bias_ahead);
             if (ok && !bar_wait(ready + 8 * use.s, use.phase)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
@@ -1318,6 +1320,10 @@ cudaError_t launch_product(const ProductLaunch& p, int tile_n, int sms, cudaStre
   if (p.g_products) return tile_n == 256 ? launch_one<256, kSteps>(p, sms, stream) : launch_one<128, kSteps>(p, sms, stream);
   if (p.inl[0].epi == kEpiStore)
     return tile_n == 256 ? launch_one<256, kBackward>(p, sms, stream) : launch_one<128, kBackward>(p, sms, stream);
+  if (p.chunked) {
+    if (tile_n == 256) return launch_one<256, kForwardLong>(p, sms, stream);
+    return tile_n == 128 ? launch_one<128, kForwardLong>(p, sms, stream) : launch_one<64, kForwardLong>(p, sms, stream);
+  }
   if (tile_n == 256) return launch_one<256, kForward>(p, sms, stream);
   if (tile_n == 128) return launch_one<128, kForward>(p, sms, stream);
   return tile_n == 64 ? launch_one<64, kForward>(p, sms, stream) : launch_one<32, kForward>(p, sms, stream);

@@ -386,7 +386,8 @@ ddl_status_t ddl_selftest_wait_timeout(ddl_plan_t plan, uint32_t limit_us, void*
  * dy tokens x out_features, all of the handle's 16-bit type (DDL_FP16 or
  * DDL_BF16), rows at a stride of ld elements (ld >= columns, at most 2^31), at
  * any 2-byte address (column blocks of one wider buffer among them); bias has out_features elements of that type.  Sums run in
- * binary32 and are rounded once.  Rows that do not start at 16-byte boundaries
+ * binary32 and are rounded once; the tensor core truncates its additions, which costs a 16-bit result of one-sign terms at
+ * most a quarter of its half unit.  Rows that do not start at 16-byte boundaries
  * (base and stride) are copied to the handle's workspace first; results do not
  * change.
  *

@@ -553,3 +553,54 @@ def test_binary32_dw_is_no_less_exact_than_binary32(ddl, tokens, n_in, n_out, dt
             plain += float((dz.float().t() @ x.float() - want).norm() / want.norm())
         layer.check()
     assert own <= 1.5 * plain + 3 * 2.0 ** -24, (own / 3, plain / 3)
+
+
+def _one_sign(seed, rows, cols, dtype, top):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    return ((0.5 + 0.5 * torch.rand(rows, cols, generator=gen, device="cuda")) * top).to(TYPES[dtype])
+
+
+def _sums_in_64(a, b):
+    """a b^T of long rows, in pieces."""
+    return sum(p.double() @ q.double().t() for p, q in zip(a.split(1 << 17, 1), b.split(1 << 17, 1)))
+
+
+LONG = [(3, 1 << 22, 16), (40, 1 << 21, 136), (100, 1 << 19, 136), (300, 1 << 18, 520), (2304, 20001, 2312)]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("rows, long, cols", LONG)
+def test_long_sums_of_one_sign(ddl, rows, long, cols, dtype):
+    """Forward, dx and binary16 dw over the longest contractions: besides its rounding, a result may lose a quarter of half a
+    unit in the last place to its sum (and a twentieth to the sums of its parts)."""
+    bound = 1.3 * U[dtype]
+    top = 16.0 / long  # sums of about ten
+    a, b = _one_sign(1, rows, long, dtype, 1.0), _one_sign(2, cols, long, dtype, 2.0 ** 12 * top if dtype == "f16" else top)
+    want = _sums_in_64(a, b)
+    y, clean = _blank(rows, cols, dtype)
+    z, _ = _blank(rows, cols, dtype)
+    r = _one_sign(3, rows, cols, dtype, 1.0)
+    with ddl.Linear(long, cols, rows, dtype, "none") as layer:
+        layer.forward(a, b, y)
+        layer.check()
+        _within(y, want, bound * want)
+        assert clean()
+    with ddl.Linear(long, cols, rows, dtype, "relu") as layer:
+        layer.forward(a, b, y, residual=r, z=z)
+        layer.check()
+        _within(z, want, bound * want)
+        _within(y, want + r.double(), bound * (want + r.double()))
+    # dx[rows][cols] = dy[rows][long] w[long][cols]
+    w = b.t().contiguous()
+    dx, clean = _blank(rows, cols, dtype)
+    with ddl.Linear(cols, long, rows, dtype, "none") as layer:
+        layer.backward(a, w=w, dx=dx)
+        layer.check()
+    _within(dx, want, bound * want)
+    assert clean()
+    # dw[rows][cols] = dy[long][rows]^T x[long][cols], in binary16 (bfloat16 layers too)
+    dy, dw = a.t().contiguous(), _blank(rows, cols, "f16")[0]
+    with ddl.Linear(cols, rows, long, dtype, "none") as layer:
+        layer.backward(dy, w, dw=dw)
+        layer.check()
+    _within(dw, want, 1.3 * U["f16"] * want)
