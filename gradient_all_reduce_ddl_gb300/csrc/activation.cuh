@@ -138,9 +138,9 @@ __device__ __forceinline__ float normal_cdf(float z, float* e) {
   return z < 0.f ? tail : 1.f - tail;
 }
 
+// The slopes that dy is multiplied by (ReLU's selects instead).
 __device__ __forceinline__ float act_slope(float z, int act) {
   switch (act) {
-    case kActRelu: return z > 0.f ? 1.f : 0.f;
     case kActGelu: {
       float e;
       const float phi = normal_cdf(z, &e);

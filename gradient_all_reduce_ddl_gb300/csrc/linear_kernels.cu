@@ -88,7 +88,10 @@ __device__ __forceinline__ void dz_rows(const LinearPrep& p, int64_t r0, int64_t
     uint32_t out[4][kMaxPlanes];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if (ACT != kActNone) {
+      if (ACT == kActRelu) {  // a closed unit passes nothing on, whatever dy is
+        v[2 * j] = z[2 * j] > 0.f ? v[2 * j] : 0.f;
+        v[2 * j + 1] = z[2 * j + 1] > 0.f ? v[2 * j + 1] : 0.f;
+      } else if (ACT != kActNone) {
         v[2 * j] *= act_slope(z[2 * j], ACT);
         v[2 * j + 1] *= act_slope(z[2 * j + 1], ACT);
       }

@@ -400,7 +400,7 @@ ddl_status_t ddl_selftest_wait_timeout(ddl_plan_t plan, uint32_t limit_us, void*
 
 typedef enum {
   DDL_ACT_NONE = 0,
-  DDL_ACT_RELU = 1,  /* max(z, 0); slope 0 at 0 */
+  DDL_ACT_RELU = 1,  /* max(z, 0); where z <= 0 dz is 0, whatever dy is */
   DDL_ACT_GELU = 2,  /* z Phi(z), Phi the normal distribution function (no tanh approximation) */
   DDL_ACT_SILU = 3   /* z / (1 + exp(-z)) */
 } ddl_act_t;

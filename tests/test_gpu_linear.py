@@ -604,3 +604,26 @@ def test_long_sums_of_one_sign(ddl, rows, long, cols, dtype):
         layer.backward(dy, w, dw=dw)
         layer.check()
     _within(dw, want, 1.3 * U["f16"] * want)
+
+
+@pytest.mark.parametrize("n_out", [40, 37])  # rows that allow vectors, and rows that do not
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_closed_relu_units_pass_nothing_on(ddl, dtype, n_out):
+    """ReLU's slope selects: whatever dy is at a unit with z <= 0, dx, dw and db are what a zero there gives."""
+    T, K = 70, 64
+    dy, x = _normal(1, T, n_out, dtype), _normal(2, T, K, dtype)
+    w, z = _normal(3, n_out, K, dtype, 0.1), _normal(4, T, n_out, dtype)
+    zeros = dy.clone()
+    for t, n, g, at in ((3, 5, math.inf, -1.0), (4, 6, -math.inf, 0.0), (5, 7, math.nan, -0.0), (69, 36, math.inf, -6e4)):
+        dy[t, n], zeros[t, n], z[t, n] = g, 0.0, at
+    got, want = [(_blank(T, K, dtype)[0], _blank(n_out, K, "f32")[0], _blank(1, n_out, "f32")[0][0]) for _ in range(2)]
+    with ddl.Linear(K, n_out, T, dtype, "relu") as layer:
+        for g, (dx, dw, db) in ((dy, got), (zeros, want)):
+            layer.backward(g, x, w, z=z, dx=dx, dw=dw, db=db)
+        layer.check()
+        for a, b in zip(got, want):
+            assert bool(torch.isfinite(b).all()) and torch.equal(a, b)
+        z[3, 5] = 1.0  # an open unit does pass it on
+        layer.backward(dy, z=z, db=got[2])
+        layer.check()
+    assert float(got[2][5]) == math.inf
