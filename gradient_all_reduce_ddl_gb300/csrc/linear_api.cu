@@ -286,8 +286,11 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
                                  const void* w, size_t ldw, const void* z, size_t ldz, void* dx, size_t lddx, void* dw,
                                  size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate, void* stream) {
   if (!h || tokens > (size_t)h->max_tokens || (grad_dtype != DDL_FP32 && grad_dtype != DDL_FP16)) return DDL_ERR_INVALID_ARG;
-  if (!dx && !dw && !db) return DDL_ERR_INVALID_ARG;
   const int64_t T = (int64_t)tokens, K = h->n_in, N = h->n_out;
+  if (!dw && !db) {
+    if (T == 0) return DDL_OK;  // dx, given or not, has no elements
+    if (!dx) return DDL_ERR_INVALID_ARG;
+  }
   const int ge = grad_dtype == DDL_FP32 ? 4 : 2;
   if (T > 0 && (!dy || (dw && !x) || (dx && !w) || (h->act != ddl::kActNone && !z))) return DDL_ERR_INVALID_ARG;
   const bool has_z = h->act != ddl::kActNone;

@@ -422,7 +422,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t layer, size_t tokens, const void* x
                                 size_t ldy, void* stream);
 
 /* dx (layer's type), dw, db (grad_dtype: DDL_FP32 or DDL_FP16): NULL = not
- * wanted, at least one given.  x is read for dw, w for dx, z where the
+ * wanted, at least one given where there are tokens.  x is read for dw, w for dx, z where the
  * activation is not DDL_ACT_NONE; the others may be NULL.  accumulate != 0
  * adds to dw and db (earlier micro-batches); 0 overwrites them; dx is always
  * overwritten.  dw and db need their type's alignment only.  tokens = 0 gives

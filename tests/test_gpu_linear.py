@@ -627,3 +627,11 @@ def test_closed_relu_units_pass_nothing_on(ddl, dtype, n_out):
         layer.backward(dy, z=z, db=got[2])
         layer.check()
     assert float(got[2][5]) == math.inf
+
+
+def test_no_tokens_and_dx_alone(ddl):
+    """An empty batch's dx has no elements, and torch gives it no address."""
+    with ddl.Linear(16, 8, 4, "f16", "gelu") as layer:
+        e = lambda n: torch.empty(0, n, dtype=torch.float16, device="cuda")  # noqa: E731
+        layer.backward(e(8), w=_normal(1, 8, 16, "f16"), z=e(8), dx=e(16))
+        layer.check()

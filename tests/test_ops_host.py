@@ -180,3 +180,9 @@ def test_a_failing_destroy_is_not_repeated(ddl, monkeypatch, kind):
     handle.close()
     del handle
     assert len(calls) == 1
+
+
+def test_linear_backward_of_no_tokens_without_dw_and_db_queues_nothing(ddl):
+    with _layer(ddl) as layer:
+        ddl.ddl_linear_backward(layer.handle, 0, None, 0, None, 0, B, 16, None, 0, None, 0, None, 0, None, ddl.DDL_FP32,
+                                False, 0)
