@@ -190,7 +190,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   for (const Mat* m : {&mx, &mw, &my, &mz, &mr, &mb})
     if (reinterpret_cast<uintptr_t>(m->p) % 2) return DDL_ERR_INVALID_ARG;
   // y may be the residual itself (each element is read before it is written, by the same thread)
-  const bool in_place = residual && residual == y && ldr == ldy;
+  const bool in_place = residual && residual == y && (ldr == ldy || T == 1);  // one row: its stride says nothing
   const Operand outs[2] = {{my, 2}, {mz, 2}}, ins[4] = {{mx, 2}, {mw, 2}, {mb, 2}, {in_place ? Mat{nullptr, 0, 0, 1} : mr, 2}};
   if (!distinct(outs, 2, ins, 4)) return DDL_ERR_INVALID_ARG;
 

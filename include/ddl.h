@@ -415,7 +415,7 @@ ddl_status_t ddl_linear_create(size_t max_tokens, size_t in_features, size_t out
 
 /* bias, residual, z: NULL = absent.  z, if given, receives the
  * pre-activations that ddl_linear_backward reads.  y may be the residual
- * itself (same pointer and stride).  tokens = 0 queues nothing.  One launch,
+ * itself (same pointer and, but for one token, stride).  tokens = 0 queues nothing.  One launch,
  * and one before it where an operand's rows are unaligned. */
 ddl_status_t ddl_linear_forward(ddl_linear_t layer, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
                                 const void* bias, const void* residual, size_t ldr, void* z, size_t ldz, void* y,

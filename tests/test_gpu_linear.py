@@ -635,3 +635,15 @@ def test_no_tokens_and_dx_alone(ddl):
         e = lambda n: torch.empty(0, n, dtype=torch.float16, device="cuda")  # noqa: E731
         layer.backward(e(8), w=_normal(1, 8, 16, "f16"), z=e(8), dx=e(16))
         layer.check()
+
+
+def test_residual_in_place_of_one_row(ddl):
+    """A single row's stride says nothing about where its elements are."""
+    x, w, r = _normal(1, 1, 64, "f16"), _normal(2, 96, 64, "f16", 0.1), _normal(3, 1, 96, "f16")
+    with ddl.Linear(64, 96, 150, "f16", "silu") as layer:
+        apart, _ = _blank(1, 96, "f16")
+        layer.forward(x, w, apart, residual=r)
+        ddl.ddl_linear_forward(layer.handle, 1, x.data_ptr(), 64, w.data_ptr(), 64, None, r.data_ptr(), 96, None, 0,
+                               r.data_ptr(), 104)
+        layer.check()
+    assert torch.equal(apart, r)
