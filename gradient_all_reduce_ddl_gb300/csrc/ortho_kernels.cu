@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(kThreads) norms_kernel(const __grid_constant__
 }
 
 template <int V>
-__device__ __forceinline__ void planes_item(const OrthoPrep& p, const OrthoMatrix& m, const OrthoItem& it, float scale) {
+__device__ __forceinline__ void planes_item(const OrthoPrep& p, const OrthoMatrix& m, const OrthoItem& it, float power,
+                                            float scale) {
   const Walk walk = Walk::of<V>(it);
   for (uint32_t i0 = threadIdx.x; i0 < walk.total; i0 += kThreads * kGroups) {
     int64_t plane[kGroups];
@@ -182,7 +183,7 @@ __device__ __forceinline__ void planes_item(const OrthoPrep& p, const OrthoMatri
 #pragma unroll
       for (int j = 0; j < V; ++j) {
         const float w = !p.mom ? u[k][j] : p.nesterov ? u[k][j] + p.mu * v[k][j] : v[k][j];
-        x[j] = w * scale;
+        x[j] = w * power * scale;
         h[j] = __half2float(__float2half_rn(x[j]));
         l[j] = x[j] - h[j];
       }
@@ -193,7 +194,7 @@ __device__ __forceinline__ void planes_item(const OrthoPrep& p, const OrthoMatri
 }
 
 __global__ void __launch_bounds__(kThreads) planes_kernel(const __grid_constant__ OrthoPrep p) {
-  __shared__ float inv;
+  __shared__ float power, inv;
   const OrthoItem it = p.items[blockIdx.x];  // the handle's tables, written before any launch
   const OrthoMatrix m = p.matrices[it.matrix];
   tc::griddep_launch();
@@ -201,12 +202,17 @@ __global__ void __launch_bounds__(kThreads) planes_kernel(const __grid_constant_
   double s = 0;
   for (int i = threadIdx.x; i < m.n_items; i += kThreads) s += p.partial[m.item0 + i];
   s = block_sum(s);
-  if (threadIdx.x == 0) inv = (float)((double)kPlaneScale / (sqrt(s) + (double)p.eps));
+  if (threadIdx.x == 0) {
+    // of norms below 2^-60 (eps may be zero) a part of the factor is a power of two: binary32 would not hold the whole
+    const double norm = sqrt(s) + (double)p.eps;
+    power = norm < 0x1p-60 ? 0x1p60f : 1.f;
+    inv = (float)((double)kPlaneScale / (norm * (double)power));
+  }
   __syncthreads();
   if (m.vec && p.vec)
-    planes_item<4>(p, m, it, inv);
+    planes_item<4>(p, m, it, power, inv);
   else
-    planes_item<1>(p, m, it, inv);
+    planes_item<1>(p, m, it, power, inv);
 }
 
 template <int V>

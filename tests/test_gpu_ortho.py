@@ -292,3 +292,18 @@ def test_no_less_exact_than_binary32(ddl, rows, cols):
             plain += float((_newton_schulz(g).double() - want).norm() / want.norm())
         o.check()
     assert own <= 1.5 * plain + 4 * 2.0 ** -21, (own / 4, plain / 4)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("power", [-117, -100, 100])
+def test_without_eps_the_scale_does_not_matter(ddl, power, dtype):
+    """eps = 0 is accepted: X = G / |G| then, however small or large G is (its elements stay normal numbers here)."""
+    g = _gradient(64, 80).to(TYPES[dtype])
+    scaled = (g.float() * 2.0 ** (power / 2) * 2.0 ** (power / 2)).to(TYPES[dtype])
+    keep = scaled.float().abs() >= 2.0 ** -126
+    g, scaled = torch.where(keep, g, 0), torch.where(keep, scaled, 0)
+    out = torch.empty_like(scaled)
+    with ddl.Ortho([(0, 64, 80)], dtype, eps=0.0) as o:
+        o.run(scaled.view(-1), out.view(-1))
+        o.check()
+    _check(out, g, dtype, eps=0.0)
