@@ -19,9 +19,10 @@ OUT = os.path.join(HERE, "libddl.so")
 BUILD = os.path.join(ROOT, "_build", "ddl")
 
 SOURCES = ["plan.cpp", "ddl_api.cu", "fold_kernels.cu", "step_kernels.cu", "noalloc.cu", "sgd_kernels.cu",
-           "product_kernels.cu", "linear_kernels.cu", "linear_api.cu", "ortho_kernels.cu", "ortho_api.cu"]
+           "product_kernels.cu", "product_selftest.cu", "linear_kernels.cu", "linear_api.cu", "ortho_kernels.cu",
+           "ortho_api.cu"]
 # contractions with no bit-exact contract: fused multiply-adds allowed
-FMA_SOURCES = {"product_kernels.cu", "linear_kernels.cu", "ortho_kernels.cu"}
+FMA_SOURCES = {"product_kernels.cu", "product_selftest.cu", "linear_kernels.cu", "ortho_kernels.cu"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC,-Wall",
          "-I", INCLUDE, "-I", CSRC]

@@ -44,6 +44,18 @@ struct Range {
   bool wraps() const { return hi < lo; }
 };
 
+// The arguments of a wait self-test; false if the limit is longer than the kernel's own.
+inline bool give_up_of(uint32_t limit_us, uint32_t products, uint32_t loads_even, uint32_t loads_odd, GiveUp* g) {
+  const uint64_t ns = (uint64_t)limit_us * 1000ull;
+  if (ns > kWaitLimitNs) return false;
+  *g = GiveUp{true, ns, products, {loads_even, loads_odd}};
+  return true;
+}
+
+inline cudaError_t launch(const ProductLaunch& p, int tile_n, int sms, cudaStream_t stream) {
+  return p.give_up.armed ? launch_product_selftest(p, tile_n, sms, stream) : launch_product(p, tile_n, sms, stream);
+}
+
 inline uint64_t round8(uint64_t n) { return (n + 7) / 8 * 8; }
 
 // How a product is laid on the SMs: tiles of 128 x 128 on a CTA or 256 x 256 on a pair, and how many parts of the

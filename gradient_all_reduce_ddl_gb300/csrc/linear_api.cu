@@ -27,6 +27,7 @@ struct ddl_linear {
   int sms = 0;
   ddl::Residency room = {};
   uint32_t* d_err = nullptr;
+  ddl::GiveUp give_up;  // of the next launch
   Buffer x, w, dz[ddl::kMaxPlanes], partial, done;
 };
 
@@ -69,6 +70,13 @@ ddl_status_t bind(ddl_linear* h) {
   h->d_err = err;
   h->device = dev;
   return DDL_OK;
+}
+
+// A self-test is of one launch.
+ddl::GiveUp take_give_up(ddl_linear* h) {
+  const ddl::GiveUp g = h->give_up;
+  h->give_up = ddl::GiveUp();
+  return g;
 }
 
 ddl_status_t need(Buffer* b, size_t bytes) {
@@ -233,8 +241,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   if ((st = aligned(mw, N, &h->w, &prep, &aw)) != DDL_OK) return st;
   if (prep.n_packs && (st = ddl::status_of(ddl::launch_linear_prep(prep, s))) != DDL_OK) return st;
 
-  ddl::ProductLaunch L;
-  std::memset(&L, 0, sizeof(L));
+  ddl::ProductLaunch L = {};
   L.bf16 = h->type == ddl::kBF16;
   // boxes of a tile's rows
   const int narrow = std::min(tile_n, ddl::kTileM);
@@ -267,6 +274,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
   L.splits = splits;
   L.chunked = chunked;
   L.err = h->d_err;
+  L.give_up = take_give_up(h);
   P.in0 = P.in1 = P.out0 = P.out1 = -1;
   // rows that TMA can address, of whole 16-byte pieces, let the epilogue move whole boxes
   L.boxes = !swap && L.splits == 1 && N % 8 == 0 && my.tma() && (!z || mz.tma()) && (!residual || mr.tma()) &&
@@ -279,7 +287,7 @@ ddl_status_t ddl_linear_forward(ddl_linear_t h, size_t tokens, const void* x, si
     if (residual) P.in0 = 4;
     if (residual && !map_of(&L, 4, mr, ddl::kSlabCols)) return DDL_ERR_CUDA;
   }
-  return ddl::status_of(ddl::launch_product(L, tile_n, h->sms, s));
+  return ddl::status_of(ddl::launch(L, tile_n, h->sms, s));
 }
 
 ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, size_t ldy, const void* x, size_t ldx,
@@ -380,10 +388,10 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
   if ((st = ddl::status_of(ddl::launch_linear_prep(prep, s))) != DDL_OK) return st;
   if (!dx && !dw) return DDL_OK;
 
-  ddl::ProductLaunch L;
-  std::memset(&L, 0, sizeof(L));
+  ddl::ProductLaunch L = {};
   L.bf16 = !f16;
   L.err = h->d_err;
+  L.give_up = take_give_up(h);
   const int maps = std::max(1, n_planes);
   for (int k = 0; k < maps; ++k)
     if (!map_of(&L, k, n_planes ? Mat{h->dz[k].p, T, N, ldp} : mdy, ddl::kBlockK)) return DDL_ERR_CUDA;
@@ -468,7 +476,12 @@ ddl_status_t ddl_linear_backward(ddl_linear_t h, size_t tokens, const void* dy, 
     if (dw && !(ge == 4 ? map32_of(&L, 5, mdw) : map_of(&L, 5, mdw, ddl::kSlabCols))) return DDL_ERR_CUDA;
     if (dx && !map_of(&L, 6, mdx, ddl::kSlabCols)) return DDL_ERR_CUDA;
   }
-  return ddl::status_of(ddl::launch_product(L, tile_n, h->sms, s));
+  return ddl::status_of(ddl::launch(L, tile_n, h->sms, s));
+}
+
+ddl_status_t ddl_linear_selftest_wait_timeout(ddl_linear_t h, uint32_t limit_us, uint32_t products, uint32_t loads_even,
+                                              uint32_t loads_odd) {
+  return h && ddl::give_up_of(limit_us, products, loads_even, loads_odd, &h->give_up) ? DDL_OK : DDL_ERR_INVALID_ARG;
 }
 
 ddl_status_t ddl_linear_check(ddl_linear_t h, void* stream) {

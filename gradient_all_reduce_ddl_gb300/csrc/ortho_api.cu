@@ -46,6 +46,7 @@ struct ddl_ortho {
   int sms = 0;
   ddl::Residency room = {};
   bool ready = false;
+  ddl::GiveUp give_up;  // of the next call's products
   uint32_t* d_err = nullptr;
   void* d_planes = nullptr;  // one block: every plane
   CUtensorMap* d_maps = nullptr;
@@ -419,13 +420,14 @@ ddl_status_t bind(ddl_ortho* o) {
 
 // The products of every step; the result is iterate steps & 1.
 ddl_status_t products(ddl_ortho* o, cudaStream_t s) {
-  ddl::ProductLaunch L;
-  std::memset(&L, 0, sizeof(L));
+  ddl::ProductLaunch L = {};
   L.g_maps = o->d_maps;
   L.err = o->d_err;
   L.ca = o->coeff[0];
   L.cb = o->coeff[1];
   L.cc = o->coeff[2];
+  L.give_up = o->give_up;
+  o->give_up = ddl::GiveUp();  // a self-test is of one call
   for (int k = 0; k < o->steps; ++k) {
     const int order[3] = {k & 1 ? kGram1 : kGram0, kPoly, k & 1 ? kApply1 : kApply0};
     for (int kind : order) {
@@ -437,7 +439,7 @@ ddl_status_t products(ddl_ortho* o, cudaStream_t s) {
       L.n_tiles = st.workers;
       L.splits = st.splits;
       L.boxes = st.splits == 1;
-      const cudaError_t e = ddl::launch_product(L, st.tile, o->sms, s);
+      const cudaError_t e = ddl::launch(L, st.tile, o->sms, s);
       if (e != cudaSuccess) return ddl::status_of(e);
     }
   }
@@ -578,6 +580,11 @@ ddl_status_t ddl_ortho_muon(ddl_ortho_t o, const void* grad, int n_copies, float
   f.n_copies = n_copies;
   f.vec = vec;
   return update(o, p, &f, s);
+}
+
+ddl_status_t ddl_ortho_selftest_wait_timeout(ddl_ortho_t o, uint32_t limit_us, uint32_t products, uint32_t loads_even,
+                                             uint32_t loads_odd) {
+  return o && ddl::give_up_of(limit_us, products, loads_even, loads_odd, &o->give_up) ? DDL_OK : DDL_ERR_INVALID_ARG;
 }
 
 ddl_status_t ddl_ortho_check(ddl_ortho_t o, void* stream) {

@@ -24,6 +24,8 @@ constexpr int kMaxPasses = 3;
 // polynomials stay below 16 in magnitude (a polynomial that lets them grow past it gives NaN); the smallest lo is 2^-36.
 constexpr float kPlaneScale = 4096.f;
 constexpr int kMaxMaps = 8;      // tensor maps carried in the launch record
+constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s for each of the kernel's waits
+constexpr uint32_t kNever = ~0u;
 
 enum ElemType : int { kF32 = 0, kF16 = 1, kBF16 = 2 };
 enum ActKind : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
@@ -80,6 +82,15 @@ struct alignas(16) Tile {
 };
 constexpr int32_t kNoTile = 0x7FFFFFFF;
 
+// The self-test's stops, and what its waits are bounded by (else kWaitLimitNs): roles end where something would keep them
+// waiting, and the others' waits run out.
+struct GiveUp {
+  bool armed = false;
+  uint64_t wait_ns = kWaitLimitNs;
+  uint32_t products = kNever;            // chunks after which a CTA's (or pair's) products stop
+  uint32_t loads[2] = {kNever, kNever};  // K blocks after which a CTA's loads stop (even and odd CTA of a pair)
+};
+
 // Launch record.  Grouped launches read products, tiles and maps from device
 // memory; single launches carry up to two products and their maps here.
 struct ProductLaunch {
@@ -100,6 +111,7 @@ struct ProductLaunch {
   int32_t bf16;             // operands are bfloat16, else binary16
   uint32_t* err;
   float ca, cb, cc;         // Newton-Schulz coefficients
+  GiveUp give_up;           // read by launch_product_selftest's kernels only
 };
 
 // Clusters of 1, 2, 4 and 8 CTAs of the product kernel that the current device holds at a time.
@@ -111,6 +123,8 @@ cudaError_t product_residency(int sms, Residency* r);
 // tile_n: 128, 64 or 32 output columns per 128-row tile; 256: 256 x 256 tiles on CTA pairs.  Grouped
 // launches and kEpiStore take 128 or 256.
 cudaError_t launch_product(const ProductLaunch& p, int tile_n, int sms, cudaStream_t stream);
+// The same kernels with p.give_up's stops.
+cudaError_t launch_product_selftest(const ProductLaunch& p, int tile_n, int sms, cudaStream_t stream);
 
 // Tensor map of a row-major 16-bit matrix (rows x cols, ld elements between rows; 16-byte aligned base and row stride):
 // boxes of 64 columns (operands, 128-byte swizzle) or 32 (the epilogue's slabs, 64-byte swizzle) x box_rows.

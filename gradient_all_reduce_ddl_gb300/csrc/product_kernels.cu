@@ -42,7 +42,10 @@
 // which are added through memory by the one that comes last.
 //
 // Every wait is bounded.  One that runs out sets kErrProductWait; the CTA then
-// waits (bounded too) for its own loads and products, frees its TMEM and ends.
+// waits (bounded too) for its own loads and products, frees its TMEM and ends.  A
+// pair's loads all count on the even CTA's barriers, so it is told how far the odd
+// one came, makes up for what either did not ask for, and waits for both's loads
+// before either ends (end_loads).
 
 #include <algorithm>
 #include <atomic>
@@ -62,6 +65,14 @@ constexpr int kThreads = 384;  // warp 3 only fills the first warpgroup
 constexpr int kEpiWarps = 8;
 constexpr int kBoxBytes = kBoxRows * kBlockK * 2;
 constexpr int kABytes = kTileM * kBlockK * 2;
+
+// This file is compiled twice: as it is, and (product_selftest.cu) with stops that make its waits run out.  Looking for them
+// would cost every launch 0.2 us.
+#ifdef DDL_PRODUCT_SELFTEST
+constexpr bool kSelfTest = true;
+#else
+constexpr bool kSelfTest = false;
+#endif
 
 // What a launch is for; each has its own epilogues (and registers: one that spilled would go to L2 for it, since shared
 // memory leaves no L1).
@@ -253,17 +264,43 @@ struct Shape {
   __device__ __forceinline__ float scale(int pass) const { return pass == 0 ? scale0 : pass == 1 ? scale1 : scale2; }
 };
 
-// A place in the ring of stages, and the parity of its next use.
+// A place in a ring, and how often that was gone round (modulo 2^32).
 struct Slot {
-  uint32_t s = 0, phase = 0;
+  uint32_t s = 0, lap = 0;
+  __device__ __forceinline__ uint32_t parity() const { return lap & 1u; }
   template <int STAGES>
   __device__ __forceinline__ void next() {
     if (++s == STAGES) {
       s = 0;
-      phase ^= 1u;
+      ++lap;
     }
   }
+  // uses so far, modulo 2^32
+  template <int STAGES>
+  __device__ __forceinline__ uint32_t uses() const {
+    return lap * STAGES + s;
+  }
 };
+
+// After a pair gave up: waits (bounded) on the even CTA's barriers for the loads of both.  The even one would have gone on
+// at `at`; the odd one asked for `more` K blocks more than it (or fewer: < 0).  A barrier's phase ends with the even CTA's
+// arrival, which tells it of both halves, and their bytes; of a block that only one of them asked for the other's part is
+// made up here.  They differ by at most STAGES blocks, since a slot is not asked for again before the products of its last
+// use are done.
+template <int STAGES>
+__device__ __forceinline__ void end_loads(uint32_t full, uint32_t half, Slot at, int more, uint64_t limit) {
+  const int most = more > 0 ? more : 0;
+  // the last use of every slot, counted from the even CTA's next one; of a slot without any, the lap before the first, which
+  // counts as done
+  for (int n = most - STAGES; n < most; ++n) {
+    const int back = (int)at.s + n;  // -STAGES .. 2 STAGES - 2
+    const int slot = (back + STAGES) % STAGES, laps = (back + STAGES) / STAGES - 1;
+    const uint32_t bar = full + 8 * slot;
+    if (n >= more) bar_complete(bar, half);
+    if (n >= 0) bar_expect(bar, half);
+    if (!bar_wait(bar, (at.lap + laps) & 1u, limit)) break;
+  }
+}
 
 // Makes a tensor map that the host wrote into device memory usable by this thread's TMA operations.
 __device__ __forceinline__ void acquire_map(const CUtensorMap* map) {
@@ -740,6 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2 * kStages + 5 + 2 * kBufs];
   __shared__ uint32_t tmem_slot;
+  __shared__ uint32_t load_slot, load_lap;  // PAIR: where this CTA's loads would have gone on
+  __shared__ uint32_t broken, drains;       // PAIR: a CTA of the cluster gave up; this pair's products were cut short
   __shared__ int joins;                  // this CTA's part of a tile was the last: it finishes the tile
   __shared__ volatile int empty_slab[kBufs];  // a slab of a part whose tile another CTA finishes
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
@@ -762,6 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       bar_init(written + 8 * b, kEpiWarps);
     }
     bar_init(drain, 1);
+    broken = drains = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 1) {
@@ -786,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
   const int first = blockIdx.x / ctas, step = gridDim.x / ctas, end = MODE == kSteps ? kNoTile : p.n_tiles;
   const int my_rows = odd * kTileM;  // this CTA's part of the tile's rows
   const CUtensorMap* maps = MODE == kSteps ? p.g_maps : p.maps;
+  const uint64_t limit = kSelfTest ? p.give_up.wait_ns : kWaitLimitNs;
 
   // The epilogue's sums want registers: 384 threads of 168 become 128 of 56 and 256 of 224 (64,512 either way).
   __syncwarp();
@@ -814,7 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           const CUtensorMap* mb = ps == 0 ? mb0 : ps == 1 ? mb1 : mb2;
           for (int kb = sh.kb0; kb < sh.kb1; ++kb, at.next<kStages>()) {
             const uint32_t s = at.s;
-            if (!bar_wait(empty + 8 * s, at.phase ^ 1u)) {
+            const bool stop = kSelfTest && at.uses<kStages>() == p.give_up.loads[odd];
+            if (stop || !bar_wait(empty + 8 * s, at.parity() ^ 1u, limit)) {
               ok = false;
               break;
             }
@@ -850,16 +892,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
       }
       if (!ok) atomicOr(p.err, kErrProductWait);
-      // Loads in flight end before the CTA does.  The odd CTA of a pair has no barrier of its own for them: its
-      // loads are done when the pair's last sums are (below), and after a wait that ran out it gives them 10 ms.
-      if (PAIR && odd) {
+      // Loads in flight end before the CTA does.
+      if constexpr (PAIR) {
+        load_slot = at.s, load_lap = at.lap;  // see the kernel's end
         if (!ok)
-          for (const uint64_t t0 = now_ns(); now_ns() - t0 < 10000000ull;) {
-          }
+          for (int r = 0; r < 2 * p.splits; ++r) st_peer(peer_addr(smem_u32(&broken), r), 1);
       } else {
-        // every slot's last use (one without any counts as done)
+        // every slot's last use, the oldest first (one without any counts as done)
         for (int k = 0; k < kStages; ++k, at.next<kStages>())
-          if (!bar_wait(full + 8 * at.s, at.phase ^ 1u)) break;
+          if (!bar_wait(full + 8 * at.s, at.parity() ^ 1u, limit)) break;
       }
     }
     if (warp == 1 && lane == 0 && !odd) {
@@ -882,14 +923,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           for (int k0 = sh.kb0; k0 < sh.kb1 && ok; k0 += chunk, ++cc) {
             const int k1 = k0 + chunk < sh.kb1 ? k0 + chunk : sh.kb1;
             const uint32_t acc = tmem + (cc & 1u) * BN;
-            if (!bar_wait(tempty + 8 * (cc & 1u), (cc >> 1 & 1u) ^ 1u)) {
+            const bool stop = kSelfTest && cc == p.give_up.products;
+            if (stop || !bar_wait(tempty + 8 * (cc & 1u), (cc >> 1 & 1u) ^ 1u, limit)) {
               ok = false;
               break;
             }
             fence_after();
             for (int kb = k0; kb < k1; ++kb, at.next<kStages>()) {
               const uint32_t s = at.s;
-              if (!bar_wait(full + 8 * s, at.phase)) {
+              if (!bar_wait(full + 8 * s, at.parity(), limit)) {
                 ok = false;
                 break;
               }
@@ -908,7 +950,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if (!ok) {
         atomicOr(p.err, kErrProductWait);
         mma_commit<PAIR>(drain, lead);  // products in flight end before the CTA does
-        bar_wait(drain, 0);
+        bar_wait(drain, 0, limit);
+        if constexpr (PAIR) {
+          for (int r = lead; r < lead + 2; ++r) st_peer(peer_addr(smem_u32(&drains), r), 1);
+          for (int r = 0; r < 2 * p.splits; ++r) st_peer(peer_addr(smem_u32(&broken), r), 1);
+        }
       }
     }
     if constexpr (BN >= 128) {
@@ -937,7 +983,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             fu.next<kBufs>();
           }
           const uint32_t buf = staging + wu.s * kSlabBytes;
-          if (!bar_wait(written + 8 * wu.s, wu.phase)) {
+          if (!bar_wait(written + 8 * wu.s, wu.parity(), limit)) {
             ok = false;
             break;
           }
@@ -953,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
         if (!ok) {
           atomicOr(p.err, kErrProductWait);
-          for (; ahead > 0; --ahead, wu.next<kBufs>()) bar_wait(ready + 8 * wu.s, wu.phase);  // loads in flight
+          for (; ahead > 0; --ahead, wu.next<kBufs>()) bar_wait(ready + 8 * wu.s, wu.parity(), limit);  // loads in flight
         }
         store_wait();
       }
@@ -1003,7 +1049,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       // The sums of this thread's 16 columns of the slabs in turn: from TMEM, or added up in registers chunk by chunk.
       float acc[DIRECT ? kHalf : BN / 2];
       const auto wait_sums = [&]() {
-        if (ok && !bar_wait(tfull + 8 * (cc & 1u), cc >> 1 & 1u)) ok = false;
+        if (ok && !bar_wait(tfull + 8 * (cc & 1u), cc >> 1 & 1u, limit)) ok = false;
         ok = __all_sync(0xffffffffu, ok);  // if not: the error word is set below, and the tile's values are not written
         fence_after();
         return ok;
@@ -1139,7 +1185,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             // it has to stay in the instruction cache
             uint4 bias[2] = {bias_ahead[0], bias_ahead[1]};
             if (is_forward(MODE) && sl + 1 < kSlabs) load_bias(P, pl.col0 + (sl + 1) * kSlab + half * kHalf, bias_ahead);
-            if (ok && !bar_wait(ready + 8 * use.s, use.phase)) ok = false;
+            if (ok && !bar_wait(ready + 8 * use.s, use.parity(), limit)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             load_slab(sl);
@@ -1205,7 +1251,35 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     }
   }
   __syncthreads();
+  if constexpr (PAIR) {
+    // A pair's loads have ended when the products that read them are done; the even CTA's products arrive at the odd one's
+    // barriers too, and have to before it ends.  (Nothing here is kept in registers from before: the epilogue needs them all.)
+    if (threadIdx.x < kStages && !broken) {
+      const uint32_t s = threadIdx.x;  // its next use would be in this lap, or in the one after
+      const uint32_t lap = load_lap + (s < load_slot);
+      if (!bar_wait(smem_u32(bars) + 8 * (kStages + s), (lap & 1u) ^ 1u, limit)) {
+        atomicOr(p.err, kErrProductWait);
+        for (int r = 0; r < 2 * p.splits; ++r) st_peer(peer_addr(smem_u32(&broken), r), 1);
+      }
+    }
+  }
   if (PAIR || S > 1) cluster_sync();  // no CTA leaves while a peer's products or sums need it
+  if constexpr (PAIR) {
+    if (broken) {  // in all CTAs of the cluster: none leaves while a peer waits for its loads
+      if (threadIdx.x == 0) {
+        const uint32_t bar = smem_u32(bars), self = cluster_rank();
+        if (drains) bar_wait(bar + 8 * (2 * kStages + 4), 0, limit);
+        if (!(self & 1)) {
+          Slot mine, theirs;
+          mine.s = load_slot, mine.lap = load_lap;
+          theirs.s = ld_peer_u32(peer_addr(smem_u32(&load_slot), self + 1));
+          theirs.lap = ld_peer_u32(peer_addr(smem_u32(&load_lap), self + 1));
+          end_loads<kStages>(bar, stage_bytes(BN), mine, (int)(theirs.uses<kStages>() - mine.uses<kStages>()), limit);
+        }
+      }
+      cluster_sync();
+    }
+  }
   if (warp == 1) {
     fence_after();
     tmem_free<PAIR>(tmem, kCols);
@@ -1246,6 +1320,7 @@ cudaError_t launch_one(const ProductLaunch& p, int sms, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, product_kernel<BN, MODE>, p);
 }
 
+#ifndef DDL_PRODUCT_SELFTEST
 template <int BN>
 cudaError_t residency(int cluster, int* n) {
   cudaError_t e = cudaFuncSetAttribute(product_kernel<BN, kSteps>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(BN));
@@ -1279,8 +1354,13 @@ EncodeFn encode_fn() {
   return fn;
 }
 
+#endif  // DDL_PRODUCT_SELFTEST
+
 }  // namespace
 
+#ifdef DDL_PRODUCT_SELFTEST
+#define launch_product launch_product_selftest
+#else
 bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld, int box_cols, int box_rows,
               bool bf16) {
   const EncodeFn fn = encode_fn();
@@ -1314,6 +1394,8 @@ cudaError_t product_residency(int sms, Residency* r) {
   if (e == cudaSuccess) e = residency<256>(8, &r->clusters[3]);
   return e;
 }
+
+#endif  // DDL_PRODUCT_SELFTEST
 
 cudaError_t launch_product(const ProductLaunch& p, int tile_n, int sms, cudaStream_t stream) {
   if (p.n_tiles <= 0) return cudaSuccess;

@@ -10,8 +10,6 @@
 namespace ddl {
 namespace tc {
 
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s per wait before giving up
-
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 __device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
@@ -24,6 +22,11 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Counts bytes that no copy will bring.
+__device__ __forceinline__ void bar_complete(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 
 __device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
@@ -45,11 +48,11 @@ __device__ __forceinline__ uint64_t now_ns() {
 }
 
 // Waits for the phase of the given parity; false once the limit has passed.
-__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
   for (int i = 0; i < 64; ++i)
     if (bar_try(bar, parity)) return true;
   const uint64_t t0 = now_ns();
-  while (now_ns() - t0 < kWaitLimitNs)
+  while (now_ns() - t0 < limit_ns)
     if (bar_try(bar, parity)) return true;
   return false;
 }
@@ -274,6 +277,16 @@ __device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
                : "r"(addr)
                : "memory");
   return v;
+}
+
+__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 __device__ __forceinline__ float ld_peer(uint32_t addr) {

@@ -44,7 +44,7 @@ EXPORTS = [
     "ddl_allreduce_slab", "ddl_noalloc_check",
     "ddl_linear_create", "ddl_linear_forward", "ddl_linear_backward", "ddl_linear_check", "ddl_linear_destroy",
     "ddl_ortho_create", "ddl_ortho_set_polynomial", "ddl_ortho_run", "ddl_ortho_muon", "ddl_ortho_check",
-    "ddl_ortho_destroy",
+    "ddl_ortho_destroy", "ddl_linear_selftest_wait_timeout", "ddl_ortho_selftest_wait_timeout",
 ]
 
 
@@ -99,12 +99,14 @@ _sig("ddl_linear_forward", _i, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _vp, _sz, _vp,
 _sig("ddl_linear_backward", _i, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _i, _i, _vp)
 _sig("ddl_linear_check", _i, _vp, _vp)
 _sig("ddl_linear_destroy", _i, _vp)
+_sig("ddl_linear_selftest_wait_timeout", _i, _vp, *[ctypes.c_uint32] * 4)
 _sig("ddl_ortho_create", _i, _i, _P(ddl_matrix_t), _i, _P(_vp))
 _sig("ddl_ortho_set_polynomial", _i, _vp, _i, _f, _f, _f, _f)
 _sig("ddl_ortho_run", _i, _vp, _vp, _vp, _vp)
 _sig("ddl_ortho_muon", _i, _vp, _vp, _i, _P(_vp), _vp, _f, _f, _f, _i, _vp)
 _sig("ddl_ortho_check", _i, _vp, _vp)
 _sig("ddl_ortho_destroy", _i, _vp)
+_sig("ddl_ortho_selftest_wait_timeout", _i, _vp, *[ctypes.c_uint32] * 4)
 
 
 class DDLError(RuntimeError):
@@ -332,6 +334,14 @@ def ddl_linear_check(layer, stream=None):
     _ok(_lib.ddl_linear_check(layer, _stream_handle(stream)), "ddl_linear_check")
 
 
+_NEVER = 0xFFFFFFFF
+
+
+def ddl_linear_selftest_wait_timeout(layer, limit_us, products=_NEVER, loads_even=_NEVER, loads_odd=_NEVER):
+    _ok(_lib.ddl_linear_selftest_wait_timeout(layer, limit_us, products, loads_even, loads_odd),
+        "ddl_linear_selftest_wait_timeout")
+
+
 def ddl_linear_destroy(layer):
     _ok(_lib.ddl_linear_destroy(layer), "ddl_linear_destroy")
 
@@ -363,6 +373,11 @@ def ddl_ortho_muon(ortho, grad, param_bufs, mom, lr, momentum=0.95, weight_decay
 
 def ddl_ortho_check(ortho, stream=None):
     _ok(_lib.ddl_ortho_check(ortho, _stream_handle(stream)), "ddl_ortho_check")
+
+
+def ddl_ortho_selftest_wait_timeout(ortho, limit_us, products=_NEVER, loads_even=_NEVER, loads_odd=_NEVER):
+    _ok(_lib.ddl_ortho_selftest_wait_timeout(ortho, limit_us, products, loads_even, loads_odd),
+        "ddl_ortho_selftest_wait_timeout")
 
 
 def ddl_ortho_destroy(ortho):

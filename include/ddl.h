@@ -441,6 +441,15 @@ ddl_status_t ddl_linear_backward(ddl_linear_t layer, size_t tokens, const void* 
  * the calls since the last check are not valid). */
 ddl_status_t ddl_linear_check(ddl_linear_t layer, void* stream);
 
+/* Self-test of that failure path, for the layer's next forward or backward
+ * call: every wait in its product kernel ends after limit_us (at most 2 s, the
+ * usual limit), and its products stop after `products` accumulations, or the loads
+ * of even or odd CTAs after so many blocks of 64 of a contraction (UINT32_MAX:
+ * never).  What waits for them gives up; the call's results are not valid, and
+ * ddl_linear_check reports it.  Nothing faults or hangs.  Host-only. */
+ddl_status_t ddl_linear_selftest_wait_timeout(ddl_linear_t layer, uint32_t limit_us, uint32_t products,
+                                              uint32_t loads_even, uint32_t loads_odd);
+
 /* Frees the handle and its workspace, whatever it returns.  NULL is accepted. */
 ddl_status_t ddl_linear_destroy(ddl_linear_t layer);
 
@@ -498,8 +507,11 @@ ddl_status_t ddl_ortho_run(ddl_ortho_t ortho, const void* in, void* out, void* s
 ddl_status_t ddl_ortho_muon(ddl_ortho_t ortho, const void* grad, int n_copies, float* const* param_bufs, float* mom,
                             float lr, float momentum, float weight_decay, int nesterov, void* stream);
 
-/* As ddl_linear_check, ddl_linear_destroy. */
+/* As ddl_linear_check, ddl_linear_selftest_wait_timeout (of every product of
+ * the next call), ddl_linear_destroy. */
 ddl_status_t ddl_ortho_check(ddl_ortho_t ortho, void* stream);
+ddl_status_t ddl_ortho_selftest_wait_timeout(ddl_ortho_t ortho, uint32_t limit_us, uint32_t products,
+                                             uint32_t loads_even, uint32_t loads_odd);
 ddl_status_t ddl_ortho_destroy(ddl_ortho_t ortho);
 
 /* A static string for a status code. */

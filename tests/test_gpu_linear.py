@@ -647,3 +647,46 @@ def test_residual_in_place_of_one_row(ddl):
                                r.data_ptr(), 104)
         layer.check()
     assert torch.equal(apart, r)
+
+
+STOPS = [dict(products=0), dict(products=1), dict(loads_even=0), dict(loads_even=3), dict(loads_odd=0), dict(loads_odd=3),
+         dict(loads_even=2, loads_odd=6), dict(loads_even=7, loads_odd=4), dict(products=1, loads_even=6)]
+
+
+@pytest.mark.parametrize("stop", STOPS, ids=str)
+@pytest.mark.parametrize("tokens, n_in, n_out, dtype", [
+    (8, 2048, 520, "f16"), (50, 2048, 264, "bf16"), (150, 1024, 136, "f16"), (150, 1024, 131, "f16"), (300, 40000, 264, "f16"),
+    (2304, 1536, 2304, "bf16"), (2304, 1536, 2301, "bf16"), (2304, 20001, 2304, "f16"),
+])
+def test_waits_that_run_out_end_the_call(ddl, tokens, n_in, n_out, dtype, stop):
+    """A role of the product kernel stops, what waits for it gives up: the call ends, the error word tells, and the calls
+    after it are right.  (A stop beyond what a CTA has to do is none.)"""
+    x, w = _normal(1, tokens, n_in, dtype), _normal(2, n_out, n_in, dtype, n_in ** -0.5)
+    dy, r = _normal(3, tokens, n_out, dtype), _normal(4, tokens, n_out, dtype)
+
+    def outs():
+        return _blank(tokens, n_out, dtype)[0], _blank(tokens, n_in, dtype)[0], _blank(n_out, n_in, "f32")[0]
+    want, void, got = outs(), outs(), outs()
+    with ddl.Linear(n_in, n_out, tokens, dtype, "none") as layer:
+        def forward(o):
+            layer.forward(x, w, o[0], residual=r)
+
+        def backward(o):
+            layer.backward(dy, x, w, dx=o[1], dw=o[2])
+        forward(want), backward(want)
+        layer.check()
+        for call in (forward, backward):
+            ddl.ddl_linear_selftest_wait_timeout(layer.handle, 500, **stop)
+            call(void)
+            if stop.get("products") == 0 or stop.get("loads_even") == 0:
+                with pytest.raises(ddl.DDLError) as e:
+                    layer.check()
+                assert e.value.status == ddl.DDL_ERR_DEVICE_CHECK
+            else:
+                try:
+                    layer.check()
+                except ddl.DDLError as e:
+                    assert e.status == ddl.DDL_ERR_DEVICE_CHECK
+            forward(got), backward(got)
+            layer.check()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

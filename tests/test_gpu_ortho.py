@@ -307,3 +307,34 @@ def test_without_eps_the_scale_does_not_matter(ddl, power, dtype):
         o.run(scaled.view(-1), out.view(-1))
         o.check()
     _check(out, g, dtype, eps=0.0)
+
+
+@pytest.mark.parametrize("stop", [dict(products=0), dict(products=2), dict(loads_even=0), dict(loads_even=6), dict(loads_odd=0),
+                                  dict(loads_odd=6), dict(loads_even=3, loads_odd=8), dict(loads_even=8, loads_odd=3)], ids=str)
+@pytest.mark.parametrize("shapes", [[(64, 147)], [(1024, 1024)], [(1024, 4096)] * 4, [(2049, 1023)], [(64, 64), (2048, 2050)]],
+                         ids=str)
+def test_waits_that_run_out_end_the_call(ddl, shapes, stop):
+    """A role of the product kernels stops, what waits for it gives up: the call ends, the error word tells, and the calls
+    after it are right.  (A stop beyond what a CTA has to do is none.)"""
+    mats, at = [], 0
+    for r, c in shapes:
+        mats.append((at, r, c))
+        at += r * c
+    flat = torch.cat([_gradient(r, c, k).view(-1) for k, (r, c) in enumerate(shapes)])
+    with ddl.Ortho(mats) as o:
+        want = o.run(flat, torch.empty_like(flat))
+        o.check()
+        ddl.ddl_ortho_selftest_wait_timeout(o.handle, 300, **stop)
+        o.run(flat, torch.empty_like(flat))
+        if stop.get("products") == 0 or stop.get("loads_even") == 0:
+            with pytest.raises(ddl.DDLError) as e:
+                o.check()
+            assert e.value.status == ddl.DDL_ERR_DEVICE_CHECK
+        else:
+            try:
+                o.check()
+            except ddl.DDLError as e:
+                assert e.status == ddl.DDL_ERR_DEVICE_CHECK
+        got = o.run(flat, torch.empty_like(flat))
+        o.check()
+    assert torch.equal(want, got)

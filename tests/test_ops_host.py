@@ -186,3 +186,12 @@ def test_linear_backward_of_no_tokens_without_dw_and_db_queues_nothing(ddl):
     with _layer(ddl) as layer:
         ddl.ddl_linear_backward(layer.handle, 0, None, 0, None, 0, B, 16, None, 0, None, 0, None, 0, None, ddl.DDL_FP32,
                                 False, 0)
+
+
+@pytest.mark.parametrize("limit, want", [(0, "DDL_OK"), (2_000_000, "DDL_OK"), (2_000_001, "DDL_ERR_INVALID_ARG")])
+def test_wait_selftests_refuse_longer_limits(ddl, limit, want):
+    with _layer(ddl) as layer, ddl.Ortho([(0, 4, 4)]) as o:
+        assert _status(ddl, ddl.ddl_linear_selftest_wait_timeout, layer.handle, limit) == getattr(ddl, want)
+        assert _status(ddl, ddl.ddl_ortho_selftest_wait_timeout, o.handle, limit) == getattr(ddl, want)
+    assert ddl._lib.ddl_linear_selftest_wait_timeout(None, 1, 0, 0, 0) == ddl.DDL_ERR_INVALID_ARG
+    assert ddl._lib.ddl_ortho_selftest_wait_timeout(None, 1, 0, 0, 0) == ddl.DDL_ERR_INVALID_ARG
