@@ -3,7 +3,7 @@
 // whose rows are not 16-byte aligned.  One launch for all of it: small layers are
 // bound by launches (256 x 1000 column sums: 4.6 us).  Large ones are bound by HBM traffic
 // (with binary32 gradients a bfloat16 dz reads 4 and writes 6 bytes an element: 8192 x
-// 8192 with GELU 133 us, 5.0 TB/s of 6.8) and by the slope's arithmetic.
+// 8192 with GELU 127 us, 5.3 TB/s of 6.8) and by the slope's arithmetic.
 #include "activation.cuh"
 #include "linear_kernels.h"
 #include "product.h"

@@ -15,16 +15,17 @@
 // alternate, so the epilogue of one chunk or tile runs under the products of the
 // next.
 //
-// What bounds it.  256 x 256 x 64 takes a pair 0.28 us at full clocks and 0.34 under
-// the power cap of long runs: 8192 x 8192 -> 4096 without an epilogue runs at the
-// library's speed (300 us, 1830 TFLOP/s).  A launch adds 4 to 9 us and its last epilogue
-// 3 (no activation) to 10 us (GELU, residual, pre-activations): 8192 x 4096 -> 4096 takes
-// 152 and 173 us against the library's 135 for the product alone.  128 x 128 tiles
+// What bounds it.  256 x 256 x 64 takes a pair 0.28 us at full clocks (about 1.95 GHz, short
+// bursts) and 0.34 under the power cap of long runs (1.7 GHz).  In bursts 8192 x 8192 -> 4096
+// without an epilogue takes 308 us, the library 300 (1830 TFLOP/s).  A launch adds 4 to 9 us
+// and its last epilogue 3 (no activation) to 10 us (GELU, residual, pre-activations):
+// 8192 x 4096 -> 4096 takes 156 and 179 us against the library's 141 for the product alone
+// (all three 5 % less on another GB300), and the second 189 under the cap.  128 x 128 tiles
 // are bound by shared memory (0.31 us for 128 x 128 x 64, half a pair's rate) and are
 // taken where pairs would leave SMs idle (choose_layout).  An epilogue slab costs its
 // warps 1100 cycles, most of it latency of some 150 instructions, and 800 more with
-// GELU: layers with less than 1024 inputs are bound by that (8192 x 512 -> 4096: 40 and
-// 71 us).  Two groups of epilogue warps on alternate slabs gained 3 us without and lost
+// GELU: layers with less than 1024 inputs are bound by that (8192 x 512 -> 4096: 41 and
+// 72 us).  Two groups of epilogue warps on alternate slabs gained 3 us without and lost
 // 4 us with GELU (registers), six stages and two slabs nothing: neither is here.
 //
 // The tensor core adds with truncation: a long sum of one sign loses about

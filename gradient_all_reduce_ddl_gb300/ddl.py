@@ -605,7 +605,8 @@ class Linear:
     """A linear layer y = act(x w^T + bias) + residual and its backward pass
     (owns a ddl_linear_t).  Tensors are the caller's: 16-bit of ``dtype``, rows
     contiguous at any stride; gradients binary32 or binary16, e.g. views into a
-    rank's flat gradient buffer."""
+    rank's flat gradient buffer.  Nothing is recorded for autograd, whatever
+    requires_grad says: backward() is the caller's to call."""
 
     def __init__(self, in_features, out_features, max_tokens, dtype="f16", act="none"):
         self.n_in, self.n_out, self.max_tokens, self.dtype, self.act = in_features, out_features, max_tokens, dtype, act

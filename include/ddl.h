@@ -429,9 +429,11 @@ ddl_status_t ddl_linear_forward(ddl_linear_t layer, size_t tokens, const void* x
  * empty sums.  One launch for both products, and one before it for dz, the
  * bias gradient and copies of unaligned operands, as far as there are any.
  * Repeated calls give the same bits.
- * Rounding: binary32 gradients sum dz to 22 bits (DDL_FP16) or 24 bits
+ * Rounding: binary32 gradients keep dz to 22 bits (DDL_FP16) or 24 bits
  * (DDL_BF16), dx and binary16 gradients to 22 or 16 bits, whatever the number
- * of tokens (exact for DDL_ACT_NONE and DDL_ACT_RELU). */
+ * of tokens (exact for DDL_ACT_NONE and DDL_ACT_RELU).  dz itself is dy times
+ * a slope that is computed to 2^-20 (GELU and SiLU: approximate exponential and
+ * reciprocal); db sums it in binary32. */
 ddl_status_t ddl_linear_backward(ddl_linear_t layer, size_t tokens, const void* dy, size_t ldy, const void* x,
                                  size_t ldx, const void* w, size_t ldw, const void* z, size_t ldz, void* dx, size_t lddx,
                                  void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate, void* stream);
@@ -467,9 +469,10 @@ ddl_status_t ddl_linear_destroy(ddl_linear_t layer);
  * A handle covers the matrices of one flat buffer (the rank buffers' layout);
  * all of them go through each product in one launch.  Elements outside every
  * matrix are neither read nor written.  Ownership, device binding and threads
- * as for the linear layers; all device memory (8 to 16 bytes per element, and
- * up to 40 MB for sums where long products are shared out) is allocated by the
- * first GPU call. */
+ * as for the linear layers; all device memory is allocated by the first GPU
+ * call: for a matrix of r x c elements, s = min(r, c), with p(n) = n rounded up to 8,
+ * 8 r p(c) + 8 s p(s) bytes (8 to 16 an element where the padding is small), and
+ * up to 40 MB for sums where long products are shared out. */
 
 typedef struct {
   size_t offset;  /* first element in the flat buffers */
