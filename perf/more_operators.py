@@ -39,7 +39,7 @@ def _adam(name, tensors, state, grad="f32", copies=1, operands="", clip=0.0, sca
 def listed():
     return [
         # scoring one example with a classifier's head (ResNet-50's fc, 2048 -> 1000): latency
-        _loss("loss fc, 1 token", "loss", 1, 2048, 1000, "f16", bias=True),
+        _loss("loss fc 1 token", "loss", 1, 2048, 1000, "f16", bias=True),
         # log probabilities of a few tokens over a large vocabulary: the weights are the traffic
         _loss("loss 16 tokens", "loss", 16, 4096, 65536, "bf16"),
         # a ragged validation batch with odd sizes, smoothed labels and padding
@@ -53,15 +53,15 @@ def listed():
         # a language model's head in training
         _loss("train batch", "train", 8192, 2048, 65536, "bf16", ignored=0.05),
         # what Muon leaves of ResNet-50 (batch norms' vectors, the fc's bias), four workers: latency
-        _adam("adamw vectors, 4 workers", "resnet50 vectors", "f32", copies=4),
+        _adam("adamw vectors 4 workers", "resnet50 vectors", "f32", copies=4),
         # all of ResNet-50's tensors, 16 workers
-        _adam("adamw resnet50, 16 workers", "resnet50", "f32", copies=16),
+        _adam("adamw resnet50 16 workers", "resnet50", "f32", copies=16),
         # a language model with 8-bit states, clipped, with the layers' bfloat16 weights
-        _adam("adamw language model, 8 bits", "lm", "8bit", operands="bf16", clip=1.0),
+        _adam("adamw language model 8 bits", "lm", "8bit", operands="bf16", clip=1.0),
         # odd tensors packed one after the other, binary16 gradients with a loss scale, two workers, 8-bit states
-        _adam("adamw ragged, 8 bits", "4099,1001*777,31,777,1,5003*301,129", "8bit", grad="f16", copies=2, scale=1 / 1024),
+        _adam("adamw ragged 8 bits", "4099,1001*777,31,777,1,5003*301,129", "8bit", grad="f16", copies=2, scale=1 / 1024),
         # four blocks of a language model, binary16 gradients with a loss scale, clipped, binary16 weights for the layers
-        _adam("adamw blocks, 2 workers", "2048*2048,2048*2048,8192*2048,2048*8192,2048", "f32", grad="f16", copies=2,
+        _adam("adamw blocks 2 workers", "2048*2048,2048*2048,8192*2048,2048*8192,2048", "f32", grad="f16", copies=2,
               operands="f16", clip=0.5, scale=1 / 1024),
     ]
 
