@@ -45,6 +45,7 @@ EXPORTS = [
     "ddl_linear_create", "ddl_linear_forward", "ddl_linear_backward", "ddl_linear_check", "ddl_linear_destroy",
     "ddl_ortho_create", "ddl_ortho_set_polynomial", "ddl_ortho_run", "ddl_ortho_muon", "ddl_ortho_check",
     "ddl_ortho_destroy", "ddl_linear_selftest_wait_timeout", "ddl_ortho_selftest_wait_timeout",
+    "ddl_adam_create", "ddl_adam_set_betas", "ddl_adam_blocks", "ddl_adam_step", "ddl_adam_destroy",
 ]
 
 
@@ -55,6 +56,11 @@ class ddl_topology_t(ctypes.Structure):
 class ddl_matrix_t(ctypes.Structure):
     _fields_ = [("offset", ctypes.c_size_t), ("rows", ctypes.c_size_t), ("cols", ctypes.c_size_t),
                 ("ld", ctypes.c_size_t)]
+
+
+class ddl_tensor_t(ctypes.Structure):
+    _fields_ = [("offset", ctypes.c_size_t), ("count", ctypes.c_size_t), ("lr_scale", ctypes.c_float),
+                ("decay_scale", ctypes.c_float)]
 
 
 _vp, _i, _sz, _u64, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_float
@@ -107,6 +113,12 @@ _sig("ddl_ortho_muon", _i, _vp, _vp, _i, _P(_vp), _vp, _f, _f, _f, _i, _vp)
 _sig("ddl_ortho_check", _i, _vp, _vp)
 _sig("ddl_ortho_destroy", _i, _vp)
 _sig("ddl_ortho_selftest_wait_timeout", _i, _vp, *[ctypes.c_uint32] * 4)
+
+_sig("ddl_adam_create", _i, _i, _P(ddl_tensor_t), _i, _i, _P(_vp))
+_sig("ddl_adam_set_betas", _i, _vp, *[ctypes.c_double] * 3)
+_sig("ddl_adam_blocks", _i, _vp, _P(_sz))
+_sig("ddl_adam_step", _i, _vp, _vp, _i, _P(_vp), _P(_vp), _i, _vp, _vp, _vp, _vp, _f, _f, _f, _f, _vp, _vp)
+_sig("ddl_adam_destroy", _i, _vp)
 
 
 class DDLError(RuntimeError):
@@ -382,6 +394,42 @@ def ddl_ortho_selftest_wait_timeout(ortho, limit_us, products=_NEVER, loads_even
 
 def ddl_ortho_destroy(ortho):
     _ok(_lib.ddl_ortho_destroy(ortho), "ddl_ortho_destroy")
+
+
+def ddl_adam_create(tensors, grad_dtype, state_bits):
+    """tensors: (offset, count), (offset, count, lr_scale) or (offset, count, lr_scale, decay_scale) each."""
+    arr = (ddl_tensor_t * max(1, len(tensors)))()
+    for a, t in zip(arr, tensors):
+        a.offset, a.count = int(t[0]), int(t[1])
+        a.lr_scale = float(t[2]) if len(t) > 2 else 1.0
+        a.decay_scale = float(t[3]) if len(t) > 3 else 1.0
+    h = ctypes.c_void_p()
+    _ok(_lib.ddl_adam_create(len(tensors), arr, grad_dtype, state_bits, ctypes.byref(h)), "ddl_adam_create")
+    return h
+
+
+def ddl_adam_set_betas(adam, beta1, beta2, eps):
+    _ok(_lib.ddl_adam_set_betas(adam, beta1, beta2, eps), "ddl_adam_set_betas")
+
+
+def ddl_adam_blocks(adam):
+    n = ctypes.c_size_t()
+    _ok(_lib.ddl_adam_blocks(adam, ctypes.byref(n)), "ddl_adam_blocks")
+    return n.value
+
+
+def ddl_adam_step(adam, grad, param_bufs, operand_bufs, operand_dtype, m, v, scales, step, lr, weight_decay=0.0,
+                  grad_scale=1.0, max_norm=0.0, norm=None, stream=None):
+    """operand_bufs, scales, norm: None where there are none."""
+    g, pm, pv, ps = _dev_ptrs([grad, m, v, step])
+    sc, nm = (None if t is None else _dev_ptrs([t])[0] for t in (scales, norm))
+    out = None if operand_bufs is None else _ptr_array(_dev_ptrs(operand_bufs))
+    _ok(_lib.ddl_adam_step(adam, g, len(param_bufs), _ptr_array(_dev_ptrs(param_bufs)), out, operand_dtype, pm, pv, sc, ps,
+                           lr, weight_decay, grad_scale, max_norm, nm, _stream_handle(stream)), "ddl_adam_step")
+
+
+def ddl_adam_destroy(adam):
+    _ok(_lib.ddl_adam_destroy(adam), "ddl_adam_destroy")
 
 
 # -- convenience object --------------------------------------------------------
@@ -699,6 +747,83 @@ class Ortho:
         handle, self.handle = self.handle, None  # destroyed once, also where that reports an error
         if handle is not None:
             ddl_ortho_destroy(handle)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001 - interpreter shutdown
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class Adam:
+    """AdamW steps over the tensors of flat buffers, on every rank's copy of the
+    parameters (owns a ddl_adam_t).  tensors: (offset, count), optionally with the
+    tensor's factors of lr and weight_decay, in elements; dtype: the gradient's;
+    state: "f32" or "8bit"."""
+
+    def __init__(self, tensors, dtype="f32", state="f32", betas=(0.9, 0.999), eps=1e-8):
+        self.tensors = [tuple(t) for t in tensors]
+        self.dtype, self.state = dtype, state
+        self.extent = max((int(t[0]) + int(t[1]) for t in self.tensors), default=0)
+        import torch
+        self._grad, self._f32, self._i64 = _torch_dtype(dtype), torch.float32, torch.int64
+        self._state = {"f32": (torch.float32,), "8bit": (torch.uint8, torch.float8_e4m3fn)}[state]
+        self.handle = None
+        self.handle = ddl_adam_create(self.tensors, OPERAND_DTYPES[dtype], 8 if state == "8bit" else 32)
+        ddl_adam_set_betas(self.handle, *betas, eps)
+        self.n_blocks = ddl_adam_blocks(self.handle)
+
+    def _flat(self, t, dtypes, name, n=None):
+        n = self.extent if n is None else n
+        if t.dim() != 1 or t.numel() < n or t.dtype not in dtypes or not t.is_cuda or (t.numel() > 1 and t.stride(0) != 1):
+            raise ValueError(f"{name}: expected a contiguous CUDA vector of {dtypes[0]} with at least {n} elements")
+        return t
+
+    def new_state(self, device="cuda"):
+        """The states before the first step, as step() takes them: m, v, step and (8 bits) scales."""
+        import torch
+        state = {k: torch.zeros(self.extent, dtype=self._state[0], device=device) for k in ("m", "v")}
+        state["step"] = torch.zeros(1, dtype=torch.int64, device=device)
+        if self.state == "8bit":
+            state["scales"] = torch.zeros(2, self.n_blocks, device=device)
+        return state
+
+    def step(self, grad, params, m, v, step, lr, weight_decay=0.0, scales=None, operands=None, grad_scale=1.0, max_norm=0.0,
+             norm=None, stream=None):
+        """Updates every copy in params (a list, one per rank), the states and
+        the step count (one int64 on the device) in place; writes the copies'
+        16-bit operands and the gradient's norm where they are given."""
+        f32 = (self._f32,)
+        out_dtype = DDL_FP16
+        if operands is not None:
+            if len(operands) != len(params):
+                raise ValueError(f"operands: {len(operands)} buffers for {len(params)} copies")
+            kinds = {"torch.float16": DDL_FP16, "torch.bfloat16": DDL_BF16}
+            if any(str(o.dtype) not in kinds for o in operands[:1]):
+                raise ValueError(f"operands: dtype {operands[0].dtype}, expected torch.float16 or torch.bfloat16")
+            out_dtype = kinds[str(operands[0].dtype)] if len(operands) else DDL_FP16
+            operands = [self._flat(o, (operands[0].dtype,), "operands") for o in operands]
+        if scales is not None:
+            if self.state != "8bit" or not scales.is_contiguous():
+                raise ValueError("scales: a contiguous tensor, with 8-bit states only")
+            scales = self._flat(scales.view(-1), f32, "scales", 2 * self.n_blocks)
+            if scales.numel() != 2 * self.n_blocks:
+                raise ValueError(f"scales: expected {2 * self.n_blocks} elements")
+        ddl_adam_step(self.handle, self._flat(grad, (self._grad,), "grad"), [self._flat(p, f32, "params") for p in params],
+                      operands, out_dtype, self._flat(m, self._state, "m"), self._flat(v, self._state, "v"), scales,
+                      self._flat(step, (self._i64,), "step", 1), lr, weight_decay, grad_scale, max_norm,
+                      None if norm is None else self._flat(norm, f32, "norm", 1), stream)
+
+    def close(self):
+        handle, self.handle = self.handle, None  # destroyed once, also where that reports an error
+        if handle is not None:
+            ddl_adam_destroy(handle)
 
     def __del__(self):
         try:

@@ -517,6 +517,74 @@ ddl_status_t ddl_ortho_selftest_wait_timeout(ddl_ortho_t ortho, uint32_t limit_u
                                              uint32_t loads_even, uint32_t loads_odd);
 ddl_status_t ddl_ortho_destroy(ddl_ortho_t ortho);
 
+/* ---------------------------------------------------------------------------
+ * AdamW over many tensors at once.  What the Muon step leaves alone (embeddings,
+ * heads, norms, biases), or every tensor: one launch updates all tensors of the
+ * flat buffers, on every rank's copy of the parameters, from the averaged
+ * gradient.  With t the number of this step (1, 2, ...),
+ *   g' = c g;   m = beta1 m + (1 - beta1) g';   v = beta2 v + (1 - beta2) g'^2
+ *   p = p (1 - lr wd) - lr / (1 - beta1^t)  m / (sqrt(v / (1 - beta2^t)) + eps)
+ * where c = grad_scale, times min(1, max_norm / (norm + 1e-6)) if max_norm > 0,
+ * norm = |grad_scale| times the 2-norm of the gradients of all tensors; lr and
+ * wd are the call's, times the tensor's factors.  Products and sums are
+ * binary32, rounded one by one; the norm is summed in binary64.
+ *
+ * States: binary32, or 8 bits with a binary32 scale per block of 128 elements
+ * (counted from each tensor's first; its last block may be shorter).  m is
+ * kept as e4m3 numbers x, m = x s with s = (largest |m| of the block) / 448,
+ * and of v the square root is kept likewise.  A root that is not zero is never
+ * kept as zero; a block whose largest value is below 2^-100 is kept as zeros,
+ * and an infinite or NaN value as NaN.  The step itself uses the new m and v
+ * before they are rounded.  All-zero buffers are the states before step 1.
+ *
+ * A handle's device binding, threads, ownership and overlap rules are those of
+ * the linear layers; its device memory is allocated by the first GPU call.
+ * Non-finite gradients go through the formulas as IEEE arithmetic has it. */
+
+typedef struct {
+  size_t offset, count; /* elements of the flat buffers */
+  float lr_scale;       /* of lr, for this tensor */
+  float decay_scale;    /* of weight_decay; 0 for tensors that do not decay */
+} ddl_tensor_t;
+
+typedef struct ddl_adam* ddl_adam_t;
+
+/* n_tensors >= 1 tensors of 1..2^48 elements that do not overlap; elements
+ * outside of them are neither read nor written.  grad_dtype DDL_FP32 or
+ * DDL_FP16 (DDL_BF16: DDL_ERR_UNSUPPORTED); state_bits 32 or 8.  The constants
+ * start as beta1 = 0.9, beta2 = 0.999, eps = 1e-8.  The array is copied.  Host-only. */
+ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dtype_t grad_dtype, int state_bits,
+                             ddl_adam_t* out);
+
+/* Other constants, 0 <= beta < 1 and eps > 0 (in binary32, too).  Host-only. */
+ddl_status_t ddl_adam_set_betas(ddl_adam_t adam, double beta1, double beta2, double eps);
+
+/* Blocks of 128 of all tensors: the scales of one 8-bit state.  Host-only. */
+ddl_status_t ddl_adam_blocks(ddl_adam_t adam, size_t* n);
+
+/* One step on n_copies (1..256) parameter copies, each updated from its own
+ * values.  All buffers are flat, distinct, and aligned to their type.
+ *  grad            the averaged gradient, of the handle's type
+ *  operand_bufs    NULL, or a 16-bit buffer per copy (operand_dtype: DDL_FP16 or
+ *                  DDL_BF16) that receives the new parameters, rounded: the
+ *                  layers' weights
+ *  m, v            the states, binary32 or one byte an element
+ *  scales          8-bit states: m's block scales, then v's, tensor by tensor in
+ *                  the order of ddl_adam_create (2 x ddl_adam_blocks); else NULL
+ *  step            one number in device memory: steps done so far, >= 0.  The call
+ *                  adds one, so that a captured call replays as the next step
+ *  max_norm        0: no clipping
+ *  norm            NULL, or one binary32 in device memory that receives the norm
+ * One launch, and one before it where a norm is asked for.  Repeated calls on
+ * the same values give the same bits. */
+ddl_status_t ddl_adam_step(ddl_adam_t adam, const void* grad, int n_copies, float* const* param_bufs,
+                           void* const* operand_bufs, ddl_dtype_t operand_dtype, void* m, void* v, float* scales,
+                           int64_t* step, float lr, float weight_decay, float grad_scale, float max_norm, float* norm,
+                           void* stream);
+
+/* Frees the handle and its tables, whatever it returns.  NULL is accepted. */
+ddl_status_t ddl_adam_destroy(ddl_adam_t adam);
+
 /* A static string for a status code. */
 const char* ddl_status_string(ddl_status_t status);
 
