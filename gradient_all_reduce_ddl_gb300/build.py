@@ -20,9 +20,10 @@ BUILD = os.path.join(ROOT, "_build", "ddl")
 
 SOURCES = ["plan.cpp", "ddl_api.cu", "fold_kernels.cu", "step_kernels.cu", "noalloc.cu", "sgd_kernels.cu",
            "product_kernels.cu", "product_selftest.cu", "linear_kernels.cu", "linear_api.cu", "ortho_kernels.cu",
-           "ortho_api.cu", "adam_kernels.cu", "adam_api.cu"]
+           "ortho_api.cu", "xent_kernels.cu", "xent_api.cu", "adam_kernels.cu", "adam_api.cu"]
 # contractions with no bit-exact contract: fused multiply-adds allowed
-FMA_SOURCES = {"product_kernels.cu", "product_selftest.cu", "linear_kernels.cu", "ortho_kernels.cu"}
+FMA_SOURCES = {"product_kernels.cu", "product_selftest.cu", "linear_kernels.cu", "ortho_kernels.cu",
+               "xent_kernels.cu"}
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-fmad=false", "-Xcompiler", "-fPIC,-Wall",
          "-I", INCLUDE, "-I", CSRC]

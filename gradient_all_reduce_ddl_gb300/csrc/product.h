@@ -34,7 +34,9 @@ enum EpilogueKind : int {
   kEpiStore = 1,   // out = D (+ out)
   kEpiGram = 2,    // planes of D, and of its transpose
   kEpiPoly = 3,    // planes of b C + c D (C, D symmetric), and of the transpose
-  kEpiApply = 4    // planes of a C + D
+  kEpiApply = 4,   // planes of a C + D
+  kEpiLoss = 5,    // logits z = D + bias: what their softmax needs (Softmax)
+  kEpiGrad = 6     // planes of the loss's gradient in the logits (Softmax)
 };
 
 // One product.  A is M x K, B is N x K; a_mn / b_mn: stored with the rows
@@ -91,6 +93,27 @@ struct GiveUp {
   uint32_t loads[2] = {kNever, kNever};  // K blocks after which a CTA's loads stop (even and odd CTA of a pair)
 };
 
+// kEpiLoss and kEpiGrad: the logits are D (M tokens x N entries of the vocabulary) plus the bias.
+struct Softmax {
+  const int64_t* labels;
+  int64_t first, vocab;   // these are the logits of entries first, first + 1, ... of a vocabulary
+  const void* bias;       // NULL: none
+  int32_t bias_vec;       // it begins at a 16-byte boundary
+  // kEpiLoss: of every token (rows of `tokens`) and part of the vocabulary, without the label's logit
+  int64_t tokens;
+  float2* part;      // the largest logit and the sum of exp(z - largest)
+  float* part_sum;   // NULL, or the sum of the logits (with the label's)
+  float* picked;     // the label's logit, where it is one of these
+  // kEpiGrad: dz = coef (exp(z - lse) - off - on [entry is the label]), 0 for tokens whose label is outside [0, vocab)
+  const float* lse;
+  const float* coef;   // NULL: ones
+  const float* scale;  // NULL, or what dz's planes are multiplied by
+  float on, off;
+  int32_t planes;      // 1 or 2
+  float* db;           // NULL, or the sums of dz (x scale) over every 32 tokens, or over a split tile's shares of them
+  int64_t ld_db;
+};
+
 // Launch record.  Grouped launches read products, tiles and maps from device
 // memory; single launches carry up to two products and their maps here.
 struct ProductLaunch {
@@ -110,6 +133,8 @@ struct ProductLaunch {
   int32_t chunked;          // kEpiLinear: the contraction is longer than its chunk (tiles of 64 columns or more)
   int32_t bf16;             // operands are bfloat16, else binary16
   uint32_t* err;
+  const float* post;        // kEpiStore: NULL, or a further factor of the sums, in device memory
+  Softmax soft;             // kEpiLoss, kEpiGrad
   float ca, cb, cc;         // Newton-Schulz coefficients
   GiveUp give_up;           // read by launch_product_selftest's kernels only
 };
@@ -135,6 +160,6 @@ bool make_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, 
 bool make_map32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t ld);
 
 // Error word bits of these kernels.
-enum : uint32_t { kErrProductWait = 16u };
+enum : uint32_t { kErrProductWait = 16u, kErrLabel = 32u };
 
 }  // namespace ddl

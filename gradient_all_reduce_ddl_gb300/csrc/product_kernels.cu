@@ -77,8 +77,10 @@ constexpr bool kSelfTest = false;
 
 // What a launch is for; each has its own epilogues (and registers: one that spilled would go to L2 for it, since shared
 // memory leaves no L1).
-enum : int { kForward, kBackward, kSteps, kForwardLong };
+enum : int { kForward, kBackward, kSteps, kForwardLong, kLoss, kGrad };
 __host__ __device__ constexpr bool is_forward(int mode) { return mode == kForward || mode == kForwardLong; }
+// One product, carried in the launch record, whose operands' rows are contiguous along the contraction.
+__host__ __device__ constexpr bool is_single(int mode) { return mode != kBackward && mode != kSteps; }
 
 // Per CTA: a pair (tile_n 256) splits both operands' rows between its CTAs.
 __host__ __device__ constexpr int b_rows(int bn) { return bn == 256 ? 128 : bn; }
@@ -729,6 +731,326 @@ __device__ __forceinline__ void joined_mirror(const Product& P, uint32_t base, i
   }
 }
 
+// -- softmax epilogues ---------------------------------------------------------------
+//
+// Loss: with the largest logit m and the sum s = sum exp(z - m) of every part of the vocabulary, lse = log sum exp z is the
+// logarithm of one more such sum over the parts.  The label's own logit is kept out of m and s and stored apart: the loss
+// of a token that the model is sure of, log(1 + s exp(m - z_label)), would be lost in the rounding of lse.
+// Gradient: exp(z - lse) needs nothing of other entries, so the logits' products are done again and dz is made from them.
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// exp(x) as 2^(x log2 e): 0 for -infinity, NaN for NaN.
+__device__ __forceinline__ float exp_of(float x) { return exp2_fast(x * kLog2e); }
+
+__device__ __forceinline__ float bias_one(const ProductLaunch& p, int n) {
+  return from16(__ldg(static_cast<const uint16_t*>(p.soft.bias) + n), p.inl[0].type);
+}
+
+// Adds the bias of 16 entries n.. (entries from N on get none).
+__device__ __forceinline__ void add_bias16(const ProductLaunch& p, float* v, int n) {
+  const Product& P = p.inl[0];
+  if (p.soft.bias_vec && n + 16 <= P.N) {
+    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.soft.bias) + n);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      float t[8];
+      unpack8(__ldg(from + g), P.type, t);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[8 * g + k] += t[k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 16; ++k)
+      if (n + k < P.N) v[k] += bias_one(p, n + k);
+  }
+}
+
+// The sum of exp(v - most) over values of which most is the largest: 0 where all are -infinity, infinite where +infinity is
+// among them.
+template <int N>
+__device__ __forceinline__ float exp_sum(const float (&v)[N], float most) {
+  const float m = fabsf(most) == INFINITY ? 0.f : most;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k & 3] += exp_of(v[k] - m);
+  return (s[0] + s[1]) + (s[2] + s[3]);
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+// A thread's half of a tile's row: token m, of every 32 columns from col0 the 16 of `half`.
+template <int BN>
+__device__ __forceinline__ void loss_row(const ProductLaunch& p, float (&v)[BN / 2], int m, int half, int col0) {
+  const Product& P = p.inl[0];
+  const Softmax& e = p.soft;
+  const auto column = [&](int k) { return col0 + (k >> 4) * kSlab + half * (kSlab / 2) + (k & 15); };
+  if (e.bias) {
+#pragma unroll
+    for (int k = 0; k < BN / 2; k += 16) add_bias16(p, v + k, column(k));
+  }
+  const bool edge = col0 + BN > P.N;
+  const bool in = m < P.M;
+  const int64_t at = (int64_t)(col0 / BN * 2 + half) * e.tokens + m;
+  if (e.part_sum) {
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < BN / 2; ++k) s[k & 3] += !edge || column(k) < P.N ? v[k] : 0.f;
+    if (in) e.part_sum[at] = (s[0] + s[1]) + (s[2] + s[3]);
+  }
+  if (edge) {
+#pragma unroll
+    for (int k = 0; k < BN / 2; ++k)
+      if (column(k) >= P.N) v[k] = -INFINITY;
+  }
+  const int64_t label = in ? __ldg(e.labels + m) : -1;
+  if (label >= col0 && label < min(col0 + BN, P.N)) {
+    const int n = (int)label;
+    if ((n - col0) / 16 % 2 == half) {
+      float z = 0.f;
+#pragma unroll
+      for (int k = 0; k < BN / 2; ++k)
+        if (column(k) == n) {
+          z = v[k];
+          v[k] = -INFINITY;
+        }
+      e.picked[m] = z;
+    }
+  }
+  float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+  for (int k = 0; k < BN / 2; ++k) most[k & 3] = fmaxf(most[k & 3], v[k]);
+  const float mx = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+  const float s = exp_sum(v, mx);
+  if (in) e.part[at] = make_float2(mx, s);
+}
+
+// Rows [r0, r1) of a tile whose contraction was split: a warp along a row.
+template <int BN>
+__device__ __forceinline__ void loss_rows(const ProductLaunch& p, int row0, int col0, int lane, int ew, int r0, int r1,
+                                          const ClusterSums sums) {
+  constexpr int kFours = BN <= 128 ? 1 : BN / 128;
+  const Product& P = p.inl[0];
+  const Softmax& e = p.soft;
+#pragma unroll 1
+  for (int r = r0 + ew; r < r1; r += kEpiWarps) {
+    const int m = row0 + r;
+    if (m >= P.M) break;
+    const int64_t label = __ldg(e.labels + m);
+    float v[4 * kFours], all = 0.f, most = -INFINITY;
+#pragma unroll
+    for (int f = 0; f < kFours; ++f) {
+      const int c = 128 * f + 4 * lane;
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      if (c < BN) sums.four((r * pitch(BN) + c) * 4, t);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int n = col0 + c + k;
+        if (c < BN && n < P.N) {
+          if (e.bias) t[k] += bias_one(p, n);
+          all += t[k];
+          if (n == label) {
+            e.picked[m] = t[k];
+            t[k] = -INFINITY;
+          }
+        } else {
+          t[k] = -INFINITY;
+        }
+        most = fmaxf(most, t[k]);
+        v[4 * f + k] = t[k];
+      }
+    }
+    most = warp_max(most);
+    const float s = warp_sum(exp_sum(v, most));
+    const int64_t at = (int64_t)(col0 / BN) * e.tokens + m;
+    if (e.part_sum) all = warp_sum(all);
+    if (lane == 0) {
+      e.part[at] = make_float2(most, s);
+      if (e.part_sum) e.part_sum[at] = all;
+    }
+  }
+}
+
+// Few tokens: the tile's rows are entries of the vocabulary, [r0, r0 + rows) of them from row0, its columns tokens from
+// col0; a warp takes four tokens at a time.  rows is 16, 32, 64 or 128.
+template <int COLS, class Sums>
+__device__ __forceinline__ void loss_columns(const ProductLaunch& p, int row0, int col0, int lane, int ew, int r0, int rows,
+                                             int part, const Sums sums) {
+  constexpr int kRows = kTileM / 32;  // a lane's rows
+  const Product& P = p.inl[0];        // P.M entries, P.N tokens
+  const Softmax& e = p.soft;
+#pragma unroll 1
+  for (int c = 4 * ew; c < COLS; c += 4 * kEpiWarps) {
+    if (col0 + c >= P.N) break;
+    float v[4][kRows], all[4] = {0.f, 0.f, 0.f, 0.f};
+    int64_t label[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) label[k] = col0 + c + k < P.N ? __ldg(e.labels + col0 + c + k) : -1;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const int r = lane + 32 * i, n = row0 + r0 + r;
+      const bool in = r < rows && n < P.M;
+      float t[4] = {0.f, 0.f, 0.f, 0.f};
+      if (in) sums.four(((r0 + r) * pitch(COLS) + c) * 4, t);
+      const float b = in && e.bias ? bias_one(p, n) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        t[k] += b;
+        if (in) all[k] += t[k];
+        if (in && n == label[k]) e.picked[col0 + c + k] = t[k];
+        v[k][i] = in && n != label[k] ? t[k] : -INFINITY;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float most = v[k][0];
+#pragma unroll
+      for (int i = 1; i < kRows; ++i) most = fmaxf(most, v[k][i]);
+      most = warp_max(most);
+      const float s = warp_sum(exp_sum(v[k], most));
+      if (e.part_sum) all[k] = warp_sum(all[k]);
+      const int64_t at = (int64_t)part * e.tokens + col0 + c + k;
+      if (lane == 0 && col0 + c + k < P.N) {
+        e.part[at] = make_float2(most, s);
+        if (e.part_sum) e.part_sum[at] = all[k];
+      }
+    }
+  }
+}
+
+// What the gradient needs of a token.
+struct GradRow {
+  float lse, by;  // by: its coefficient times the planes' scale
+  int label;      // counted from the piece's first entry; outside of it: -1
+  bool valid;
+  __device__ __forceinline__ void load(const Softmax& e, int m, int rows, int entries) {
+    lse = by = 0.f;
+    label = -1;
+    valid = false;
+    if (m >= rows) return;
+    const int64_t y = __ldg(e.labels + m);
+    valid = y >= 0 && y < e.vocab;
+    if (y >= e.first && y < e.first + entries) label = (int)(y - e.first);
+    lse = __ldg(e.lse + m);
+    by = (e.coef ? __ldg(e.coef + m) : 1.f) * (e.scale ? __ldcg(e.scale) : 1.f);
+  }
+  // dz (x scale) of entry n, whose logit is z
+  __device__ __forceinline__ float of(float z, int n, const Softmax& e) const {
+    float d = exp_of(z - lse) - e.off;
+    if (n == label) d -= e.on;
+    return valid ? d * by : 0.f;
+  }
+};
+
+// The planes of two neighbours: 16 bits, and what their rounding lost (in binary16 2^11 times that).  An infinite or NaN
+// value is in the first plane alone.
+__device__ __forceinline__ void grad_planes(float x, float y, int type, uint32_t* hi, uint32_t* lo) {
+  *hi = to16x2(x, y, type);
+  const float2 h = from16x2(*hi, type);
+  const float up = type == kBF16 ? 1.f : 2048.f;
+  x = fabsf(h.x) <= FLT_MAX ? (x - h.x) * up : 0.f;
+  y = fabsf(h.y) <= FLT_MAX ? (y - h.y) * up : 0.f;
+  *lo = to16x2(x, y, type);
+}
+
+// The sums over a warp's 32 rows of its lanes' 16 columns each: the lane's are of column (lane / 2) on return.  Each step
+// halves the columns that a lane goes on with.
+__device__ __forceinline__ float column_sums16(const float* v, int lane) {
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) x[k] = v[k];
+#pragma unroll
+  for (int d = 16, w = 8; d > 1; d >>= 1, w >>= 1) {
+    const bool up = lane & d;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k >= w) break;
+      const float give = up ? x[k] : x[k + w], keep = up ? x[k + w] : x[k];
+      x[k] = keep + __shfl_xor_sync(0xffffffffu, give, d);
+    }
+  }
+  return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
+}
+
+// 16 columns n.. of row m, from logits to planes in the slab.
+__device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, const GradRow& g, uint32_t buf, int row, int half,
+                                          int m0, int n) {
+  const Product& P = p.inl[0];
+  const Softmax& e = p.soft;
+  if (e.bias) add_bias16(p, v, n);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) v[k] = g.of(v[k], n + k, e);
+  uint32_t hi[8], lo[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], P.type, &hi[k], &lo[k]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t at = piece(buf, row, 2 * half + h);
+    st_shared16(at, make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]));
+    if (e.planes == 2) st_shared16(at + kPlaneBytes, make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]));
+  }
+  if (e.db) {
+    const int lane = row & 31, c = n + (lane >> 1);
+    const float s = column_sums16(v, lane);
+    if (!(lane & 1) && c < P.N && m0 + (row & ~31) < P.M) e.db[(int64_t)((m0 + row) >> 5) * e.ld_db + c] = s;
+  }
+}
+
+// Rows [r0, r1) of a tile whose contraction was split: a warp along a row, four columns a lane.  The planes' rows are
+// padded to 8 columns, so that a group of 4 that begins inside the matrix is whole.
+template <int BN>
+__device__ __forceinline__ void grad_rows(const ProductLaunch& p, int row0, int col0, int lane, int ew, int r0, int r1, int q,
+                                          int S, uint32_t staging, const ClusterSums sums) {
+  const Product& P = p.inl[0];
+  const Softmax& e = p.soft;
+#pragma unroll 1
+  for (int c = 4 * lane; c < BN; c += 128) {
+    const int n = col0 + c;
+    float total[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int r = r0 + ew; r < r1; r += kEpiWarps) {
+      const int m = row0 + r;
+      if (m >= P.M || n >= P.N) break;
+      GradRow g;
+      g.load(e, m, P.M, P.N);
+      float v[4];
+      sums.four((r * pitch(BN) + c) * 4, v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (e.bias && n + k < P.N) v[k] += bias_one(p, n + k);
+        v[k] = g.of(v[k], n + k, e);
+        total[k] += v[k];
+      }
+      uint32_t hi[2], lo[2];
+      grad_planes(v[0], v[1], P.type, &hi[0], &lo[0]);
+      grad_planes(v[2], v[3], P.type, &hi[1], &lo[1]);
+      *reinterpret_cast<uint2*>(P.p_hi + (int64_t)m * P.ldp + n) = make_uint2(hi[0], hi[1]);
+      if (e.planes == 2) *reinterpret_cast<uint2*>(P.p_lo + (int64_t)m * P.ldp + n) = make_uint2(lo[0], lo[1]);
+    }
+    if (e.db) {  // the same for all warps
+      st_shared4(staging + (ew * 128 + 4 * lane) * 4, total);
+      bar_sync_epilogue();
+      if (ew < 4) {
+        const int k = 32 * ew + lane, at = col0 + (c - 4 * lane) + k;
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < kEpiWarps; ++w) s += ld_shared(staging + (w * 128 + k) * 4);
+        if (at < P.N && row0 < P.M) e.db[((int64_t)(row0 / kTileM) * S + q) * e.ld_db + at] = s;
+      }
+      bar_sync_epilogue();
+    }
+  }
+}
+
 // One walk over the slabs of a CTA's tiles: the warp that moves the boxes has two, for what it prepares and for what
 // it stores.
 template <int BN, int MODE>
@@ -744,7 +1066,7 @@ struct Slabs {
     if (t >= end) return;
     const Place pl = place<BN, MODE>(p, t, step);
     row0 = pl.row0, col0 = pl.col0, following = pl.next;
-    const Product& P = is_forward(MODE) ? p.inl[0] : *pl.P;
+    const Product& P = is_single(MODE) ? p.inl[0] : *pl.P;
     in0 = P.in0, in1 = P.in1, out0 = P.out0, out1 = P.out1;
     f32 = MODE == kBackward && P.out_type == kF32;
     rows = P.M;
@@ -872,7 +1194,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
               bar_expect(bar, stage_bytes(BN));
             }
 #pragma unroll
-            for (int h = 0; h < (is_forward(MODE) ? 1 : kTileM / kBoxRows); ++h) {
+            for (int h = 0; h < (is_single(MODE) ? 1 : kTileM / kBoxRows); ++h) {
               const int row = pl.row0 + my_rows + h * kBoxRows;
               const int x = sh.a_mn ? row : kb * kBlockK, y = sh.a_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
@@ -881,7 +1203,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
                 tma_box(sa + h * kBoxBytes, ma, bar, x, y);
             }
 #pragma unroll
-            for (int h = 0; h < (is_forward(MODE) ? 1 : (b_rows(BN) + kBoxRows - 1) / kBoxRows); ++h) {
+            for (int h = 0; h < (is_single(MODE) ? 1 : (b_rows(BN) + kBoxRows - 1) / kBoxRows); ++h) {
               const int row = pl.col0 + my_rows + h * kBoxRows;
               const int x = sh.b_mn ? row : kb * kBlockK, y = sh.b_mn ? kb * kBlockK : row;
               if constexpr (PAIR)
@@ -1019,11 +1341,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     for (int t = first, next; t < end; t = next) {
       const Place pl = place<BN, MODE>(p, t, step);
       next = pl.next;
-      const Product& G = is_forward(MODE) ? p.inl[0] : *pl.P;
+      const Product& G = is_single(MODE) ? p.inl[0] : *pl.P;
       const Shape sh(G, pl.k0, pl.k1, q, S);
       if (t == first) griddep_wait();
       // what the epilogue reads from HBM comes to L2 while the products run
-      if constexpr (MODE != kSteps) {
+      if constexpr (is_forward(MODE) || MODE == kBackward) {
         if (S == 1 && !G.swap && !p.boxes) {
           const int m = pl.row0 + my_rows + row;
           if (m < G.M) {
@@ -1044,8 +1366,12 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
       }
       // in registers (no indexed access); a forward launch's only product is read as a parameter
-      const Product copy = is_forward(MODE) ? Product{} : G;
-      const Product& P = is_forward(MODE) ? p.inl[0] : copy;
+      const Product copy = is_single(MODE) ? Product{} : G;
+      const Product& P = is_single(MODE) ? p.inl[0] : copy;
+      const float post = MODE == kBackward && p.post ? __ldcg(p.post) : 1.f;
+      GradRow grad_row = {};
+      if constexpr (MODE == kGrad)
+        if (S == 1) grad_row.load(p.soft, pl.row0 + my_rows + row, P.M, P.N);
       const uint32_t lanes = (uint32_t)(quad * 32) << 16;
       // The sums of this thread's 16 columns of the slabs in turn: from TMEM, or added up in registers chunk by chunk.
       float acc[DIRECT ? kHalf : BN / 2];
@@ -1074,7 +1400,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
 #pragma unroll
         for (int k = 0; k < BN / 2; ++k) acc[k] = 0.f;
         for (int ps = 0; ps < sh.n_pass; ++ps) {
-          const float scale = sh.scale(ps);
+          const float scale = MODE == kBackward ? sh.scale(ps) * post : sh.scale(ps);
           const int chunk = sh.chunk(ps);
           for (int k0 = sh.kb0; k0 < sh.kb1; k0 += chunk) {
             if (!wait_sums()) {
@@ -1176,8 +1502,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         }
       }
       bool boxes = false;
-      if constexpr (BN >= 128) boxes = MODE == kSteps || p.boxes;
-      if (boxes) {
+      if constexpr (BN >= 128) boxes = MODE == kSteps || MODE == kGrad || (MODE != kLoss && p.boxes);
+      if constexpr (MODE == kLoss) {
+        if (!P.swap) {
+          if (ok) loss_row<BN>(p, acc, pl.row0 + my_rows + row, half, pl.col0);
+        } else {
+#pragma unroll 1
+          for (int sl = 0; sl < kSlabs; ++sl) {
+            bar_sync_epilogue();  // the slab before has been read
+#pragma unroll
+            for (int k = 0; k < kHalf; k += 4) st_shared4(staging + (row * kSlabPitch + half * kHalf + k) * 4, &acc[k]);
+            next_slab();
+            bar_sync_epilogue();
+            if (ok)
+              loss_columns<kSlab>(p, pl.row0, pl.col0 + sl * kSlab, lane, ew, 0, kTileM, pl.row0 / kTileM, OwnSums{staging});
+          }
+        }
+      } else if (boxes) {
         if constexpr (BN >= 128) {
           uint4 bias_ahead[2] = {};
           if constexpr (is_forward(MODE)) load_bias(P, pl.col0 + half * kHalf, bias_ahead);
@@ -1190,7 +1531,10 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             load_slab(sl);
-            if (!skip)
+            if constexpr (MODE == kGrad)
+              slab_grad(p, acc, grad_row, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
+                        pl.col0 + sl * kSlab + half * kHalf);
+            else if (!skip)
               slab_values<MODE>(P, p, acc, bias, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
                                 pl.col0 + sl * kSlab + half * kHalf, pl.mirror);
             fence_async();
@@ -1202,7 +1546,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             next_slab();
           }
         }
-      } else if constexpr (MODE != kSteps) {
+      } else if constexpr (is_forward(MODE) || MODE == kBackward) {
 #pragma unroll 1
         for (int sl = 0; sl < kSlabs; ++sl) {
           if (ok) load_slab(sl);
@@ -1240,6 +1584,15 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             bar_sync_epilogue();
             joined_mirror<BN>(P, ring, pl.row0 + my_rows, pl.col0, q * share, share, ew * 32 + lane);
           }
+        } else if constexpr (MODE == kLoss) {
+          const int share = kTileM / S;
+          if (!P.swap)
+            loss_rows<BN>(p, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, sums);
+          else
+            loss_columns<BN>(p, pl.row0, pl.col0, lane, ew, q * share, share, pl.row0 / kTileM * S + q, sums);
+        } else if constexpr (MODE == kGrad) {
+          const int share = kTileM / S;
+          grad_rows<BN>(p, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, q, S, staging, sums);
         } else {
           // this CTA finishes its share of the rows
           const int share = kTileM / S;
@@ -1403,6 +1756,13 @@ cudaError_t launch_product(const ProductLaunch& p, int tile_n, int sms, cudaStre
   if (p.g_products) return tile_n == 256 ? launch_one<256, kSteps>(p, sms, stream) : launch_one<128, kSteps>(p, sms, stream);
   if (p.inl[0].epi == kEpiStore)
     return tile_n == 256 ? launch_one<256, kBackward>(p, sms, stream) : launch_one<128, kBackward>(p, sms, stream);
+  if (p.inl[0].epi == kEpiGrad)
+    return tile_n == 256 ? launch_one<256, kGrad>(p, sms, stream) : launch_one<128, kGrad>(p, sms, stream);
+  if (p.inl[0].epi == kEpiLoss) {
+    if (tile_n == 256) return launch_one<256, kLoss>(p, sms, stream);
+    if (tile_n == 128) return launch_one<128, kLoss>(p, sms, stream);
+    return tile_n == 64 ? launch_one<64, kLoss>(p, sms, stream) : launch_one<32, kLoss>(p, sms, stream);
+  }
   if (p.chunked) {
     if (tile_n == 256) return launch_one<256, kForwardLong>(p, sms, stream);
     return tile_n == 128 ? launch_one<128, kForwardLong>(p, sms, stream) : launch_one<64, kForwardLong>(p, sms, stream);

@@ -1,0 +1,170 @@
+// xent_kernels.cu -- the passes around the products of the softmax cross entropy:
+// joining the vocabulary's parts, the planes' scale, the bias gradient, rounding
+// dx's sums.  All of them read what the products left in L2; small calls are bound by
+// their launches.
+#include "activation.cuh"
+#include "product.h"
+#include "tc_ptx.cuh"
+#include "xent_kernels.h"
+
+namespace ddl {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+// sum exp(z - most) over parts of it
+struct LogSum {
+  float most, sum;
+  __device__ __forceinline__ void add(float m, float s) {
+    const float top = fmaxf(most, m);
+    // equal ones, infinite ones among them, keep their sums; a NaN in a sum stays
+    sum = sum * (most == top ? 1.f : expf(most - top)) + s * (m == top ? 1.f : expf(m - top));
+    most = top;
+  }
+};
+
+// TX tokens per CTA, its other threads share out the parts.
+template <int TX>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ XentJoin p) {
+  constexpr int TY = kThreads / TX;
+  __shared__ float2 shared[TY][TX];
+  __shared__ float shared_sum[TY][TX];
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int64_t t = (int64_t)blockIdx.x * TX + tx;
+  LogSum l = {-INFINITY, 0.f};
+  float all = 0.f;
+  if (t < p.tokens) {
+#pragma unroll 4
+    for (int k = ty; k < p.n_parts; k += TY) {
+      const float2 u = __ldcg(p.part + (int64_t)k * p.ld + t);
+      l.add(u.x, u.y);
+    }
+    if (p.part_sum) {
+#pragma unroll 4
+      for (int k = ty; k < p.n_parts; k += TY) all += __ldcg(p.part_sum + (int64_t)k * p.ld + t);
+    }
+  }
+  shared[ty][tx] = make_float2(l.most, l.sum);
+  shared_sum[ty][tx] = all;
+#pragma unroll
+  for (int d = TY / 2; d; d >>= 1) {
+    __syncthreads();
+    if (ty < d) {
+      const float2 u = shared[ty + d][tx];
+      l.add(u.x, u.y);
+      all += shared_sum[ty + d][tx];
+      shared[ty][tx] = make_float2(l.most, l.sum);
+      shared_sum[ty][tx] = all;
+    }
+  }
+  if (ty > 0 || t >= p.tokens) return;
+  const int64_t y = p.labels[t];
+  float loss = 0.f, lse;
+  if (y < 0 || y >= p.vocab) {
+    lse = l.most + logf(l.sum);
+    if (y >= p.vocab) {
+      loss = NAN;
+      atomicOr(p.err, kErrLabel);
+    }
+  } else {
+    // lse - z, with z the label's logit: what the others add to it, or what is left of them
+    const float z = __ldcg(p.picked + t);
+    loss = z >= l.most ? log1pf(l.sum * expf(l.most - z)) : (l.most - z) + logf(l.sum + expf(z - l.most));
+    LogSum every = l;
+    every.add(z, 1.f);
+    lse = every.most + logf(every.sum);
+    if (p.part_sum) loss += p.smoothing * (z - all / (float)p.vocab);
+  }
+  if (p.loss) p.loss[t] = loss;
+  if (p.lse) p.lse[t] = lse;
+}
+
+__global__ void __launch_bounds__(1024) scale_kernel(const __grid_constant__ XentScale p) {
+  __shared__ uint32_t shared[32];
+  tc::griddep_launch();
+  tc::griddep_wait();
+  uint32_t most = 0;  // largest finite magnitude: as bits they order as the numbers do
+  for (int64_t t = threadIdx.x; t < p.tokens; t += 1024) {
+    const int64_t y = p.labels[t];
+    const uint32_t b = __float_as_uint(p.coef ? p.coef[t] : 1.f) & 0x7FFFFFFFu;
+    if (y >= 0 && y < p.vocab && b < 0x7F800000u && b > most) most = b;
+  }
+  most = __reduce_max_sync(0xFFFFFFFFu, most);
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = most;
+  __syncthreads();
+  if (threadIdx.x >= 32) return;
+  most = __reduce_max_sync(0xFFFFFFFFu, shared[threadIdx.x]);
+  if (threadIdx.x == 0) {
+    int e = 14 - ((int)(most >> 23) - 127);  // of subnormal numbers and zero: the most below
+    e = e > 120 ? 120 : e < -100 ? -100 : e;
+    p.scale[0] = __uint_as_float((uint32_t)(127 + e) << 23);
+    p.scale[1] = __uint_as_float((uint32_t)(127 - e) << 23);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) bias_kernel(const __grid_constant__ XentBias p) {
+  __shared__ float shared[kWarps][32];
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  float s = 0.f;
+  if (c < p.cols) {
+#pragma unroll 4
+    for (int64_t g = warp; g < p.groups; g += kWarps) s += __ldcg(p.part + g * p.ld + c);
+  }
+  shared[warp][lane] = s;
+  __syncthreads();
+  if (warp > 0 || c >= p.cols) return;
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) s += shared[w][lane];
+  if (p.scale) s *= __ldcg(p.scale);
+  if (p.f32) {
+    float* o = static_cast<float*>(p.db) + c;
+    *o = p.accumulate ? *o + s : s;
+  } else {
+    __half* o = static_cast<__half*>(p.db) + c;
+    *o = __float2half_rn(p.accumulate ? __half2float(*o) + s : s);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) round_kernel(const __grid_constant__ XentRound p) {
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t across = (p.cols + 255) / 256;
+  const int64_t r = blockIdx.x / across * kWarps + warp, c0 = blockIdx.x % across * 256 + lane;
+  if (r >= p.rows) return;
+  float v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = c0 + 32 * k < p.cols ? __ldcs(p.src + r * p.ld + c0 + 32 * k) : 0.f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (c0 + 32 * k < p.cols) p.dst[r * p.ldd + c0 + 32 * k] = to16(v[k], p.type);
+}
+
+}  // namespace
+
+cudaError_t launch_xent_join(const XentJoin& p, cudaStream_t stream) {
+  if (p.tokens >= 1024) return tc::launch_early(join_kernel<32>, dim3((unsigned)((p.tokens + 31) / 32)), kThreads, stream, p);
+  if (p.tokens >= 64) return tc::launch_early(join_kernel<8>, dim3((unsigned)((p.tokens + 7) / 8)), kThreads, stream, p);
+  return tc::launch_early(join_kernel<1>, dim3((unsigned)p.tokens), kThreads, stream, p);
+}
+
+cudaError_t launch_xent_scale(const XentScale& p, cudaStream_t stream) {
+  return tc::launch_early(scale_kernel, dim3(1), 1024, stream, p);
+}
+
+cudaError_t launch_xent_bias(const XentBias& p, cudaStream_t stream) {
+  return tc::launch_early(bias_kernel, dim3((unsigned)((p.cols + 31) / 32)), kThreads, stream, p);
+}
+
+cudaError_t launch_xent_round(const XentRound& p, cudaStream_t stream) {
+  const int64_t blocks = (p.rows + kWarps - 1) / kWarps * ((p.cols + 255) / 256);
+  if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  return tc::launch_early(round_kernel, dim3((unsigned)blocks), kThreads, stream, p);
+}
+
+}  // namespace ddl

@@ -1,0 +1,56 @@
+// xent_kernels.h -- the passes around the loss's products (internal).
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace ddl {
+
+// Joins the vocabulary's parts: lse and loss of every token.
+struct XentJoin {
+  const float2* part;     // [n_parts][ld]: largest logit and sum of exp(z - largest), without the label's
+  const float* part_sum;  // NULL, or sums of the logits
+  const float* picked;    // the label's logit
+  int64_t ld, tokens;
+  int32_t n_parts;
+  const int64_t* labels;
+  int64_t vocab;
+  float smoothing;
+  float* loss;  // NULL: not wanted
+  float* lse;   // NULL: not wanted
+  uint32_t* err;
+};
+cudaError_t launch_xent_join(const XentJoin& p, cudaStream_t stream);
+
+// scale[0] = a power of two that brings the largest coefficient of a token with a label into [2^14, 2^15), scale[1] its
+// inverse: binary16 then holds dz = coef (exp(z - lse) - ...) of every token, and small probabilities as normal numbers.
+struct XentScale {
+  const float* coef;  // NULL: ones
+  const int64_t* labels;
+  int64_t tokens, vocab;
+  float* scale;
+};
+cudaError_t launch_xent_scale(const XentScale& p, cudaStream_t stream);
+
+// db (+)= scale * the sums of `groups` rows.
+struct XentBias {
+  const float* part;  // [groups][ld]
+  int64_t ld, groups, cols;
+  const float* scale;  // NULL: 1
+  void* db;
+  int32_t f32, accumulate;
+};
+cudaError_t launch_xent_bias(const XentBias& p, cudaStream_t stream);
+
+// 16-bit rows of binary32 sums.
+struct XentRound {
+  const float* src;
+  int64_t ld;
+  uint16_t* dst;
+  int64_t ldd, rows, cols;
+  int32_t type;
+};
+cudaError_t launch_xent_round(const XentRound& p, cudaStream_t stream);
+
+}  // namespace ddl

@@ -45,6 +45,8 @@ EXPORTS = [
     "ddl_linear_create", "ddl_linear_forward", "ddl_linear_backward", "ddl_linear_check", "ddl_linear_destroy",
     "ddl_ortho_create", "ddl_ortho_set_polynomial", "ddl_ortho_run", "ddl_ortho_muon", "ddl_ortho_check",
     "ddl_ortho_destroy", "ddl_linear_selftest_wait_timeout", "ddl_ortho_selftest_wait_timeout",
+    "ddl_xent_create", "ddl_xent_forward", "ddl_xent_backward", "ddl_xent_check", "ddl_xent_selftest_wait_timeout",
+    "ddl_xent_destroy",
     "ddl_adam_create", "ddl_adam_set_betas", "ddl_adam_blocks", "ddl_adam_step", "ddl_adam_destroy",
 ]
 
@@ -114,6 +116,12 @@ _sig("ddl_ortho_check", _i, _vp, _vp)
 _sig("ddl_ortho_destroy", _i, _vp)
 _sig("ddl_ortho_selftest_wait_timeout", _i, _vp, *[ctypes.c_uint32] * 4)
 
+_sig("ddl_xent_create", _i, _sz, _sz, _sz, _i, _f, _P(_vp))
+_sig("ddl_xent_forward", _i, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _vp, _vp, _vp, _vp)
+_sig("ddl_xent_backward", _i, _vp, _sz, _vp, _sz, _vp, _sz, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp, _i, _i, _vp)
+_sig("ddl_xent_check", _i, _vp, _vp)
+_sig("ddl_xent_destroy", _i, _vp)
+_sig("ddl_xent_selftest_wait_timeout", _i, _vp, *[ctypes.c_uint32] * 4)
 _sig("ddl_adam_create", _i, _i, _P(ddl_tensor_t), _i, _i, _P(_vp))
 _sig("ddl_adam_set_betas", _i, _vp, *[ctypes.c_double] * 3)
 _sig("ddl_adam_blocks", _i, _vp, _P(_sz))
@@ -394,6 +402,37 @@ def ddl_ortho_selftest_wait_timeout(ortho, limit_us, products=_NEVER, loads_even
 
 def ddl_ortho_destroy(ortho):
     _ok(_lib.ddl_ortho_destroy(ortho), "ddl_ortho_destroy")
+
+
+def ddl_xent_create(max_tokens, in_features, vocab, dtype, smoothing=0.0):
+    h = ctypes.c_void_p()
+    _ok(_lib.ddl_xent_create(max_tokens, in_features, vocab, dtype, smoothing, ctypes.byref(h)), "ddl_xent_create")
+    return h
+
+
+def ddl_xent_forward(xent, tokens, x, ldx, w, ldw, bias, labels, loss, lse, stream=None):
+    """Device pointers (or None) and row strides in elements."""
+    _ok(_lib.ddl_xent_forward(xent, tokens, x, ldx, w, ldw, bias, labels, loss, lse, _stream_handle(stream)),
+        "ddl_xent_forward")
+
+
+def ddl_xent_backward(xent, tokens, x, ldx, w, ldw, bias, labels, lse, dloss, dx, lddx, dw, lddw, db, grad_dtype,
+                      accumulate=False, stream=None):
+    """Device pointers (or None) and row strides in elements."""
+    _ok(_lib.ddl_xent_backward(xent, tokens, x, ldx, w, ldw, bias, labels, lse, dloss, dx, lddx, dw, lddw, db, grad_dtype,
+                               1 if accumulate else 0, _stream_handle(stream)), "ddl_xent_backward")
+
+
+def ddl_xent_check(xent, stream=None):
+    _ok(_lib.ddl_xent_check(xent, _stream_handle(stream)), "ddl_xent_check")
+
+
+def ddl_xent_selftest_wait_timeout(xent, limit_us, products=_NEVER, loads_even=_NEVER, loads_odd=_NEVER):
+    _ok(_lib.ddl_xent_selftest_wait_timeout(xent, limit_us, products, loads_even, loads_odd), "ddl_xent_selftest_wait_timeout")
+
+
+def ddl_xent_destroy(xent):
+    _ok(_lib.ddl_xent_destroy(xent), "ddl_xent_destroy")
 
 
 def ddl_adam_create(tensors, grad_dtype, state_bits):
@@ -747,6 +786,65 @@ class Ortho:
         handle, self.handle = self.handle, None  # destroyed once, also where that reports an error
         if handle is not None:
             ddl_ortho_destroy(handle)
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:  # noqa: BLE001 - interpreter shutdown
+            pass
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        self.close()
+
+
+class CrossEntropy:
+    """Softmax cross entropy of a linear head z = x w^T + bias over a vocabulary,
+    and its backward pass; the logits are never kept (owns a ddl_xent_t).  Tensors
+    are the caller's, as for Linear; labels are int64, negative ones ignored; loss,
+    lse and dloss are binary32.  Nothing is recorded for autograd."""
+
+    def __init__(self, in_features, vocab, max_tokens, dtype="f16", smoothing=0.0):
+        self.n_in, self.vocab, self.max_tokens, self.dtype, self.smoothing = in_features, vocab, max_tokens, dtype, smoothing
+        self._dtype, self._f32 = _torch_dtype(dtype), _torch_dtype("f32")
+        import torch
+        self._i64 = torch.int64
+        self.handle = None
+        self.handle = ddl_xent_create(max_tokens, in_features, vocab, OPERAND_DTYPES[dtype], smoothing)
+
+    def forward(self, x, w, labels, loss, lse=None, bias=None, stream=None):
+        """Writes every token's loss (and the logarithm of its softmax sum, where given); returns loss.  Either may be None."""
+        t, d = x.shape[0], self._dtype
+        px, ldx = _matrix(x, t, self.n_in, d, "x")
+        pw, ldw = _matrix(w, self.vocab, self.n_in, d, "w")
+        ddl_xent_forward(self.handle, t, px, ldx, pw, ldw, _vector(bias, self.vocab, d, "bias"),
+                         _vector(labels, t, self._i64, "labels"), _vector(loss, t, self._f32, "loss"),
+                         _vector(lse, t, self._f32, "lse"), stream)
+        return loss
+
+    def backward(self, x, w, labels, lse, dloss=None, bias=None, dx=None, dw=None, db=None, accumulate=False, stream=None):
+        """From forward's lse and the gradient of every token's loss (None: ones) writes dx; writes dw and db, or adds to them."""
+        t, d = x.shape[0], self._dtype
+        some = dw if dw is not None else db
+        g, grad_dtype = (None, DDL_FP32) if some is None else (some.dtype, _grad_dtype(some))
+        px, ldx = _matrix(x, t, self.n_in, d, "x")
+        pw, ldw = _matrix(w, self.vocab, self.n_in, d, "w")
+        pdx, lddx = _matrix(dx, t, self.n_in, d, "dx")
+        pdw, lddw = _matrix(dw, self.vocab, self.n_in, g, "dw")
+        ddl_xent_backward(self.handle, t, px, ldx, pw, ldw, _vector(bias, self.vocab, d, "bias"),
+                          _vector(labels, t, self._i64, "labels"), _vector(lse, t, self._f32, "lse"),
+                          _vector(dloss, t, self._f32, "dloss"), pdx, lddx, pdw, lddw, _vector(db, self.vocab, g, "db"),
+                          grad_dtype, accumulate, stream)
+
+    def check(self, stream=None):
+        ddl_xent_check(self.handle, stream)
+
+    def close(self):
+        handle, self.handle = self.handle, None  # destroyed once, also where that reports an error
+        if handle is not None:
+            ddl_xent_destroy(handle)
 
     def __del__(self):
         try:

@@ -518,6 +518,64 @@ ddl_status_t ddl_ortho_selftest_wait_timeout(ddl_ortho_t ortho, uint32_t limit_u
 ddl_status_t ddl_ortho_destroy(ddl_ortho_t ortho);
 
 /* ---------------------------------------------------------------------------
+ * Softmax cross entropy of a linear head: the loss, and with its gradient the
+ * start of the backward pass.  The logits of a large vocabulary (tokens x vocab)
+ * are never kept: the forward pass joins the softmax sums of parts of the
+ * vocabulary, the backward pass makes the logits again, a piece of the
+ * vocabulary at a time.
+ *
+ *   z = x w^T + bias;   lse = log sum_v exp(z_v);   q = (1 - smoothing) [v = label] + smoothing / vocab
+ *   loss = lse - sum_v q_v z_v
+ *   dz = dloss (exp(z - lse) - q);   dx = dz w;   dw (+)= dz^T x;   db (+)= sum over tokens of dz
+ *
+ * x, w, bias and dx are of the handle's 16-bit type, strides and alignment as
+ * for the linear layers; labels are 64-bit, loss, lse and dloss binary32, one
+ * per token.  A token whose label is negative has loss 0 and no gradient
+ * (whatever its logits and dloss are; its row of x has to be finite, as 0 times
+ * it is part of dw).  A label of vocab or more makes the token's loss NaN, leaves
+ * it without a gradient, and is reported by ddl_xent_check.  Logits may be
+ * infinite: a bias of -infinity takes an entry out of the softmax.
+ *
+ * A handle's device binding, threads, ownership, checks and overlap rules are
+ * those of the linear layers.  Its workspace: 8 bytes per token and 64 entries
+ * of the vocabulary (at most 512 MB), twice 2 bytes per token and entry of a
+ * piece (at most 2^28 of them, or 256 entries), 4 bytes per token and feature
+ * where there are several pieces, copies of x and w whose rows are not aligned. */
+
+typedef struct ddl_xent* ddl_xent_t;
+
+/* max_tokens 1..2^20, in_features and vocab 1..2^22, 0 <= smoothing < 1.  dtype
+ * DDL_FP32 returns DDL_ERR_UNSUPPORTED.  Host-only. */
+ddl_status_t ddl_xent_create(size_t max_tokens, size_t in_features, size_t vocab, ddl_dtype_t dtype, float smoothing,
+                             ddl_xent_t* out);
+
+/* bias: NULL = none.  loss, lse: at least one (the backward pass reads lse).
+ * tokens = 0 queues nothing.  Logits and sums are binary32; the loss of a token
+ * that the model is sure of keeps its relative precision (it is not made as a
+ * difference of two near numbers). */
+ddl_status_t ddl_xent_forward(ddl_xent_t xent, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
+                              const void* bias, const int64_t* labels, float* loss, float* lse, void* stream);
+
+/* dloss: the gradient of each token's loss, e.g. 1 / tokens (NULL = ones).  dx,
+ * dw, db, grad_dtype, accumulate: as for ddl_linear_backward.  Repeated calls
+ * give the same bits.  Rounding: dz is kept to the 16 bits of the handle's type in
+ * dx, and in binary16 gradients of a DDL_FP16 handle; in other gradients dw takes
+ * it to 16 (DDL_BF16) or 22 bits (DDL_FP16).  DDL_FP16 scales dz by a power of
+ * two on the way, so that small and large dloss lose nothing. */
+ddl_status_t ddl_xent_backward(ddl_xent_t xent, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
+                               const void* bias, const int64_t* labels, const float* lse, const float* dloss, void* dx,
+                               size_t lddx, void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate,
+                               void* stream);
+
+/* As ddl_linear_check (labels of vocab or more are reported, too),
+ * ddl_linear_selftest_wait_timeout (of the next call's first product),
+ * ddl_linear_destroy. */
+ddl_status_t ddl_xent_check(ddl_xent_t xent, void* stream);
+ddl_status_t ddl_xent_selftest_wait_timeout(ddl_xent_t xent, uint32_t limit_us, uint32_t products, uint32_t loads_even,
+                                            uint32_t loads_odd);
+ddl_status_t ddl_xent_destroy(ddl_xent_t xent);
+
+/* ---------------------------------------------------------------------------
  * AdamW over many tensors at once.  What the Muon step leaves alone (embeddings,
  * heads, norms, biases), or every tensor: one launch updates all tensors of the
  * flat buffers, on every rank's copy of the parameters, from the averaged
