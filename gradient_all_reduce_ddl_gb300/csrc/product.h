@@ -107,7 +107,7 @@ struct Softmax {
   // kEpiGrad: dz = coef (exp(z - lse) - off - on [entry is the label]), 0 for tokens whose label is outside [0, vocab)
   const float* lse;
   const float* coef;   // NULL: ones
-  const float* scale;  // NULL, or what dz's planes are multiplied by
+  const float* scale;  // what dz's planes are multiplied by
   float on, off;
   int32_t planes;      // 1 or 2
   float* db;           // NULL, or the sums of dz (x scale) over every 32 tokens, or over a split tile's shares of them

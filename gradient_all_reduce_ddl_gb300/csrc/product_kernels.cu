@@ -941,7 +941,7 @@ struct GradRow {
     valid = y >= 0 && y < e.vocab;
     if (y >= e.first && y < e.first + entries) label = (int)(y - e.first);
     lse = __ldg(e.lse + m);
-    by = (e.coef ? __ldg(e.coef + m) : 1.f) * (e.scale ? __ldcg(e.scale) : 1.f);
+    by = (e.coef ? __ldg(e.coef + m) : 1.f) * __ldcg(e.scale);
   }
   // dz (x scale) of entry n, whose logit is z
   __device__ __forceinline__ float of(float z, int n, const Softmax& e) const {

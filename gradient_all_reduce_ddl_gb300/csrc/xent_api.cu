@@ -268,7 +268,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   const int n_planes = std::max(1, dw_planes);
   for (int k = 0; k < n_planes; ++k)
     if ((st = need(&h->planes[k], plane_elems(h) * 2)) != DDL_OK) return st;
-  if (f16 && (st = need(&h->scale, 2 * sizeof(float))) != DDL_OK) return st;
+  if ((st = need(&h->scale, 2 * sizeof(float))) != DDL_OK) return st;
   const int64_t most_sums = std::max<int64_t>(kSplitSums, (int64_t)plane_elems(h) / 32 + (int64_t)round8((uint64_t)V));
   if (db && (st = need(&h->db, (size_t)most_sums * 4)) != DDL_OK) return st;
   const int64_t ld32 = (int64_t)round8((uint64_t)K);
@@ -280,11 +280,9 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   if ((st = aligned(mx, h->max_tokens, &h->x, &prep, &ax)) != DDL_OK) return st;
   if ((st = aligned(mw, V, &h->w, &prep, &aw)) != DDL_OK) return st;
   if (prep.n_packs && (st = status_of(launch_linear_prep(prep, s))) != DDL_OK) return st;
-  float* scale = f16 ? static_cast<float*>(h->scale.p) : nullptr;
-  if (f16) {
-    const XentScale sc = {dloss, labels, T, V, scale};
-    if ((st = status_of(launch_xent_scale(sc, s))) != DDL_OK) return st;
-  }
+  float* scale = static_cast<float*>(h->scale.p);
+  const XentScale sc = {dloss, labels, T, V, f16, scale};
+  if ((st = status_of(launch_xent_scale(sc, s))) != DDL_OK) return st;
   const GiveUp give_up = take_give_up(h);
 
   const int64_t ldp = (int64_t)round8((uint64_t)piece);
@@ -345,7 +343,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
         b.ld = ldp;
         b.groups = splits == 1 ? blocks_of(T, 32) : blocks_of(T, kTileM) * splits;
         b.cols = n;
-        b.scale = scale ? scale + 1 : nullptr;
+        b.scale = scale + 1;
         b.db = static_cast<char*>(db) + v0 * ge;
         b.f32 = ge == 4;
         b.accumulate = accumulate ? 1 : 0;
@@ -357,7 +355,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
     ProductLaunch L = {};
     L.bf16 = !f16;
     L.err = h->d_err;
-    L.post = scale ? scale + 1 : nullptr;
+    L.post = scale + 1;
     for (int k = 0; k < n_planes; ++k)
       if (!map_of(&L, k, mp[k], kBlockK)) return DDL_ERR_CUDA;
     if ((dw && !map_of(&L, 3, ax, kBlockK)) || (dx && !map_of(&L, 4, bw, kBlockK))) return DDL_ERR_CUDA;

@@ -97,10 +97,10 @@ __global__ void __launch_bounds__(1024) scale_kernel(const __grid_constant__ Xen
   if (threadIdx.x >= 32) return;
   most = __reduce_max_sync(0xFFFFFFFFu, shared[threadIdx.x]);
   if (threadIdx.x == 0) {
-    int e = 14 - ((int)(most >> 23) - 127);  // of subnormal numbers and zero: the most below
-    e = e > 120 ? 120 : e < -100 ? -100 : e;
-    p.scale[0] = __uint_as_float((uint32_t)(127 + e) << 23);
-    p.scale[1] = __uint_as_float((uint32_t)(127 - e) << 23);
+    // (no coefficient, or one whose inverse binary32 does not hold: the nearest that it does)
+    const float by = p.f16 ? 0x1p-14f : 1.f, top = fminf(fmaxf(__uint_as_float(most), 0x1p-100f), 0x1p100f);
+    p.scale[0] = 1.f / (top * by);
+    p.scale[1] = top * by;
   }
 }
 

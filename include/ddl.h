@@ -560,8 +560,8 @@ ddl_status_t ddl_xent_forward(ddl_xent_t xent, size_t tokens, const void* x, siz
  * dw, db, grad_dtype, accumulate: as for ddl_linear_backward.  Repeated calls
  * give the same bits.  Rounding: dz is kept to the 16 bits of the handle's type in
  * dx, and in binary16 gradients of a DDL_FP16 handle; in other gradients dw takes
- * it to 16 (DDL_BF16) or 22 bits (DDL_FP16).  DDL_FP16 scales dz by a power of
- * two on the way, so that small and large dloss lose nothing. */
+ * it to 16 (DDL_BF16) or 22 bits (DDL_FP16).  On the way dz is divided by the largest
+ * dloss, so that no size of dloss loses anything. */
 ddl_status_t ddl_xent_backward(ddl_xent_t xent, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
                                const void* bias, const int64_t* labels, const float* lse, const float* dloss, void* dx,
                                size_t lddx, void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate,
