@@ -2,6 +2,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstddef>
 #include <cstring>
@@ -94,7 +95,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
   a->blocks = blocks;
   // few elements: short items, so that every SM has some
   uint64_t per = ddl::kAdamItemBlocks;
-  while (per > 1 && blocks < per * 152 * 32) per /= 2;
+  while (per > 1 && blocks < per * 152 * 3) per /= 2;
   try {
     std::vector<const ddl_tensor_t*> by(n_tensors);
     for (int i = 0; i < n_tensors; ++i) by[i] = tensors + i;
@@ -125,7 +126,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
 }
 
 ddl_status_t ddl_adam_set_betas(ddl_adam_t a, double beta1, double beta2, double eps) {
-  if (!a || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !((float)eps > 0.f) || !std::isfinite((float)eps))
+  if (!a || !(beta1 >= 0.0 && beta1 < 1.0) || !(beta2 >= 0.0 && beta2 < 1.0) || !((float)eps >= FLT_MIN) || !std::isfinite((float)eps))
     return DDL_ERR_INVALID_ARG;
   a->beta1 = beta1;
   a->beta2 = beta2;

@@ -747,33 +747,46 @@ __device__ __forceinline__ float bias_one(const ProductLaunch& p, int n) {
   return from16(__ldg(static_cast<const uint16_t*>(p.soft.bias) + n), p.inl[0].type);
 }
 
-// Adds the bias of 16 entries n.. (entries from N on get none).
-__device__ __forceinline__ void add_bias16(const ProductLaunch& p, float* v, int n) {
-  const Product& P = p.inl[0];
-  if (p.soft.bias_vec && n + 16 <= P.N) {
-    const uint4* from = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.soft.bias) + n);
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      float t[8];
-      unpack8(__ldg(from + g), P.type, t);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[8 * g + k] += t[k];
-    }
+// The bias of 16 entries n.. as it is stored; zeros without one, and from entry N on.
+__device__ __forceinline__ void load_bias16(const ProductLaunch& p, int n, uint4 (&b)[2]) {
+  b[0] = b[1] = make_uint4(0, 0, 0, 0);
+  if (!p.soft.bias) return;
+  const uint16_t* from = static_cast<const uint16_t*>(p.soft.bias) + n;
+  const int left = p.inl[0].N - n;
+  if (p.soft.bias_vec && left >= 16) {
+    b[0] = __ldg(reinterpret_cast<const uint4*>(from));
+    b[1] = __ldg(reinterpret_cast<const uint4*>(from) + 1);
   } else {
+    uint32_t w[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k)
-      if (n + k < P.N) v[k] += bias_one(p, n + k);
+    for (int k = 0; k < 8; ++k) {
+      w[k] = 2 * k < left ? __ldg(from + 2 * k) : 0;
+      if (2 * k + 1 < left) w[k] |= (uint32_t)__ldg(from + 2 * k + 1) << 16;
+    }
+    b[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    b[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+__device__ __forceinline__ void add_bias16(const ProductLaunch& p, float* v, const uint4 (&b)[2]) {
+  if (!p.soft.bias) return;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    float t[8];
+    unpack8(b[g], p.inl[0].type, t);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[8 * g + k] += t[k];
   }
 }
 
-// The sum of exp(v - most) over values of which most is the largest: 0 where all are -infinity, infinite where +infinity is
-// among them.
+// What a sum of exp(z - most) is taken relative to: where all are -infinity the sum is then 0, where +infinity is among them
+// infinite.
+__device__ __forceinline__ float base_of(float most) { return fabsf(most) == INFINITY ? 0.f : most; }
+
 template <int N>
-__device__ __forceinline__ float exp_sum(const float (&v)[N], float most) {
-  const float m = fabsf(most) == INFINITY ? 0.f : most;
+__device__ __forceinline__ float exp_sum(const float (&v)[N], float base) {
   float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k = 0; k < N; ++k) s[k & 3] += exp_of(v[k] - m);
+  for (int k = 0; k < N; ++k) s[k & 3] += exp_of(v[k] - base);
   return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
@@ -788,51 +801,66 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// A thread's half of a tile's row: token m, of every 32 columns from col0 the 16 of `half`.
-template <int BN>
-__device__ __forceinline__ void loss_row(const ProductLaunch& p, float (&v)[BN / 2], int m, int half, int col0) {
-  const Product& P = p.inl[0];
-  const Softmax& e = p.soft;
-  const auto column = [&](int k) { return col0 + (k >> 4) * kSlab + half * (kSlab / 2) + (k & 15); };
-  if (e.bias) {
-#pragma unroll
-    for (int k = 0; k < BN / 2; k += 16) add_bias16(p, v + k, column(k));
+// A thread's half of a tile's row, two slabs at a time (one copy of the code: straight through 128 values it would be larger
+// than the instruction cache, which short contractions wait for).
+struct LossRow {
+  float most, sum, all;
+  int64_t label;
+  uint4 bias[2][2];  // of the next two slabs
+  __device__ __forceinline__ LossRow(const ProductLaunch& p, int m, int n) : most(-INFINITY), sum(0.f), all(0.f) {
+    label = m < p.inl[0].M ? __ldg(p.soft.labels + m) : -1;
+    load_bias16(p, n, bias[0]);
+    load_bias16(p, n + kSlab, bias[1]);
   }
-  const bool edge = col0 + BN > P.N;
-  const bool in = m < P.M;
-  const int64_t at = (int64_t)(col0 / BN * 2 + half) * e.tokens + m;
-  if (e.part_sum) {
-    float s[4] = {0.f, 0.f, 0.f, 0.f};
+  // The 16 columns from n and from n + kSlab; more: two further slabs follow.
+  __device__ __forceinline__ void add(const ProductLaunch& p, float (&v)[32], int m, int n, bool more) {
+    const Softmax& e = p.soft;
+    const int N = p.inl[0].N;
+    add_bias16(p, v, bias[0]);
+    add_bias16(p, v + 16, bias[1]);
+    if (more) {
+      load_bias16(p, n + 2 * kSlab, bias[0]);
+      load_bias16(p, n + 3 * kSlab, bias[1]);
+    }
+    if (n + kSlab + 16 > N) {
 #pragma unroll
-    for (int k = 0; k < BN / 2; ++k) s[k & 3] += !edge || column(k) < P.N ? v[k] : 0.f;
-    if (in) e.part_sum[at] = (s[0] + s[1]) + (s[2] + s[3]);
-  }
-  if (edge) {
+      for (int k = 0; k < 32; ++k) {
+        const bool in = n + (k >> 4) * kSlab + (k & 15) < N;
+        all += in ? v[k] : 0.f;
+        if (!in) v[k] = -INFINITY;
+      }
+    } else if (e.part_sum) {
+      float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int k = 0; k < BN / 2; ++k)
-      if (column(k) >= P.N) v[k] = -INFINITY;
-  }
-  const int64_t label = in ? __ldg(e.labels + m) : -1;
-  if (label >= col0 && label < min(col0 + BN, P.N)) {
-    const int n = (int)label;
-    if ((n - col0) / 16 % 2 == half) {
+      for (int k = 0; k < 32; ++k) s[k & 3] += v[k];
+      all += (s[0] + s[1]) + (s[2] + s[3]);
+    }
+    const int64_t at = label - n;  // 0 .. 15 or kSlab .. kSlab + 15: one of these
+    if (at >= 0 && at < kSlab + 16 && (at & 16) == 0 && label < N) {
+      const int y = (int)at;
       float z = 0.f;
 #pragma unroll
-      for (int k = 0; k < BN / 2; ++k)
-        if (column(k) == n) {
+      for (int k = 0; k < 32; ++k)
+        if ((k >> 4) * kSlab + (k & 15) == y) {
           z = v[k];
           v[k] = -INFINITY;
         }
       e.picked[m] = z;
     }
-  }
-  float most[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    float top[4] = {most, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-  for (int k = 0; k < BN / 2; ++k) most[k & 3] = fmaxf(most[k & 3], v[k]);
-  const float mx = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-  const float s = exp_sum(v, mx);
-  if (in) e.part[at] = make_float2(mx, s);
-}
+    for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], v[k]);
+    const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), base = base_of(mx);
+    sum = sum * exp_of(base_of(most) - base) + exp_sum(v, base);
+    most = mx;
+  }
+  __device__ __forceinline__ void store(const ProductLaunch& p, int m, int part) const {
+    if (m >= p.inl[0].M) return;
+    const int64_t at = (int64_t)part * p.soft.tokens + m;
+    p.soft.part[at] = make_float2(most, sum);
+    if (p.soft.part_sum) p.soft.part_sum[at] = all;
+  }
+};
 
 // Rows [r0, r1) of a tile whose contraction was split: a warp along a row.
 template <int BN>
@@ -870,7 +898,7 @@ __device__ __forceinline__ void loss_rows(const ProductLaunch& p, int row0, int 
       }
     }
     most = warp_max(most);
-    const float s = warp_sum(exp_sum(v, most));
+    const float s = warp_sum(exp_sum(v, base_of(most)));
     const int64_t at = (int64_t)(col0 / BN) * e.tokens + m;
     if (e.part_sum) all = warp_sum(all);
     if (lane == 0) {
@@ -916,7 +944,7 @@ __device__ __forceinline__ void loss_columns(const ProductLaunch& p, int row0, i
 #pragma unroll
       for (int i = 1; i < kRows; ++i) most = fmaxf(most, v[k][i]);
       most = warp_max(most);
-      const float s = warp_sum(exp_sum(v[k], most));
+      const float s = warp_sum(exp_sum(v[k], base_of(most)));
       if (e.part_sum) all[k] = warp_sum(all[k]);
       const int64_t at = (int64_t)part * e.tokens + col0 + c + k;
       if (lane == 0 && col0 + c + k < P.N) {
@@ -927,38 +955,51 @@ __device__ __forceinline__ void loss_columns(const ProductLaunch& p, int row0, i
   }
 }
 
-// What the gradient needs of a token.
+// What the gradient needs of a token.  exp(z - lse) = 2^(z log2 e - h) 2^-l with h + l = lse log2 e: one multiply-add, whose
+// rounding is that of the difference, and a factor.
 struct GradRow {
-  float lse, by;  // by: its coefficient times the planes' scale
-  int label;      // counted from the piece's first entry; outside of it: -1
+  float high;      // h
+  float by_p, by;  // the coefficient times the planes' scale, with and without 2^-l
+  int label;       // counted from the piece's first entry; outside of it: -1
   bool valid;
   __device__ __forceinline__ void load(const Softmax& e, int m, int rows, int entries) {
-    lse = by = 0.f;
+    high = by_p = by = 0.f;
     label = -1;
     valid = false;
     if (m >= rows) return;
     const int64_t y = __ldg(e.labels + m);
     valid = y >= 0 && y < e.vocab;
     if (y >= e.first && y < e.first + entries) label = (int)(y - e.first);
-    lse = __ldg(e.lse + m);
+    const float lse = __ldg(e.lse + m);
     by = (e.coef ? __ldg(e.coef + m) : 1.f) * __ldcg(e.scale);
+    high = lse * kLog2e;
+    by_p = by * exp2_fast(-fmaf(lse, kLog2e, -high));
   }
-  // dz (x scale) of entry n, whose logit is z
-  __device__ __forceinline__ float of(float z, int n, const Softmax& e) const {
-    float d = exp_of(z - lse) - e.off;
-    if (n == label) d -= e.on;
-    return valid ? d * by : 0.f;
+  // dz (x scale) of N entries from n, whose logits are z
+  template <int N>
+  __device__ __forceinline__ void of(float* z, int n, const Softmax& e) const {
+    const float less = -e.off * by;
+#pragma unroll
+    for (int k = 0; k < N; ++k) z[k] = fmaf(exp2_fast(fmaf(z[k], kLog2e, -high)), by_p, less);
+    if (label >= n && label < n + N) {
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        if (n + k == label) z[k] -= e.on * by;
+    }
+    if (!valid) {
+#pragma unroll
+      for (int k = 0; k < N; ++k) z[k] = 0.f;
+    }
   }
 };
 
-// The planes of two neighbours: 16 bits, and what their rounding lost (in binary16 2^11 times that).  An infinite or NaN
-// value is in the first plane alone.
+// The planes of two neighbours: 16 bits, and what their rounding lost (in binary16 2^11 times that).  (Of an infinite value
+// the second is NaN, but the sums of the first plane are infinite or NaN then, and stand.)
 __device__ __forceinline__ void grad_planes(float x, float y, int type, uint32_t* hi, uint32_t* lo) {
   *hi = to16x2(x, y, type);
   const float2 h = from16x2(*hi, type);
-  const float up = type == kBF16 ? 1.f : 2048.f;
-  x = fabsf(h.x) <= FLT_MAX ? (x - h.x) * up : 0.f;
-  y = fabsf(h.y) <= FLT_MAX ? (y - h.y) * up : 0.f;
+  x -= h.x, y -= h.y;
+  if (type == kF16) x *= 2048.f, y *= 2048.f;
   *lo = to16x2(x, y, type);
 }
 
@@ -982,22 +1023,29 @@ __device__ __forceinline__ float column_sums16(const float* v, int lane) {
 }
 
 // 16 columns n.. of row m, from logits to planes in the slab.
-__device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, const GradRow& g, uint32_t buf, int row, int half,
-                                          int m0, int n) {
-  const Product& P = p.inl[0];
-  const Softmax& e = p.soft;
-  if (e.bias) add_bias16(p, v, n);
-#pragma unroll
-  for (int k = 0; k < 16; ++k) v[k] = g.of(v[k], n + k, e);
+template <int TYPE>
+__device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, bool two) {
   uint32_t hi[8], lo[8];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], P.type, &hi[k], &lo[k]);
+  for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], TYPE, &hi[k], &lo[k]);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t at = piece(buf, row, 2 * half + h);
     st_shared16(at, make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]));
-    if (e.planes == 2) st_shared16(at + kPlaneBytes, make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]));
+    if (two) st_shared16(at + kPlaneBytes, make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]));
   }
+}
+
+__device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, const GradRow& g, const uint4 (&bias)[2], uint32_t buf,
+                                          int row, int half, int m0, int n) {
+  const Product& P = p.inl[0];
+  const Softmax& e = p.soft;
+  add_bias16(p, v, bias);
+  g.of<16>(v, n, e);
+  if (P.type == kBF16)
+    slab_planes<kBF16>(v, buf, row, half, e.planes == 2);
+  else
+    slab_planes<kF16>(v, buf, row, half, e.planes == 2);
   if (e.db) {
     const int lane = row & 31, c = n + (lane >> 1);
     const float s = column_sums16(v, lane);
@@ -1025,11 +1073,11 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, int row0, int 
       float v[4];
       sums.four((r * pitch(BN) + c) * 4, v);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 4; ++k)
         if (e.bias && n + k < P.N) v[k] += bias_one(p, n + k);
-        v[k] = g.of(v[k], n + k, e);
-        total[k] += v[k];
-      }
+      g.of<4>(v, n, e);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) total[k] += v[k];
       uint32_t hi[2], lo[2];
       grad_planes(v[0], v[1], P.type, &hi[0], &lo[0]);
       grad_planes(v[2], v[3], P.type, &hi[1], &lo[1]);
@@ -1505,7 +1553,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       if constexpr (BN >= 128) boxes = MODE == kSteps || MODE == kGrad || (MODE != kLoss && p.boxes);
       if constexpr (MODE == kLoss) {
         if (!P.swap) {
-          if (ok) loss_row<BN>(p, acc, pl.row0 + my_rows + row, half, pl.col0);
+          if constexpr (BN >= 128) {
+            const int m = pl.row0 + my_rows + row, n0 = pl.col0 + half * kHalf;
+            LossRow lr(p, m, n0);
+#pragma unroll 1
+            for (int sl = 0; sl < kSlabs && pl.col0 + sl * kSlab < P.N; sl += 2) {
+              float v[2 * kHalf];
+#pragma unroll
+              for (int k = 0; k < 2 * kHalf; ++k) v[k] = acc[k];
+              lr.add(p, v, m, n0 + sl * kSlab, sl + 2 < kSlabs);
+#pragma unroll
+              for (int k = 0; k + 2 * kHalf < BN / 2; ++k) acc[k] = acc[k + 2 * kHalf];
+            }
+            if (ok) lr.store(p, m, pl.col0 / BN * 2 + half);
+          }
         } else {
 #pragma unroll 1
           for (int sl = 0; sl < kSlabs; ++sl) {
@@ -1522,17 +1583,19 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         if constexpr (BN >= 128) {
           uint4 bias_ahead[2] = {};
           if constexpr (is_forward(MODE)) load_bias(P, pl.col0 + half * kHalf, bias_ahead);
+          if constexpr (MODE == kGrad) load_bias16(p, pl.col0 + half * kHalf, bias_ahead);
 #pragma unroll 1
           for (int sl = 0; sl < kSlabs && pl.col0 + sl * kSlab < P.N; ++sl, use.next<kBufs>()) {  // one copy of the code:
             // it has to stay in the instruction cache
             uint4 bias[2] = {bias_ahead[0], bias_ahead[1]};
             if (is_forward(MODE) && sl + 1 < kSlabs) load_bias(P, pl.col0 + (sl + 1) * kSlab + half * kHalf, bias_ahead);
+            if (MODE == kGrad && sl + 1 < kSlabs) load_bias16(p, pl.col0 + (sl + 1) * kSlab + half * kHalf, bias_ahead);
             if (ok && !bar_wait(ready + 8 * use.s, use.parity(), limit)) ok = false;
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             load_slab(sl);
             if constexpr (MODE == kGrad)
-              slab_grad(p, acc, grad_row, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
+              slab_grad(p, acc, grad_row, bias, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
                         pl.col0 + sl * kSlab + half * kHalf);
             else if (!skip)
               slab_values<MODE>(P, p, acc, bias, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,

@@ -585,7 +585,8 @@ ddl_status_t ddl_xent_destroy(ddl_xent_t xent);
  * where c = grad_scale, times min(1, max_norm / (norm + 1e-6)) if max_norm > 0,
  * norm = |grad_scale| times the 2-norm of the gradients of all tensors; lr and
  * wd are the call's, times the tensor's factors.  Products and sums are
- * binary32, rounded one by one; the norm is summed in binary64.
+ * binary32, rounded one by one; roots and quotients are good to 2 units in the
+ * last place (a v below 2^-126 has the root 0); the norm is good to 2^-22 of itself.
  *
  * States: binary32, or 8 bits with a binary32 scale per block of 128 elements
  * (counted from each tensor's first; its last block may be shorter).  m is
@@ -614,7 +615,7 @@ typedef struct ddl_adam* ddl_adam_t;
 ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dtype_t grad_dtype, int state_bits,
                              ddl_adam_t* out);
 
-/* Other constants, 0 <= beta < 1 and eps > 0 (in binary32, too).  Host-only. */
+/* Other constants, 0 <= beta < 1 and eps >= 2^-126.  Host-only. */
 ddl_status_t ddl_adam_set_betas(ddl_adam_t adam, double beta1, double beta2, double eps);
 
 /* Blocks of 128 of all tensors: the scales of one 8-bit state.  Host-only. */
