@@ -145,7 +145,7 @@ def ddl_status_string(status: int) -> str:
 
 
 def _ptr_array(ptrs):
-    return (ctypes.c_void_p * len(ptrs))(*[int(p) for p in ptrs])
+    return (_vp * len(ptrs))(*ptrs)
 
 
 def _dev_ptrs(bufs):
@@ -667,13 +667,13 @@ def _matrix(t, rows, cols, dtype, name):
 def _vector(t, n, dtype, name):
     if t is None:
         return None
+    if t.dtype is dtype and t.is_cuda and t.dim() == 1 and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
     if t.shape != (n,):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {(n,)}")
     if t.dtype is not dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if not t.is_cuda or (n > 1 and t.stride(0) != 1):
-        raise ValueError(f"{name}: expected a contiguous CUDA vector")
-    return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous CUDA vector")
 
 
 def _torch_dtype(name):
@@ -871,17 +871,18 @@ class Adam:
         self.extent = max((int(t[0]) + int(t[1]) for t in self.tensors), default=0)
         import torch
         self._grad, self._f32, self._i64 = _torch_dtype(dtype), torch.float32, torch.int64
+        self._operands = {torch.float16: DDL_FP16, torch.bfloat16: DDL_BF16}
         self._state = {"f32": (torch.float32,), "8bit": (torch.uint8, torch.float8_e4m3fn)}[state]
         self.handle = None
         self.handle = ddl_adam_create(self.tensors, OPERAND_DTYPES[dtype], 8 if state == "8bit" else 32)
         ddl_adam_set_betas(self.handle, *betas, eps)
         self.n_blocks = ddl_adam_blocks(self.handle)
 
-    def _flat(self, t, dtypes, name, n=None):
-        n = self.extent if n is None else n
-        if t.dim() != 1 or t.numel() < n or t.dtype not in dtypes or not t.is_cuda or (t.numel() > 1 and t.stride(0) != 1):
-            raise ValueError(f"{name}: expected a contiguous CUDA vector of {dtypes[0]} with at least {n} elements")
-        return t
+    def _flat(self, t, dtypes, name, n):
+        """The address of a vector of at least n elements."""
+        if t.dtype in dtypes and t.is_cuda and t.dim() == 1 and t.numel() >= n and t.is_contiguous():
+            return t.data_ptr()
+        raise ValueError(f"{name}: expected a contiguous CUDA vector of {dtypes[0]} with at least {n} elements")
 
     def new_state(self, device="cuda"):
         """The states before the first step, as step() takes them: m, v, step and (8 bits) scales."""
@@ -897,26 +898,25 @@ class Adam:
         """Updates every copy in params (a list, one per rank), the states and
         the step count (one int64 on the device) in place; writes the copies'
         16-bit operands and the gradient's norm where they are given."""
-        f32 = (self._f32,)
-        out_dtype = DDL_FP16
+        flat, f32, n = self._flat, (self._f32,), self.extent
+        out, out_dtype = None, DDL_FP16
         if operands is not None:
             if len(operands) != len(params):
                 raise ValueError(f"operands: {len(operands)} buffers for {len(params)} copies")
-            kinds = {"torch.float16": DDL_FP16, "torch.bfloat16": DDL_BF16}
-            if any(str(o.dtype) not in kinds for o in operands[:1]):
-                raise ValueError(f"operands: dtype {operands[0].dtype}, expected torch.float16 or torch.bfloat16")
-            out_dtype = kinds[str(operands[0].dtype)] if len(operands) else DDL_FP16
-            operands = [self._flat(o, (operands[0].dtype,), "operands") for o in operands]
+            kind = operands[0].dtype if len(operands) else None
+            if kind not in self._operands:
+                raise ValueError(f"operands: dtype {kind}, expected torch.float16 or torch.bfloat16")
+            out_dtype = self._operands[kind]
+            out = _ptr_array([flat(o, (kind,), "operands", n) for o in operands])
         if scales is not None:
-            if self.state != "8bit" or not scales.is_contiguous():
-                raise ValueError("scales: a contiguous tensor, with 8-bit states only")
-            scales = self._flat(scales.view(-1), f32, "scales", 2 * self.n_blocks)
-            if scales.numel() != 2 * self.n_blocks:
-                raise ValueError(f"scales: expected {2 * self.n_blocks} elements")
-        ddl_adam_step(self.handle, self._flat(grad, (self._grad,), "grad"), [self._flat(p, f32, "params") for p in params],
-                      operands, out_dtype, self._flat(m, self._state, "m"), self._flat(v, self._state, "v"), scales,
-                      self._flat(step, (self._i64,), "step", 1), lr, weight_decay, grad_scale, max_norm,
-                      None if norm is None else self._flat(norm, f32, "norm", 1), stream)
+            if self.state != "8bit" or not scales.is_contiguous() or scales.numel() != 2 * self.n_blocks:
+                raise ValueError(f"scales: a contiguous tensor of {2 * self.n_blocks} elements, with 8-bit states only")
+            scales = flat(scales.view(-1), f32, "scales", 2 * self.n_blocks)
+        _ok(_lib.ddl_adam_step(self.handle, flat(grad, (self._grad,), "grad", n), len(params),
+                               _ptr_array([flat(p, f32, "params", n) for p in params]), out, out_dtype,
+                               flat(m, self._state, "m", n), flat(v, self._state, "v", n), scales,
+                               flat(step, (self._i64,), "step", 1), lr, weight_decay, grad_scale, max_norm,
+                               None if norm is None else flat(norm, f32, "norm", 1), _stream_handle(stream)), "ddl_adam_step")
 
     def close(self):
         handle, self.handle = self.handle, None  # destroyed once, also where that reports an error
