@@ -107,7 +107,8 @@ struct Softmax {
   // kEpiGrad: dz = coef (exp(z - lse) - off - on [entry is the label]), 0 for tokens whose label is outside [0, vocab)
   const float* lse;
   const float* coef;   // NULL: ones
-  const float* scale;  // what dz's planes are multiplied by
+  int32_t scaled;      // scale[] is there (XentScale); else the launch makes it
+  float* scale;        // [0] what dz's planes are multiplied by, [1] its inverse
   float on, off;
   int32_t planes;      // 1 or 2
   float* db;           // NULL, or the sums of dz (x scale) over every 32 tokens, or over a split tile's shares of them

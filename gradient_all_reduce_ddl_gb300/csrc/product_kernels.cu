@@ -56,6 +56,7 @@
 #include "activation.cuh"
 #include "product.h"
 #include "tc_ptx.cuh"
+#include "xent.cuh"
 
 namespace ddl {
 namespace {
@@ -962,7 +963,7 @@ struct GradRow {
   float by_p, by;  // the coefficient times the planes' scale, with and without 2^-l
   int label;       // counted from the piece's first entry; outside of it: -1
   bool valid;
-  __device__ __forceinline__ void load(const Softmax& e, int m, int rows, int entries) {
+  __device__ __forceinline__ void load(const Softmax& e, float scale, int m, int rows, int entries) {
     high = by_p = by = 0.f;
     label = -1;
     valid = false;
@@ -971,7 +972,7 @@ struct GradRow {
     valid = y >= 0 && y < e.vocab;
     if (y >= e.first && y < e.first + entries) label = (int)(y - e.first);
     const float lse = __ldg(e.lse + m);
-    by = (e.coef ? __ldg(e.coef + m) : 1.f) * __ldcg(e.scale);
+    by = (e.coef ? __ldg(e.coef + m) : 1.f) * scale;
     high = lse * kLog2e;
     by_p = by * exp2_fast(-fmaf(lse, kLog2e, -high));
   }
@@ -1056,7 +1057,7 @@ __device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, cons
 // Rows [r0, r1) of a tile whose contraction was split: a warp along a row, four columns a lane.  The planes' rows are
 // padded to 8 columns, so that a group of 4 that begins inside the matrix is whole.
 template <int BN>
-__device__ __forceinline__ void grad_rows(const ProductLaunch& p, int row0, int col0, int lane, int ew, int r0, int r1, int q,
+__device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, int row0, int col0, int lane, int ew, int r0, int r1, int q,
                                           int S, uint32_t staging, const ClusterSums sums) {
   const Product& P = p.inl[0];
   const Softmax& e = p.soft;
@@ -1069,7 +1070,7 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, int row0, int 
       const int m = row0 + r;
       if (m >= P.M || n >= P.N) break;
       GradRow g;
-      g.load(e, m, P.M, P.N);
+      g.load(e, scale, m, P.M, P.N);
       float v[4];
       sums.four((r * pitch(BN) + c) * 4, v);
 #pragma unroll
@@ -1097,6 +1098,25 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, int row0, int 
       bar_sync_epilogue();
     }
   }
+}
+
+// dz's scale, from the coefficients of all tokens; every CTA makes it, under its first products.
+__device__ __forceinline__ float launch_scale(const ProductLaunch& p, int thread, uint32_t shared) {
+  const Softmax& e = p.soft;
+  if (e.scaled) return __ldcg(e.scale);
+  uint32_t most = 0;
+#pragma unroll 4
+  for (int t = thread; t < p.inl[0].M; t += kEpiWarps * 32) most = max(most, coef_bits(e.coef, e.labels, t, e.vocab));
+  most = __reduce_max_sync(0xffffffffu, most);
+  const uint32_t at = shared + (thread >> 5) * 4;
+  if ((thread & 31) == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(most) : "memory");
+  bar_sync_epilogue();
+#pragma unroll
+  for (int w = 0; w < kEpiWarps; ++w) most = max(most, __float_as_uint(ld_shared(shared + 4 * w)));
+  bar_sync_epilogue();
+  const float2 u = dz_scale(most, p.inl[0].type == kF16);
+  if (blockIdx.x == 0 && thread == 0) e.scale[0] = u.x, e.scale[1] = u.y;
+  return u.x;
 }
 
 // One walk over the slabs of a CTA's tiles: the warp that moves the boxes has two, for what it prepares and for what
@@ -1386,6 +1406,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     uint32_t cc = 0;
     Slot use;
     bool ok = true;
+    float grad_scale = 0.f;
+    if constexpr (MODE == kGrad) {
+      griddep_wait();
+      grad_scale = launch_scale(p, ew * 32 + lane, staging);
+    }
     for (int t = first, next; t < end; t = next) {
       const Place pl = place<BN, MODE>(p, t, step);
       next = pl.next;
@@ -1419,7 +1444,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       const float post = MODE == kBackward && p.post ? __ldcg(p.post) : 1.f;
       GradRow grad_row = {};
       if constexpr (MODE == kGrad)
-        if (S == 1) grad_row.load(p.soft, pl.row0 + my_rows + row, P.M, P.N);
+        if (S == 1) grad_row.load(p.soft, grad_scale, pl.row0 + my_rows + row, P.M, P.N);
       const uint32_t lanes = (uint32_t)(quad * 32) << 16;
       // The sums of this thread's 16 columns of the slabs in turn: from TMEM, or added up in registers chunk by chunk.
       float acc[DIRECT ? kHalf : BN / 2];
@@ -1655,7 +1680,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             loss_columns<BN>(p, pl.row0, pl.col0, lane, ew, q * share, share, pl.row0 / kTileM * S + q, sums);
         } else if constexpr (MODE == kGrad) {
           const int share = kTileM / S;
-          grad_rows<BN>(p, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, q, S, staging, sums);
+          grad_rows<BN>(p, grad_scale, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, q, S, staging, sums);
         } else {
           // this CTA finishes its share of the rows
           const int share = kTileM / S;

@@ -285,8 +285,9 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   if ((st = aligned(mw, V, &h->w, &prep, &aw)) != DDL_OK) return st;
   if (prep.n_packs && (st = status_of(launch_linear_prep(prep, s))) != DDL_OK) return st;
   float* scale = static_cast<float*>(h->scale.p);
+  const bool many = T > kScaleTokens;
   const XentScale sc = {dloss, labels, T, V, f16, scale};
-  if ((st = status_of(launch_xent_scale(sc, s))) != DDL_OK) return st;
+  if (many && (st = status_of(launch_xent_scale(sc, s))) != DDL_OK) return st;
   const GiveUp give_up = take_give_up(h);
 
   const int64_t ldp = (int64_t)round8((uint64_t)piece);
@@ -334,6 +335,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       set_softmax(h, &L.soft, labels, v0, bias);
       L.soft.lse = lse;
       L.soft.coef = dloss;
+      L.soft.scaled = many;
       L.soft.scale = scale;
       L.soft.on = 1.f - h->smoothing;
       L.soft.off = h->smoothing / (float)V;

@@ -5,6 +5,7 @@
 #include "activation.cuh"
 #include "product.h"
 #include "tc_ptx.cuh"
+#include "xent.cuh"
 #include "xent_kernels.h"
 
 namespace ddl {
@@ -85,22 +86,16 @@ __global__ void __launch_bounds__(1024) scale_kernel(const __grid_constant__ Xen
   __shared__ uint32_t shared[32];
   tc::griddep_launch();
   tc::griddep_wait();
-  uint32_t most = 0;  // largest finite magnitude: as bits they order as the numbers do
-  for (int64_t t = threadIdx.x; t < p.tokens; t += 1024) {
-    const int64_t y = p.labels[t];
-    const uint32_t b = __float_as_uint(p.coef ? p.coef[t] : 1.f) & 0x7FFFFFFFu;
-    if (y >= 0 && y < p.vocab && b < 0x7F800000u && b > most) most = b;
-  }
+  uint32_t most = 0;
+  for (int64_t t = threadIdx.x; t < p.tokens; t += 1024) most = max(most, coef_bits(p.coef, p.labels, t, p.vocab));
   most = __reduce_max_sync(0xFFFFFFFFu, most);
   if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = most;
   __syncthreads();
   if (threadIdx.x >= 32) return;
   most = __reduce_max_sync(0xFFFFFFFFu, shared[threadIdx.x]);
   if (threadIdx.x == 0) {
-    // (no coefficient, or one whose inverse binary32 does not hold: the nearest that it does)
-    const float by = p.f16 ? 0x1p-14f : 1.f, top = fminf(fmaxf(__uint_as_float(most), 0x1p-100f), 0x1p100f);
-    p.scale[0] = 1.f / (top * by);
-    p.scale[1] = top * by;
+    const float2 u = dz_scale(most, p.f16);
+    p.scale[0] = u.x, p.scale[1] = u.y;
   }
 }
 

@@ -35,6 +35,8 @@ struct XentScale {
   int32_t f16;
   float* scale;
 };
+// (Launches of up to kScaleTokens tokens make it themselves: kEpiGrad.)
+constexpr int64_t kScaleTokens = 16384;
 cudaError_t launch_xent_scale(const XentScale& p, cudaStream_t stream);
 
 // db (+)= scale * the sums of `groups` rows.
