@@ -167,8 +167,20 @@ ddl_status_t ddl_xent_forward(ddl_xent_t h, size_t tokens, const void* x, size_t
     const bool swap = n <= kFewTokens;
     int tile_n = n <= 32 ? 32 : 64, splits = 1;
     int64_t tiles = blocks_of(V, kTileM);
+    int tile_rows = kTileM;
     if (swap) {
       while (splits < 8 && tiles * splits * 2 <= h->sms && steps >= 4 * splits) splits *= 2;
+      // The weights are the traffic.  Where every SM has a tile or more, tiles of fewer rows may share them out more evenly:
+      // the fewest rows for the busiest SM (a vocabulary of 65,536, 4096 features: 98.9 us with 128 rows, 95.2 with 120, 92.5 with
+      // 112).  A block of 64 takes an SM 0.31 us however few rows it has, which is what 108 of them take from HBM: 96 rows 111 us.
+      if (splits == 1 && tiles > h->sms) {
+        int64_t most = blocks_of(tiles, h->sms) * tile_rows;
+        for (int rows = kTileM - 8; rows >= 112; rows -= 8) {
+          const int64_t busy = blocks_of(blocks_of(V, rows), h->sms) * rows;
+          if (busy < most) most = busy, tile_rows = rows;
+        }
+        tiles = blocks_of(V, tile_rows);
+      }
     } else {
       const auto count = [&](int tile) { return blocks_of(n, tile) * blocks_of(V, tile); };
       const Layout l = choose_layout([&](int tile, int workers) { return blocks_of(count(tile), workers) * steps; }, count, steps,
@@ -182,7 +194,7 @@ ddl_status_t ddl_xent_forward(ddl_xent_t h, size_t tokens, const void* x, size_t
     L.bf16 = h->type == kBF16;
     const Mat bx{static_cast<const uint16_t*>(ax.p) + t0 * ax.ld, n, K, ax.ld};
     const int narrow = std::min(tile_n, kTileM);
-    if (!map_of(&L, 0, bx, kBlockK, swap ? narrow : kTileM) || !map_of(&L, 1, aw, kBlockK, swap ? kTileM : narrow))
+    if (!map_of(&L, 0, bx, kBlockK, swap ? narrow : kTileM) || !map_of(&L, 1, aw, kBlockK, swap ? tile_rows : narrow))
       return DDL_ERR_CUDA;
     Product& P = L.inl[0];
     P.M = (int32_t)(swap ? V : n);
@@ -200,6 +212,7 @@ ddl_status_t ddl_xent_forward(ddl_xent_t h, size_t tokens, const void* x, size_t
     L.n_inl = 1;
     L.inl_tiles[0] = L.n_tiles = (int32_t)tiles;
     L.splits = splits;
+    L.tile_rows = tile_rows;
     L.err = h->d_err;
     L.give_up = take_give_up(h);
     set_softmax(h, &L.soft, labels + t0, 0, bias);
