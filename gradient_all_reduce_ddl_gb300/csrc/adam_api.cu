@@ -4,8 +4,6 @@
 #include <algorithm>
 #include <cfloat>
 #include <cmath>
-#include <cstddef>
-#include <cstring>
 #include <new>
 #include <stdexcept>
 #include <vector>
@@ -150,9 +148,8 @@ ddl_status_t ddl_adam_step(ddl_adam_t a, const void* grad, int n_copies, float* 
   if (!(max_norm >= 0.f) || !std::isfinite(max_norm)) return DDL_ERR_INVALID_ARG;
   if (n_copies > ddl::kMaxAdamCopies) return DDL_ERR_UNSUPPORTED;
   const uint64_t n = a->extent, ge = a->grad_type == ddl::kF32 ? 4 : 2, se = a->bits == 8 ? 1 : 4;
-  ddl::AdamStep p;
-  std::memset(&p, 0, offsetof(ddl::AdamStep, params));
-  p.out[0] = nullptr;
+  ddl::AdamStep p = {};
+  ddl::AdamCopies<ddl::kMaxAdamCopies> copies;  // the first n_copies are set
   // everything a call writes is apart from everything else
   struct Piece {
     const void* p;
@@ -169,10 +166,11 @@ ddl_status_t ddl_adam_step(ddl_adam_t a, const void* grad, int n_copies, float* 
   bool vec = aligned(grad, 4 * ge) && aligned(m, 4 * se) && aligned(v, 4 * se);
   for (int r = 0; r < n_copies; ++r) {
     if (!param_bufs[r] || (operand_bufs && !operand_bufs[r])) return DDL_ERR_INVALID_ARG;
-    pieces[k++] = {p.params[r] = param_bufs[r], n * 4, 4};
+    pieces[k++] = {copies.params[r] = param_bufs[r], n * 4, 4};
+    copies.out[r] = operand_bufs ? operand_bufs[r] : nullptr;
     vec = vec && aligned(param_bufs[r], 16);
     if (operand_bufs) {
-      pieces[k++] = {p.out[r] = operand_bufs[r], n * 2, 2};
+      pieces[k++] = {operand_bufs[r], n * 2, 2};
       vec = vec && aligned(operand_bufs[r], 8);
     }
   }
@@ -213,9 +211,10 @@ ddl_status_t ddl_adam_step(ddl_adam_t a, const void* grad, int n_copies, float* 
   p.bits = a->bits;
   p.vec = vec;
   p.n_copies = n_copies;
+  p.operands = operand_bufs != nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (p.norm && (st = ddl::status_of(ddl::launch_adam_norm(p, a->sms, s))) != DDL_OK) return st;
-  return ddl::status_of(ddl::launch_adam_step(p, a->sms, s));
+  return ddl::status_of(ddl::launch_adam_step(p, copies, a->sms, s));
 }
 
 ddl_status_t ddl_adam_destroy(ddl_adam_t a) {

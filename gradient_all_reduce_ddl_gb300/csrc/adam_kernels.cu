@@ -193,8 +193,8 @@ __device__ __forceinline__ void share_of(const AdamItem& it, uint32_t* first, ui
 }
 
 // NB blocks of 128 elements in a row (V = 1: one, of len elements), whose loads are all issued before the first is used.
-template <int BITS, int V, int NB>
-__device__ __forceinline__ void blocks_step(const AdamStep& p, const Factors& f, const AdamItem& it, uint32_t first,
+template <int BITS, int V, int NB, class Copies>
+__device__ __forceinline__ void blocks_step(const AdamStep& p, const Copies& to, const Factors& f, const AdamItem& it, uint32_t first,
                                             uint32_t len, int lane) {
   const int64_t at0 = (int64_t)(it.begin + first);
   const uint32_t block = it.block + first / kAdamBlock;
@@ -217,7 +217,7 @@ __device__ __forceinline__ void blocks_step(const AdamStep& p, const Factors& f,
   for (int k = 0; k < kCopies; ++k)
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (k < p.n_copies) load32<V>(p.params[k] + at0 + b * kAdamBlock, len, lane, t[k][b]);
+      if (k < p.n_copies) load32<V>(to.params[k] + at0 + b * kAdamBlock, len, lane, t[k][b]);
   const float size = f.size * it.lr, keep = 1.f - p.lr * it.lr * p.weight_decay * it.decay;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
@@ -253,7 +253,7 @@ __device__ __forceinline__ void blocks_step(const AdamStep& p, const Factors& f,
       for (int k = 0; k < kCopies; ++k)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          if (c + k < p.n_copies) load32<V>(p.params[c + k] + at0 + b * kAdamBlock, len, lane, t[k][b]);
+          if (c + k < p.n_copies) load32<V>(to.params[c + k] + at0 + b * kAdamBlock, len, lane, t[k][b]);
     }
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) {
@@ -263,15 +263,16 @@ __device__ __forceinline__ void blocks_step(const AdamStep& p, const Factors& f,
         const int64_t at = at0 + b * kAdamBlock;
 #pragma unroll
         for (int j = 0; j < 4; ++j) t[k][b][j] = t[k][b][j] * keep - g[b][j];
-        store32<V>(p.params[c + k] + at, len, lane, t[k][b]);
-        if (p.out[0]) store16<V>(p.out[c + k], at, p.out_type, len, lane, t[k][b]);
+        store32<V>(to.params[c + k] + at, len, lane, t[k][b]);
+        if (p.operands) store16<V>(to.out[c + k], at, p.out_type, len, lane, t[k][b]);
       }
     }
   }
 }
 
-template <int BITS>
-__global__ void __launch_bounds__(kThreads, min_ctas(BITS)) step_kernel(const __grid_constant__ AdamStep p) {
+template <int BITS, int COPIES>
+__global__ void __launch_bounds__(kThreads, min_ctas(BITS))
+    step_kernel(const __grid_constant__ AdamStep p, const __grid_constant__ AdamCopies<COPIES> to) {
   const int lane = threadIdx.x & 31;
   AdamItem next = p.items[blockIdx.x];  // the handle's table, written before any launch
   tc::griddep_launch();
@@ -289,17 +290,17 @@ __global__ void __launch_bounds__(kThreads, min_ctas(BITS)) step_kernel(const __
     share_of(it, &first, &end);
     if (p.vec && it.begin % 4 == 0) {
       if (first + 2 * kAdamBlock <= end) {
-        blocks_step<BITS, 4, 2>(p, f, it, first, kAdamBlock, lane);
+        blocks_step<BITS, 4, 2>(p, to, f, it, first, kAdamBlock, lane);
         continue;
       }
       if (first + kAdamBlock <= end) {
-        blocks_step<BITS, 4, 1>(p, f, it, first, kAdamBlock, lane);
+        blocks_step<BITS, 4, 1>(p, to, f, it, first, kAdamBlock, lane);
         first += kAdamBlock;
       }
     }
 #pragma unroll 1
     for (; first < end; first += kAdamBlock)
-      blocks_step<BITS, 1, 1>(p, f, it, first, end - first < kAdamBlock ? end - first : kAdamBlock, lane);
+      blocks_step<BITS, 1, 1>(p, to, f, it, first, end - first < kAdamBlock ? end - first : kAdamBlock, lane);
   }
   // the last CTA counts the step: every other one has read the count
   __syncthreads();
@@ -402,9 +403,15 @@ cudaError_t launch_adam_norm(const AdamStep& p, int sms, cudaStream_t stream) {
   return tc::launch_early(norm_kernel, dim3(grid), kThreads, stream, p);
 }
 
-cudaError_t launch_adam_step(const AdamStep& p, int sms, cudaStream_t stream) {
-  return p.bits == 8 ? tc::launch_early(step_kernel<8>, dim3(grid_of(p, sms, waves(8))), kThreads, stream, p)
-                     : tc::launch_early(step_kernel<32>, dim3(grid_of(p, sms, waves(32))), kThreads, stream, p);
+cudaError_t launch_adam_step(const AdamStep& p, const AdamCopies<kMaxAdamCopies>& c, int sms, cudaStream_t stream) {
+  const dim3 grid(grid_of(p, sms, waves(p.bits)));
+  if (p.n_copies > kFewAdamCopies)
+    return p.bits == 8 ? tc::launch_early(step_kernel<8, kMaxAdamCopies>, grid, kThreads, stream, p, c)
+                       : tc::launch_early(step_kernel<32, kMaxAdamCopies>, grid, kThreads, stream, p, c);
+  AdamCopies<kFewAdamCopies> few = {};
+  for (int k = 0; k < p.n_copies; ++k) few.params[k] = c.params[k], few.out[k] = c.out[k];
+  return p.bits == 8 ? tc::launch_early(step_kernel<8, kFewAdamCopies>, grid, kThreads, stream, p, few)
+                     : tc::launch_early(step_kernel<32, kFewAdamCopies>, grid, kThreads, stream, p, few);
 }
 
 }  // namespace ddl

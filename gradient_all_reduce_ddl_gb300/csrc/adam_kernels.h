@@ -44,11 +44,18 @@ struct AdamStep {
   int32_t bits;       // of the states: 32 or 8
   int32_t vec;        // every buffer allows accesses of four elements at multiples of four
   int32_t n_copies;
-  float* params[kMaxAdamCopies];
-  void* out[kMaxAdamCopies];  // out[0] NULL: no operand copies
+  int32_t operands;   // there are operand copies
 };
 
+// The parameter copies; launches of a few carry a shorter record (one of 4 KB takes the host longer).
+template <int N>
+struct AdamCopies {
+  float* params[N];
+  void* out[N];
+};
+constexpr int kFewAdamCopies = 16;
+
 cudaError_t launch_adam_norm(const AdamStep& p, int sms, cudaStream_t stream);
-cudaError_t launch_adam_step(const AdamStep& p, int sms, cudaStream_t stream);
+cudaError_t launch_adam_step(const AdamStep& p, const AdamCopies<kMaxAdamCopies>& c, int sms, cudaStream_t stream);
 
 }  // namespace ddl

@@ -394,17 +394,26 @@ def test_labels_past_the_vocabulary_are_reported(ddl, t):
         assert not dx[bad].any()
 
 
-def test_pieces_of_the_vocabulary(ddl):
-    """More logits than a piece holds: three pieces, the last one ragged; dx is added over them."""
-    t, k, v = 16384, 64, 40001
-    h = Head(t, k, v, "bf16", bias=True, seed=18).solve()
-    with ddl.CrossEntropy(k, v, t, "bf16") as head:
+@pytest.mark.parametrize("t, k, v, dtype", [(16384, 64, 40001, "bf16"), (16384, 65, 20001, "f16")])
+def test_pieces_of_the_vocabulary(ddl, t, k, v, dtype):
+    """More logits than a piece holds: three or two pieces, the last one ragged; dx is added over them, in odd rows, too."""
+    h = Head(t, k, v, dtype, bias=True, seed=18).solve()
+    with ddl.CrossEntropy(k, v, t, dtype) as head:
         loss, lse = h.forward(ddl, head)
         dx, dw, db = torch.empty_like(h.x), torch.empty(v, k, device="cuda"), torch.empty(v, device="cuda")
         head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, bias=h.bias, dx=dx, dw=dw, db=db)
         head.check()
     h.check_forward(loss, lse)
     h.check_backward(dx, dw, db)
+
+
+@pytest.mark.parametrize("t", [16384, 16385, 20000])
+def test_many_tokens(ddl, t):
+    """On either side of the number up to which the gradient launch makes dz's scale itself."""
+    h = Head(t, 40, 50, "f16", bias=True, seed=24, dloss=torch.rand(t, generator=_gen(4), device="cuda") * 1e-9)
+    h.dloss[-1] = 1e-3  # the largest is the last
+    h.labels[-1] = 7
+    _run(ddl, h)
 
 
 def test_bands_of_tokens(ddl):
