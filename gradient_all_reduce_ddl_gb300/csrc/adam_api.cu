@@ -93,7 +93,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
   a->blocks = blocks;
   // few elements: short items, so that every SM has some
   uint64_t per = ddl::kAdamItemBlocks;
-  while (per > 1 && blocks < per * 152 * 3) per /= 2;
+  while (per > 1 && blocks < per * 152 * 6) per /= 2;
   try {
     std::vector<const ddl_tensor_t*> by(n_tensors);
     for (int i = 0; i < n_tensors; ++i) by[i] = tensors + i;

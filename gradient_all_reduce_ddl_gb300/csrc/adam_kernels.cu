@@ -7,7 +7,7 @@
 // Bound by HBM: 28 bytes an element with binary32 states and one copy, 8 (10 with a
 // 16-bit operand copy) for each further copy; 16.1 with 8-bit states, whose coding also
 // takes 60 instructions an element.  One launch covers every tensor: a CTA takes an
-// item of up to 2048 elements of one tensor, each of its warps one or two
+// item of up to 1024 elements of one tensor, each of its warps one or two
 // neighbouring blocks of 128, four elements per lane, so that a block's largest value (the
 // 8-bit states' scale) is one warp reduction, the work does not depend on how long the
 // tensors are, and what the SMs have in flight lies together (warps that walk 1024 elements
@@ -24,7 +24,7 @@
 namespace ddl {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = 128, kWarps = kThreads / 32;
 constexpr float kTop = 448.f;             // e4m3's largest number
 constexpr float kLeast = 0x1p-100f;       // blocks whose largest value is below this are kept as zeros
 constexpr uint32_t kCodeNan = 0x7F;
@@ -158,12 +158,12 @@ __device__ __forceinline__ float store_codes(void* base, int64_t at, uint32_t le
 
 // -- the step -----------------------------------------------------------------------
 
-// Occupancy and grid, by the states' width.  336 M elements with 8-bit states: four CTAs an SM (64 registers, five of them
-// spilled) 1250 us with the norm's pass, three 1290, five 1420, one block at a time instead of two 1460; four CTAs an SM in
-// the grid, 4 % longer with twice as many.  25.6 M elements of 16 copies with binary32 states: three CTAs of 80 registers 564
-// us, two 566, four 575, and a grid of four times the CTAs that fit 564, of those that fit 576.
-__host__ __device__ constexpr int min_ctas(int bits) { return bits == 32 ? 3 : 4; }
-constexpr int waves(int bits) { return bits == 32 ? 12 : 4; }
+// Occupancy and grid, by the states' width.  336 M elements with 8-bit states, the norm's pass among them: seven CTAs of 128
+// threads an SM (72 registers) 1222 us, eight (64, some spilled) 1248, six 1231, four of 256 threads 1272, three 1286; loads of
+// the next item before this one's arithmetic 1277 (112 registers), one block at a time instead of two 1460.  25.6 M elements
+// of 16 copies with binary32 states: a grid of four times the CTAs that fit 565 us, of those that fit 576.
+__host__ __device__ constexpr int min_ctas(int bits) { return bits == 32 ? 6 : 7; }
+constexpr int waves(int bits) { return bits == 32 ? 24 : 7; }
 
 // What the step count and the norm make of the parameters, in every thread.
 struct Factors {
@@ -185,7 +185,7 @@ __device__ __forceinline__ float inverse_of(float x) {
   return y;
 }
 
-// This warp's part [first, end) of an item: a block of each eight, or two neighbours of each sixteen.
+// This warp's part [first, end) of an item: a block of each four, or two neighbours of each eight.
 __device__ __forceinline__ void share_of(const AdamItem& it, uint32_t* first, uint32_t* end) {
   const uint32_t share = it.len > kWarps * kAdamBlock ? 2 * kAdamBlock : kAdamBlock;
   *first = (threadIdx.x >> 5) * share;
@@ -398,7 +398,7 @@ unsigned grid_of(const AdamStep& p, int sms, int most) {
 }  // namespace
 
 cudaError_t launch_adam_norm(const AdamStep& p, int sms, cudaStream_t stream) {
-  unsigned grid = grid_of(p, sms, 8);
+  unsigned grid = grid_of(p, sms, 12);
   if (grid > kMaxNormParts) grid = kMaxNormParts;
   return tc::launch_early(norm_kernel, dim3(grid), kThreads, stream, p);
 }

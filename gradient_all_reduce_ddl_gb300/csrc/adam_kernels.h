@@ -8,7 +8,7 @@
 namespace ddl {
 
 constexpr int kAdamBlock = 128;      // elements that share the scales of an 8-bit state: four per lane of a warp
-constexpr int kAdamItemBlocks = 16;  // the most blocks a CTA takes at a time
+constexpr int kAdamItemBlocks = 8;   // the most blocks a CTA takes at a time
 constexpr int kMaxAdamCopies = 256;  // parameter copies
 constexpr int kMaxNormParts = 2048;  // CTAs of the norm's pass
 
