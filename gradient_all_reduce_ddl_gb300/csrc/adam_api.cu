@@ -16,6 +16,7 @@ struct ddl_adam {
   std::vector<ddl::AdamItem> items;
   uint64_t extent = 0;  // elements of the flat buffers that the tensors reach
   uint64_t blocks = 0;
+  bool odd = false;  // a tensor does not begin at a multiple of four
   int grad_type, bits;
   double beta1 = 0.9, beta2 = 0.999, eps = 1e-8;
   int device = -1;
@@ -75,6 +76,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
   if (grad_dtype != DDL_FP32 && grad_dtype != DDL_FP16 && grad_dtype != DDL_BF16) return DDL_ERR_INVALID_ARG;
   constexpr uint64_t kMost = 1ull << 48;
   uint64_t total = 0, extent = 0, blocks = 0;
+  bool odd = false;
   for (int i = 0; i < n_tensors; ++i) {
     const ddl_tensor_t& t = tensors[i];
     if (t.count < 1 || t.offset > kMost || t.count > kMost) return DDL_ERR_INVALID_ARG;
@@ -82,6 +84,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
     extent = std::max(extent, (uint64_t)t.offset + t.count);
     total += t.count;
     blocks += (t.count + ddl::kAdamBlock - 1) / ddl::kAdamBlock;
+    odd = odd || t.offset % 4 != 0;
     if (total > kMost) return DDL_ERR_INVALID_ARG;
   }
   if (grad_dtype == DDL_BF16 || blocks > 0xFFFFFFFFull) return DDL_ERR_UNSUPPORTED;
@@ -91,6 +94,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
   a->bits = state_bits;
   a->extent = extent;
   a->blocks = blocks;
+  a->odd = odd;
   // few elements: short items, so that every SM has some
   uint64_t per = ddl::kAdamItemBlocks;
   while (per > 1 && blocks < per * 152 * 6) per /= 2;
@@ -210,6 +214,7 @@ ddl_status_t ddl_adam_step(ddl_adam_t a, const void* grad, int n_copies, float* 
   p.out_type = operand_dtype == DDL_BF16 ? ddl::kBF16 : ddl::kF16;
   p.bits = a->bits;
   p.vec = vec;
+  p.odd = !vec || a->odd;
   p.n_copies = n_copies;
   p.operands = operand_bufs != nullptr;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -43,6 +43,7 @@ struct AdamStep {
   int32_t out_type;   // ElemType of the operand copies
   int32_t bits;       // of the states: 32 or 8
   int32_t vec;        // every buffer allows accesses of four elements at multiples of four
+  int32_t odd;        // not so, or a tensor does not begin at one
   int32_t n_copies;
   int32_t operands;   // there are operand copies
 };
