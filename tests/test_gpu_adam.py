@@ -176,7 +176,7 @@ def test_unaligned_buffers(ddl, state, shift):
     Problem(ddl, [(0, 640), (641, 300)], state, "f16", 2, "f16", seed=shift, shift=shift).run()
 
 
-@pytest.mark.parametrize("copies", [16, 256])
+@pytest.mark.parametrize("copies", [16, 17, 256])
 def test_many_copies(ddl, copies):
     Problem(ddl, [(0, 1000), (1001, 333)], "8bit", copies=copies, operands="bf16", seed=2).run()
 
@@ -317,6 +317,19 @@ def test_against_torch_adamw(ddl):
     # three steps of at most 4 u |p| + 34 u U each, |p| < 5 and U < 3.2 lr; m's and v's own errors are counted in U's
     assert float((p.double() - ref.detach()).abs().max()) <= 3 * (20 + 34 * 3.2 * lr + 50 * lr) * U
     assert math.isclose(float(s["step"]), 3)
+
+
+def test_memory_that_is_short(ddl, monkeypatch):
+    pr = Problem(ddl, ODD, "8bit", seed=14)
+    before = [x.clone() for x in (pr.m, pr.v, pr.step_count)]
+    monkeypatch.setenv("DDL_INJECT_ALLOC_FAILURE", "1")
+    with pytest.raises(ddl.DDLError) as e:
+        pr.adam.step(pr.grad, pr.params, pr.m, pr.v, pr.step_count, 1e-2, scales=pr.scales)
+    assert e.value.status == ddl.DDL_ERR_OOM
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(before, (pr.m, pr.v, pr.step_count)))
+    monkeypatch.delenv("DDL_INJECT_ALLOC_FAILURE")
+    pr.run()
 
 
 def test_checks_of_the_object(ddl):

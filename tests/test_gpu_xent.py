@@ -185,6 +185,15 @@ def test_sizes(ddl, t, k, v, dtype):
     _run(ddl, Head(t, k, v, dtype, bias=(t + v) % 2 == 1, smoothing=0.1 if t % 3 == 0 else 0.0, seed=t + v))
 
 
+@pytest.mark.parametrize("t, k, v", [(1, 64, 65536), (16, 320, 40000), (32, 72, 19457), (33, 130, 20011), (64, 1032, 70001)])
+def test_few_tokens_large_vocabularies(ddl, t, k, v):
+    """More tiles than SMs: several in a row, of 128 rows or fewer, the last ones cut."""
+    h = Head(t, k, v, "bf16", bias=True, smoothing=0.1, seed=t + v).solve()
+    with ddl.CrossEntropy(k, v, t, "bf16", smoothing=0.1) as head:
+        h.check_forward(*h.forward(ddl, head))
+        head.check()
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("grad, accumulate", [("f16", False), ("f16", True), ("f32", True)])
 @pytest.mark.parametrize("t, k, v", [(7, 40, 33), (200, 96, 515), (700, 1030, 1100)])
@@ -558,6 +567,29 @@ def test_waits_that_run_out_are_reported(ddl, t, k, v, stop):
             assert reported or stop not in (dict(products=0), dict(loads_even=0))
             assert all(torch.equal(a, b) for a, b in zip(want, _everything(ddl, head, h)))
             head.check()
+
+
+def test_memory_that_is_short(ddl, monkeypatch):
+    """A failed allocation is reported and queues nothing; the next call makes up for it."""
+    h = Head(100, 63, 90, "f16", bias=True, seed=51).solve()
+    with ddl.CrossEntropy(63, 90, 100, "f16") as head:
+        dx, dw = torch.empty_like(h.x), torch.full((90, 63), 7.0, device="cuda")
+        monkeypatch.setenv("DDL_INJECT_ALLOC_FAILURE", "1")
+        with pytest.raises(ddl.DDLError) as e:
+            h.forward(ddl, head)
+        assert e.value.status == ddl.DDL_ERR_OOM
+        monkeypatch.delenv("DDL_INJECT_ALLOC_FAILURE")
+        loss, lse = h.forward(ddl, head)
+        h.check_forward(loss, lse)
+        monkeypatch.setenv("DDL_INJECT_ALLOC_FAILURE", "1")
+        with pytest.raises(ddl.DDLError) as e:
+            head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, bias=h.bias, dx=dx, dw=dw)
+        assert e.value.status == ddl.DDL_ERR_OOM
+        torch.cuda.synchronize()
+        assert bool((dw == 7).all())
+        monkeypatch.delenv("DDL_INJECT_ALLOC_FAILURE")
+        head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, bias=h.bias, dx=dx, dw=dw)
+        h.check_backward(dx, dw)
 
 
 def test_checks_of_the_object(ddl):
