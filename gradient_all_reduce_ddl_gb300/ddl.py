@@ -879,10 +879,10 @@ class Adam:
         self.n_blocks = ddl_adam_blocks(self.handle)
 
     def _flat(self, t, dtypes, name, n):
-        """The address of a vector of at least n elements."""
-        if t.dtype in dtypes and t.is_cuda and t.dim() == 1 and t.numel() >= n and t.is_contiguous():
+        """The address of a buffer of at least n elements."""
+        if t.dtype in dtypes and t.is_cuda and t.numel() >= n and t.is_contiguous():
             return t.data_ptr()
-        raise ValueError(f"{name}: expected a contiguous CUDA vector of {dtypes[0]} with at least {n} elements")
+        raise ValueError(f"{name}: expected a contiguous CUDA tensor of {dtypes[0]} with at least {n} elements")
 
     def new_state(self, device="cuda"):
         """The states before the first step, as step() takes them: m, v, step and (8 bits) scales."""
@@ -909,9 +909,9 @@ class Adam:
             out_dtype = self._operands[kind]
             out = _ptr_array([flat(o, (kind,), "operands", n) for o in operands])
         if scales is not None:
-            if self.state != "8bit" or not scales.is_contiguous() or scales.numel() != 2 * self.n_blocks:
-                raise ValueError(f"scales: a contiguous tensor of {2 * self.n_blocks} elements, with 8-bit states only")
-            scales = flat(scales.view(-1), f32, "scales", 2 * self.n_blocks)
+            if self.state != "8bit" or scales.numel() != 2 * self.n_blocks:
+                raise ValueError(f"scales: a tensor of {2 * self.n_blocks} elements, with 8-bit states only")
+            scales = flat(scales, f32, "scales", 0)
         _ok(_lib.ddl_adam_step(self.handle, flat(grad, (self._grad,), "grad", n), len(params),
                                _ptr_array([flat(p, f32, "params", n) for p in params]), out, out_dtype,
                                flat(m, self._state, "m", n), flat(v, self._state, "v", n), scales,
