@@ -24,44 +24,64 @@ struct LogSum {
   }
 };
 
-// TX tokens per CTA, its other threads share out the parts.
+// TX tokens per CTA (1, 8 or 32), its other threads share out the parts: those of a warp join by shuffles, the warps through
+// shared memory.
 template <int TX>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ XentJoin p) {
-  constexpr int TY = kThreads / TX;
-  __shared__ float2 shared[TY][TX];
-  __shared__ float shared_sum[TY][TX];
+  constexpr int TY = kThreads / TX, kBatch = TX == 32 ? 8 : 4;
+  __shared__ float2 shared[kWarps][TX];
+  __shared__ float shared_sum[kWarps][TX];
   tc::griddep_launch();
   tc::griddep_wait();
-  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+  const int tx = threadIdx.x % TX, ty = threadIdx.x / TX, warp = threadIdx.x >> 5;
   const int64_t t = (int64_t)blockIdx.x * TX + tx;
+  const bool in = t < p.tokens, writes = ty == 0 && in;
+  int64_t y = -1;
+  float z = 0.f;
+  if (writes) {
+    y = p.labels[t];
+    z = __ldcg(p.picked + t);  // not set without a label
+  }
   LogSum l = {-INFINITY, 0.f};
   float all = 0.f;
-  if (t < p.tokens) {
-#pragma unroll 4
-    for (int k = ty; k < p.n_parts; k += TY) {
-      const float2 u = __ldcg(p.part + (int64_t)k * p.ld + t);
-      l.add(u.x, u.y);
+  if (in) {
+    for (int k0 = ty; k0 < p.n_parts; k0 += kBatch * TY) {
+      float2 u[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        u[k] = k0 + k * TY < p.n_parts ? __ldcg(p.part + (int64_t)(k0 + k * TY) * p.ld + t) : make_float2(-INFINITY, 0.f);
+      // as add(), of all of them
+      float most = l.most, s = 0.f;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) most = fmaxf(most, u[k].x);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) s += u[k].y * (u[k].x == most ? 1.f : expf(u[k].x - most));
+      l.sum = l.sum * (l.most == most ? 1.f : expf(l.most - most)) + s;
+      l.most = most;
     }
     if (p.part_sum) {
 #pragma unroll 4
       for (int k = ty; k < p.n_parts; k += TY) all += __ldcg(p.part_sum + (int64_t)k * p.ld + t);
     }
   }
-  shared[ty][tx] = make_float2(l.most, l.sum);
-  shared_sum[ty][tx] = all;
 #pragma unroll
-  for (int d = TY / 2; d; d >>= 1) {
-    __syncthreads();
-    if (ty < d) {
-      const float2 u = shared[ty + d][tx];
-      l.add(u.x, u.y);
-      all += shared_sum[ty + d][tx];
-      shared[ty][tx] = make_float2(l.most, l.sum);
-      shared_sum[ty][tx] = all;
-    }
+  for (int d = 16; d >= TX; d >>= 1) {
+    const float m = __shfl_xor_sync(0xFFFFFFFFu, l.most, d), s = __shfl_xor_sync(0xFFFFFFFFu, l.sum, d);
+    l.add(m, s);
+    all += __shfl_xor_sync(0xFFFFFFFFu, all, d);
   }
-  if (ty > 0 || t >= p.tokens) return;
-  const int64_t y = p.labels[t];
+  if ((threadIdx.x & 31) < TX) {
+    shared[warp][tx] = make_float2(l.most, l.sum);
+    shared_sum[warp][tx] = all;
+  }
+  __syncthreads();
+  if (!writes) return;
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) {
+    const float2 u = shared[w][tx];
+    l.add(u.x, u.y);
+    all += shared_sum[w][tx];
+  }
   float loss = 0.f, lse;
   if (y < 0 || y >= p.vocab) {
     lse = l.most + logf(l.sum);
@@ -71,7 +91,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     }
   } else {
     // lse - z, with z the label's logit: what the others add to it, or what is left of them
-    const float z = __ldcg(p.picked + t);
     loss = z >= l.most ? log1pf(l.sum * expf(l.most - z)) : (l.most - z) + logf(l.sum + expf(z - l.most));
     LogSum every = l;
     every.add(z, 1.f);
