@@ -208,6 +208,63 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   }
 }
 
+// Copies alone: without the registers of the other work twice the warps fit an SM, and rows are copied in words of two
+// elements, two rows of a warp at a time.  A row that begins in the middle of a word is read in the words around its elements, and
+// put together from neighbouring lanes' halves; the last columns go element by element.  20,011 x 1001: 15.6 us cold, 21.7 in the kernel above.
+__device__ __forceinline__ void pack_words(const Pack& p, uint32_t block) {
+  constexpr int kWords = kPackCols / 64, kBatch = 2;
+  const int lane = threadIdx.x & 31;
+  const uint32_t across = (uint32_t)((p.cols + kPackCols - 1) / kPackCols);
+  const int64_t row0 = (int64_t)(block / across) * kPackRows + (threadIdx.x >> 5), c0 = (int64_t)(block % across) * kPackCols;
+  if (c0 + kPackCols >= p.cols) {
+    pack_block(p, block);
+    return;
+  }
+#pragma unroll 1
+  for (int i0 = 0; i0 < kPackRows / kWarps; i0 += kBatch) {
+    uint32_t w[kBatch][kWords + 1];
+    bool odd[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t r = row0 + (i0 + i) * kWarps < p.rows ? row0 + (i0 + i) * kWarps : p.rows - 1;
+      const uint16_t* row = p.src + r * p.ld + c0;
+      odd[i] = reinterpret_cast<uintptr_t>(row) & 2;
+      // the word before the row's first element may be another's: its half alone
+      const bool half = odd[i] && c0 == 0 && lane == 0;
+      const uint32_t* words = reinterpret_cast<const uint32_t*>(row - (odd[i] ? 1 : 0));
+      w[i][0] = half ? (uint32_t)row[0] << 16 : words[half ? 1 : lane];
+#pragma unroll
+      for (int j = 1; j < kWords; ++j) w[i][j] = words[lane + 32 * j];
+      w[i][kWords] = row[kPackCols - 1];
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int64_t r = row0 + (i0 + i) * kWarps;
+      if (r >= p.rows) break;
+      uint32_t* to = reinterpret_cast<uint32_t*>(p.dst + r * p.ldp + c0);
+#pragma unroll
+      for (int j = 0; j < kWords; ++j) {
+        uint32_t v = w[i][j];
+        if (odd[i]) {
+          const uint32_t down = __shfl_down_sync(0xffffffffu, v, 1), next = __shfl_sync(0xffffffffu, w[i][j + 1], 0);
+          v = __byte_perm(v, lane == 31 ? next : down, 0x5432);
+        }
+        to[lane + 32 * j] = v;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 6) pack_kernel(const __grid_constant__ LinearPrep p) {
+  tc::griddep_launch();
+  tc::griddep_wait();
+  const uint32_t first = (uint32_t)((p.pack[0].rows + kPackRows - 1) / kPackRows * ((p.pack[0].cols + kPackCols - 1) / kPackCols));
+  if (blockIdx.x < first)
+    pack_words(p.pack[0], blockIdx.x);
+  else
+    pack_words(p.pack[1], blockIdx.x - first);
+}
+
 }  // namespace
 
 float plane_scale(int type, int n, int k) {
@@ -221,6 +278,7 @@ cudaError_t launch_linear_prep(const LinearPrep& p, cudaStream_t stream) {
     blocks += ((p.pack[k].rows + kPackRows - 1) / kPackRows) * ((p.pack[k].cols + kPackCols - 1) / kPackCols);
   if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+  if (!p.has_dz) return tc::launch_early(pack_kernel, dim3((unsigned)blocks), kThreads, stream, p);
   const auto kernel = p.type == kBF16 ? (p.vec ? prep_kernel<kBF16, true> : prep_kernel<kBF16, false>)
                                       : (p.vec ? prep_kernel<kF16, true> : prep_kernel<kF16, false>);
   return tc::launch_early(kernel, dim3((unsigned)blocks), kThreads, stream, p);
