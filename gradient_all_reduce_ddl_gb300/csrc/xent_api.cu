@@ -34,12 +34,12 @@ constexpr int64_t kFewTokens = 64;            // up to here they are the narrow 
 constexpr int64_t kMostParts = 1ll << 26;     // of a forward launch, over its tokens: 512 MB
 constexpr int64_t kPieceElems = 1ll << 28;    // tokens x entries of a piece of the vocabulary: 512 MB a plane
 constexpr int64_t kPieceStep = 256;           // pieces begin at whole tiles
-// K blocks of logits that stay in the tensor core's truncating accumulator.
-// (forward, gradient).  The products run on under an epilogue for two chunks: with short ones they wait for it.  8192 tokens, 4096
-// features, a vocabulary of 65,536: 2852, 2649, 2543 us with 4, 8, 16 blocks, and a training step of 2048 features 7634, 7281,
-// 7119 us.  Relative errors of the loss 1.8, 3.7, 7.8e-7 (products in binary32: 6.9e-7) and of binary32 dw 1.5, 1.6, 2.0e-6
-// (1.8e-6).
-constexpr int32_t kLossChunk = 8, kGradChunk = 16;
+// K blocks of logits that stay in the tensor core's truncating accumulator.  The products run on under an epilogue for two
+// chunks: with short ones they wait for it.  8192 tokens, 4096 features, a vocabulary of 65,536: 2852, 2649, 2543 us with 4, 8,
+// 16 blocks, and a training step of 2048 features 7634, 7281, 7119 us; relative errors of the loss 1.8, 3.7, 7.8e-7 (products in
+// binary32: 6.6e-7) and of binary32 dw 1.7, 1.6, 2.0e-6 (1.75e-6).  The gradient takes the loss's chunk: what truncation takes
+// from z it then takes from lse, too (with 16 blocks under a loss of 8 dw is 3.0e-6 off).
+constexpr int32_t kLogitChunk = 8;
 
 ddl_status_t bind(ddl_xent* h) {
   int dev = -1;
@@ -204,7 +204,7 @@ ddl_status_t ddl_xent_forward(ddl_xent_t h, size_t tokens, const void* x, size_t
     P.a[0] = swap ? 1 : 0;
     P.b[0] = swap ? 0 : 1;
     P.scale[0] = 1.f;
-    P.chunk[0] = P.chunk[1] = kLossChunk;
+    P.chunk[0] = P.chunk[1] = kLogitChunk;
     P.epi = kEpiLoss;
     P.swap = swap;
     P.type = h->type;
@@ -330,7 +330,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       P.a[0] = 0;
       P.b[0] = 1;
       P.scale[0] = 1.f;
-      P.chunk[0] = P.chunk[1] = kGradChunk;
+      P.chunk[0] = P.chunk[1] = kLogitChunk;
       P.epi = kEpiGrad;
       P.type = h->type;
       P.in0 = P.in1 = -1;
