@@ -74,7 +74,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
   *out = nullptr;
   if (n_tensors < 1 || !tensors || (state_bits != 32 && state_bits != 8)) return DDL_ERR_INVALID_ARG;
   if (grad_dtype != DDL_FP32 && grad_dtype != DDL_FP16 && grad_dtype != DDL_BF16) return DDL_ERR_INVALID_ARG;
-  constexpr uint64_t kMost = 1ull << 48;
+  constexpr uint64_t kMost = 1ull << 48, kMostElems = 1ull << 35;  // the second: more than the states of which fill the device
   uint64_t total = 0, extent = 0, blocks = 0;
   bool odd = false;
   for (int i = 0; i < n_tensors; ++i) {
@@ -87,7 +87,7 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
     odd = odd || t.offset % 4 != 0;
     if (total > kMost) return DDL_ERR_INVALID_ARG;
   }
-  if (grad_dtype == DDL_BF16 || blocks > 0xFFFFFFFFull) return DDL_ERR_UNSUPPORTED;
+  if (grad_dtype == DDL_BF16 || total > kMostElems || blocks > 0xFFFFFFFFull) return DDL_ERR_UNSUPPORTED;
   ddl_adam* a = new (std::nothrow) ddl_adam();
   if (!a) return DDL_ERR_OOM;
   a->grad_type = grad_dtype == DDL_FP16 ? ddl::kF16 : ddl::kF32;

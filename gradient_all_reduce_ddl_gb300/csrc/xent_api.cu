@@ -189,7 +189,6 @@ ddl_status_t ddl_xent_forward(ddl_xent_t h, size_t tokens, const void* x, size_t
       splits = l.splits;
       tiles = count(tile_n);
     }
-    if (tiles * 8 > kMaxTiles) return DDL_ERR_UNSUPPORTED;
     ProductLaunch L = {};
     L.bf16 = h->type == kBF16;
     const Mat bx{static_cast<const uint16_t*>(ax.p) + t0 * ax.ld, n, K, ax.ld};

@@ -610,7 +610,8 @@ typedef struct ddl_adam* ddl_adam_t;
 
 /* n_tensors >= 1 tensors of 1..2^48 elements that do not overlap; elements
  * outside of them are neither read nor written.  grad_dtype DDL_FP32 or
- * DDL_FP16 (DDL_BF16: DDL_ERR_UNSUPPORTED); state_bits 32 or 8.  The constants
+ * DDL_FP16 (DDL_BF16, and more than 2^35 elements in all: DDL_ERR_UNSUPPORTED);
+ * state_bits 32 or 8.  The constants
  * start as beta1 = 0.9, beta2 = 0.999, eps = 1e-8.  The array is copied.  Host-only. */
 ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dtype_t grad_dtype, int state_bits,
                              ddl_adam_t* out);

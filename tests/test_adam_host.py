@@ -31,6 +31,7 @@ def _status(ddl, fn, *args):
     ([((1 << 48) + 1, 4)], 0, 32, "DDL_ERR_INVALID_ARG"),
     ([(0, (1 << 48) + 1)], 0, 32, "DDL_ERR_INVALID_ARG"),
     ([(0, 1 << 41)], 0, 8, "DDL_ERR_UNSUPPORTED"),
+    ([(0, 1 << 34), (1 << 40, (1 << 34) + 1)], 0, 32, "DDL_ERR_UNSUPPORTED"),
     ([(0, 4, float("nan"))], 0, 32, "DDL_ERR_INVALID_ARG"),
     ([(0, 4, 1.0, float("inf"))], 0, 32, "DDL_ERR_INVALID_ARG"),
 ])
