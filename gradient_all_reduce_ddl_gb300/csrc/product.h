@@ -111,6 +111,7 @@ struct Softmax {
   float* scale;        // [0] what dz's planes are multiplied by, [1] its inverse
   float on, off;
   int32_t planes;      // 1 or 2
+  float* resid;        // NULL, or of every token what rounding to the first plane takes from the label's dz (x scale)
   float* db;           // NULL, or the sums of dz (x scale) over every 32 tokens, or over a split tile's shares of them
   int64_t ld_db;
 };

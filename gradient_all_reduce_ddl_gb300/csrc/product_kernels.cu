@@ -971,10 +971,12 @@ __device__ __forceinline__ void loss_columns(const ProductLaunch& p, int row0, i
 struct GradRow {
   float high;      // h
   float by_p, by;  // the coefficient times the planes' scale, with and without 2^-l
+  int token;
   int label;       // counted from the piece's first entry; outside of it: -1
   bool valid;
   __device__ __forceinline__ void load(const Softmax& e, float scale, int m, int rows, int entries) {
     high = by_p = by = 0.f;
+    token = m;
     label = -1;
     valid = false;
     if (m >= rows) return;
@@ -988,14 +990,18 @@ struct GradRow {
   }
   // dz (x scale) of N entries from n, whose logits are z
   template <int N>
-  __device__ __forceinline__ void of(float* z, int n, const Softmax& e) const {
+  __device__ __forceinline__ void of(float* z, int n, const Softmax& e, int type) const {
     const float less = -e.off * by;
 #pragma unroll
     for (int k = 0; k < N; ++k) z[k] = fmaf(exp2_fast(fmaf(z[k], kLog2e, -high)), by_p, less);
     if (label >= n && label < n + N) {
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        if (n + k == label) z[k] -= e.on * by;
+        if (n + k == label) {
+          z[k] -= e.on * by;
+          // (nothing of an infinite or NaN value)
+          if (e.resid) e.resid[token] = fabsf(z[k]) <= FLT_MAX ? z[k] - from16(to16(z[k], type), type) : 0.f;
+        }
     }
     if (!valid) {
 #pragma unroll
@@ -1052,7 +1058,7 @@ __device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, cons
   const Product& P = p.inl[0];
   const Softmax& e = p.soft;
   add_bias16(p, v, bias);
-  g.of<16>(v, n, e);
+  g.of<16>(v, n, e, P.type);
   if (P.type == kBF16)
     slab_planes<kBF16>(v, buf, row, half, e.planes == 2);
   else
@@ -1086,7 +1092,7 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, i
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         if (e.bias && n + k < P.N) v[k] += bias_one(p, n + k);
-      g.of<4>(v, n, e);
+      g.of<4>(v, n, e, P.type);
 #pragma unroll
       for (int k = 0; k < 4; ++k) total[k] += v[k];
       uint32_t hi[2], lo[2];

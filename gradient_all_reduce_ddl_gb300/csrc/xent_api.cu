@@ -20,7 +20,7 @@ struct ddl_xent {
   ddl::Residency room = {};
   uint32_t* d_err = nullptr;
   ddl::GiveUp give_up;  // of the next call's first product
-  ddl::Buffer x, w, part, part_sum, picked, planes[2], scale, db, dx;
+  ddl::Buffer x, w, part, part_sum, picked, planes[2], scale, resid, db, dx;
 };
 
 namespace {
@@ -277,8 +277,8 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
     return status_of(e);
   }
 
-  // dz is kept to 16 bits of its operands' type in dx, whose own rounding is as coarse, and in binary16 gradients of
-  // binary16 layers; else to two such planes, 16 or 22 bits.
+  // dz is kept to 16 bits of its operands' type in dx (but for the label's, see XentRound), whose own rounding is as coarse, and
+  // in binary16 gradients of binary16 layers; else to two such planes, 16 or 22 bits.
   const bool f16 = h->type == kF16;
   const int dw_planes = !dw ? 0 : f16 && grad_dtype == DDL_FP16 ? 1 : 2;
   const int n_planes = std::max(1, dw_planes);
@@ -288,7 +288,9 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   const int64_t most_sums = std::max<int64_t>(kSplitSums, (int64_t)plane_elems(h) / 32 + (int64_t)round8((uint64_t)V));
   if (db && (st = need(&h->db, (size_t)most_sums * 4)) != DDL_OK) return st;
   const int64_t ld32 = (int64_t)round8((uint64_t)K);
-  if (dx && piece < V && (st = need(&h->dx, (size_t)h->max_tokens * (size_t)ld32 * 4)) != DDL_OK) return st;
+  if (dx && ((st = need(&h->dx, (size_t)h->max_tokens * (size_t)ld32 * 4)) != DDL_OK ||
+             (st = need(&h->resid, (size_t)h->max_tokens * 4)) != DDL_OK))
+    return st;
   LinearPrep prep;
   std::memset(&prep, 0, sizeof(prep));
   prep.type = h->type;
@@ -352,6 +354,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       L.soft.on = 1.f - h->smoothing;
       L.soft.off = h->smoothing / (float)V;
       L.soft.planes = n_planes;
+      L.soft.resid = dx ? static_cast<float*>(h->resid.p) : nullptr;
       L.soft.db = db ? static_cast<float*>(h->db.p) : nullptr;
       L.soft.ld_db = ldp;
       if ((st = status_of(launch(L, l.tile, h->sms, s))) != DDL_OK) return st;
@@ -371,9 +374,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
     if (!dx && !dw) continue;
 
     const Mat ow{dw ? static_cast<char*>(dw) + v0 * (int64_t)lddw * ge : nullptr, n, K, (int64_t)lddw};
-    const bool whole = piece >= V;  // dx in one go, else its sums over the pieces are kept in binary32
-    const Mat ox = whole ? mdx : Mat{h->dx.p, T, K, ld32};
-    const int xe = whole ? 2 : 4;
+    const Mat ox{h->dx.p, T, ld32, ld32};  // dx's sums over the pieces, with their rows' padding
     const auto dw_count = [&](int tile) { return blocks_of(n, tile) * blocks_of(K, tile); };
     const auto dx_count = [&](int tile) { return blocks_of(T, tile) * blocks_of(K, tile); };
     const int64_t dw_steps = blocks_of(T, kBlockK) * dw_planes, dx_steps = blocks_of(n, kBlockK);
@@ -429,9 +430,9 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       P.scale[0] = 1.f;
       P.chunk[0] = P.chunk[1] = (int32_t)long_chunk(h->type);
       P.epi = kEpiStore;
-      P.out_type = whole ? h->type : (int)kF32;
+      P.out_type = kF32;
       P.accumulate = v0 > 0;
-      P.vec = ox.vec4(xe);
+      P.vec = 1;
       P.in0 = v0 > 0 ? 6 : -1;
       P.out0 = 6;
       P.in1 = P.out1 = -1;
@@ -453,12 +454,11 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       if (with_dw && !dw_first) add_dw(L, l.tile);
       L.n_tiles = L.inl_tiles[0] + L.inl_tiles[1];
       L.splits = l.splits;
-      L.boxes = L.splits == 1 && (!with_dw || (ge == 4 ? ow.tma32() : ow.tma())) && (!with_dx || (xe == 4 ? ox.tma32() : ox.tma())) &&
-                K % 8 == 0;
+      L.boxes = L.splits == 1 && (!with_dw || ((ge == 4 ? ow.tma32() : ow.tma()) && K % 8 == 0));
       if (L.boxes) {
         // a binary16 gradient's map takes the operands' element type: TMA moves its bits only
         if (with_dw && !(ge == 4 ? map32_of(&L, 5, ow) : map_of(&L, 5, ow, kSlabCols))) return DDL_ERR_CUDA;
-        if (with_dx && !(xe == 4 ? map32_of(&L, 6, ox) : map_of(&L, 6, ox, kSlabCols))) return DDL_ERR_CUDA;
+        if (with_dx && !map32_of(&L, 6, ox)) return DDL_ERR_CUDA;
       }
       return status_of(launch(L, l.tile, h->sms, s));
     };
@@ -474,8 +474,9 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
     }
     if ((st = products(dw != nullptr, dx != nullptr, both)) != DDL_OK) return st;
   }
-  if (dx && piece < V) {
-    const XentRound r = {static_cast<const float*>(h->dx.p), ld32, static_cast<uint16_t*>(dx), (int64_t)lddx, T, K, h->type};
+  if (dx) {
+    const XentRound r = {static_cast<const float*>(h->dx.p), ld32, static_cast<uint16_t*>(dx), (int64_t)lddx, T, K, h->type,
+                         labels, V, static_cast<const float*>(h->resid.p), scale + 1, static_cast<const uint16_t*>(aw.p), aw.ld};
     return status_of(launch_xent_round(r, s));
   }
   return DDL_OK;
@@ -505,7 +506,7 @@ ddl_status_t ddl_xent_destroy(ddl_xent_t h) {
   if (!h) return DDL_OK;
   cudaError_t e = cudaSuccess;
   for (void* p : {(void*)h->d_err, h->x.p, h->w.p, h->part.p, h->part_sum.p, h->picked.p, h->planes[0].p, h->planes[1].p,
-                  h->scale.p, h->db.p, h->dx.p})
+                  h->scale.p, h->resid.p, h->db.p, h->dx.p})
     if (p) {
       const cudaError_t f = cudaFree(p);  // waits for the device
       if (e == cudaSuccess) e = f;

@@ -155,6 +155,13 @@ __global__ void __launch_bounds__(kThreads) round_kernel(const __grid_constant__
   float v[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) v[k] = c0 + 32 * k < p.cols ? __ldcs(p.src + r * p.ld + c0 + 32 * k) : 0.f;
+  const int64_t y = p.labels[r];
+  if (y >= 0 && y < p.vocab) {
+    const float by = __ldcg(p.resid + r) * __ldcg(p.inverse);
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (c0 + 32 * k < p.cols) v[k] = fmaf(by, from16(p.w[y * p.ldw + c0 + 32 * k], p.type), v[k]);
+  }
 #pragma unroll
   for (int k = 0; k < 8; ++k)
     if (c0 + 32 * k < p.cols) p.dst[r * p.ldd + c0 + 32 * k] = to16(v[k], p.type);
