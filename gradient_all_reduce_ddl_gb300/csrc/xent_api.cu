@@ -303,6 +303,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   const XentScale sc = {dloss, labels, T, V, f16, scale};
   if (many && (st = status_of(launch_xent_scale(sc, s))) != DDL_OK) return st;
   const GiveUp give_up = take_give_up(h);
+  XentEnd end = {};  // what follows the products
 
   const int64_t ldp = (int64_t)round8((uint64_t)piece);
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
@@ -359,17 +360,17 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       L.soft.ld_db = ldp;
       if ((st = status_of(launch(L, l.tile, h->sms, s))) != DDL_OK) return st;
       if (db) {
-        XentBias b = {};
-        b.part = L.soft.db;
-        b.ld = ldp;
-        b.groups = splits == 1 ? blocks_of(T, 32) : blocks_of(T, kTileM) * splits;
-        b.cols = n;
-        b.scale = scale + 1;
-        b.db = static_cast<char*>(db) + v0 * ge;
-        b.f32 = ge == 4;
-        b.accumulate = accumulate ? 1 : 0;
-        if ((st = status_of(launch_xent_bias(b, s))) != DDL_OK) return st;
+        end.bias.part = L.soft.db;
+        end.bias.ld = ldp;
+        end.bias.groups = splits == 1 ? blocks_of(T, 32) : blocks_of(T, kTileM) * splits;
+        end.bias.cols = n;
+        end.bias.scale = scale + 1;
+        end.bias.db = static_cast<char*>(db) + v0 * ge;
+        end.bias.f32 = ge == 4;
+        end.bias.accumulate = accumulate ? 1 : 0;
       }
+      // the last piece's goes with dx
+      if (v0 + n < V && (st = status_of(launch_xent_end(end, s))) != DDL_OK) return st;
     }
     if (!dx && !dw) continue;
 
@@ -474,12 +475,10 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
     }
     if ((st = products(dw != nullptr, dx != nullptr, both)) != DDL_OK) return st;
   }
-  if (dx) {
-    const XentRound r = {static_cast<const float*>(h->dx.p), ld32, static_cast<uint16_t*>(dx), (int64_t)lddx, T, K, h->type,
-                         labels, V, static_cast<const float*>(h->resid.p), scale + 1, static_cast<const uint16_t*>(aw.p), aw.ld};
-    return status_of(launch_xent_round(r, s));
-  }
-  return DDL_OK;
+  if (dx)
+    end.round = {static_cast<const float*>(h->dx.p), ld32, static_cast<uint16_t*>(dx), (int64_t)lddx, T, K, h->type,
+                 labels, V, static_cast<const float*>(h->resid.p), scale + 1, static_cast<const uint16_t*>(aw.p), aw.ld};
+  return status_of(launch_xent_end(end, s));
 }
 
 ddl_status_t ddl_xent_selftest_wait_timeout(ddl_xent_t h, uint32_t limit_us, uint32_t products, uint32_t loads_even,

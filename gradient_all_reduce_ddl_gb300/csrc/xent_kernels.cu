@@ -1,6 +1,6 @@
 // xent_kernels.cu -- the passes around the products of the softmax cross entropy:
-// joining the vocabulary's parts, the planes' scale of many tokens, the bias
-// gradient, rounding dx's sums.  All of them read what the products left in L2, and
+// joining the vocabulary's parts, the planes' scale of many tokens, and, in one
+// launch, the bias gradient and the rounding of dx's sums.  All of them read what the products left in L2, and
 // small calls are bound by their launches (a join 3 us in a sequence).  8192 tokens x 512
 // parts are joined in 14 us, 8192 x 2048 sums rounded in 13 (7.4 TB/s, part of it from L2).
 #include "activation.cuh"
@@ -119,12 +119,10 @@ __global__ void __launch_bounds__(1024) scale_kernel(const __grid_constant__ Xen
   }
 }
 
-__global__ void __launch_bounds__(kThreads) bias_kernel(const __grid_constant__ XentBias p) {
+__device__ __forceinline__ void bias_columns(const XentBias& p, int64_t block) {
   __shared__ float shared[kWarps][32];
-  tc::griddep_launch();
-  tc::griddep_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+  const int64_t c = block * 32 + lane;
   float s = 0.f;
   if (c < p.cols) {
 #pragma unroll 4
@@ -145,12 +143,10 @@ __global__ void __launch_bounds__(kThreads) bias_kernel(const __grid_constant__ 
   }
 }
 
-__global__ void __launch_bounds__(kThreads) round_kernel(const __grid_constant__ XentRound p) {
-  tc::griddep_launch();
-  tc::griddep_wait();
+__device__ __forceinline__ void round_rows(const XentRound& p, int64_t block) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t across = (p.cols + 255) / 256;
-  const int64_t r = blockIdx.x / across * kWarps + warp, c0 = blockIdx.x % across * 256 + lane;
+  const int64_t r = block / across * kWarps + warp, c0 = block % across * 256 + lane;
   if (r >= p.rows) return;
   float v[8];
 #pragma unroll
@@ -167,6 +163,17 @@ __global__ void __launch_bounds__(kThreads) round_kernel(const __grid_constant__
     if (c0 + 32 * k < p.cols) p.dst[r * p.ldd + c0 + 32 * k] = to16(v[k], p.type);
 }
 
+int64_t bias_blocks(const XentBias& p) { return p.db ? (p.cols + 31) / 32 : 0; }
+
+__global__ void __launch_bounds__(kThreads) end_kernel(const __grid_constant__ XentEnd p, uint32_t first) {
+  tc::griddep_launch();
+  tc::griddep_wait();
+  if (blockIdx.x < first)
+    bias_columns(p.bias, blockIdx.x);
+  else
+    round_rows(p.round, blockIdx.x - first);
+}
+
 }  // namespace
 
 cudaError_t launch_xent_join(const XentJoin& p, cudaStream_t stream) {
@@ -179,14 +186,11 @@ cudaError_t launch_xent_scale(const XentScale& p, cudaStream_t stream) {
   return tc::launch_early(scale_kernel, dim3(1), 1024, stream, p);
 }
 
-cudaError_t launch_xent_bias(const XentBias& p, cudaStream_t stream) {
-  return tc::launch_early(bias_kernel, dim3((unsigned)((p.cols + 31) / 32)), kThreads, stream, p);
-}
-
-cudaError_t launch_xent_round(const XentRound& p, cudaStream_t stream) {
-  const int64_t blocks = (p.rows + kWarps - 1) / kWarps * ((p.cols + 255) / 256);
+cudaError_t launch_xent_end(const XentEnd& p, cudaStream_t stream) {
+  const int64_t first = bias_blocks(p.bias), blocks = first + (p.round.rows + kWarps - 1) / kWarps * ((p.round.cols + 255) / 256);
+  if (blocks == 0) return cudaSuccess;
   if (blocks > 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
-  return tc::launch_early(round_kernel, dim3((unsigned)blocks), kThreads, stream, p);
+  return tc::launch_early(end_kernel, dim3((unsigned)blocks), kThreads, stream, p, (uint32_t)first);
 }
 
 }  // namespace ddl

@@ -25,9 +25,8 @@ cudaError_t launch_xent_join(const XentJoin& p, cudaStream_t stream);
 
 // scale[0] = 1 / c, scale[1] = c, with c the largest coefficient of a token with a label (binary16: 2^-14 times that): the
 // planes hold dz / c.  Where all coefficients are the same, as in a mean, dz / c of an unlikely label is nearly -1, whose
-// rounding loses nothing; that of -c would be the same for every token and not average out (dw of 8192 tokens, a vocabulary of
-// 65,536, bfloat16).  And binary16 holds the dz of every token, small
-// probabilities as normal numbers.
+// rounding loses nothing; that of -c would be the same for every token and not average out.  And binary16 holds the dz of
+// every token, small probabilities as normal numbers.
 struct XentScale {
   const float* coef;  // NULL: ones
   const int64_t* labels;
@@ -47,7 +46,6 @@ struct XentBias {
   void* db;
   int32_t f32, accumulate;
 };
-cudaError_t launch_xent_bias(const XentBias& p, cudaStream_t stream);
 
 // dx: 16-bit rows of binary32 sums, to which comes what the plane's rounding took from the label's dz, times the label's row of
 // w.  That one number is most of dz where the label is not likely, and its rounding would be the whole row's error.
@@ -64,6 +62,11 @@ struct XentRound {
   const uint16_t* w;
   int64_t ldw;
 };
-cudaError_t launch_xent_round(const XentRound& p, cudaStream_t stream);
+// Both in one launch, as far as there are any (db, rows).
+struct XentEnd {
+  XentBias bias;
+  XentRound round;
+};
+cudaError_t launch_xent_end(const XentEnd& p, cudaStream_t stream);
 
 }  // namespace ddl
