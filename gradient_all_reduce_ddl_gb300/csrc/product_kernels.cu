@@ -1498,16 +1498,23 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             }
             const uint32_t at = tmem + (cc & 1u) * BN + half * kHalf + lanes;
             const auto add_sums = [&](auto lower) {
+              if constexpr (kSlabs == 1) {
+                float v[kHalf];
+                tmem_ld16(at, v);
 #pragma unroll
-              for (int sl = 0; sl < kSlabs; sl += 2) {
-                float v[2 * kHalf];
-                tmem_ld16x2(at + sl * kSlab, at + (sl + 1) * kSlab, v);
+                for (int k = 0; k < kHalf; ++k) acc[k] += scale * v[k];
+              } else {
 #pragma unroll
-                for (int k = 0; k < 2 * kHalf; ++k) {
-                  float& a = acc[sl * kHalf + k];
-                  // an infinite or NaN sum of the first planes stands: the lower ones' products with what made it so are
-                  // infinite too, of either sign, or NaN
-                  if (!decltype(lower)::value || fabsf(a) <= FLT_MAX) a += scale * v[k];
+                for (int sl = 0; sl < kSlabs; sl += 2) {
+                  float v[2 * kHalf];
+                  tmem_ld16x2(at + sl * kSlab, at + (sl + 1) * kSlab, v);
+#pragma unroll
+                  for (int k = 0; k < 2 * kHalf; ++k) {
+                    float& a = acc[sl * kHalf + k];
+                    // an infinite or NaN sum of the first planes stands: the lower ones' products with what made it so are
+                    // infinite too, of either sign, or NaN
+                    if (!decltype(lower)::value || fabsf(a) <= FLT_MAX) a += scale * v[k];
+                  }
                 }
               }
             };
