@@ -110,7 +110,8 @@ struct Softmax {
   int32_t scaled;      // scale[] is there (XentScale); else the launch makes it
   float* scale;        // [0] what dz's planes are multiplied by, [1] its inverse
   float on, off;
-  int32_t planes;      // 1 or 2
+  int32_t planes;      // 1 to 3 (the third for bfloat16 alone)
+  uint16_t* third;     // the third plane, in rows as the others'
   float* resid;        // NULL, or of every token what rounding to the first plane takes from the label's dz (x scale)
   float* db;           // NULL, or the sums of dz (x scale) over every 32 tokens, or over a split tile's shares of them
   int64_t ld_db;

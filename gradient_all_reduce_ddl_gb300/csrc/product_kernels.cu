@@ -1010,14 +1010,16 @@ struct GradRow {
   }
 };
 
-// The planes of two neighbours: 16 bits, and what their rounding lost (in binary16 2^11 times that).  (Of an infinite value
-// the second is NaN, but the sums of the first plane are infinite or NaN then, and stand.)
-__device__ __forceinline__ void grad_planes(float x, float y, int type, uint32_t* hi, uint32_t* lo) {
-  *hi = to16x2(x, y, type);
-  const float2 h = from16x2(*hi, type);
+// The planes of two neighbours: 16 bits, what their rounding lost (in binary16 2^11 times that), and what that one's lost.  (Of
+// an infinite value the others are NaN, but the sums of the first plane are infinite or NaN then, and stand.)
+__device__ __forceinline__ void grad_planes(float x, float y, int type, uint32_t (&out)[3]) {
+  out[0] = to16x2(x, y, type);
+  float2 h = from16x2(out[0], type);
   x -= h.x, y -= h.y;
   if (type == kF16) x *= 2048.f, y *= 2048.f;
-  *lo = to16x2(x, y, type);
+  out[1] = to16x2(x, y, type);
+  h = from16x2(out[1], type);
+  out[2] = to16x2(x - h.x, y - h.y, type);
 }
 
 // The sums over a warp's 32 rows of its lanes' 16 columns each: the lane's are of column (lane / 2) on return.  Each step
@@ -1041,15 +1043,20 @@ __device__ __forceinline__ float column_sums16(const float* v, int lane) {
 
 // 16 columns n.. of row m, from logits to planes in the slab.
 template <int TYPE>
-__device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, bool two) {
-  uint32_t hi[8], lo[8];
+__device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, const ProductLaunch& p, int m, int n) {
+  const Softmax& e = p.soft;
+  uint32_t u[8][3];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], TYPE, &hi[k], &lo[k]);
+  for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], TYPE, u[k]);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint32_t at = piece(buf, row, 2 * half + h);
-    st_shared16(at, make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]));
-    if (two) st_shared16(at + kPlaneBytes, make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]));
+    const auto words = [&](int plane) { return make_uint4(u[4 * h][plane], u[4 * h + 1][plane], u[4 * h + 2][plane], u[4 * h + 3][plane]); };
+    st_shared16(at, words(0));
+    if (e.planes >= 2) st_shared16(at + kPlaneBytes, words(1));
+    // few tokens: it need not go by boxes
+    if (TYPE == kBF16 && e.planes == 3 && m < p.inl[0].M && n + 8 * h < p.inl[0].ldp)
+      *reinterpret_cast<uint4*>(e.third + (int64_t)m * p.inl[0].ldp + n + 8 * h) = words(2);
   }
 }
 
@@ -1060,9 +1067,9 @@ __device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, cons
   add_bias16(p, v, bias);
   g.of<16>(v, n, e, P.type);
   if (P.type == kBF16)
-    slab_planes<kBF16>(v, buf, row, half, e.planes == 2);
+    slab_planes<kBF16>(v, buf, row, half, p, m0 + row, n);
   else
-    slab_planes<kF16>(v, buf, row, half, e.planes == 2);
+    slab_planes<kF16>(v, buf, row, half, p, m0 + row, n);
   if (e.db) {
     const int lane = row & 31, c = n + (lane >> 1);
     const float s = column_sums16(v, lane);
@@ -1095,11 +1102,13 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, i
       g.of<4>(v, n, e, P.type);
 #pragma unroll
       for (int k = 0; k < 4; ++k) total[k] += v[k];
-      uint32_t hi[2], lo[2];
-      grad_planes(v[0], v[1], P.type, &hi[0], &lo[0]);
-      grad_planes(v[2], v[3], P.type, &hi[1], &lo[1]);
-      *reinterpret_cast<uint2*>(P.p_hi + (int64_t)m * P.ldp + n) = make_uint2(hi[0], hi[1]);
-      if (e.planes == 2) *reinterpret_cast<uint2*>(P.p_lo + (int64_t)m * P.ldp + n) = make_uint2(lo[0], lo[1]);
+      uint32_t u[2][3];
+      grad_planes(v[0], v[1], P.type, u[0]);
+      grad_planes(v[2], v[3], P.type, u[1]);
+      const int64_t to = (int64_t)m * P.ldp + n;
+      *reinterpret_cast<uint2*>(P.p_hi + to) = make_uint2(u[0][0], u[1][0]);
+      if (e.planes >= 2) *reinterpret_cast<uint2*>(P.p_lo + to) = make_uint2(u[0][1], u[1][1]);
+      if (e.planes == 3) *reinterpret_cast<uint2*>(e.third + to) = make_uint2(u[0][2], u[1][2]);
     }
     if (e.db) {  // the same for all warps
       st_shared4(staging + (ew * 128 + 4 * lane) * 4, total);

@@ -20,7 +20,7 @@ struct ddl_xent {
   ddl::Residency room = {};
   uint32_t* d_err = nullptr;
   ddl::GiveUp give_up;  // of the next call's first product
-  ddl::Buffer x, w, part, part_sum, picked, planes[2], scale, resid, db, dx;
+  ddl::Buffer x, w, part, part_sum, picked, planes[3], scale, resid, db, dx;
 };
 
 namespace {
@@ -38,8 +38,14 @@ constexpr int64_t kPieceStep = 256;           // pieces begin at whole tiles
 // chunks: with short ones they wait for it.  8192 tokens, 4096 features, a vocabulary of 65,536: 2852, 2649, 2543 us with 4, 8,
 // 16 blocks, and a training step of 2048 features 7634, 7281, 7119 us; relative errors of the loss 1.8, 3.7, 7.8e-7 (products in
 // binary32: 6.6e-7) and of binary32 dw 1.7, 1.6, 2.0e-6 (1.75e-6).  The gradient takes the loss's chunk: what truncation takes
-// from z it then takes from lse, too (with 16 blocks under a loss of 8 dw is 3.0e-6 off).
-constexpr int32_t kLogitChunk = 8;
+// from z it then takes from lse, too (with 16 blocks under a loss of 8 dw is 3.0e-6 off).  8 blocks.
+// Few tokens' losses are not averaged over many: 6 blocks (3 tokens, 512 features: 1.4 -> 0.8e-6 off; 16 tokens, 4096 features,
+// 65,536 entries 93.0, 94.3, 97.5 us with 8, 6, 4).
+int32_t logit_chunk(int64_t tokens) { return tokens <= kFewTokens ? 6 : 8; }
+// Up to so many tokens binary32 dw of bfloat16 heads takes dz in three planes: with two, its error is 1.4 to 2.8e-6 where the
+// tokens' weights differ, which for more tokens is what sums in binary32 lose themselves (8192: 1.75e-6), while a third pass
+// costs a fifth of the products.
+constexpr int64_t kThreePlanes = 1024;
 
 ddl_status_t bind(ddl_xent* h) {
   int dev = -1;
@@ -75,10 +81,10 @@ int64_t piece_of(int64_t vocab, int64_t tokens) {
   return std::min(vocab, blocks_of(blocks_of(vocab, pieces), kPieceStep) * kPieceStep);
 }
 
-// Elements of a plane: the most of any number of tokens.
-size_t plane_elems(const ddl_xent* h) {
-  const int64_t all = h->max_tokens * (int64_t)round8((uint64_t)h->vocab);
-  return (size_t)std::min(all, std::max(kPieceElems, h->max_tokens * kPieceStep));
+// Elements of a plane: the most of any number of tokens (of up to kThreePlanes: third).
+size_t plane_elems(const ddl_xent* h, bool third = false) {
+  const int64_t tokens = third ? std::min(h->max_tokens, kThreePlanes) : h->max_tokens;
+  return (size_t)std::min(tokens * (int64_t)round8((uint64_t)h->vocab), std::max(kPieceElems, tokens * kPieceStep));
 }
 
 // Sums of the bias gradient: a row per 32 tokens of a piece, or, where a contraction is split, per share of a tile's.
@@ -203,7 +209,7 @@ ddl_status_t ddl_xent_forward(ddl_xent_t h, size_t tokens, const void* x, size_t
     P.a[0] = swap ? 1 : 0;
     P.b[0] = swap ? 0 : 1;
     P.scale[0] = 1.f;
-    P.chunk[0] = P.chunk[1] = kLogitChunk;
+    P.chunk[0] = P.chunk[1] = logit_chunk(T);
     P.epi = kEpiLoss;
     P.swap = swap;
     P.type = h->type;
@@ -278,12 +284,12 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   }
 
   // dz is kept to 16 bits of its operands' type in dx (but for the label's, see XentRound), whose own rounding is as coarse, and
-  // in binary16 gradients of binary16 layers; else to two such planes, 16 or 22 bits.
+  // in binary16 gradients of binary16 layers; else to two such planes, 16 or 22 bits, or three, 24.
   const bool f16 = h->type == kF16;
-  const int dw_planes = !dw ? 0 : f16 && grad_dtype == DDL_FP16 ? 1 : 2;
+  const int dw_planes = !dw ? 0 : f16 && grad_dtype == DDL_FP16 ? 1 : !f16 && grad_dtype == DDL_FP32 && T <= kThreePlanes ? 3 : 2;
   const int n_planes = std::max(1, dw_planes);
   for (int k = 0; k < n_planes; ++k)
-    if ((st = need(&h->planes[k], plane_elems(h) * 2)) != DDL_OK) return st;
+    if ((st = need(&h->planes[k], plane_elems(h, k == 2) * 2)) != DDL_OK) return st;
   if ((st = need(&h->scale, 2 * sizeof(float))) != DDL_OK) return st;
   const int64_t most_sums = std::max<int64_t>(kSplitSums, (int64_t)plane_elems(h) / 32 + (int64_t)round8((uint64_t)V));
   if (db && (st = need(&h->db, (size_t)most_sums * 4)) != DDL_OK) return st;
@@ -309,7 +315,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   for (int64_t v0 = 0; v0 < V; v0 += piece) {
     const int64_t n = std::min(piece, V - v0);
     const Mat bw{static_cast<const uint16_t*>(aw.p) + v0 * aw.ld, n, K, aw.ld};
-    const Mat mp[2] = {{h->planes[0].p, T, n, ldp}, {h->planes[1].p, T, n, ldp}};
+    const Mat mp[3] = {{h->planes[0].p, T, n, ldp}, {h->planes[1].p, T, n, ldp}, {h->planes[2].p, T, n, ldp}};
     {
       const int64_t steps = blocks_of(K, kBlockK);
       const auto count = [&](int tile) { return blocks_of(T, tile) * blocks_of(n, tile); };
@@ -322,7 +328,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       L.bf16 = !f16;
       const int narrow = std::min(l.tile, kTileM);
       if (!map_of(&L, 0, ax, kBlockK, kTileM) || !map_of(&L, 1, bw, kBlockK, narrow)) return DDL_ERR_CUDA;
-      for (int k = 0; k < n_planes; ++k)
+      for (int k = 0; k < std::min(n_planes, 2); ++k)
         if (!map_of(&L, 2 + k, mp[k], kSlabCols)) return DDL_ERR_CUDA;
       Product& P = L.inl[0];
       P.M = (int32_t)T;
@@ -332,12 +338,12 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       P.a[0] = 0;
       P.b[0] = 1;
       P.scale[0] = 1.f;
-      P.chunk[0] = P.chunk[1] = kLogitChunk;
+      P.chunk[0] = P.chunk[1] = logit_chunk(T);
       P.epi = kEpiGrad;
       P.type = h->type;
       P.in0 = P.in1 = -1;
       P.out0 = 2;
-      P.out1 = n_planes == 2 ? 3 : -1;
+      P.out1 = n_planes >= 2 ? 3 : -1;
       P.p_hi = static_cast<uint16_t*>(h->planes[0].p);
       P.p_lo = static_cast<uint16_t*>(h->planes[1].p);
       P.ldp = ldp;
@@ -355,6 +361,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       L.soft.on = 1.f - h->smoothing;
       L.soft.off = h->smoothing / (float)V;
       L.soft.planes = n_planes;
+      L.soft.third = static_cast<uint16_t*>(h->planes[2].p);
       L.soft.resid = dx ? static_cast<float*>(h->resid.p) : nullptr;
       L.soft.db = db ? static_cast<float*>(h->db.p) : nullptr;
       L.soft.ld_db = ldp;
@@ -504,7 +511,7 @@ ddl_status_t ddl_xent_check(ddl_xent_t h, void* stream) {
 ddl_status_t ddl_xent_destroy(ddl_xent_t h) {
   if (!h) return DDL_OK;
   cudaError_t e = cudaSuccess;
-  for (void* p : {(void*)h->d_err, h->x.p, h->w.p, h->part.p, h->part_sum.p, h->picked.p, h->planes[0].p, h->planes[1].p,
+  for (void* p : {(void*)h->d_err, h->x.p, h->w.p, h->part.p, h->part_sum.p, h->picked.p, h->planes[0].p, h->planes[1].p, h->planes[2].p,
                   h->scale.p, h->resid.p, h->db.p, h->dx.p})
     if (p) {
       const cudaError_t f = cudaFree(p);  // waits for the device

@@ -416,6 +416,23 @@ def test_pieces_of_the_vocabulary(ddl, t, k, v, dtype):
     h.check_backward(dx, dw, db)
 
 
+@pytest.mark.parametrize("t", [3, 64, 65, 500, 1024, 1025])
+@pytest.mark.parametrize("k, v", [(96, 1500), (1030, 333)])
+def test_binary32_dw_of_bfloat16_heads(ddl, t, k, v):
+    """As exact as sums in binary32: the 2-norm of the error, with weights that differ, in two or three planes of dz.  Two keep
+    dz to 2^-17 of itself, uniformly off (2^-17 / sqrt 3 of the norm); the logits are off by 16 roundings of 2^-24 of their
+    size, up to 16, twice."""
+    h = Head(t, k, v, "bf16", bias=True, seed=25).solve()
+    dw = torch.empty(v, k, device="cuda")
+    with ddl.CrossEntropy(k, v, t, "bf16") as head:
+        _, lse = h.forward(ddl, head)
+        head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, bias=h.bias, dw=dw)
+    h.check_backward(None, dw)
+    want = h.dz.t() @ h.x.double()
+    off = float((dw.double() - want).norm() / want.norm())
+    assert off <= 2.0 ** -17 / math.sqrt(3) * (t > 1024) + 2 * 16 * 16 * 2.0 ** -24
+
+
 @pytest.mark.parametrize("t", [16384, 16385, 20000])
 def test_many_tokens(ddl, t):
     """On either side of the number up to which the gradient launch makes dz's scale itself."""
