@@ -38,14 +38,17 @@ constexpr int64_t kPieceStep = 256;           // pieces begin at whole tiles
 // chunks: with short ones they wait for it.  8192 tokens, 4096 features, a vocabulary of 65,536: 2852, 2649, 2543 us with 4, 8,
 // 16 blocks, and a training step of 2048 features 7634, 7281, 7119 us; relative errors of the loss 1.8, 3.7, 7.8e-7 (products in
 // binary32: 6.6e-7) and of binary32 dw 1.7, 1.6, 2.0e-6 (1.75e-6).  The gradient takes the loss's chunk: what truncation takes
-// from z it then takes from lse, too (with 16 blocks under a loss of 8 dw is 3.0e-6 off).  8 blocks.
-// Few tokens' losses are not averaged over many: 6 blocks (3 tokens, 512 features: 1.4 -> 0.8e-6 off; 16 tokens, 4096 features,
-// 65,536 entries 93.0, 94.3, 97.5 us with 8, 6, 4).
-int32_t logit_chunk(int64_t tokens) { return tokens <= kFewTokens ? 6 : 8; }
-// Up to so many tokens binary32 dw of bfloat16 heads takes dz in three planes: with two, its error is 1.4 to 2.8e-6 where the
-// tokens' weights differ, which for more tokens is what sums in binary32 lose themselves (8192: 1.75e-6), while a third pass
-// costs a fifth of the products.
-constexpr int64_t kThreePlanes = 1024;
+// from z it then takes from lse, too (with 16 blocks under a loss of 8 dw is 3.0e-6 off): 8 blocks.
+// Few tokens' losses are not averaged over many: up to 64 tokens 6 blocks (3 tokens, 512 features: 1.4 -> 0.8e-6 off; 16 tokens,
+// 4096 features, 65,536 entries 93.0, 94.3, 97.5 us with 8, 6, 4), and of up to 8, whose weights are few tiles, 2 (one token,
+// 2048 features, 1000 entries: 2.1 -> 0.9e-6 off, 8.4 -> 8.5 us).
+int32_t logit_chunk(const ddl_xent* h, int64_t tokens) {
+  return tokens > kFewTokens ? 8 : tokens > 8 || blocks_of(h->vocab, kTileM) > h->sms ? 6 : 2;
+}
+// Up to so many tokens binary32 dw of bfloat16 heads takes dz in three planes: with two, its error is 1.4 to 2.8e-6, which for
+// more tokens is what sums in binary32 lose themselves (2112: 0.7e-6, 8192: 1.75e-6), while a third pass costs a fifth of the
+// products.
+constexpr int64_t kThreePlanes = 4096;
 
 ddl_status_t bind(ddl_xent* h) {
   int dev = -1;
@@ -209,7 +212,7 @@ ddl_status_t ddl_xent_forward(ddl_xent_t h, size_t tokens, const void* x, size_t
     P.a[0] = swap ? 1 : 0;
     P.b[0] = swap ? 0 : 1;
     P.scale[0] = 1.f;
-    P.chunk[0] = P.chunk[1] = logit_chunk(T);
+    P.chunk[0] = P.chunk[1] = logit_chunk(h, T);
     P.epi = kEpiLoss;
     P.swap = swap;
     P.type = h->type;
@@ -338,7 +341,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       P.a[0] = 0;
       P.b[0] = 1;
       P.scale[0] = 1.f;
-      P.chunk[0] = P.chunk[1] = logit_chunk(T);
+      P.chunk[0] = P.chunk[1] = logit_chunk(h, T);
       P.epi = kEpiGrad;
       P.type = h->type;
       P.in0 = P.in1 = -1;

@@ -539,7 +539,7 @@ ddl_status_t ddl_ortho_destroy(ddl_ortho_t ortho);
  * A handle's device binding, threads, ownership, checks and overlap rules are
  * those of the linear layers.  Its workspace: 8 bytes per token and 64 entries
  * of the vocabulary (at most 512 MB), twice 2 bytes per token and entry of a
- * piece (at most 2^28 of them, or 256 entries; once more for up to 1024 tokens of
+ * piece (at most 2^28 of them, or 256 entries; once more for up to 4096 tokens of
  * DDL_BF16), 4 bytes per token and feature for dx, copies of x and w whose rows are not aligned. */
 
 typedef struct ddl_xent* ddl_xent_t;
@@ -561,7 +561,7 @@ ddl_status_t ddl_xent_forward(ddl_xent_t xent, size_t tokens, const void* x, siz
  * give the same bits.  Rounding: dz is kept to the 16 bits of the handle's type in
  * dx (the label's, which is most of it, to 24) and in binary16 gradients of a
  * DDL_FP16 handle; in other gradients dw takes it to 22 bits (DDL_FP16) or 16
- * (DDL_BF16; 24 in binary32 gradients of up to 1024 tokens).  On the way dz is
+ * (DDL_BF16; 24 in binary32 gradients of up to 4096 tokens).  On the way dz is
  * divided by the largest dloss, so that no size of dloss loses anything. */
 ddl_status_t ddl_xent_backward(ddl_xent_t xent, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
                                const void* bias, const int64_t* labels, const float* lse, const float* dloss, void* dx,
