@@ -862,7 +862,8 @@ struct LossRow {
 #pragma unroll
     for (int k = 0; k < 32; ++k) top[k & 3] = fmaxf(top[k & 3], v[k]);
     const float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])), base = base_of(mx);
-    sum = sum * exp_of(base_of(most) - base) + exp_sum(v, base);
+    // (a sum of nothing, of most -infinity, stays 0 whatever the new base is)
+    sum = sum * (most == mx ? 1.f : exp_of(most - mx)) + exp_sum(v, base);
     most = mx;
   }
   __device__ __forceinline__ void store(const ProductLaunch& p, int m, int part) const {

@@ -678,3 +678,71 @@ def test_a_training_step_of_all_operators(ddl):
         handle.check()
     for handle in (layer, head, adam, plan):
         handle.close()
+
+
+class LowHead(Head):
+    """A head whose bias is far below zero on some entries.  Its sum with the products rounds to binary32 (and loses them where
+    its half unit is above them, from 2^30 on): the reference's logits are rounded likewise, and off by the products' own error and, below that, one
+    rounding more.  Gradients are those of the call's own lse."""
+
+    def __init__(self, t, k, v, dtype, low, entries, masked=0, **more):
+        super().__init__(t, k, v, dtype, bias=True, ignored=0.1, **more)
+        self.bias[entries] = low
+        self.bias[:masked] = float("-inf")
+        if masked:
+            self.labels = torch.where(self.labels >= 0, self.labels.clamp(min=masked), self.labels)
+
+    def solve(self):
+        x, w = self.x.double(), self.w.double()
+        self.z = (x @ w.t() + self.bias.double()).float().double()
+        size = torch.where(self.z.abs() < 2.0 ** 30, self.z.abs(), 0.0)
+        self.ez = torch.where(self.z.isfinite(), (self.k + 16) * 2.0 ** -23 * (x.abs() @ w.abs().t()) + 2.0 ** -23 * size, 0.0)
+        top = self.z.amax(1, keepdim=True)
+        near = self.z > top - 40 - self.ez  # what is left of the others is less than 2^-24 of any sum
+        self.e = torch.where(near, self.ez, 0.0).amax(1)
+        self.lse = torch.logsumexp(self.z, 1)
+        self.valid = self.labels >= 0
+        y = torch.where(self.valid, self.labels, self.v - 1)  # (an entry that is never masked)
+        zy = self.z.gather(1, y[:, None])
+        r = torch.logsumexp(self.z.scatter(1, y[:, None], float("-inf")) - zy, 1)
+        own = torch.nn.functional.softplus(r)
+        self.loss = torch.where(self.valid, own, 0.0)
+        e = torch.maximum(self.e, self.ez.gather(1, y[:, None])[:, 0])
+        self.loss_bound = (2 * e + 2.0 ** -16) * torch.sigmoid(r) + 4 * U["f32"] * own + 1e-30
+        self.lse_bound = self.e + 2.0 ** -16 + 2 * U["f32"] * self.lse.abs()
+        return self
+
+    def solve_backward(self, lse):
+        """dz and its error, from the lse that the call is given."""
+        d = self.z - lse.double()[:, None]
+        q = torch.zeros_like(self.z)
+        q[torch.arange(self.t, device="cuda"), self.labels.clamp(min=0)] = 1.0
+        p = torch.exp(d)
+        c = torch.where(self.valid, self.dloss.double(), 0.0)[:, None]
+        self.dz = torch.where(self.valid[:, None], (p - q) * c, 0.0)
+        rel = torch.where(p > 0, 2 * self.ez + 2.0 ** -22 * d.abs() + 2.0 ** -20, 0.0)
+        self.dz_err = c.abs() * (p * torch.expm1(rel) + 4 * U["f32"] * (p + q))
+        self.floor = 2.0 ** -39 * float(c.abs().max()) if self.dtype == "f16" else 0.0
+
+
+def _check_low(ddl, t, k, v, dtype, low):
+    """Low entries everywhere, neighbours from a tile's edge, on the last tile, and behind entries masked with -infinity."""
+    with ddl.CrossEntropy(k, v, t, dtype) as head:
+        for first, count, masked in ((0, v, 0), (0, 50, 0), (128, 128, 0), (256, 300, 0), (v // 256 * 256, 256, 0), (100, v, 100),
+                                     (300, v, 300)):
+            h = LowHead(t, k, v, dtype, low, slice(first, first + count), masked, seed=t + first).solve()
+            loss, lse = h.forward(ddl, head)
+            h.check_forward(loss, lse)
+            h.solve_backward(lse)
+            dx, dw, db = torch.empty_like(h.x), torch.empty(v, k, device="cuda"), torch.empty(v, device="cuda")
+            head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, bias=h.bias, dx=dx, dw=dw, db=db)
+            h.check_backward(dx, dw, db)
+            head.check()
+
+
+@pytest.mark.parametrize("dtype, low", [("bf16", -100.0), ("bf16", -1e4), ("f16", -300.0), ("f16", torch.finfo(torch.float16).min)])
+@pytest.mark.parametrize("k, v", [(64, 700), (1024, 700), (64, 5003)])
+@pytest.mark.parametrize("t", [4, 64, 65, 150, 333])
+def test_finite_logits_far_below_zero(ddl, t, k, v, dtype, low):
+    """A softmax does not change with a shift: entries that a large negative bias takes out leave finite losses and gradients."""
+    _check_low(ddl, t, k, v, dtype, low)
