@@ -967,16 +967,16 @@ __device__ __forceinline__ void loss_columns(const ProductLaunch& p, int row0, i
   }
 }
 
-// What the gradient needs of a token.  exp(z - lse) = 2^(z log2 e - h) 2^-l with h + l = lse log2 e: one multiply-add, whose
-// rounding is that of the difference, and a factor.
+// What the gradient needs of a token.  exp(z - lse) by the difference itself: where both are large (a mask of binary32's lowest
+// number on every entry) it is small and exact, while z log2 e would overflow, or its rounding be more than the difference.
 struct GradRow {
-  float high;      // h
-  float by_p, by;  // the coefficient times the planes' scale, with and without 2^-l
+  float lse;
+  float by;        // the coefficient times the planes' scale
   int token;
   int label;       // counted from the piece's first entry; outside of it: -1
   bool valid;
   __device__ __forceinline__ void load(const Softmax& e, float scale, int m, int rows, int entries) {
-    high = by_p = by = 0.f;
+    lse = by = 0.f;
     token = m;
     label = -1;
     valid = false;
@@ -984,17 +984,15 @@ struct GradRow {
     const int64_t y = __ldg(e.labels + m);
     valid = y >= 0 && y < e.vocab;
     if (y >= e.first && y < e.first + entries) label = (int)(y - e.first);
-    const float lse = __ldg(e.lse + m);
+    lse = __ldg(e.lse + m);
     by = (e.coef ? __ldg(e.coef + m) : 1.f) * scale;
-    high = lse * kLog2e;
-    by_p = by * exp2_fast(-fmaf(lse, kLog2e, -high));
   }
   // dz (x scale) of N entries from n, whose logits are z
   template <int N>
   __device__ __forceinline__ void of(float* z, int n, const Softmax& e, int type) const {
     const float less = -e.off * by;
 #pragma unroll
-    for (int k = 0; k < N; ++k) z[k] = fmaf(exp2_fast(fmaf(z[k], kLog2e, -high)), by_p, less);
+    for (int k = 0; k < N; ++k) z[k] = fmaf(exp_of(z[k] - lse), by, less);
     if (label >= n && label < n + N) {
 #pragma unroll
       for (int k = 0; k < N; ++k)

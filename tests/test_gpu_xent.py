@@ -746,3 +746,11 @@ def _check_low(ddl, t, k, v, dtype, low):
 def test_finite_logits_far_below_zero(ddl, t, k, v, dtype, low):
     """A softmax does not change with a shift: entries that a large negative bias takes out leave finite losses and gradients."""
     _check_low(ddl, t, k, v, dtype, low)
+
+
+@pytest.mark.parametrize("k, v", [(64, 700), (1024, 700), (64, 5003)])
+@pytest.mark.parametrize("t", [4, 64, 65, 333])
+@pytest.mark.parametrize("low", [-1e12, torch.finfo(torch.bfloat16).min])
+def test_logits_as_low_as_numbers_go(ddl, t, k, v, low):
+    """The same with a mask of the type's lowest number, whose product with log2 e is none."""
+    _check_low(ddl, t, k, v, "bf16", low)
