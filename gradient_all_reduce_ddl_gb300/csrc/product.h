@@ -93,6 +93,9 @@ struct GiveUp {
   uint32_t loads[2] = {kNever, kNever};  // K blocks after which a CTA's loads stop (even and odd CTA of a pair)
 };
 
+// Sums of logits are kept times this, so that those of up to 2^22 entries are numbers where their mean is one.
+constexpr float kSumScale = 0x1p-24f;
+
 // kEpiLoss and kEpiGrad: the logits are D (M tokens x N entries of the vocabulary) plus the bias.
 struct Softmax {
   const int64_t* labels;
@@ -102,7 +105,7 @@ struct Softmax {
   // kEpiLoss: of every token (rows of `tokens`) and part of the vocabulary, without the label's logit
   int64_t tokens;
   float2* part;      // the largest logit and the sum of exp(z - largest)
-  float* part_sum;   // NULL, or the sum of the logits (with the label's)
+  float* part_sum;   // NULL, or kSumScale times the sum of the logits (with the label's)
   float* picked;     // the label's logit, where it is one of these
   // kEpiGrad: dz = coef (exp(z - lse) - off - on [entry is the label]), 0 for tokens whose label is outside [0, vocab)
   const float* lse;

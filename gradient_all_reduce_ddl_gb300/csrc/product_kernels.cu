@@ -837,13 +837,13 @@ struct LossRow {
 #pragma unroll
       for (int k = 0; k < 32; ++k) {
         const bool in = n + (k >> 4) * kSlab + (k & 15) < N;
-        all += in ? v[k] : 0.f;
+        all = fmaf(in ? v[k] : 0.f, kSumScale, all);
         if (!in) v[k] = -INFINITY;
       }
     } else if (e.part_sum) {
       float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 32; ++k) s[k & 3] += v[k];
+      for (int k = 0; k < 32; ++k) s[k & 3] = fmaf(v[k], kSumScale, s[k & 3]);
       all += (s[0] + s[1]) + (s[2] + s[3]);
     }
     const int64_t at = label - n;  // 0 .. 15 or kSlab .. kSlab + 15: one of these
@@ -897,7 +897,7 @@ __device__ __forceinline__ void loss_rows(const ProductLaunch& p, int row0, int 
         const int n = col0 + c + k;
         if (c < BN && n < P.N) {
           if (e.bias) t[k] += bias_one(p, n);
-          all += t[k];
+          all = fmaf(t[k], kSumScale, all);
           if (n == label) {
             e.picked[m] = t[k];
             t[k] = -INFINITY;
@@ -945,7 +945,7 @@ __device__ __forceinline__ void loss_columns(const ProductLaunch& p, int row0, i
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         t[k] += b;
-        if (in) all[k] += t[k];
+        if (in) all[k] = fmaf(t[k], kSumScale, all[k]);
         if (in && n == label[k]) e.picked[col0 + c + k] = t[k];
         v[k][i] = in && n != label[k] ? t[k] : -INFINITY;
       }

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     LogSum every = l;
     every.add(z, 1.f);
     lse = every.most + logf(every.sum);
-    if (p.part_sum) loss += p.smoothing * (z - all / (float)p.vocab);
+    if (p.part_sum) loss += p.smoothing * (z - all / ((float)p.vocab * kSumScale));
   }
   if (p.loss) p.loss[t] = loss;
   if (p.lse) p.lse[t] = lse;

@@ -10,7 +10,7 @@ namespace ddl {
 // Joins the vocabulary's parts: lse and loss of every token.
 struct XentJoin {
   const float2* part;     // [n_parts][ld]: largest logit and sum of exp(z - largest), without the label's
-  const float* part_sum;  // NULL, or sums of the logits
+  const float* part_sum;  // NULL, or kSumScale times sums of the logits
   const float* picked;    // the label's logit
   int64_t ld, tokens;
   int32_t n_parts;

@@ -754,3 +754,18 @@ def test_finite_logits_far_below_zero(ddl, t, k, v, dtype, low):
 def test_logits_as_low_as_numbers_go(ddl, t, k, v, low):
     """The same with a mask of the type's lowest number, whose product with log2 e is none."""
     _check_low(ddl, t, k, v, "bf16", low)
+
+
+@pytest.mark.parametrize("t, k", [(4, 64), (64, 1024), (65, 64), (150, 1024), (333, 64)])
+def test_mean_of_large_logits(ddl, t, k):
+    """Smoothing takes the mean of the logits: it is a number where their sum is none.  Half of the entries at -2^127 make it
+    -2^126 exactly, next to which the other logits are lost; 1 - smoothing is a power of two."""
+    v = 512
+    h = Head(t, k, v, "bf16", bias=True, seed=19, ignored=0.0)
+    h.bias[::2] = -2.0 ** 127
+    h.labels |= 1  # an entry that is left
+    with ddl.CrossEntropy(k, v, t, "bf16", smoothing=0.5) as head:
+        loss, lse = h.forward(ddl, head)
+        head.check()
+    assert bool(lse.isfinite().all())
+    assert bool((loss == 2.0 ** 125).all())
