@@ -769,3 +769,41 @@ def test_mean_of_large_logits(ddl, t, k):
         head.check()
     assert bool(lse.isfinite().all())
     assert bool((loss == 2.0 ** 125).all())
+
+
+@pytest.mark.parametrize("t, k, v", [(3, 64, 500), (200, 96, 1500), (700, 130, 2049)])
+def test_calls_that_follow_each_other_at_once(ddl, t, k, v):
+    """Launches begin while the one before them ends: a forward pass reads labels and a bias that were just written, a backward
+    pass the lse of a forward pass, an optimizer's step the gradients, and the next forward pass the bias that it wrote.  The
+    same bits as with a pause after each."""
+    hs = [Head(t, k, v, "bf16", bias=True, smoothing=0.1, seed=31 + i) for i in range(3)]
+    width = v + (v & 1)
+
+    def chain(pause):
+        x, w, labels, dloss = (a.clone() for a in (hs[0].x.contiguous(), hs[0].w.contiguous(), hs[0].labels, hs[0].dloss))
+        bias32, bias16 = torch.zeros(width, device="cuda"), torch.zeros(width, dtype=torch.bfloat16, device="cuda")
+        db, out = torch.zeros(width, device="cuda"), []
+        with ddl.CrossEntropy(k, v, t, "bf16", smoothing=0.1) as head, ddl.Adam([(0, v)]) as adam:
+            state = adam.new_state()
+            for i in range(12):
+                h = hs[i % 3]
+                for to, new in ((x, h.x), (w, h.w), (dloss, h.dloss), (labels, h.labels)):
+                    to.copy_(new)
+                    pause()
+                loss, lse = torch.empty(t, device="cuda"), torch.empty(t, device="cuda")
+                dx, dw = torch.empty_like(x), torch.empty(v, k, device="cuda")
+                pause()
+                head.forward(x, w, labels, loss, lse, bias=bias16[:v])
+                pause()
+                head.backward(x, w, labels, lse, dloss=dloss, bias=bias16[:v], dx=dx, dw=dw, db=db[:v])
+                pause()
+                adam.step(db, [bias32], lr=0.1, operands=[bias16], **state)
+                pause()
+                out += [loss, lse, dx, dw, bias32.clone()]
+                pause()
+            torch.cuda.synchronize()
+            head.check()
+        return out
+    want = chain(torch.cuda.synchronize)
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))

@@ -91,3 +91,16 @@ def test_check_before_any_gpu_call(ddl):
         ddl.ddl_xent_check(head.handle, 0)
         assert _status(ddl, ddl.ddl_xent_selftest_wait_timeout, head.handle, 2_000_001) == ddl.DDL_ERR_INVALID_ARG
     head.close()  # twice is fine
+
+
+def test_no_read_only_loads_of_what_a_launch_before_may_write():
+    """Kernels that start while the launch before them ends read nothing but the library's own tables as read-only memory."""
+    import os
+    import re
+
+    from gradient_all_reduce_ddl_gb300.build import CSRC
+    for name in sorted(os.listdir(CSRC)):
+        with open(os.path.join(CSRC, name), encoding="utf-8") as f:
+            code = re.sub(r"//[^\n]*", "", f.read())
+        loads = re.findall(r"__ldg\(\s*(\w+)|ld\.global\.nc", code)
+        assert set(loads) <= {"tile"}, name
