@@ -3,6 +3,8 @@
 // launch, the bias gradient and the rounding of dx's sums.  All of them read what the products left in L2, and
 // small calls are bound by their launches (a join 3 us in a sequence).  8192 tokens x 512
 // parts are joined in 14 us, 8192 x 2048 sums rounded in 13 (7.4 TB/s, part of it from L2).
+#include <cfloat>
+
 #include "activation.cuh"
 #include "product.h"
 #include "tc_ptx.cuh"
@@ -155,8 +157,8 @@ __device__ __forceinline__ void round_rows(const XentRound& p, int64_t block) {
   if (y >= 0 && y < p.vocab) {
     const float by = __ldcg(p.resid + r) * __ldcg(p.inverse);
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (c0 + 32 * k < p.cols) v[k] = fmaf(by, from16(p.w[y * p.ldw + c0 + 32 * k], p.type), v[k]);
+    for (int k = 0; k < 8; ++k)  // (an infinite or NaN sum stands: the rest, or its zero, times the weight that made it so may be NaN)
+      if (c0 + 32 * k < p.cols && fabsf(v[k]) <= FLT_MAX) v[k] = fmaf(by, from16(p.w[y * p.ldw + c0 + 32 * k], p.type), v[k]);
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k)

@@ -807,3 +807,23 @@ def test_calls_that_follow_each_other_at_once(ddl, t, k, v):
     want = chain(torch.cuda.synchronize)
     for _ in range(3):
         assert all(torch.equal(a, b) for a, b in zip(chain(lambda: None), want))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t", [5, 150])
+def test_an_infinite_weight_of_the_label(ddl, t, dtype):
+    """A label whose logit is -infinity has dz = -dloss, a finite number (no rest where it is a power of two): dx is infinite where the
+    label's weight is, as the products have it, and not NaN."""
+    h = Head(t, 64, 300, dtype, seed=29, ignored=0.0, sure=0.0)
+    h.labels[:] = 1 + h.labels % 299
+    h.labels[1] = 0
+    h.x[:, 7] = -h.x[:, 7].abs().clamp(min=0.5)
+    h.w[0, 7] = float("inf")
+    dloss = torch.full((t,), 0.5, device="cuda")
+    dx = torch.empty_like(h.x)
+    with ddl.CrossEntropy(64, 300, t, dtype) as head:
+        loss, lse = h.forward(ddl, head)
+        assert bool(lse.isfinite().all()) and float(loss[1]) == float("inf")
+        head.backward(h.x, h.w, h.labels, lse, dloss=dloss, dx=dx)
+    assert float(dx[1, 7]) == float("-inf")
+    assert bool(dx[1, :7].isfinite().all()) and bool(dx[1, 8:].isfinite().all())
