@@ -101,8 +101,8 @@ __host__ __device__ constexpr int smem_bytes(int bn, int mode) {
 // -- element access -------------------------------------------------------------
 //
 // This grid may be resident while the launch before it still writes what is read here (bias, labels, lse, weights of tokens): after
-// griddep_wait() such data is read by ordinary or L2 loads, never by ld.global.nc (__ldg), which asks for memory that nothing
-// writes while the kernel lives and need not keep its place after the wait.
+// griddep_wait() such data is read by ordinary loads, never by ld.global.nc (__ldg), which asks for memory that nothing writes
+// while the kernel lives.  (Past L1, as __ldcg reads, a warp's common bias comes late: a small training step 48.9 us, 45.2 so.)
 
 template <int V>
 __device__ __forceinline__ void load16(const void* base, int64_t at, int type, float (&v)[V]) {
@@ -577,7 +577,7 @@ __device__ __forceinline__ void slab_linear_act(const Product& P, float* v, cons
 __device__ __forceinline__ void load_bias(const Product& P, int n, uint4 (&bias)[2]) {
 #pragma unroll
   for (int g = 0; g < 2; ++g)
-    bias[g] = P.bias && n + 8 * g < P.N ? __ldcg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.bias) + n + 8 * g))
+    bias[g] = P.bias && n + 8 * g < P.N ? *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(P.bias) + n + 8 * g)
                                         : make_uint4(0, 0, 0, 0);
 }
 
@@ -759,7 +759,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float exp_of(float x) { return exp2_fast(x * kLog2e); }
 
 __device__ __forceinline__ float bias_one(const ProductLaunch& p, int n) {
-  return from16(__ldcg(static_cast<const uint16_t*>(p.soft.bias) + n), p.inl[0].type);
+  return from16(static_cast<const uint16_t*>(p.soft.bias)[n], p.inl[0].type);
 }
 
 // The bias of 16 entries n.. as it is stored; zeros without one, and from entry N on.
@@ -769,14 +769,14 @@ __device__ __forceinline__ void load_bias16(const ProductLaunch& p, int n, uint4
   const uint16_t* from = static_cast<const uint16_t*>(p.soft.bias) + n;
   const int left = p.inl[0].N - n;
   if (p.soft.bias_vec && left >= 16) {
-    b[0] = __ldcg(reinterpret_cast<const uint4*>(from));
-    b[1] = __ldcg(reinterpret_cast<const uint4*>(from) + 1);
+    b[0] = *reinterpret_cast<const uint4*>(from);
+    b[1] = *(reinterpret_cast<const uint4*>(from) + 1);
   } else {
     uint32_t w[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      w[k] = 2 * k < left ? __ldcg(from + 2 * k) : 0;
-      if (2 * k + 1 < left) w[k] |= (uint32_t)__ldcg(from + 2 * k + 1) << 16;
+      w[k] = 2 * k < left ? from[2 * k] : 0;
+      if (2 * k + 1 < left) w[k] |= (uint32_t)from[2 * k + 1] << 16;
     }
     b[0] = make_uint4(w[0], w[1], w[2], w[3]);
     b[1] = make_uint4(w[4], w[5], w[6], w[7]);
@@ -823,7 +823,7 @@ struct LossRow {
   int64_t label;
   uint4 bias[2][2];  // of the next two slabs
   __device__ __forceinline__ LossRow(const ProductLaunch& p, int m, int n) : most(-INFINITY), sum(0.f), all(0.f) {
-    label = m < p.inl[0].M ? __ldcg(p.soft.labels + m) : -1;
+    label = m < p.inl[0].M ? p.soft.labels[m] : -1;
     load_bias16(p, n, bias[0]);
     load_bias16(p, n + kSlab, bias[1]);
   }
@@ -889,7 +889,7 @@ __device__ __forceinline__ void loss_rows(const ProductLaunch& p, int row0, int 
   for (int r = r0 + ew; r < r1; r += kEpiWarps) {
     const int m = row0 + r;
     if (m >= P.M) break;
-    const int64_t label = __ldcg(e.labels + m);
+    const int64_t label = e.labels[m];
     float v[4 * kFours], all = 0.f, most = -INFINITY;
 #pragma unroll
     for (int f = 0; f < kFours; ++f) {
@@ -938,7 +938,7 @@ __device__ __forceinline__ void loss_columns(const ProductLaunch& p, int row0, i
     float v[4][kRows], all[4] = {0.f, 0.f, 0.f, 0.f};
     int64_t label[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) label[k] = col0 + c + k < P.N ? __ldcg(e.labels + col0 + c + k) : -1;
+    for (int k = 0; k < 4; ++k) label[k] = col0 + c + k < P.N ? e.labels[col0 + c + k] : -1;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
       const int r = lane + 32 * i, n = row0 + r0 + r;
@@ -985,11 +985,11 @@ struct GradRow {
     label = -1;
     valid = false;
     if (m >= rows) return;
-    const int64_t y = __ldcg(e.labels + m);
+    const int64_t y = e.labels[m];
     valid = y >= 0 && y < e.vocab;
     if (y >= e.first && y < e.first + entries) label = (int)(y - e.first);
-    lse = __ldcg(e.lse + m);
-    by = (e.coef ? __ldcg(e.coef + m) : 1.f) * scale;
+    lse = e.lse[m];
+    by = (e.coef ? e.coef[m] : 1.f) * scale;
   }
   // dz (x scale) of N entries from n, whose logits are z
   template <int N>
