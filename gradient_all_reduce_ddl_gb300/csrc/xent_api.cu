@@ -39,11 +39,12 @@ constexpr int64_t kPieceStep = 256;           // pieces begin at whole tiles
 // 16 blocks, and a training step of 2048 features 7634, 7281, 7119 us; relative errors of the loss 1.8, 3.7, 7.8e-7 (products in
 // binary32: 6.6e-7) and of binary32 dw 1.7, 1.6, 2.0e-6 (1.75e-6).  The gradient takes the loss's chunk: what truncation takes
 // from z it then takes from lse, too (with 16 blocks under a loss of 8 dw is 3.0e-6 off): 8 blocks.
-// Few tokens' losses are not averaged over many: up to 64 tokens 6 blocks (3 tokens, 512 features: 1.4 -> 0.8e-6 off; 16 tokens,
-// 4096 features, 65,536 entries 93.0, 94.3, 97.5 us with 8, 6, 4), and of up to 8, whose weights are few tiles, 2 (one token,
-// 2048 features, 1000 entries: 2.1 -> 0.9e-6 off, 8.4 -> 8.5 us).
+// Few tokens' losses are not averaged over many: up to 64 tokens 6 blocks (16 tokens, 4096 features, 65,536 entries: 93.0, 93.3,
+// 96.9, 102, 111, 136 us with 8, 6, 4, 3, 2, 1; with 6 the loss of 9 to 64 is 2.5 to 2.9e-7 off, products in binary32 3 to 6e-7).  Of
+// up to 8 tokens 2 (one token over the same: of 32 losses the worst 3.8, 2.1, 1.2, 1.6e-6 off with 6, 4, 2, 1, products in binary32
+// 0.9e-6; 89.3, 92.6, 106, 131 us), and 1 where the weights are few tiles (2048 features, 1000 entries: 9.7 -> 9.9 us from 2).
 int32_t logit_chunk(const ddl_xent* h, int64_t tokens) {
-  return tokens > kFewTokens ? 8 : tokens > 8 || blocks_of(h->vocab, kTileM) > h->sms ? 6 : 2;
+  return tokens > kFewTokens ? 8 : tokens > 8 ? 6 : blocks_of(h->vocab, kTileM) > h->sms ? 2 : 1;
 }
 // Up to so many tokens binary32 dw of bfloat16 heads takes dz in three planes: with two, its error is 1.4 to 2.8e-6, which for
 // more tokens is what sums in binary32 lose themselves (2112: 0.7e-6, 8192: 1.75e-6), while a third pass costs a fifth of the

@@ -827,3 +827,25 @@ def test_an_infinite_weight_of_the_label(ddl, t, dtype):
         head.backward(h.x, h.w, h.labels, lse, dloss=dloss, dx=dx)
     assert float(dx[1, 7]) == float("-inf")
     assert bool(dx[1, :7].isfinite().all()) and bool(dx[1, 8:].isfinite().all())
+
+
+@pytest.mark.parametrize("k, v, c", [(512, 1000, 1), (2048, 1000, 1), (4096, 300, 1), (1024, 20011, 2), (4096, 20011, 2)])
+@pytest.mark.parametrize("t", [1, 3, 8])
+def test_losses_of_a_few_tokens(ddl, t, k, v, c):
+    """They are not averaged: their logits leave the truncating accumulator after c blocks of 64.  With u = 2^-24 and n blocks, of
+    a label's logit z that all blocks add to alike, each of the 4 c additions loses up to half a unit, a quarter on average, 0.36 u, of
+    1/(4 c), 2/(4 c) ... of the c blocks' sum: 0.18 (4 c + 1) u z in all.  The n / c additions after that round 1, 2 ... of n / c parts
+    of z by 0.42 u: root of 0.06 n / c, u z.  The root mean square over tokens is within 1.5 times both, times what a logit's error
+    does to the loss."""
+    square = count = 0
+    n = -(-k // 64)
+    with ddl.CrossEntropy(k, v, t, "bf16") as head:
+        for seed in range(-(-96 // t)):
+            h = Head(t, k, v, "bf16", seed=100 + 7 * seed, ignored=0.0, sure=torch.full((t, 1), 8.0, device="cuda")).solve()
+            loss, _ = h.forward(ddl, head)
+            zy = h.z.gather(1, h.labels[:, None])
+            miss = torch.sigmoid(torch.logsumexp(h.z.scatter(1, h.labels[:, None], float("-inf")) - zy, 1))
+            square += float((((loss.double() - h.loss) / (miss * zy[:, 0])) ** 2).sum())
+            count += t
+    off = math.sqrt(square / count)
+    assert off <= 1.5 * math.sqrt((0.18 * (4 * c + 1)) ** 2 + 0.06 * n / c) * U["f32"], f"{off / U['f32']:.2f} u"
