@@ -111,9 +111,9 @@ struct Softmax {
   const float* lse;
   const float* coef;   // NULL: ones
   int32_t scaled;      // scale[] is there (XentScale); else the launch makes it
-  float* scale;        // [0] what dz's planes are multiplied by, [1] its inverse
+  float* scale;        // [0] what dz's planes are multiplied by, [1] its inverse, [2] (an integer) the planes that there are
   float on, off;
-  int32_t planes;      // 1 to 3 (the third for bfloat16 alone)
+  int32_t planes;      // at most, 1 to 3 (the third for bfloat16 alone)
   uint16_t* third;     // the third plane, in rows as the others'
   float* resid;        // NULL, or of every token what rounding to the first plane takes from the label's dz (x scale)
   float* db;           // NULL, or the sums of dz (x scale) over every 32 tokens, or over a split tile's shares of them
@@ -141,6 +141,7 @@ struct ProductLaunch {
   int32_t bf16;             // operands are bfloat16, else binary16
   uint32_t* err;
   const float* post;        // kEpiStore: NULL, or a further factor of the sums, in device memory
+  const int32_t* passes;    // kEpiStore: NULL, or the most passes of any product, in device memory
   Softmax soft;             // kEpiLoss, kEpiGrad
   float ca, cb, cc;         // Newton-Schulz coefficients
   GiveUp give_up;           // read by launch_product_selftest's kernels only

@@ -274,6 +274,12 @@ struct Shape {
   __device__ __forceinline__ float scale(int pass) const { return pass == 0 ? scale0 : pass == 1 ? scale1 : scale2; }
 };
 
+// The most passes of any product, after griddep_wait: the same for every role.
+template <int MODE>
+__device__ __forceinline__ int most_passes(const ProductLaunch& p) {
+  return MODE == kBackward && p.passes ? __ldcg(p.passes) : kMaxPasses;
+}
+
 // A place in a ring, and how often that was gone round (modulo 2^32).
 struct Slot {
   uint32_t s = 0, lap = 0;
@@ -1046,8 +1052,8 @@ __device__ __forceinline__ float column_sums16(const float* v, int lane) {
 
 // 16 columns n.. of row m, from logits to planes in the slab.
 template <int TYPE>
-__device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, const ProductLaunch& p, int m, int n) {
-  const Softmax& e = p.soft;
+__device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, const ProductLaunch& p, int planes, int m,
+                                            int n) {
   uint32_t u[8][3];
 #pragma unroll
   for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], TYPE, u[k]);
@@ -1056,23 +1062,23 @@ __device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int ro
     const uint32_t at = piece(buf, row, 2 * half + h);
     const auto words = [&](int plane) { return make_uint4(u[4 * h][plane], u[4 * h + 1][plane], u[4 * h + 2][plane], u[4 * h + 3][plane]); };
     st_shared16(at, words(0));
-    if (e.planes >= 2) st_shared16(at + kPlaneBytes, words(1));
+    if (planes >= 2) st_shared16(at + kPlaneBytes, words(1));
     // few tokens: it need not go by boxes
-    if (TYPE == kBF16 && e.planes == 3 && m < p.inl[0].M && n + 8 * h < p.inl[0].ldp)
-      *reinterpret_cast<uint4*>(e.third + (int64_t)m * p.inl[0].ldp + n + 8 * h) = words(2);
+    if (TYPE == kBF16 && planes == 3 && m < p.inl[0].M && n + 8 * h < p.inl[0].ldp)
+      *reinterpret_cast<uint4*>(p.soft.third + (int64_t)m * p.inl[0].ldp + n + 8 * h) = words(2);
   }
 }
 
 __device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, const GradRow& g, const uint4 (&bias)[2], uint32_t buf,
-                                          int row, int half, int m0, int n) {
+                                          int planes, int row, int half, int m0, int n) {
   const Product& P = p.inl[0];
   const Softmax& e = p.soft;
   add_bias16(p, v, bias);
   g.of<16>(v, n, e, P.type);
   if (P.type == kBF16)
-    slab_planes<kBF16>(v, buf, row, half, p, m0 + row, n);
+    slab_planes<kBF16>(v, buf, row, half, p, planes, m0 + row, n);
   else
-    slab_planes<kF16>(v, buf, row, half, p, m0 + row, n);
+    slab_planes<kF16>(v, buf, row, half, p, planes, m0 + row, n);
   if (e.db) {
     const int lane = row & 31, c = n + (lane >> 1);
     const float s = column_sums16(v, lane);
@@ -1083,7 +1089,7 @@ __device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, cons
 // Rows [r0, r1) of a tile whose contraction was split: a warp along a row, four columns a lane.  The planes' rows are
 // padded to 8 columns, so that a group of 4 that begins inside the matrix is whole.
 template <int BN>
-__device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, int row0, int col0, int lane, int ew, int r0, int r1, int q,
+__device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, int planes, int row0, int col0, int lane, int ew, int r0, int r1, int q,
                                           int S, uint32_t staging, const ClusterSums sums) {
   const Product& P = p.inl[0];
   const Softmax& e = p.soft;
@@ -1110,8 +1116,8 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, i
       grad_planes(v[2], v[3], P.type, u[1]);
       const int64_t to = (int64_t)m * P.ldp + n;
       *reinterpret_cast<uint2*>(P.p_hi + to) = make_uint2(u[0][0], u[1][0]);
-      if (e.planes >= 2) *reinterpret_cast<uint2*>(P.p_lo + to) = make_uint2(u[0][1], u[1][1]);
-      if (e.planes == 3) *reinterpret_cast<uint2*>(e.third + to) = make_uint2(u[0][2], u[1][2]);
+      if (planes >= 2) *reinterpret_cast<uint2*>(P.p_lo + to) = make_uint2(u[0][1], u[1][1]);
+      if (planes == 3) *reinterpret_cast<uint2*>(e.third + to) = make_uint2(u[0][2], u[1][2]);
     }
     if (e.db) {  // the same for all warps
       st_shared4(staging + (ew * 128 + 4 * lane) * 4, total);
@@ -1128,22 +1134,35 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, i
   }
 }
 
-// dz's scale, from the coefficients of all tokens; every CTA makes it, under its first products.
-__device__ __forceinline__ float launch_scale(const ProductLaunch& p, int thread, uint32_t shared) {
+// dz's scale, and in *planes how many there are, from the coefficients of all tokens; every CTA makes them, under its first products.
+__device__ __forceinline__ float launch_scale(const ProductLaunch& p, int thread, uint32_t shared, int* planes) {
   const Softmax& e = p.soft;
-  if (e.scaled) return __ldcg(e.scale);
-  uint32_t most = 0;
+  if (e.scaled) {
+    *planes = __float_as_int(__ldcg(e.scale + 2));
+    return __ldcg(e.scale);
+  }
+  uint32_t most = 0, counted = 0;
 #pragma unroll 4
-  for (int t = thread; t < p.inl[0].M; t += kEpiWarps * 32) most = max(most, coef_bits(e.coef, e.labels, t, e.vocab));
+  for (int t = thread; t < p.inl[0].M; t += kEpiWarps * 32) {
+    const uint32_t b = coef_bits(e.coef, e.labels, t, e.vocab);
+    most = max(most, b);
+    counted += b != 0;
+  }
   most = __reduce_max_sync(0xffffffffu, most);
-  const uint32_t at = shared + (thread >> 5) * 4;
-  if ((thread & 31) == 0) asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(most) : "memory");
+  counted = __reduce_add_sync(0xffffffffu, counted);
+  const uint32_t at = shared + (thread >> 5) * 8;
+  if ((thread & 31) == 0) asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(most), "r"(counted) : "memory");
   bar_sync_epilogue();
+  counted = 0;
 #pragma unroll
-  for (int w = 0; w < kEpiWarps; ++w) most = max(most, __float_as_uint(ld_shared(shared + 4 * w)));
+  for (int w = 0; w < kEpiWarps; ++w) {
+    most = max(most, __float_as_uint(ld_shared(shared + 8 * w)));
+    counted += __float_as_uint(ld_shared(shared + 8 * w + 4));
+  }
   bar_sync_epilogue();
   const float2 u = dz_scale(most, p.inl[0].type == kF16);
-  if (blockIdx.x == 0 && thread == 0) e.scale[0] = u.x, e.scale[1] = u.y;
+  *planes = planes_of(counted, e.planes);
+  if (blockIdx.x == 0 && thread == 0) e.scale[0] = u.x, e.scale[1] = u.y, e.scale[2] = __int_as_float(*planes);
   return u.x;
 }
 
@@ -1254,6 +1273,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     if (warp == 0 && lane == 0) {
       Slot at;
       bool ok = true;
+      int passes = kMaxPasses;
       for (int t = first, next; t < end && ok; t = next) {
         const Place pl = place<BN, MODE>(p, t, step);
         next = pl.next;
@@ -1268,8 +1288,11 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
           acquire_map(mb0);
           acquire_map(mb1);
         }
-        if (t == first) griddep_wait();
-        for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
+        if (t == first) {
+          griddep_wait();
+          passes = most_passes<MODE>(p);
+        }
+        for (int ps = 0; ps < min(sh.n_pass, passes) && ok; ++ps) {
           const CUtensorMap* ma = ps == 0 ? ma0 : ps == 1 ? ma1 : ma2;
           const CUtensorMap* mb = ps == 0 ? mb0 : ps == 1 ? mb1 : mb2;
           for (int kb = sh.kb0; kb < sh.kb1; ++kb, at.next<kStages>()) {
@@ -1327,6 +1350,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       Slot at;
       bool ok = true;
       griddep_wait();
+      const int passes = most_passes<MODE>(p);
       for (int t = first, next; t < end && ok; t = next) {
         const Place pl = place<BN, MODE>(p, t, step);
         next = pl.next;
@@ -1337,7 +1361,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
         const uint64_t desc_a = smem_desc(ring, sh.a_mn ? kBoxBytes : 16, 1024);
         const uint64_t desc_b = smem_desc(ring + kABytes, sh.b_mn ? kBoxBytes : 16, 1024);
         const uint64_t step_a = (sh.a_mn ? 2048 : 32) >> 4, step_b = (sh.b_mn ? 2048 : 32) >> 4;
-        for (int ps = 0; ps < sh.n_pass && ok; ++ps) {
+        for (int ps = 0; ps < min(sh.n_pass, passes) && ok; ++ps) {
           const int chunk = sh.chunk(ps);
           for (int k0 = sh.kb0; k0 < sh.kb1 && ok; k0 += chunk, ++cc) {
             const int k1 = k0 + chunk < sh.kb1 ? k0 + chunk : sh.kb1;
@@ -1435,16 +1459,20 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
     Slot use;
     bool ok = true;
     float grad_scale = 0.f;
+    int planes = 0, passes = kMaxPasses;
     if constexpr (MODE == kGrad) {
       griddep_wait();
-      grad_scale = launch_scale(p, ew * 32 + lane, staging);
+      grad_scale = launch_scale(p, ew * 32 + lane, staging, &planes);
     }
     for (int t = first, next; t < end; t = next) {
       const Place pl = place<BN, MODE>(p, t, step);
       next = pl.next;
       const Product& G = is_single(MODE) ? p.inl[0] : *pl.P;
       const Shape sh(G, pl.k0, pl.k1, q, S);
-      if (t == first) griddep_wait();
+      if (t == first) {
+        griddep_wait();
+        passes = most_passes<MODE>(p);
+      }
       // what the epilogue reads from HBM comes to L2 while the products run
       if constexpr (is_forward(MODE) || MODE == kBackward) {
         if (S == 1 && !G.swap && !p.boxes) {
@@ -1500,7 +1528,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
       } else {
 #pragma unroll
         for (int k = 0; k < BN / 2; ++k) acc[k] = 0.f;
-        for (int ps = 0; ps < sh.n_pass; ++ps) {
+        for (int ps = 0; ps < min(sh.n_pass, passes); ++ps) {
           const float scale = MODE == kBackward ? sh.scale(ps) * post : sh.scale(ps);
           const int chunk = sh.chunk(ps);
           for (int k0 = sh.kb0; k0 < sh.kb1; k0 += chunk) {
@@ -1655,7 +1683,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             if (!ok) break;
             load_slab(sl);
             if constexpr (MODE == kGrad)
-              slab_grad(p, acc, grad_row, bias, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
+              slab_grad(p, acc, grad_row, bias, staging + use.s * kSlabBytes, planes, row, half, pl.row0 + my_rows,
                         pl.col0 + sl * kSlab + half * kHalf);
             else if (!skip)
               slab_values<MODE>(P, p, acc, bias, staging + use.s * kSlabBytes, row, half, pl.row0 + my_rows,
@@ -1715,7 +1743,7 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             loss_columns<BN>(p, pl.row0, pl.col0, lane, ew, q * share, share, first * S + q, sums);
         } else if constexpr (MODE == kGrad) {
           const int share = kTileM / S;
-          grad_rows<BN>(p, grad_scale, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, q, S, staging, sums);
+          grad_rows<BN>(p, grad_scale, planes, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, q, S, staging, sums);
         } else {
           // this CTA finishes its share of the rows
           const int share = kTileM / S;

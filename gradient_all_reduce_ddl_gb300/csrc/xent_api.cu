@@ -9,6 +9,7 @@
 #include "ddl.h"
 #include "layer_util.h"
 #include "product.h"
+#include "xent.cuh"
 #include "xent_kernels.h"
 
 struct ddl_xent {
@@ -46,10 +47,6 @@ constexpr int64_t kPieceStep = 256;           // pieces begin at whole tiles
 int32_t logit_chunk(const ddl_xent* h, int64_t tokens) {
   return tokens > kFewTokens ? 8 : tokens > 8 ? 6 : blocks_of(h->vocab, kTileM) > h->sms ? 2 : 1;
 }
-// Up to so many tokens binary32 dw of bfloat16 heads takes dz in three planes: with two, its error is 1.4 to 2.8e-6, which for
-// more tokens is what sums in binary32 lose themselves (2112: 0.7e-6, 8192: 1.75e-6), while a third pass costs a fifth of the
-// products.
-constexpr int64_t kThreePlanes = 4096;
 
 ddl_status_t bind(ddl_xent* h) {
   int dev = -1;
@@ -85,10 +82,9 @@ int64_t piece_of(int64_t vocab, int64_t tokens) {
   return std::min(vocab, blocks_of(blocks_of(vocab, pieces), kPieceStep) * kPieceStep);
 }
 
-// Elements of a plane: the most of any number of tokens (of up to kThreePlanes: third).
-size_t plane_elems(const ddl_xent* h, bool third = false) {
-  const int64_t tokens = third ? std::min(h->max_tokens, kThreePlanes) : h->max_tokens;
-  return (size_t)std::min(tokens * (int64_t)round8((uint64_t)h->vocab), std::max(kPieceElems, tokens * kPieceStep));
+// Elements of a plane: the most of any number of tokens.
+size_t plane_elems(const ddl_xent* h) {
+  return (size_t)std::min(h->max_tokens * (int64_t)round8((uint64_t)h->vocab), std::max(kPieceElems, h->max_tokens * kPieceStep));
 }
 
 // Sums of the bias gradient: a row per 32 tokens of a piece, or, where a contraction is split, per share of a tile's.
@@ -288,13 +284,14 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   }
 
   // dz is kept to 16 bits of its operands' type in dx (but for the label's, see XentRound), whose own rounding is as coarse, and
-  // in binary16 gradients of binary16 layers; else to two such planes, 16 or 22 bits, or three, 24.
+  // in binary16 gradients of binary16 layers; else to two such planes, 16 or 22 bits, or in binary32 gradients of bfloat16 layers,
+  // if not many tokens count (planes_of), to three, 24.
   const bool f16 = h->type == kF16;
-  const int dw_planes = !dw ? 0 : f16 && grad_dtype == DDL_FP16 ? 1 : !f16 && grad_dtype == DDL_FP32 && T <= kThreePlanes ? 3 : 2;
+  const int dw_planes = !dw ? 0 : f16 && grad_dtype == DDL_FP16 ? 1 : !f16 && grad_dtype == DDL_FP32 ? 3 : 2;
   const int n_planes = std::max(1, dw_planes);
   for (int k = 0; k < n_planes; ++k)
-    if ((st = need(&h->planes[k], plane_elems(h, k == 2) * 2)) != DDL_OK) return st;
-  if ((st = need(&h->scale, 2 * sizeof(float))) != DDL_OK) return st;
+    if ((st = need(&h->planes[k], plane_elems(h) * 2)) != DDL_OK) return st;
+  if ((st = need(&h->scale, 3 * sizeof(float))) != DDL_OK) return st;
   const int64_t most_sums = std::max<int64_t>(kSplitSums, (int64_t)plane_elems(h) / 32 + (int64_t)round8((uint64_t)V));
   if (db && (st = need(&h->db, (size_t)most_sums * 4)) != DDL_OK) return st;
   const int64_t ld32 = (int64_t)round8((uint64_t)K);
@@ -310,7 +307,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   if (prep.n_packs && (st = status_of(launch_linear_prep(prep, s))) != DDL_OK) return st;
   float* scale = static_cast<float*>(h->scale.p);
   const bool many = T > kScaleTokens;
-  const XentScale sc = {dloss, labels, T, V, f16, scale};
+  const XentScale sc = {dloss, labels, T, V, f16, n_planes, scale};
   if (many && (st = status_of(launch_xent_scale(sc, s))) != DDL_OK) return st;
   const GiveUp give_up = take_give_up(h);
   XentEnd end = {};  // what follows the products
@@ -389,7 +386,8 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
     const Mat ox{h->dx.p, T, ld32, ld32};  // dx's sums over the pieces, with their rows' padding
     const auto dw_count = [&](int tile) { return blocks_of(n, tile) * blocks_of(K, tile); };
     const auto dx_count = [&](int tile) { return blocks_of(T, tile) * blocks_of(K, tile); };
-    const int64_t dw_steps = blocks_of(T, kBlockK) * dw_planes, dx_steps = blocks_of(n, kBlockK);
+    // (a guess, where which tokens count decides)
+    const int64_t dw_steps = blocks_of(T, kBlockK) * (T > (int64_t)kExactTokens ? std::min(dw_planes, 2) : dw_planes), dx_steps = blocks_of(n, kBlockK);
     const auto layout = [&](bool with_dw, bool with_dx) {
       // the product with the longer contraction first; the workers take the tiles in turn
       const bool dw_first = with_dw && (!with_dx || dw_steps >= dx_steps);
@@ -457,6 +455,7 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
       L.bf16 = !f16;
       L.err = h->d_err;
       L.post = scale + 1;
+      if (with_dw && dw_planes == 3) L.passes = reinterpret_cast<const int32_t*>(scale + 2);
       for (int k = 0; k < n_planes; ++k)
         if (!map_of(&L, k, mp[k], kBlockK)) return DDL_ERR_CUDA;
       if ((with_dw && !map_of(&L, 3, ax, kBlockK)) || (with_dx && !map_of(&L, 4, bw, kBlockK))) return DDL_ERR_CUDA;

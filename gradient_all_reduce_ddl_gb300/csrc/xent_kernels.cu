@@ -105,19 +105,25 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 __global__ void __launch_bounds__(1024) scale_kernel(const __grid_constant__ XentScale p) {
-  __shared__ uint32_t shared[32];
+  __shared__ uint32_t shared[2][32];
   tc::griddep_launch();
   tc::griddep_wait();
-  uint32_t most = 0;
-  for (int64_t t = threadIdx.x; t < p.tokens; t += 1024) most = max(most, coef_bits(p.coef, p.labels, t, p.vocab));
+  uint32_t most = 0, counted = 0;
+  for (int64_t t = threadIdx.x; t < p.tokens; t += 1024) {
+    const uint32_t b = coef_bits(p.coef, p.labels, t, p.vocab);
+    most = max(most, b);
+    counted += b != 0;
+  }
   most = __reduce_max_sync(0xFFFFFFFFu, most);
-  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = most;
+  counted = __reduce_add_sync(0xFFFFFFFFu, counted);
+  if ((threadIdx.x & 31) == 0) shared[0][threadIdx.x >> 5] = most, shared[1][threadIdx.x >> 5] = counted;
   __syncthreads();
   if (threadIdx.x >= 32) return;
-  most = __reduce_max_sync(0xFFFFFFFFu, shared[threadIdx.x]);
+  most = __reduce_max_sync(0xFFFFFFFFu, shared[0][threadIdx.x]);
+  counted = __reduce_add_sync(0xFFFFFFFFu, shared[1][threadIdx.x]);
   if (threadIdx.x == 0) {
     const float2 u = dz_scale(most, p.f16);
-    p.scale[0] = u.x, p.scale[1] = u.y;
+    p.scale[0] = u.x, p.scale[1] = u.y, p.scale[2] = __int_as_float(planes_of(counted, p.planes));
   }
 }
 

@@ -32,7 +32,8 @@ struct XentScale {
   const int64_t* labels;
   int64_t tokens, vocab;
   int32_t f16;
-  float* scale;
+  int32_t planes;  // at most
+  float* scale;    // [2]: as an integer, how many planes dw takes (planes_of)
 };
 // (Launches of up to kScaleTokens tokens make it themselves: kEpiGrad.)
 constexpr int64_t kScaleTokens = 16384;

@@ -849,3 +849,52 @@ def test_losses_of_a_few_tokens(ddl, t, k, v, c):
             count += t
     off = math.sqrt(square / count)
     assert off <= 1.5 * math.sqrt((0.18 * (4 * c + 1)) ** 2 + 0.06 * n / c) * U["f32"], f"{off / U['f32']:.2f} u"
+
+
+@pytest.mark.parametrize("t", [64, 500, 2000, 4097, 6144, 6145, 9000, 17000])
+@pytest.mark.parametrize("k, v, ignored", [(96, 700, 0.0), (96, 700, 0.99), (1030, 333, 0.0), (1030, 333, 0.95)])
+def test_binary32_dw_keeps_dz_by_the_tokens_that_count(ddl, t, k, v, ignored):
+    """A bfloat16 head's, whatever tokens of the call are ignored or weigh nothing.  u = 2^-24; small logits, so that their own errors
+    are far below it, and dz from the call's own lse.  dz takes 3 roundings; the tensor core truncates 4 sums of a block of 64
+    tokens by half a unit at most, c blocks in a row (1, 2, 4 up to 640, 2048 and more tokens), and the rest are sums in binary32,
+    whose roundings average out: (3 + 4 c + sqrt(t / 64 c)) u, 6e-7 to 1.6e-6 of the norm.  Where more than 6144 tokens count, dz
+    has two planes: the second rounds what the first left to half a unit of it: 2^-16 of a power of two that is 0.72 of the number in
+    both, evenly (1 / sqrt 3 each): 0.52 / 3 of 2^-16, 2.6e-6, which fails the first bound."""
+    h = Head(t, k, v, "bf16", seed=26, ignored=ignored, sure=0.0)
+    h.w.mul_(0.02)
+    h.labels[0] = 5
+    if ignored == 0.95:  # these weigh nothing instead
+        h.dloss[h.labels < 0] = 0.0
+        h.labels.clamp_(min=0)
+    h.solve()
+    dw = torch.empty(v, k, device="cuda")
+    with ddl.CrossEntropy(k, v, t, "bf16") as head:
+        _, lse = h.forward(ddl, head)
+        head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, dw=dw)
+        head.check()
+    p = torch.exp(h.z - lse.double()[:, None])
+    p[torch.arange(t, device="cuda"), h.labels.clamp(min=0)] -= 1.0
+    dz = p * torch.where(h.valid, h.dloss.double(), 0.0)[:, None]
+    want = dz.t() @ h.x.double()
+    c = 1 if t <= 640 else 2 if t <= 2048 else 4
+    off = float((dw.double() - want).norm() / want.norm())
+    counted = int((h.valid & (h.dloss != 0)).sum())
+    assert off <= (3 + 4 * c + math.sqrt(t / (64 * c))) * U["f32"] + (counted > 6144) * 0.52 / 3 * 2.0 ** -16
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t, k, v", [(70, 256, 1500), (600, 1030, 2050)])
+def test_dx_is_nearly_as_exact_as_its_rounding(ddl, t, k, v, dtype):
+    """Of dx's plane of dz the label's value, which is most of dz here, is corrected: the rest, of norm 1 / sqrt(v) of it, adds
+    less than a thousandth in quadrature to what storing dx rounds.  Without the correction the two are alike: 1.4."""
+    h = Head(t, k, v, dtype, seed=27, ignored=0.0, sure=0.0)
+    h.w.mul_(0.1)
+    h.dloss *= 256.0
+    h.solve()
+    dx = torch.empty_like(h.x)
+    with ddl.CrossEntropy(k, v, t, dtype) as head:
+        _, lse = h.forward(ddl, head)
+        head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, dx=dx)
+    want = h.dz @ h.w.double()
+    stored = want.to(dx.dtype).double()
+    assert float((dx.double() - want).norm()) <= 1.05 * float((stored - want).norm())
