@@ -14,7 +14,8 @@
 // each on their own: 1720 us for the 336 M elements below).
 //
 // Products and sums are rounded one by one (no fused multiply-adds), as in the fused
-// SGD update, so that the states are the same bits as in a step-by-step evaluation.
+// SGD update, so that binary32 states are the same bits as in a step-by-step evaluation; of
+// 8-bit ones a code can be the neighbour's where the root lies next to the middle of two.
 #include <cuda_fp8.h>
 
 #include "activation.cuh"
@@ -172,12 +173,13 @@ struct Factors {
   float root;   // 1 / sqrt(1 - b2^t)
 };
 
-// To 2 units in the last place; a v below 2^-126 has the root 0.  The roots are stored in 8 bits or not at all, and the step
-// is far below the parameter.
+// To 2 units in the last place, also of numbers below the normal range, which the instruction takes for 0.  The roots are stored in
+// 8 bits or not at all, and the step is far below the parameter.  (Correctly rounded: 336 M elements 1188 -> 1271 us.)
 __device__ __forceinline__ float root_of(float x) {
+  const bool low = x < 0x1p-100f;
   float y;
-  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+  asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(low ? x * 0x1p64f : x));
+  return low ? y * 0x1p-32f : y;
 }
 __device__ __forceinline__ float inverse_of(float x) {
   float y;

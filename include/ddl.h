@@ -587,7 +587,7 @@ ddl_status_t ddl_xent_destroy(ddl_xent_t xent);
  * norm = |grad_scale| times the 2-norm of the gradients of all tensors; lr and
  * wd are the call's, times the tensor's factors.  Products and sums are
  * binary32, rounded one by one; roots and quotients are good to 2 units in the
- * last place (a v below 2^-126 has the root 0); the norm is good to 2^-22 of itself.
+ * last place; the norm is good to 2^-22 of itself.
  *
  * States: binary32, or 8 bits with a binary32 scale per block of 128 elements
  * (counted from each tensor's first; its last block may be shorter).  m is

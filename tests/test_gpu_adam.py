@@ -346,3 +346,28 @@ def test_checks_of_the_object(ddl):
         with pytest.raises(ddl.DDLError) as e:  # memory of another kind
             ddl.ddl_adam_step(adam.handle, pinned, [x.clone()], None, ddl.DDL_FP16, s["m"], s["v"], s["scales"], s["step"], 0.1)
         assert e.value.status == ddl.DDL_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("state", ["f32", "8bit"])
+@pytest.mark.parametrize("eps", [2.0 ** -126, 1e-30, 1e-20])
+@pytest.mark.parametrize("sigma", [1e-17, 1e-18, 1e-19])
+def test_roots_of_tiny_second_moments(ddl, state, eps, sigma):
+    """v of gradients that small is below binary32's normal range, where it has an absolute error of half of 2^-149; its root is an
+    ordinary number, by which the step divides.  Of a new state (m = 0.1 g, v = 0.001 g^2 in binary32) the step is lr m / 0.1 /
+    (sqrt(v / 0.001) + eps): 40 u of it, and what v's two roundings below the normal range, 2^-149 in all, are of its root."""
+    n, lr = 1000, 1e-2
+    g = torch.randn(n, generator=_gen(15), device="cuda") * sigma
+    with ddl.Adam([(0, n)], state=state, eps=eps) as adam:
+        p, s = torch.zeros(n, device="cuda"), adam.new_state()
+        adam.step(g, [p], lr=lr, **s)
+    g = g.double()
+    v = 0.001 * g * g
+    known = v > 2.0 ** -143
+    assert bool(known.float().mean() > 0.5)
+    want = -lr * g / ((v / 0.001).sqrt() + eps)
+    bound = (40 * U + 2.0 ** -149 / v) * want.abs()
+    assert float(((p.double() - want).abs() / bound)[known].max()) <= 1.0
+    if state == "8bit":  # a root that is not zero is not kept as zero
+        assert bool((s["v"][known] != 0).all())
+    else:
+        assert float(((s["v"].double() - v).abs() - 3 * U * v - 2.0 ** -149)[known].max()) <= 0
