@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kThreads) prep_kernel(const __grid_constant__ 
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t across = (p.cols + kDzCols - 1) / kDzCols, down = (p.rows + p.block_rows - 1) / p.block_rows;
   int64_t block = blockIdx.x;
-  const int64_t dz_blocks = p.has_dz ? across * down : 0;
+  const int64_t dz_blocks = across * down;
   if (block >= dz_blocks) {
     block -= dz_blocks;
     const int64_t first = (p.pack[0].rows + kPackRows - 1) / kPackRows * ((p.pack[0].cols + kPackCols - 1) / kPackCols);

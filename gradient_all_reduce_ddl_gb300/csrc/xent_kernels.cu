@@ -141,7 +141,7 @@ __device__ __forceinline__ void bias_columns(const XentBias& p, int64_t block) {
   if (warp > 0 || c >= p.cols) return;
 #pragma unroll
   for (int w = 1; w < kWarps; ++w) s += shared[w][lane];
-  if (p.scale) s *= __ldcg(p.scale);
+  s *= __ldcg(p.scale);
   if (p.f32) {
     float* o = static_cast<float*>(p.db) + c;
     *o = p.accumulate ? *o + s : s;

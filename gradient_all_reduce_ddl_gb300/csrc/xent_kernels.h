@@ -43,7 +43,7 @@ cudaError_t launch_xent_scale(const XentScale& p, cudaStream_t stream);
 struct XentBias {
   const float* part;  // [groups][ld]
   int64_t ld, groups, cols;
-  const float* scale;  // NULL: 1
+  const float* scale;
   void* db;
   int32_t f32, accumulate;
 };
