@@ -95,9 +95,10 @@ ddl_status_t ddl_adam_create(int n_tensors, const ddl_tensor_t* tensors, ddl_dty
   a->extent = extent;
   a->blocks = blocks;
   a->odd = odd;
-  // few elements: short items, so that every SM has some
+  // few elements: short items, so that every SM has some (of a GB300's: no device is asked before the first GPU call)
+  constexpr uint64_t kSms = 152, kCtas = 6;
   uint64_t per = ddl::kAdamItemBlocks;
-  while (per > 1 && blocks < per * 152 * 6) per /= 2;
+  while (per > 1 && blocks < per * kSms * kCtas) per /= 2;
   try {
     std::vector<const ddl_tensor_t*> by(n_tensors);
     for (int i = 0; i < n_tensors; ++i) by[i] = tensors + i;

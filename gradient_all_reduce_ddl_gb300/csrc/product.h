@@ -1,7 +1,7 @@
 // product.h -- launch records of the matrix products (internal).
 //
-// One kernel carries every product of the linear layers and of the
-// Newton-Schulz steps: D = sum over passes of scale * A B^T on the tensor
+// One kernel carries every product of the linear layers, of the softmax cross
+// entropy and of the Newton-Schulz steps: D = sum over passes of scale * A B^T on the tensor
 // cores, then an epilogue on the binary32 sums.  Passes let an operand be the
 // sum of several 16-bit planes (two of binary16 hold x 2^12 = hi + lo to 22
 // bits), which is how results that are kept in binary32 get products of more

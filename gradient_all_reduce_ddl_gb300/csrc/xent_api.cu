@@ -284,7 +284,8 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
   }
 
   // dz is kept to 16 bits of its operands' type in dx (but for the label's, see XentRound), whose own rounding is as coarse, and
-  // in binary16 gradients of binary16 layers; else to two such planes, 16 or 22 bits, or in binary32 gradients of bfloat16 layers,
+  // in binary16 gradients of binary16 layers, which end 1.35 times their own rounding off (517 tokens, 771 features, 5003 entries
+  // 2.8e-4; with two planes 2.1e-4 and 61.4 -> 65.6 us backward; 2048, 2048, 8192: 182 -> 228); else to two such planes, 16 or 22 bits, or in binary32 gradients of bfloat16 layers,
   // if not many tokens count (planes_of), to three, 24.
   const bool f16 = h->type == kF16;
   const int dw_planes = !dw ? 0 : f16 && grad_dtype == DDL_FP16 ? 1 : !f16 && grad_dtype == DDL_FP32 ? 3 : 2;

@@ -537,10 +537,14 @@ ddl_status_t ddl_ortho_destroy(ddl_ortho_t ortho);
  * infinite: a bias of -infinity takes an entry out of the softmax.
  *
  * A handle's device binding, threads, ownership, checks and overlap rules are
- * those of the linear layers.  Its workspace: 8 bytes per token and 64 entries
- * of the vocabulary (at most 512 MB), twice 2 bytes per token and entry of a
- * piece (at most 2^28 of them, or 256 entries; once more for up to 4096 tokens of
- * DDL_BF16), 4 bytes per token and feature for dx, copies of x and w whose rows are not aligned. */
+ * those of the linear layers.  Its workspace, by what calls ask for.  Forward: 8
+ * bytes per token and 64 entries of the vocabulary (at most 512 MB), or per token and 16
+ * entries for up to 64 tokens if that is more; with smoothing half as much
+ * again; 4 per token.  Backward: per token and entry of a piece (at most 2^28 of
+ * them, or 256 entries) 2 bytes for each plane of dz (one to three: see the
+ * rounding below); for db 4 bytes per 32 of these, 4 per entry and 4 MB at least; for
+ * dx 4 bytes per token and feature, and 4 per token.  Both: copies of x and w
+ * whose rows are not aligned. */
 
 typedef struct ddl_xent* ddl_xent_t;
 
@@ -558,11 +562,20 @@ ddl_status_t ddl_xent_forward(ddl_xent_t xent, size_t tokens, const void* x, siz
 
 /* dloss: the gradient of each token's loss, e.g. 1 / tokens (NULL = ones).  dx,
  * dw, db, grad_dtype, accumulate: as for ddl_linear_backward.  Repeated calls
- * give the same bits.  Rounding: dz is kept to the 16 bits of the handle's type in
- * dx (the label's, which is most of it, to 24) and in binary16 gradients of a
- * DDL_FP16 handle; in other gradients dw takes it to 22 bits (DDL_FP16) or 16
- * (DDL_BF16; 24 in binary32 gradients of up to 4096 tokens).  On the way dz is
- * divided by the largest dloss, so that no size of dloss loses anything. */
+ * give the same bits.
+ *
+ * Rounding.  z, lse and dz are binary32 numbers, so that dz / dloss is off by up
+ * to 2^-23 |lse| (and the logits' own error) of the probability: of a token that
+ * the model is nearly sure of, whose dz is small, that can be most of it, though its loss keeps
+ * more.  From there dz is kept to the 16 bits of the handle's type in dx (the
+ * label's, which is most of it where the label is not likely, to 24) and in
+ * binary16 gradients of a DDL_FP16 handle; in other gradients dw takes it to 22
+ * bits (DDL_FP16) or 16 (DDL_BF16; 24 in binary32 gradients if at most 6144
+ * tokens of the call have a label and a dloss that is not zero).  On the way dz
+ * is divided by the largest |dloss| of the call (of those between 2^-100 and
+ * 2^100), so that the size of all of them does not matter.  In a DDL_FP16 handle
+ * parts of dz below 2^-28 of the largest |dloss| lose bits, up to 2^-39 of it each in dx
+ * and binary16 dw. */
 ddl_status_t ddl_xent_backward(ddl_xent_t xent, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
                                const void* bias, const int64_t* labels, const float* lse, const float* dloss, void* dx,
                                size_t lddx, void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate,
@@ -592,9 +605,9 @@ ddl_status_t ddl_xent_destroy(ddl_xent_t xent);
  * States: binary32, or 8 bits with a binary32 scale per block of 128 elements
  * (counted from each tensor's first; its last block may be shorter).  m is
  * kept as e4m3 numbers x, m = x s with s = (largest |m| of the block) / 448,
- * and of v the square root is kept likewise.  A root that is not zero is never
- * kept as zero; a block whose largest value is below 2^-100 is kept as zeros,
- * and an infinite or NaN value as NaN.  The step itself uses the new m and v
+ * and of v the square root is kept likewise.  A block whose largest value is
+ * below 2^-100 is kept as zeros, and an infinite or NaN value as NaN; in other
+ * blocks a root that is not zero is never kept as zero.  The step itself uses the new m and v
  * before they are rounded.  All-zero buffers are the states before step 1.
  *
  * A handle's device binding, threads, ownership and overlap rules are those of
@@ -633,7 +646,10 @@ ddl_status_t ddl_adam_blocks(ddl_adam_t adam, size_t* n);
  *  scales          8-bit states: m's block scales, then v's, tensor by tensor in
  *                  the order of ddl_adam_create (2 x ddl_adam_blocks); else NULL
  *  step            one number in device memory: steps done so far, >= 0.  The call
- *                  adds one, so that a captured call replays as the next step
+ *                  adds one, so that a captured call replays as the next step.
+ *                  (lr, weight_decay, grad_scale and max_norm are the host's
+ *                  numbers: a replay has those of the capture.  Under a schedule or a
+ *                  changing loss scale, capture again or call.)
  *  max_norm        0: no clipping
  *  norm            NULL, or one binary32 in device memory that receives the norm
  * One launch, and one before it where a norm is asked for.  Repeated calls on

@@ -898,3 +898,42 @@ def test_dx_is_nearly_as_exact_as_its_rounding(ddl, t, k, v, dtype):
     want = h.dz @ h.w.double()
     stored = want.to(dx.dtype).double()
     assert float((dx.double() - want).norm()) <= 1.05 * float((stored - want).norm())
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_token_weights_of_many_sizes(ddl, dtype):
+    """Weights from 2^-26 to 1 of the largest in one call: every token's dx is within the bound of its own dz and of 2^-39 of the
+    largest weight (binary16)."""
+    t = 300
+    dloss = 2.0 ** (12 - 26 * torch.rand(t, generator=_gen(5), device="cuda"))
+    h = Head(t, 96, 260, dtype, bias=True, smoothing=0.1, seed=28, ignored=0.1, dloss=dloss)
+    _run(ddl, h)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("t", [11, 64, 200])
+def test_gradients_of_tokens_that_are_nearly_sure(ddl, t, dtype):
+    """x w^T with w the identity: exact logits, and dx is dz.  1 - p of the labels from 1e-3 to 1e-7, where what is left of dz is lse's and
+    the exponential's rounding: 2^-23 |lse| + 2^-21 of the probability, 4 u of the difference, and the rounding of the plane (the
+    label's dz excepted) and of dx."""
+    v = 64
+    x = torch.zeros(t, v, device="cuda")
+    labels = torch.randint(0, v, (t,), generator=_gen(32), device="cuda")
+    x[torch.arange(t), labels] = torch.linspace(11, 20, t, device="cuda")
+    x, w = x.to(TYPES[dtype]), torch.eye(v, device="cuda").to(TYPES[dtype])
+    loss, lse, dx = torch.empty(t, device="cuda"), torch.empty(t, device="cuda"), torch.empty_like(x)
+    dloss = torch.full((t,), 1024.0, device="cuda")
+    with ddl.CrossEntropy(v, v, t, dtype) as head:
+        head.forward(x, w, labels, loss, lse)
+        head.backward(x, w, labels, lse, dloss=dloss, dx=dx)
+        head.check()
+    z = x.double()
+    p = torch.softmax(z, 1)
+    q = torch.nn.functional.one_hot(labels, v).double()
+    miss = (p * (1 - q)).sum(1, keepdim=True)
+    want = torch.where(q > 0, -miss, p)
+    bound = p * (2.0 ** -23 * (20 + math.log(v)) + 2.0 ** -21 + 2.0 ** -22 * (z - z.amax(1, keepdim=True)).abs()) + 4 * U["f32"] * q
+    bound = 1024 * (bound + 2 * U[dtype] * want.abs()) + TINY[dtype] + 2.0 ** -29
+    _within(dx, 1024 * want, bound)
+    small = torch.nn.functional.softplus(torch.log(miss[:, 0]) - torch.log1p(-miss[:, 0]))
+    _within(loss, small, small * 2.0 ** -15)
