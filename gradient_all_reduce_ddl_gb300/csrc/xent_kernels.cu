@@ -162,9 +162,14 @@ __device__ __forceinline__ void round_rows(const XentRound& p, int64_t block) {
   const int64_t y = p.labels[r];
   if (y >= 0 && y < p.vocab) {
     const float by = __ldcg(p.resid + r) * __ldcg(p.inverse);
+    uint16_t w[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)  // (an infinite or NaN sum stands: the rest, or its zero, times the weight that made it so may be NaN)
-      if (c0 + 32 * k < p.cols && fabsf(v[k]) <= FLT_MAX) v[k] = fmaf(by, from16(p.w[y * p.ldw + c0 + 32 * k], p.type), v[k]);
+    for (int k = 0; k < 8; ++k) w[k] = c0 + 32 * k < p.cols ? p.w[y * p.ldw + c0 + 32 * k] : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {  // (an infinite or NaN sum stands: the rest, or its zero, times the weight that made it so may be NaN)
+      const float u = fmaf(by, from16(w[k], p.type), v[k]);
+      v[k] = fabsf(v[k]) <= FLT_MAX ? u : v[k];
+    }
   }
 #pragma unroll
   for (int k = 0; k < 8; ++k)
