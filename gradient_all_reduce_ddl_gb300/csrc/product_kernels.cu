@@ -1021,14 +1021,17 @@ struct GradRow {
 
 // The planes of two neighbours: 16 bits, what their rounding lost (in binary16 2^11 times that), and what that one's lost.  (Of
 // an infinite value the others are NaN, but the sums of the first plane are infinite or NaN then, and stand.)
-__device__ __forceinline__ void grad_planes(float x, float y, int type, uint32_t (&out)[3]) {
+template <int N>
+__device__ __forceinline__ void grad_planes(float x, float y, int type, uint32_t (&out)[N]) {
   out[0] = to16x2(x, y, type);
   float2 h = from16x2(out[0], type);
   x -= h.x, y -= h.y;
   if (type == kF16) x *= 2048.f, y *= 2048.f;
   out[1] = to16x2(x, y, type);
-  h = from16x2(out[1], type);
-  out[2] = to16x2(x - h.x, y - h.y, type);
+  if constexpr (N == 3) {
+    h = from16x2(out[1], type);
+    out[2] = to16x2(x - h.x, y - h.y, type);
+  }
 }
 
 // The sums over a warp's 32 rows of its lanes' 16 columns each: the lane's are of column (lane / 2) on return.  Each step
@@ -1050,11 +1053,13 @@ __device__ __forceinline__ float column_sums16(const float* v, int lane) {
   return x[0] + __shfl_xor_sync(0xffffffffu, x[0], 1);
 }
 
-// 16 columns n.. of row m, from logits to planes in the slab.
+// 16 columns n.. of row m, from logits to planes in the slab.  A third plane is made from the values again, in little code: what it
+// adds to the loop over slabs is paid in the instruction cache by launches without it, too (8192 tokens, 2048 features, 32,768
+// entries: 797 us made with the others, 817 in a copy of its own, 776 so; 783 before calls of that size could have one).
 template <int TYPE>
 __device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, const ProductLaunch& p, int planes, int m,
                                             int n) {
-  uint32_t u[8][3];
+  uint32_t u[8][2];
 #pragma unroll
   for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], TYPE, u[k]);
 #pragma unroll
@@ -1063,9 +1068,17 @@ __device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int ro
     const auto words = [&](int plane) { return make_uint4(u[4 * h][plane], u[4 * h + 1][plane], u[4 * h + 2][plane], u[4 * h + 3][plane]); };
     st_shared16(at, words(0));
     if (planes >= 2) st_shared16(at + kPlaneBytes, words(1));
-    // few tokens: it need not go by boxes
-    if (TYPE == kBF16 && planes == 3 && m < p.inl[0].M && n + 8 * h < p.inl[0].ldp)
-      *reinterpret_cast<uint4*>(p.soft.third + (int64_t)m * p.inl[0].ldp + n + 8 * h) = words(2);
+  }
+  if (TYPE == kBF16 && __any_sync(0xffffffffu, planes == 3)) {
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4][3];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) grad_planes(h ? v[8 + 2 * k] : v[2 * k], h ? v[9 + 2 * k] : v[2 * k + 1], TYPE, w[k]);
+      // few tokens: it need not go by boxes
+      if (m < p.inl[0].M && n + 8 * h < p.inl[0].ldp)
+        *reinterpret_cast<uint4*>(p.soft.third + (int64_t)m * p.inl[0].ldp + n + 8 * h) = make_uint4(w[0][2], w[1][2], w[2][2], w[3][2]);
+    }
   }
 }
 
