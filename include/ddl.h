@@ -570,7 +570,7 @@ ddl_status_t ddl_xent_forward(ddl_xent_t xent, size_t tokens, const void* x, siz
  * more.  From there dz is kept to the 16 bits of the handle's type in dx (the
  * label's, which is most of it where the label is not likely, to 24) and in
  * binary16 gradients of a DDL_FP16 handle; in other gradients dw takes it to 22
- * bits (DDL_FP16) or 16 (DDL_BF16; 24 in binary32 gradients if at most 6144
+ * bits (DDL_FP16) or 16 (DDL_BF16; 24 in binary32 gradients if at most 4096
  * tokens of the call have a label and a dloss that is not zero).  On the way dz
  * is divided by the largest |dloss| of the call (of those between 2^-100 and
  * 2^100), so that the size of all of them does not matter.  In a DDL_FP16 handle

@@ -851,13 +851,13 @@ def test_losses_of_a_few_tokens(ddl, t, k, v, c):
     assert off <= 1.5 * math.sqrt((0.18 * (4 * c + 1)) ** 2 + 0.06 * n / c) * U["f32"], f"{off / U['f32']:.2f} u"
 
 
-@pytest.mark.parametrize("t", [64, 500, 2000, 4097, 6144, 6145, 9000, 17000])
+@pytest.mark.parametrize("t", [64, 500, 2000, 4096, 4097, 6145, 9000, 17000])
 @pytest.mark.parametrize("k, v, ignored", [(96, 700, 0.0), (96, 700, 0.99), (1030, 333, 0.0), (1030, 333, 0.95)])
 def test_binary32_dw_keeps_dz_by_the_tokens_that_count(ddl, t, k, v, ignored):
     """A bfloat16 head's, whatever tokens of the call are ignored or weigh nothing.  u = 2^-24; small logits, so that their own errors
     are far below it, and dz from the call's own lse.  dz takes 3 roundings; the tensor core truncates 4 sums of a block of 64
     tokens by half a unit at most, c blocks in a row (1, 2, 4 up to 640, 2048 and more tokens), and the rest are sums in binary32,
-    whose roundings average out: (3 + 4 c + sqrt(t / 64 c)) u, 6e-7 to 1.6e-6 of the norm.  Where more than 6144 tokens count, dz
+    whose roundings average out: (3 + 4 c + sqrt(t / 64 c)) u, 6e-7 to 1.6e-6 of the norm.  Where more than 4096 tokens count, dz
     has two planes: the second rounds what the first left to half a unit of it: 2^-16 of a power of two that is 0.72 of the number in
     both, evenly (1 / sqrt 3 each): 0.52 / 3 of 2^-16, 2.6e-6, which fails the first bound."""
     h = Head(t, k, v, "bf16", seed=26, ignored=ignored, sure=0.0)
@@ -879,7 +879,7 @@ def test_binary32_dw_keeps_dz_by_the_tokens_that_count(ddl, t, k, v, ignored):
     c = 1 if t <= 640 else 2 if t <= 2048 else 4
     off = float((dw.double() - want).norm() / want.norm())
     counted = int((h.valid & (h.dloss != 0)).sum())
-    assert off <= (3 + 4 * c + math.sqrt(t / (64 * c))) * U["f32"] + (counted > 6144) * 0.52 / 3 * 2.0 ** -16
+    assert off <= (3 + 4 * c + math.sqrt(t / (64 * c))) * U["f32"] + (counted > 4096) * 0.52 / 3 * 2.0 ** -16
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
