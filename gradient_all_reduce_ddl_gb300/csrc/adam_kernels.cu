@@ -6,7 +6,7 @@
 //
 // Bound by HBM: 28 bytes an element with binary32 states and one copy, 8 (10 with a
 // 16-bit operand copy) for each further copy; 16.1 with 8-bit states, whose coding also
-// takes 66 instructions an element (57 % of the issue slots).  One launch covers every tensor: a CTA takes an
+// takes 69 instructions an element (56 % of the issue slots).  One launch covers every tensor: a CTA takes an
 // item of up to 1024 elements of one tensor, each of its warps one or two
 // neighbouring blocks of 128, four elements per lane, so that a block's largest value (the
 // 8-bit states' scale) is one warp reduction, the work does not depend on how long the
@@ -160,7 +160,7 @@ __device__ __forceinline__ float store_codes(void* base, int64_t at, uint32_t le
 // -- the step -----------------------------------------------------------------------
 
 // Occupancy and grid, by the states' width.  336 M elements with 8-bit states, the norm's pass among them: seven CTAs of 128
-// threads an SM (72 registers) 1222 us, eight (64, some spilled) 1248, six 1231, four of 256 threads 1272, three 1286; loads of
+// threads an SM (72 registers) 1222 us (1190 since roots are scaled, see below), eight (64, some spilled) 1248, six 1231, four of 256 threads 1272, three 1286; loads of
 // the next item before this one's arithmetic 1277 (112 registers), one block at a time instead of two 1460.  25.6 M elements
 // of 16 copies with binary32 states: a grid of four times the CTAs that fit 565 us, of those that fit 576.
 __host__ __device__ constexpr int min_ctas(int bits) { return bits == 32 ? 6 : 7; }

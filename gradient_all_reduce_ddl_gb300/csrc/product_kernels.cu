@@ -753,7 +753,7 @@ __device__ __forceinline__ void joined_mirror(const Product& P, uint32_t base, i
 // of a token that the model is sure of, log(1 + s exp(m - z_label)), would be lost in the rounding of lse.
 // Gradient: exp(z - lse) needs nothing of other entries, so the logits' products are done again and dz is made from them.
 //
-// What bounds them: the products (8192 tokens, 2048 features, 65,536 entries: loss 1321 us, 1665 TFLOP/s; gradient 1466, with
+// What bounds them: the products (8192 tokens, 2048 features, 65,536 entries: loss 1312 us, 1676 TFLOP/s; gradient 1534, with
 // 2.1 GB of planes written under it).  The epilogue of a 256 x 256 tile runs under the products of two chunks, 16 blocks of
 // 64; with chunks of 4 the products waited for it (gradient 1860 us).  Joining the parts of the vocabulary, and the bias gradient's parts, in
 // here, by the CTA that comes last at a counter, costs every tile a release fence (1 to 2 us; a ragged call 90 instead of 58
