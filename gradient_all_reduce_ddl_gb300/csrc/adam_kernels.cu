@@ -160,9 +160,10 @@ __device__ __forceinline__ float store_codes(void* base, int64_t at, uint32_t le
 // -- the step -----------------------------------------------------------------------
 
 // Occupancy and grid, by the states' width.  336 M elements with 8-bit states, the norm's pass among them: seven CTAs of 128
-// threads an SM (72 registers) 1222 us (1190 since roots are scaled, see below), eight (64, some spilled) 1248, six 1231, four of 256 threads 1272, three 1286; loads of
-// the next item before this one's arithmetic 1277 (112 registers), one block at a time instead of two 1460.  25.6 M elements
-// of 16 copies with binary32 states: a grid of four times the CTAs that fit 565 us, of those that fit 576.
+// threads an SM (72 registers) 1222 us (1190 since roots are scaled, see below), eight (64, some spilled) 1248, six 1231, four of
+// 256 threads 1272, three 1286; loads of the next item before this one's arithmetic 1277 (112 registers), one block at a time
+// instead of two 1460.  25.6 M elements of 16 copies with binary32 states: a grid of four times the CTAs that fit 565 us, of those
+// that fit 576.
 __host__ __device__ constexpr int min_ctas(int bits) { return bits == 32 ? 6 : 7; }
 constexpr int waves(int bits) { return bits == 32 ? 24 : 7; }
 

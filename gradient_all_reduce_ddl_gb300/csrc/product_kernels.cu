@@ -1057,8 +1057,8 @@ __device__ __forceinline__ float column_sums16(const float* v, int lane) {
 // adds to the loop over slabs is paid in the instruction cache by launches without it, too (8192 tokens, 2048 features, 32,768
 // entries: 797 us made with the others, 817 in a copy of its own, 776 so; 783 before calls of that size could have one).
 template <int TYPE>
-__device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, const ProductLaunch& p, int planes, int m,
-                                            int n) {
+__device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int row, int half, const ProductLaunch& p, int planes,
+                                            int m, int n) {
   uint32_t u[8][2];
 #pragma unroll
   for (int k = 0; k < 8; ++k) grad_planes(v[2 * k], v[2 * k + 1], TYPE, u[k]);
@@ -1077,7 +1077,8 @@ __device__ __forceinline__ void slab_planes(const float* v, uint32_t buf, int ro
       for (int k = 0; k < 4; ++k) grad_planes(h ? v[8 + 2 * k] : v[2 * k], h ? v[9 + 2 * k] : v[2 * k + 1], TYPE, w[k]);
       // few tokens: it need not go by boxes
       if (m < p.inl[0].M && n + 8 * h < p.inl[0].ldp)
-        *reinterpret_cast<uint4*>(p.soft.third + (int64_t)m * p.inl[0].ldp + n + 8 * h) = make_uint4(w[0][2], w[1][2], w[2][2], w[3][2]);
+        *reinterpret_cast<uint4*>(p.soft.third + (int64_t)m * p.inl[0].ldp + n + 8 * h) =
+            make_uint4(w[0][2], w[1][2], w[2][2], w[3][2]);
     }
   }
 }
@@ -1102,8 +1103,8 @@ __device__ __forceinline__ void slab_grad(const ProductLaunch& p, float* v, cons
 // Rows [r0, r1) of a tile whose contraction was split: a warp along a row, four columns a lane.  The planes' rows are
 // padded to 8 columns, so that a group of 4 that begins inside the matrix is whole.
 template <int BN>
-__device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, int planes, int row0, int col0, int lane, int ew, int r0, int r1, int q,
-                                          int S, uint32_t staging, const ClusterSums sums) {
+__device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, int planes, int row0, int col0, int lane, int ew,
+                                          int r0, int r1, int q, int S, uint32_t staging, const ClusterSums sums) {
   const Product& P = p.inl[0];
   const Softmax& e = p.soft;
 #pragma unroll 1
@@ -1147,7 +1148,8 @@ __device__ __forceinline__ void grad_rows(const ProductLaunch& p, float scale, i
   }
 }
 
-// dz's scale, and in *planes how many there are, from the coefficients of all tokens; every CTA makes them, under its first products.
+// dz's scale, and in *planes how many there are, from the coefficients of all tokens; every CTA makes them, under its first
+// products.
 __device__ __forceinline__ float launch_scale(const ProductLaunch& p, int thread, uint32_t shared, int* planes) {
   const Softmax& e = p.soft;
   if (e.scaled) {
@@ -1762,7 +1764,8 @@ __global__ void __launch_bounds__(kThreads, 1) product_kernel(const __grid_const
             loss_columns<BN>(p, pl.row0, pl.col0, lane, ew, q * share, share, first * S + q, sums);
         } else if constexpr (MODE == kGrad) {
           const int share = kTileM / S;
-          grad_rows<BN>(p, grad_scale, planes, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, q, S, staging, sums);
+          grad_rows<BN>(p, grad_scale, planes, pl.row0 + my_rows, pl.col0, lane, ew, q * share, (q + 1) * share, q, S, staging,
+                        sums);
         } else {
           // this CTA finishes its share of the rows
           const int share = kTileM / S;

@@ -23,7 +23,8 @@ __device__ __forceinline__ float2 dz_scale(uint32_t most, bool f16) {
 // Binary32 dw of a bfloat16 head takes dz in three planes (24 bits) where at most so many tokens count, else in two.  Two leave
 // it 1.5 to 2.4e-6 off however many there are.  Sums in binary32 lose 1.9e-8 times the root of the number of tokens that
 // are not zero (2112: 0.7e-6, 4096: 1.2e-6, 8192: 1.75e-6), about as much from here on, while a third pass costs a fifth of the
-// products (6000 tokens, 2048 features, 65,536 entries: 4330 -> 5500 us backward; 8192: 7760 -> 9280 with the loss, 1.6e-6 -> 0.7e-6 off).
+// products (6000 tokens, 2048 features, 65,536 entries: 4330 -> 5500 us backward; 8192: 7760 -> 9280 with the loss, 1.6e-6 ->
+// 0.7e-6 off).
 constexpr uint32_t kExactTokens = 4096;
 __device__ __forceinline__ int planes_of(uint32_t counted, int most) { return most == 3 && counted > kExactTokens ? 2 : most; }
 

@@ -41,9 +41,10 @@ constexpr int64_t kPieceStep = 256;           // pieces begin at whole tiles
 // binary32: 6.6e-7) and of binary32 dw 1.7, 1.6, 2.0e-6 (1.75e-6).  The gradient takes the loss's chunk: what truncation takes
 // from z it then takes from lse, too (with 16 blocks under a loss of 8 dw is 3.0e-6 off): 8 blocks.
 // Few tokens' losses are not averaged over many: up to 64 tokens 6 blocks (16 tokens, 4096 features, 65,536 entries: 93.0, 93.3,
-// 96.9, 102, 111, 136 us with 8, 6, 4, 3, 2, 1; with 6 the loss of 9 to 64 is 2.5 to 2.9e-7 off, products in binary32 3 to 6e-7).  Of
-// up to 8 tokens 2 (one token over the same: of 32 losses the worst 3.8, 2.1, 1.2, 1.6e-6 off with 6, 4, 2, 1, products in binary32
-// 0.9e-6; 89.3, 92.6, 106, 131 us), and 1 where the weights are few tiles (2048 features, 1000 entries: 9.7 -> 9.9 us from 2).
+// 96.9, 102, 111, 136 us with 8, 6, 4, 3, 2, 1; with 6 the loss of 9 to 64 is 2.5 to 2.9e-7 off, products in binary32 3 to
+// 6e-7).  Of up to 8 tokens 2 (one token over the same: of 32 losses the worst 3.8, 2.1, 1.2, 1.6e-6 off with 6, 4, 2, 1, products in
+// binary32 0.9e-6; 89.3, 92.6, 106, 131 us), and 1 where the weights are few tiles (2048 features, 1000 entries: 8.5 -> 8.9 us in
+// graph replay from 2).
 int32_t logit_chunk(const ddl_xent* h, int64_t tokens) {
   return tokens > kFewTokens ? 8 : tokens > 8 ? 6 : blocks_of(h->vocab, kTileM) > h->sms ? 2 : 1;
 }
@@ -285,8 +286,8 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
 
   // dz is kept to 16 bits of its operands' type in dx (but for the label's, see XentRound), whose own rounding is as coarse, and
   // in binary16 gradients of binary16 layers, which end 1.35 times their own rounding off (517 tokens, 771 features, 5003 entries
-  // 2.8e-4; with two planes 2.1e-4 and 61.4 -> 65.6 us backward; 2048, 2048, 8192: 182 -> 228); else to two such planes, 16 or 22 bits, or in binary32 gradients of bfloat16 layers,
-  // if not many tokens count (planes_of), to three, 24.
+  // 2.8e-4; with two planes 2.1e-4 and 61.4 -> 65.6 us backward; 2048, 2048, 8192: 182 -> 228); else to two such planes, 16 or 22
+  // bits, or in binary32 gradients of bfloat16 layers, if not many tokens count (planes_of), to three, 24.
   const bool f16 = h->type == kF16;
   const int dw_planes = !dw ? 0 : f16 && grad_dtype == DDL_FP16 ? 1 : !f16 && grad_dtype == DDL_FP32 ? 3 : 2;
   const int n_planes = std::max(1, dw_planes);
@@ -388,7 +389,8 @@ ddl_status_t ddl_xent_backward(ddl_xent_t h, size_t tokens, const void* x, size_
     const auto dw_count = [&](int tile) { return blocks_of(n, tile) * blocks_of(K, tile); };
     const auto dx_count = [&](int tile) { return blocks_of(T, tile) * blocks_of(K, tile); };
     // (a guess, where which tokens count decides)
-    const int64_t dw_steps = blocks_of(T, kBlockK) * (T > (int64_t)kExactTokens ? std::min(dw_planes, 2) : dw_planes), dx_steps = blocks_of(n, kBlockK);
+    const int dw_passes = T > (int64_t)kExactTokens ? std::min(dw_planes, 2) : dw_planes;
+    const int64_t dw_steps = blocks_of(T, kBlockK) * dw_passes, dx_steps = blocks_of(n, kBlockK);
     const auto layout = [&](bool with_dw, bool with_dx) {
       // the product with the longer contraction first; the workers take the tiles in turn
       const bool dw_first = with_dw && (!with_dx || dw_steps >= dx_steps);

@@ -166,7 +166,8 @@ __device__ __forceinline__ void round_rows(const XentRound& p, int64_t block) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) w[k] = c0 + 32 * k < p.cols ? p.w[y * p.ldw + c0 + 32 * k] : 0;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {  // (an infinite or NaN sum stands: the rest, or its zero, times the weight that made it so may be NaN)
+    for (int k = 0; k < 8; ++k) {
+      // (an infinite or NaN sum stands: the rest, or its zero, times the weight that made it so may be NaN)
       const float u = fmaf(by, from16(w[k], p.type), v[k]);
       v[k] = fabsf(v[k]) <= FLT_MAX ? u : v[k];
     }

@@ -682,8 +682,8 @@ def test_a_training_step_of_all_operators(ddl):
 
 class LowHead(Head):
     """A head whose bias is far below zero on some entries.  Its sum with the products rounds to binary32 (and loses them where
-    its half unit is above them, from 2^30 on): the reference's logits are rounded likewise, and off by the products' own error and, below that, one
-    rounding more.  Gradients are those of the call's own lse."""
+    its half unit is above them, from 2^30 on): the reference's logits are rounded likewise, and off by the products' own error
+    and, below that, one rounding more.  Gradients are those of the call's own lse."""
 
     def __init__(self, t, k, v, dtype, low, entries, masked=0, **more):
         super().__init__(t, k, v, dtype, bias=True, ignored=0.1, **more)
@@ -937,3 +937,23 @@ def test_gradients_of_tokens_that_are_nearly_sure(ddl, t, dtype):
     _within(dx, 1024 * want, bound)
     small = torch.nn.functional.softplus(torch.log(miss[:, 0]) - torch.log1p(-miss[:, 0]))
     _within(loss, small, small * 2.0 ** -15)
+
+
+@pytest.mark.parametrize("t, k, v", [(8192, 64, 70001), (20000, 64, 30011)])
+def test_few_tokens_that_count_over_pieces_of_the_vocabulary(ddl, t, k, v):
+    """Every piece's products take the same number of planes, from a scale that the launch or a pass of its own made: the bound of
+    three planes, (3 + 4 c + sqrt(t / 64 c)) u with c = 4, for each half of the vocabulary."""
+    h = Head(t, k, v, "bf16", seed=33, ignored=0.98, sure=0.0)
+    h.w.mul_(0.02)
+    h.solve()
+    dw, dx = torch.empty(v, k, device="cuda"), torch.empty_like(h.x)
+    with ddl.CrossEntropy(k, v, t, "bf16") as head:
+        _, lse = h.forward(ddl, head)
+        head.backward(h.x, h.w, h.labels, lse, dloss=h.dloss, dx=dx, dw=dw)
+        head.check()
+    h.check_backward(dx)
+    p = torch.exp(h.z - lse.double()[:, None])
+    p[torch.arange(t, device="cuda"), h.labels.clamp(min=0)] -= 1.0
+    want = (p * torch.where(h.valid, h.dloss.double(), 0.0)[:, None]).t() @ h.x.double()
+    for part in (slice(0, v // 2), slice(v // 2, v)):
+        assert float((dw[part].double() - want[part]).norm() / want[part].norm()) <= (3 + 16 + math.sqrt(t / 256)) * U["f32"]
