@@ -567,15 +567,15 @@ ddl_status_t ddl_xent_forward(ddl_xent_t xent, size_t tokens, const void* x, siz
  * Rounding.  z, lse and dz are binary32 numbers, so that dz / dloss is off by up
  * to 2^-23 |lse| (and the logits' own error) of the probability, which is taken as
  * zero below 2^-126: of a token that the model is nearly sure of, whose dz is
- * small, that can be most of it, though its loss keeps more.  From there dz is kept to the 16 bits of the handle's type
- * in dx (the label's, which is most of it where the label is not likely, to 24)
- * and in binary16 gradients of a DDL_FP16 handle; in other gradients dw takes it
- * to 22 bits (DDL_FP16) or 16 (DDL_BF16; 24 in binary32 gradients if at most 4096
- * tokens of the call have a label and a dloss that is not zero).  On the way dz is
- * divided by the largest |dloss| of the call (taken as 2^-100 or 2^100 where it
- * lies outside), so that the size of all of them does not matter.  In a DDL_FP16
- * handle parts of dz below 2^-28 of the largest |dloss| lose bits, up to 2^-39 of
- * it each in dx and binary16 dw. */
+ * small, that can be most of it, though its loss keeps more.  From there dz is
+ * kept to the 16 bits of the handle's type in dx (the label's, which is most of it
+ * where the label is not likely, to 24) and in binary16 gradients of a DDL_FP16
+ * handle; in other gradients dw takes it to 22 bits (DDL_FP16) or 16 (DDL_BF16; 24
+ * in binary32 gradients if at most 4096 tokens of the call have a label and a
+ * dloss that is not zero).  On the way dz is divided by the largest |dloss| of the
+ * call (taken as 2^-100 or 2^100 where it lies outside), so that the size of all
+ * of them does not matter.  In a DDL_FP16 handle parts of dz below 2^-28 of the
+ * largest |dloss| lose bits, up to 2^-39 of it each in dx and binary16 dw. */
 ddl_status_t ddl_xent_backward(ddl_xent_t xent, size_t tokens, const void* x, size_t ldx, const void* w, size_t ldw,
                                const void* bias, const int64_t* labels, const float* lse, const float* dloss, void* dx,
                                size_t lddx, void* dw, size_t lddw, void* db, ddl_dtype_t grad_dtype, int accumulate,
